@@ -38,10 +38,13 @@ PA_TC_TILE_ROWS = 64
 PA_PF_TILE_ROWS = 128
 PA_PF_PAIR_ROWS = 256
 
-# Every symbol include/*.h declares (pa.h, the attention ABI; pa_probe.h, the
-# HBM read probe; pa_testing.h, the test hook).
+# Every symbol include/*.h declares (pa.h, the attention ABI; pa_cache.h, the
+# norms, rotation and 8-bit cache; pa_tree.h, attention for drafted tokens;
+# pa_probe.h, the HBM read probe; pa_testing.h, the test hook).
 EXPORTS = ("pa_plan", "pa_forward", "pa_forward_noalloc", "pa_plan_bounds", "pa_plan_device",
            "pa_forward_device_plan", "pa_status_clear", "pa_status_read", "pa_status_string",
+           "pa_qk_norm_rope", "pa_cache_write", "pa_cache_store", "pa_cache_read",
+           "pa_tree_workspace", "pa_tree_forward",
            "pa_hbm_read_probe", "pa_testing_set_wait_limit")
 PA_PLAN_COUNTS = 4
 
@@ -49,6 +52,11 @@ PA_STATUS_BIT_BLOCK_INDEX = 1
 PA_STATUS_BIT_TIMEOUT = 2
 PA_STATUS_BIT_WORKSPACE = 4
 PA_STATUS_BIT_PLAN = 8
+PA_STATUS_BIT_POSITION = 16
+PA_STATUS_BIT_TREE = 32
+
+# Most current tokens of a sequence that pa_tree_forward takes with parents.
+PA_TREE_MAX_TOKENS = 256
 
 # Size of the device array pa_forward_noalloc uses as its workspace.
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -114,6 +122,19 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.pa_status_read.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_status_string.argtypes = [ctypes.c_int]
+    lib.pa_qk_norm_rope.restype = ctypes.c_int
+    lib.pa_qk_norm_rope.argtypes = [P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P]
+    lib.pa_cache_write.restype = ctypes.c_int
+    lib.pa_cache_write.argtypes = [P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P]
+    lib.pa_cache_store.restype = ctypes.c_int
+    lib.pa_cache_store.argtypes = [P, P, i64, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P, P, P,
+                                   P, P, P]
+    lib.pa_cache_read.restype = ctypes.c_int
+    lib.pa_cache_read.argtypes = [P, P, P, P, P, P, P, P, P, i64, P, P, P, P]
+    lib.pa_tree_workspace.restype = ctypes.c_int
+    lib.pa_tree_workspace.argtypes = [cfgp, P]
+    lib.pa_tree_forward.restype = ctypes.c_int
+    lib.pa_tree_forward.argtypes = [cfgp, i64, P, P, P, P, P, P, P, P, P, P, sz, P, P]
     lib.pa_hbm_read_probe.restype = ctypes.c_int
     lib.pa_hbm_read_probe.argtypes = [P, sz, ctypes.c_int, P, P]
     lib.pa_testing_set_wait_limit.restype = ctypes.c_int
@@ -643,3 +664,7 @@ class GraphStep:
 
     def status(self):
         return pa_status_read(self.workspace, self.stream)
+
+
+from .serving import (QuantCache, TreeStep, pa_cache_config, pa_qk_norm_rope,  # noqa: E402
+                      pa_rotary, pa_tree_workspace)

@@ -10,7 +10,9 @@
 #include <mutex>
 
 #include "pa.h"
+#include "pa_cache.h"
 #include "pa_testing.h"
+#include "pa_tree.h"
 #include "pa_combine.cuh"
 #include "pa_decode_mma.cuh"
 #include "pa_decode_wide.cuh"
@@ -471,7 +473,8 @@ extern "C" pa_status pa_status_read(const void* workspace, void* stream_, uint32
   if (v & PA_STATUS_BIT_TIMEOUT) return PA_ERR_TIMEOUT;
   if (v & PA_STATUS_BIT_BLOCK_INDEX) return PA_ERR_BLOCK_INDEX;
   if (v & PA_STATUS_BIT_WORKSPACE) return PA_ERR_BUFFER_TOO_SMALL;
-  if (v & PA_STATUS_BIT_PLAN) return PA_ERR_INVALID_ARG;
+  if (v & (PA_STATUS_BIT_PLAN | PA_STATUS_BIT_POSITION | PA_STATUS_BIT_TREE))
+    return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
 

@@ -1,0 +1,44 @@
+// The 8-bit cache's element: an e4m3 code times a power of two kept per row
+// (pa_cache.h). Conversions are the hardware's (cvt.rn to and from e4m3x2);
+// the exponents are handled as bits.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace pa {
+
+constexpr int kExpMin = -32;   // least exponent a row is held with
+constexpr int kExpBias = 127;  // of the exponent byte
+
+// e: the least integer >= kExpMin with a <= 448 * 2^e, a >= 0 finite.
+// 448 = 1.75 * 2^8, so e = k - 8 for a = m * 2^k with m <= 1.75, else k - 7
+// (zero and subnormal a have k = -127 here and end at kExpMin).
+__device__ __forceinline__ int row_exponent(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int k = int(u >> 23) - 127;
+  const int e = k - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, kExpMin);
+}
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// Two values to e4m3 (lo in the low byte): nearest even, NaN for a non-finite.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  lo = isfinite(lo) ? lo : __uint_as_float(0x7fc00000u);
+  hi = isfinite(hi) ? hi : __uint_as_float(0x7fc00000u);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two e4m3 codes (low 16 bits) to fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(codes)));
+  return r;
+}
+
+}  // namespace pa

@@ -1,0 +1,77 @@
+// What the kernels of pa_tree_forward share: their parameters, the lookup of a
+// token's sequence, and the walk from a draft to its root.
+#pragma once
+
+#include "pa_device.cuh"
+#include "pa_e4m3.cuh"
+#include "pa_tree.h"
+
+namespace pa {
+
+constexpr int kTreeWords = PA_TREE_MAX_TOKENS / 32;  // ancestor bits of one draft
+
+struct TreeParams {
+  const __half* query;
+  const uint8_t *key_cache, *value_cache;  // fp16 or e4m3 bytes
+  const uint8_t *key_exps, *value_exps;
+  const int32_t *block_tables, *context_lens, *q_seqlens, *parents;
+  __half* out;
+  uint32_t* status;
+  int64_t tokens;
+  int batch, num_heads, kv_heads, group, hk, hv, block_size, num_blocks, max_blocks_per_seq;
+  int max_q;
+  float scale_log2;  // scale * log2(e)
+};
+
+// Whether sequence b's lengths keep the constraints.
+__device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int L) {
+  return q >= 0 && q <= P.max_q && L >= q &&
+         int64_t(L) <= int64_t(P.max_blocks_per_seq) * P.block_size;
+}
+
+// Sequence and index in it of token t (warp-collective); -1 past the last one.
+// A length out of range counts as its nearest valid one here, so that the
+// rows of the other sequences do not depend on the launch's shape.
+__device__ __forceinline__ int tree_sequence(const TreeParams& P, int64_t t, int lane, int& index) {
+  index = 0;
+  if (!P.q_seqlens) return t < P.batch ? int(t) : -1;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < P.batch; b0 += 32) {
+    const int n = b0 + lane < P.batch ? min(max(P.q_seqlens[b0 + lane], 0), P.max_q) : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, n > 0 && t >= before + sum - n && t < before + sum);
+    if (who) {
+      const int l = __ffs(who) - 1;
+      index = int(t - before) - __shfl_sync(0xffffffffu, sum - n, l);
+      return b0 + l;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return -1;
+}
+
+// Ancestor bits of draft i (itself among them) of the sequence whose parents
+// begin at `parents`. A parent must come before its child, so the walk ends.
+__device__ __forceinline__ void tree_ancestors(const TreeParams& P, const int32_t* parents, int i,
+                                               uint32_t (&bits)[kTreeWords]) {
+#pragma unroll
+  for (int w = 0; w < kTreeWords; ++w) bits[w] = 0;
+  while (true) {
+#pragma unroll
+    for (int w = 0; w < kTreeWords; ++w)
+      if (i >> 5 == w) bits[w] |= 1u << (i & 31);
+    const int up = parents[i];
+    if (up < 0 || up >= i) {
+      if (up != -1) set_status(P.status, PA_STATUS_BIT_TREE);
+      return;
+    }
+    i = up;
+  }
+}
+
+}  // namespace pa

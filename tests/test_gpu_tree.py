@@ -1,0 +1,305 @@
+"""pa_tree_forward on the GPU against the 64-bit reference: trees, chains and
+single tokens, over the fp16 and the 8-bit cache."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_kv_cache_206_gb300 as pa
+from . import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    torch.cuda.set_device(0)
+    return torch
+
+
+def up(torch, a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Case:
+    """A batch with its caches, on the host and on the GPU. Every cache slot
+    that no sequence uses holds NaN (and exponent bytes of 255)."""
+
+    def __init__(self, torch, bits, q, ctx, H, Hk, hk, hv, bs, kind, seed=0, sigma=1.0, behind=0,
+                 scale=0.0, poison=None):
+        rng = np.random.default_rng(seed + 13 * len(q) + hk)
+        self.batch = batch = ref.make_batch(rng, q, ctx, bs)
+        self.parents = ref.trees(rng, q, kind)
+        T = int(batch.q.sum())
+        self.tokens = T
+        self.query = rng.normal(size=(T + behind, H, hk)).astype(np.float16)
+        used = np.zeros((batch.num_blocks, bs), bool)
+        for b in range(len(q)):
+            used[batch.slots(b, 0, int(batch.ctx[b]))] = True
+        self.dev, self.real, self.exp = [], [], []
+        for hs in (hk, hv):
+            x = (sigma * rng.normal(size=(batch.num_blocks, bs, Hk, hs))
+                 * 2.0 ** rng.integers(-3, 2, (batch.num_blocks, bs, Hk, 1))).astype(np.float16)
+            if poison:
+                poison(self, x)
+            if bits == 8:
+                codes, e = ref.quantise(x.astype(np.float64))
+                codes[~used], be = 0x7F, (e + 127).astype(np.uint8)
+                be[~used] = 255
+                self.real.append(ref.decode(codes) * 2.0 ** e[..., None].astype(np.float64))
+                self.exp.append(np.swapaxes(e, 1, 2))
+                self.dev.append((up(torch, codes).view(torch.float8_e4m3fn),
+                                 up(torch, np.swapaxes(be, 1, 2))))
+            else:
+                x[~used] = np.nan
+                self.real.append(x.astype(np.float64))
+                self.exp.append(np.zeros((batch.num_blocks, Hk, bs)))
+                self.dev.append((up(torch, x), None))
+        self.scale = scale if scale > 0 else 1 / math.sqrt(hk)
+        (k, ke), (v, ve) = self.dev
+        self.step = pa.TreeStep(k, v, ke, ve, batch=len(q), num_heads=H, max_seqlen_q=max(max(q), 1),
+                                max_blocks_per_seq=batch.tables.shape[1], scale=scale)
+        par = None if self.parents is None else np.concatenate([self.parents, np.full(behind, 99, np.int32)])
+        self.args = [up(torch, a) for a in (self.query, batch.tables, batch.ctx, batch.q, par)]
+        self.out = torch.full((T + behind, H, hv), 7.0, dtype=torch.float16, device="cuda")
+
+    def run(self, stream=None):
+        return self.step.run(*self.args, self.out, stream=stream)
+
+    def check(self):
+        want, bound = ref.tree_attention(self.query[:self.tokens], *self.real, *self.exp, self.batch,
+                                         self.parents, self.scale)
+        got = self.out.cpu().numpy().astype(np.float64)
+        assert (got[self.tokens:] == 7).all()
+        err = np.abs(got[:self.tokens] - want)
+        assert np.isfinite(got).all()
+        assert (err <= bound).all(), (float((err / bound).max()), np.argwhere(err > bound)[:4])
+
+
+# q, ctx, H, Hk, hk, hv, block, kind
+CASES = [
+    ([1], [1], 1, 1, 64, 64, 16, "chain"),
+    ([1], [1], 32, 8, 128, 128, 128, "tree"),
+    ([1, 1, 1], [15, 16, 17], 8, 2, 128, 128, 16, "chain"),
+    ([1, 1], [1000, 333], 32, 8, 128, 128, 64, "chain"),
+    ([4, 4], [4, 517], 4, 4, 128, 128, 128, "chain"),
+    ([5, 0, 16, 1], [5, 40, 100, 77], 8, 2, 64, 64, 48, "tree"),
+    ([16, 3], [300, 64], 32, 8, 128, 128, 32, "tree"),
+    ([7], [200], 6, 3, 256, 256, 64, "tree"),
+    ([2, 9], [70, 31], 16, 1, 256, 256, 16, "star"),
+    ([64], [64], 8, 2, 128, 128, 64, "tree"),
+    ([64, 17], [700, 90], 8, 2, 128, 128, 128, "line"),
+    ([33], [2100], 4, 4, 64, 64, 128, "roots"),
+    ([256], [300], 2, 2, 64, 64, 64, "tree"),
+    ([100, 256], [100, 1000], 4, 1, 128, 128, 128, "tree"),
+    ([300], [400], 4, 2, 128, 128, 128, "chain"),
+    ([3, 2], [40, 9], 4, 2, 48, 80, 16, "tree"),
+    ([2], [50], 3, 1, 576, 512, 32, "tree"),
+    ([1] * 70, list(range(1, 71)), 4, 2, 64, 64, 16, "chain"),
+    ([8] * 3, [5000, 8, 2500], 28, 4, 128, 128, 128, "tree"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+@pytest.mark.parametrize("bits", [8, 16])
+def test_tree(torch, bits, case):
+    c = Case(torch, bits, *case, behind=2)
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    c.check()
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("sigma", [2.0**-9, 30.0])
+def test_small_and_large_values(torch, bits, sigma):
+    c = Case(torch, bits, [6, 1], [90, 200], 8, 2, 128, 128, 16, "tree", sigma=sigma, scale=0.01)
+    c.run()
+    c.check()
+
+
+def test_line_is_a_chain(torch):
+    """A tree whose every draft follows the one before is the chain, bit for bit."""
+    a = Case(torch, 8, [20, 7], [400, 7], 8, 2, 128, 128, 64, "line")
+    a.run()
+    got = a.out.clone()
+    a.args[4] = None
+    a.run()
+    assert torch.equal(got, a.out)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("shape", [(2, 2, 64, 64), (8, 2, 128, 128), (16, 1, 128, 128), (4, 1, 256, 256),
+                                   (2, 1, 48, 32)], ids=str)
+@pytest.mark.parametrize("bad", ["key", "value"])
+def test_drafts_that_a_row_does_not_see_do_not_touch_it(torch, bits, shape, bad):
+    """NaN and infinities in one draft's key or value reach exactly the rows
+    that have it among their ancestors."""
+    H, Hk, hk, hv = shape
+    q, ctx = [9, 12], [50, 12]
+    hit = [(0, 4), (1, 0), (1, 7)]  # (sequence, draft)
+
+    def poison(case, x):
+        which = len(case.real)  # 0 while the keys are made, 1 for the values
+        if (which == 0) != (bad == "key"):
+            return
+        for n, (b, i) in enumerate(hit):
+            blk, off = case.batch.slots(b, ctx[b] - q[b] + i, ctx[b] - q[b] + i + 1)
+            x[blk[0], off[0], :, n % 3] = [np.nan, np.inf, -np.inf][n % 3]
+
+    c = Case(torch, bits, q, ctx, H, Hk, hk, hv, 16, "tree", poison=poison)
+    c.run()
+    got = c.out.cpu().numpy()
+    touched = np.zeros(len(got), bool)
+    for b, i in hit:
+        t0 = int(c.batch.starts[b])
+        m = ref.sees(q[b], c.parents[t0:t0 + q[b]])
+        touched[t0:t0 + q[b]] |= m[:, i]
+    assert touched.any() and not touched.all()
+    assert np.isfinite(got[~touched]).all()
+    broken = ~np.isfinite(got[touched]).all(axis=(1, 2))
+    if bad == "value":
+        assert broken.all()
+    # the rows that do not see it are what they are without it
+    clean = Case(torch, bits, q, ctx, H, Hk, hk, hv, 16, "tree")
+    clean.run()
+    want, bound = ref.tree_attention(clean.query, *clean.real, *clean.exp, clean.batch, clean.parents,
+                                     clean.scale)
+    err = np.abs(got.astype(np.float64) - want)
+    assert (err[~touched] <= bound[~touched]).all()
+
+
+def test_bad_parents_lengths_and_blocks(torch):
+    c = Case(torch, 8, [4, 3], [40, 30], 8, 2, 128, 128, 16, "tree")
+    c.run()
+    good = c.out.clone()
+    par = c.parents.copy()
+    par[2], par[5] = 2, -7  # a draft that follows itself, and no draft at all: both roots
+    c.args[4] = up(torch, par)
+    c.run()
+    st, bits = c.step.status()
+    assert st == pa.PA_ERR_INVALID_ARG and bits == pa.PA_STATUS_BIT_TREE
+    par[2] = par[5] = -1
+    c.parents = par
+    c.check()
+    pa.pa_status_clear(c.step.workspace)
+    c = Case(torch, 8, [4, 3], [40, 30], 8, 2, 128, 128, 16, "tree")
+    ctx = c.batch.ctx.copy()
+    ctx[0] = 3
+    c.args[2] = up(torch, ctx)
+    c.run()
+    assert c.step.status() == (pa.PA_ERR_INVALID_ARG, pa.PA_STATUS_BIT_PLAN)
+    assert (c.out[:4] == 7).all() and torch.equal(c.out[4:], good[4:])
+    c = Case(torch, 8, [4, 3], [40, 30], 8, 2, 128, 128, 16, "tree")
+    tables = c.batch.tables.copy()
+    tables[0, 1] = c.batch.num_blocks
+    c.args[1] = up(torch, tables)
+    c.run()
+    assert c.step.status() == (pa.PA_ERR_BLOCK_INDEX, pa.PA_STATUS_BIT_BLOCK_INDEX)
+    assert torch.equal(c.out[4:], good[4:])
+
+
+def test_captured_and_replayed_with_other_lengths(torch):
+    c = Case(torch, 8, [8, 8], [900, 900], 32, 8, 128, 128, 64, "tree")
+    s = torch.cuda.Stream()
+    c.run(stream=s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        c.run()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check()
+    # shorter contexts: the same blocks, whose first tokens are all there
+    c.batch.ctx[:] = [333, 8]
+    c.args[2].copy_(up(torch, c.batch.ctx))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check()
+
+
+def test_one_step_of_speculation(torch):
+    """Store a prompt, then store a tree of drafts and attend it over the cache;
+    the prompt read back feeds the fp16 forward pass with the same result."""
+    rng = np.random.default_rng(11)
+    H, Hk, d, bs = 8, 2, 128, 16
+    ctx, q = np.array([37, 80], np.int32), np.array([6, 9], np.int32)
+    batch = ref.make_batch(rng, q, ctx + q, bs)
+    parents = ref.trees(rng, q, "tree")
+    cos = np.arange(200)[:, None] * 10000.0 ** (-np.arange(0, d, 2) / d)
+    table = up(torch, np.concatenate([np.cos(cos), np.sin(cos)], 1).astype(np.float32))
+    w = up(torch, (1 + 0.1 * rng.normal(size=d)).astype(np.float16))
+    cache = pa.QuantCache.empty(batch.num_blocks, bs, Hk, d)
+    tables = up(torch, batch.tables)
+
+    def project(n):
+        x = up(torch, rng.normal(size=(n, H + 2 * Hk, d)).astype(np.float16))
+        return x[:, :H], x[:, H:H + Hk], x[:, H + Hk:]
+
+    T = int(ctx.sum())
+    qo = torch.empty((T, H, d), dtype=torch.float16, device="cuda")
+    cache.store(*project(T), w, w, table, None, tables, up(torch, ctx), up(torch, ctx), int(ctx.max()), qo)
+    # the drafts' positions: the prompt's length plus their depth
+    depth = np.zeros(len(parents), np.int32)
+    for b in range(2):
+        t0 = int(batch.starts[b])
+        for i in range(q[b]):
+            p = parents[t0 + i]
+            depth[t0 + i] = ctx[b] if p < 0 else depth[t0 + p] + 1
+    n = int(q.sum())
+    qd = torch.empty((n, H, d), dtype=torch.float16, device="cuda")
+    cache.store(*project(n), w, w, table, up(torch, depth), tables, up(torch, ctx + q), up(torch, q),
+                int(q.max()), qd)
+    step = pa.TreeStep(cache.key, cache.value, cache.key_exps, cache.value_exps, batch=2, num_heads=H,
+                       max_seqlen_q=int(q.max()), max_blocks_per_seq=batch.tables.shape[1])
+    out = torch.empty((n, H, d), dtype=torch.float16, device="cuda")
+    step.run(qd, tables, up(torch, ctx + q), up(torch, q), up(torch, parents), out)
+    assert step.status() == (pa.PA_OK, 0)
+    # read back into an fp16 paged cache of its own blocks
+    need = -(-(ctx + q) // bs)
+    first = (np.cumsum(need) - need).astype(np.int32)
+    k16 = torch.zeros((int(need.sum()), bs, Hk, d), dtype=torch.float16, device="cuda")
+    v16 = torch.zeros_like(k16)
+    cache.read(tables, None, up(torch, ctx + q), up(torch, first * bs), int((ctx + q).max()),
+               k16.view(-1, Hk, d), v16.view(-1, Hk, d))
+    own = np.zeros((2, int(need.max())), np.int32)
+    for b in range(2):
+        own[b, :need[b]] = first[b] + np.arange(need[b])
+    half = pa.TreeStep(k16, v16, batch=2, num_heads=H, max_seqlen_q=int(q.max()),
+                       max_blocks_per_seq=own.shape[1])
+    out16 = torch.empty_like(out)
+    half.run(qd, up(torch, own), up(torch, ctx + q), up(torch, q), up(torch, parents), out16)
+    real = [t.double().cpu().numpy() for t in (k16, v16)]
+    nowhere = np.zeros((len(k16), Hk, bs))
+    flat = ref.Batch(own, ctx + q, q, bs, len(k16))
+    want, bound = ref.tree_attention(qd.cpu().numpy(), *real, nowhere, nowhere, flat, parents,
+                                     1 / math.sqrt(d))
+    # (the bound of the 8-bit cache is the larger one: weights relative to the largest p 2^ev)
+    ev = cache.value_exps.cpu().numpy().astype(np.float64) - 127
+    ev_own = np.zeros_like(nowhere)
+    for b in range(2):
+        ev_own[own[b, :need[b]]] = ev[batch.tables[b, :need[b]]]
+    _, wide = ref.tree_attention(qd.cpu().numpy(), *real, nowhere, ev_own, flat, parents, 1 / math.sqrt(d))
+    for got, limit in ((out16, bound), (out, np.maximum(bound, wide))):
+        assert (np.abs(got.cpu().numpy() - want) <= limit).all()
+    # the plain forward pass of the framework, on single tokens over the same cache
+    cfg = pa.make_config(batch=2, num_heads=H, kv_heads=Hk, head_size_k=d, block_size=bs,
+                         num_blocks=len(k16), max_blocks_per_seq=own.shape[1], num_sms=8)
+    plan = pa.pa_plan(cfg, ctx)
+    q1 = qo[[int(ctx[0]) - 1, T - 1]].contiguous()
+    a, b = torch.empty_like(q1), torch.empty_like(q1)
+    ws = torch.zeros(max(plan.workspace_bytes, 256), dtype=torch.uint8, device="cuda")
+    comb = up(torch, plan.combine) if len(plan.combine) else None
+    pa.pa_forward(cfg, q1, k16, v16, up(torch, own), up(torch, ctx), None, None, None, up(torch, plan.work),
+                  comb, ws, a)
+    one = pa.TreeStep(k16, v16, batch=2, num_heads=H, max_seqlen_q=1, max_blocks_per_seq=own.shape[1])
+    one.run(q1, up(torch, own), up(torch, ctx), None, None, b)
+    flat = ref.Batch(own, ctx, np.ones(2, np.int32), bs, len(k16))
+    want, bound = ref.tree_attention(q1.cpu().numpy(), *real, nowhere, nowhere, flat, None,
+                                     1 / math.sqrt(d))
+    # pa_forward rounds each split's partial row to fp16 as well: 2^-11 of the magnitudes
+    mags, _ = ref.tree_attention(q1.cpu().numpy(), real[0], np.abs(real[1]), nowhere, nowhere, flat, None,
+                                 1 / math.sqrt(d))
+    assert (np.abs(b.cpu().numpy() - want) <= bound).all()
+    assert (np.abs(a.cpu().numpy() - want) <= bound + 2.0**-11 * mags).all()
