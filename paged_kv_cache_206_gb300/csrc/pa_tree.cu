@@ -1,11 +1,11 @@
-// Attention for drafted tokens over a paged cache (pa_tree.h): the C entry and
-// the kernel for any head sizes.
+// Attention for drafted tokens over a paged cache (pa_tree.h): the C entry, the
+// choice of the kernel, and the kernel for any head sizes.
 #include <cuda_runtime.h>
 
 #include <cmath>
 
 #include "pa_internal.h"
-#include "pa_tree.cuh"
+#include "pa_tree_mma.cuh"
 
 namespace pa {
 
@@ -154,6 +154,23 @@ pa_status check_tree(const pa_config* cfg) {
   return PA_OK;
 }
 
+// The kernel for these head sizes and rows, if there is a faster one than
+// tree_any_kernel: the warp-level tensor instructions with the narrowest of
+// their 8-, 16- and 32-row tiles (16 at most for 256 dims) that holds a kv head's
+// rows, or several of the widest.
+bool tree_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws,
+                cudaStream_t stream, cudaError_t* e) {
+  if (c.head_size_k != c.head_size_v) return false;
+  const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
+  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  switch (c.head_size_k) {
+    case 64: *e = tree_mma_64(P, q8, nt, c.num_sms, need, ws, stream); return true;
+    case 128: *e = tree_mma_128(P, q8, nt, c.num_sms, need, ws, stream); return true;
+    case 256: *e = tree_mma_256(P, q8, nt, c.num_sms, need, ws, stream); return true;
+  }
+  return false;
+}
+
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
@@ -164,7 +181,14 @@ extern "C" pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_b
   const pa_status st = pa::check_tree(cfg);
   if (st != PA_OK) return st;
   if (!workspace_bytes) return PA_ERR_INVALID_ARG;
+  // the larger of the two caches' needs, so that it does not depend on them
   *workspace_bytes = PA_STATUS_BYTES;
+  for (const bool q8 : {false, true}) {
+    size_t need = 0;
+    cudaError_t e;
+    if (pa::tree_tiles(*cfg, pa::TreeParams{}, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
+      *workspace_bytes = need;
+  }
   return PA_OK;
 }
 
@@ -217,6 +241,9 @@ extern "C" pa_status pa_tree_forward(const pa_config* cfg, int64_t tokens, const
   P.max_q = int(max_q(c));
   P.scale_log2 = (c.scale > 0.f ? c.scale : 1.0f / std::sqrt(float(c.head_size_k))) * kLog2e;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  cudaError_t e = cudaSuccess;
+  if (tree_tiles(c, P, key_exps != nullptr, nullptr, workspace, stream, &e))
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   const unsigned grid = unsigned(tokens * c.num_heads);
   if (key_exps) tree_any_kernel<true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
   else tree_any_kernel<false><<<grid, kAnyWarps * 32, 0, stream>>>(P);
