@@ -25,8 +25,12 @@
 // reaches the drafts takes the non-finite elements out of its V rows, and adds
 // them at the end to the rows that do see them.
 //
-// Every warp streams its keys through a ring of its own with cp.async, so there
-// is no block-wide barrier between the ends of a tile.
+// Every warp is a worker of its own (pa_tree_split.cuh): it streams the keys of
+// its piece of the line through a ring with cp.async, from one tile into the
+// next without a pause, and keeps its rows' state in registers until a tile ends. There
+// is no block-wide barrier. (With a CTA as the worker, its four warps taking
+// turns at a tile's keys and merging in shared memory, the SMs stood idle 42 % of the
+// time at 64 decode steps of 1 to 4096 tokens: every tile end drained four rings.)
 #pragma once
 
 #include "pa_decode_mma.cuh"
@@ -34,29 +38,43 @@
 
 namespace pa {
 
+// A tile of the line, as the key stream leaves it for the arithmetic.
+struct TreeTile {
+  int b, q_start, q, L, kvh, r0, s0, s1;  // units [s0, s1)
+  int slot;                               // of a partial result; -1: the whole tile
+  int pad[3];
+};
+
 template <int HD, bool Q8, int NT>
 struct TreeMma {
   static constexpr int kWarps = 4;
   static constexpr int kRowBytes = HD * (Q8 ? 1 : 2);
-  static constexpr int kChunks = kRowBytes / 16;            // 16-byte chunks of a row
-  static constexpr int kElems = Q8 ? 16 : 8;                // elements of a chunk
-  static constexpr int kSub = kRowBytes <= 128 ? 32 : 16;   // keys a warp takes at a time
+  static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
+  static constexpr int kElems = Q8 ? 16 : 8;      // elements of a chunk
+  static constexpr int kSub = kRowBytes <= 128 && NT == 1 ? 32 : 16;  // keys a warp takes at a time
   static constexpr int kMT = kSub / 16;
   static constexpr int kRows = 8 * NT;
-  static constexpr uint32_t kV = kSub * kRowBytes;          // V behind K in a stage
-  static constexpr uint32_t kExps = 2 * kV;                 // then 2 x kSub exponent bytes
+  static constexpr int kLead = 2;
+  static constexpr uint32_t kV = kSub * kRowBytes;  // V behind K in a stage
+  static constexpr uint32_t kExps = 2 * kV;         // then 2 x 32 exponent bytes
   static constexpr uint32_t kStage = 2 * kV + (Q8 ? 64 : 0);
-  static constexpr int kCtas = kStage > 9000 ? 1 : 2;       // CTAs of an SM
-  static constexpr int kStages = HD == 64 && Q8 ? 5 : 3;
-  static constexpr uint32_t kRing = kWarps * kStages * kStage;
-  static constexpr int kMergeStride = HD + 4;               // floats of a merge row
-  static constexpr uint32_t kMerge = kWarps * kRows * (kMergeStride + 2) * 4;
-  static_assert(kMerge <= kRing, "the merge reuses the ring");
-  static constexpr uint32_t q_off = kRing;
-  static constexpr uint32_t mask_off = q_off + kRows * HD * 2;
-  static constexpr uint32_t bad_off = mask_off + kRows * kTreeWords * 4;
-  static constexpr uint32_t bytes = bad_off + kTreeWords * 4;
-  static_assert(bytes * kCtas + 1024 * kCtas <= 227 * 1024 + 1024, "shared memory");
+  static constexpr int kCtas = kStage > 9000 ? 1 : 2;  // CTAs of an SM
+  // a warp's shared memory: query fragments (tiles of 8 rows keep theirs in
+  // registers), what the rows see, the parents, the tiles ahead, the ring
+  static constexpr uint32_t kBudget = ((227 * 1024 - 1024 * kCtas) / kCtas / kWarps) & ~127u;
+  static constexpr int kTiles = 8;
+  static constexpr uint32_t q_off = 0;
+  static constexpr uint32_t mask_off = q_off + (NT > 1 ? kRows * HD * 2 : 0);
+  static constexpr uint32_t par_off = mask_off + kRows * kTreeWords * 4;
+  static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
+  static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
+  static constexpr uint32_t ring_off = (tile_off + kTiles * sizeof(TreeTile) + 127) & ~127u;
+  static constexpr int kFit = int((kBudget - ring_off) / kStage);
+  static constexpr int kStages = kFit < 5 ? kFit : 5;
+  static_assert(kStages >= 2 && kStages + 2 <= kTiles, "ring");
+  static constexpr uint32_t warp_bytes = (ring_off + kStages * kStage + 127) & ~127u;
+  static constexpr uint32_t bytes = kWarps * warp_bytes;
+  static_assert((bytes + 1024) * kCtas <= 228 * 1024, "shared memory");
 };
 
 // The chunk's place in its row: rows of a line or more spread over all banks.
@@ -97,127 +115,174 @@ template <int HD, bool Q8, int NT>
 __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     tree_mma_kernel(const TreeParams P, const TreeSplit S) {
   using Cfg = TreeMma<HD, Q8, NT>;
-  using Line = TreeLine<Cfg::kSub, Cfg::kRows>;
-  constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows, NW = Cfg::kWarps;
+  using Line = TreeLine<Cfg::kSub, Cfg::kRows, Cfg::kLead>;
+  constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows;
   constexpr int RB = Cfg::kRowBytes, C = Cfg::kChunks, E = Cfg::kElems;
-  constexpr int OT = HD / 16;  // m-tiles of O^T
+  constexpr int OT = HD / 16;  // m-tiles of O^T, k-steps of S^T
   constexpr unsigned FULL = 0xffffffffu;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * (Cfg::kStages * Cfg::kStage);
+  uint8_t* smem = smem_all + warp * Cfg::warp_bytes;
   uint8_t* q_s = smem + Cfg::q_off;
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + Cfg::mask_off);
+  uint8_t* par_s = smem + Cfg::par_off;
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
+  TreeTile* tile_s = reinterpret_cast<TreeTile*>(smem + Cfg::tile_off);
+  uint8_t* ring = smem + Cfg::ring_off;
+  const int worker = blockIdx.x * Cfg::kWarps + warp;
 
   const int64_t total = Line::total(P, lane);
-  const int nact = Line::ctas(total, int(gridDim.x), S.min_units);
-  if (int(blockIdx.x) >= nact) return;
-  const int64_t u0 = Line::begin(total, blockIdx.x, nact), u1 = Line::begin(total, blockIdx.x + 1, nact);
-  if (u0 >= u1) return;
-  int64_t before;
-  int q_start;
-  int b = Line::find(P, u0, lane, before, q_start);
-  if (b < 0) return;
-  typename Line::Seq seq = Line::load(P, b);
+  const int nact = Line::active(total, S.workers, S.min_units);
+  if (worker >= nact) return;
+  const int64_t u0 = Line::begin(total, worker, nact), u1 = Line::begin(total, worker + 1, nact);
   const int G = P.group, bs = P.block_size;
   const int64_t row_stride = int64_t(P.kv_heads) * RB;
 
-  for (int64_t u = u0; u < u1;) {
-    while (u >= before + seq.total(P)) {
-      before += seq.total(P);
-      q_start += seq.q;
-      seq = Line::load(P, ++b);
+  // ---- the stream of units: where it stands on the line, and in its tile
+  int64_t u = u0, before = 0;
+  int q_start = 0, b = 0, made = 0;  // tiles left for the arithmetic so far
+  if (u0 < u1) b = Line::find(P, u0, lane, before, q_start);
+  if (u0 >= u1 || b < 0) return;
+  typename Line::Seq seq = Line::load(P, b);
+  int kvh = 0, unit = 0, unit_end = 0, win0 = 0, cur = 0, next = 0;
+  // Lane l holds the blocks of 16 keys each that the units to come need: MT a
+  // unit, 32 / MT units a window, and the next window's.
+  constexpr int WIN = 32 / MT;
+  auto blocks_of = [&](int n0) {
+    const int key = (n0 + lane / MT) * SUB + (lane % MT) * 16;
+    return n0 + lane / MT < unit_end && key < seq.L
+               ? P.block_tables[int64_t(b) * P.max_blocks_per_seq + key / bs] : 0;
+  };
+  auto next_tile = [&]() {
+    while (u < u1) {
+      while (u >= before + seq.total(P)) {
+        before += seq.total(P);
+        q_start += seq.q;
+        seq = Line::load(P, ++b);
+      }
+      const int tile = int((u - before) / seq.places()), p0 = int((u - before) % seq.places());
+      const int p1 = int(min(int64_t(seq.places()), p0 + (u1 - u)));
+      const bool first = u == u0;
+      u += p1 - p0;
+      unit = max(p0 - Cfg::kLead, 0);
+      unit_end = max(p1 - Cfg::kLead, 0);
+      if (unit == unit_end) continue;  // nothing but a lead: the next worker's
+      kvh = tile / seq.tiles;
+      if (lane == 0) {
+        TreeTile& t = tile_s[made % Cfg::kTiles];
+        t.b = b;
+        t.q_start = q_start;
+        t.q = seq.q;
+        t.L = seq.L;
+        t.kvh = kvh;
+        t.r0 = (tile % seq.tiles) * NR;
+        t.s0 = unit;
+        t.s1 = unit_end;
+        t.slot = unit == 0 && unit_end == seq.units ? -1 : 2 * worker + (first ? 0 : 1);
+      }
+      ++made;
+      win0 = unit;
+      cur = blocks_of(unit);
+      next = blocks_of(unit + WIN);
+      return true;
     }
-    const int tile = int((u - before) / seq.units);
-    const int s0 = int((u - before) % seq.units);
-    const int s1 = int(min(int64_t(seq.units), s0 + (u1 - u)));
-    const int kvh = tile / seq.tiles, r0 = (tile % seq.tiles) * NR;
-    const int L = seq.L, prefix = L - seq.q;
-    const bool drafts = s1 * SUB > prefix;  // the keys reach the current tokens
-    const int nmine = s1 - s0 > warp ? (s1 - s0 - warp + NW - 1) / NW : 0;
-
-    // ---- the keys' stream. Lane l holds the blocks of 16 keys each that the
-    // units to come need: MT a unit, 32 / MT units a window, and the next window's.
-    const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;
-    constexpr int WIN = 32 / MT;
-    auto blocks_of = [&](int n0) {
-      const int n = n0 + lane / MT;
-      const int key = (s0 + warp + n * NW) * SUB + (lane % MT) * 16;
-      return n < nmine && key < L ? table[key / bs] : 0;
-    };
-    int win0 = 0, cur = blocks_of(0), next = blocks_of(WIN);
-    auto issue = [&](int n) {
-      if (n < nmine) {
-        if (n >= win0 + WIN) {
-          win0 += WIN;
-          cur = next;
-          next = blocks_of(win0 + WIN);
+    return false;
+  };
+  int issued = 0;
+  auto issue = [&]() {
+    if (unit < unit_end || next_tile()) {
+      if (unit >= win0 + WIN) {
+        win0 += WIN;
+        cur = next;
+        next = blocks_of(win0 + WIN);
+      }
+      const uint32_t dst = smem_u32(ring + (issued % Cfg::kStages) * Cfg::kStage);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int block = __shfl_sync(FULL, cur, (unit - win0) * MT + m);
+        const int key = unit * SUB + m * 16;
+        const bool ok = block >= 0 && block < P.num_blocks;
+        if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+        const int place = key % bs;
+        const int64_t base = ok && key < seq.L ? (int64_t(block) * bs + place) * row_stride + int64_t(kvh) * RB : 0;
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k) {
+          const int at = lane + 32 * k, row = at / C, ch = at % C;
+          const bool in = ok && key + row < seq.L;
+          const int64_t off = in ? base + row * row_stride + ch * 16 : 0;
+          const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(ch, row) * 16;
+          cp_async16(to, P.key_cache + off, in);
+          cp_async16(to + Cfg::kV, P.value_cache + off, in);
         }
-        const uint32_t dst = smem_u32(ring + (n % Cfg::kStages) * Cfg::kStage);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int block = __shfl_sync(FULL, cur, (n - win0) * MT + m);
-          const int key = (s0 + warp + n * NW) * SUB + m * 16;
-          const bool ok = block >= 0 && block < P.num_blocks;
-          if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
-          const int place = key % bs;
-          const int64_t base = ok && key < L ? (int64_t(block) * bs + place) * row_stride + int64_t(kvh) * RB : 0;
-#pragma unroll
-          for (int k = 0; k < C / 2; ++k) {
-            const int at = lane + 32 * k, row = at / C, ch = at % C;
-            const bool in = ok && key + row < L;
-            const int64_t off = in ? base + row * row_stride + ch * 16 : 0;
-            const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(ch, row) * 16;
-            cp_async16(to, P.key_cache + off, in);
-            cp_async16(to + Cfg::kV, P.value_cache + off, in);
-          }
-          if constexpr (Q8) {
-            if (lane < 2) {
-              const bool in = ok && key < L;
-              const int64_t off = in ? (int64_t(block) * P.kv_heads + kvh) * bs + place : 0;
-              cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + off, in);
-            }
+        if constexpr (Q8) {
+          if (lane < 2) {
+            const bool in = ok && key < seq.L;
+            const int64_t off = in ? (int64_t(block) * P.kv_heads + kvh) * bs + place : 0;
+            cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + off, in);
           }
         }
       }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int n = 0; n < Cfg::kStages; ++n) issue(n);
+      ++unit;
+    }
+    ++issued;
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int n = 0; n < Cfg::kStages; ++n) issue();
 
-    // ---- the query tile as B fragments, and what its rows see of the drafts
-    for (int at = tid; at < NT * OT * 32; at += NW * 32) {
-      const int nt = at / (OT * 32), ks = at / 32 % OT, l = at % 32;
-      const int r = r0 + nt * 8 + (l >> 2), i = r / G;
-      const int s = ks / (E / 4), j = ks % (E / 4), lc = l & 3;
-      const int ch = C >= 8 ? 2 * lc + (s & 1) + 8 * (s >> 1) : lc;
-      const int64_t t = int64_t(q_start) + i;
-      uint2 v = make_uint2(0, 0);
-      if (i < seq.q && t < P.tokens)
-        v = *reinterpret_cast<const uint2*>(P.query + (t * P.num_heads + kvh * G + r % G) * HD + ch * E + 4 * j);
-      *reinterpret_cast<uint2*>(q_s + at * 8) = v;
+  int n = 0;  // units done
+  for (int done = 0; done < made; ++done) {
+    __syncwarp();
+    const TreeTile t = tile_s[done % Cfg::kTiles];
+    const int L = t.L, prefix = L - t.q;
+    const bool drafts = t.s1 * SUB > prefix;  // the keys reach the current tokens
+
+    // ---- the query rows as B fragments: dims of the chunks 2c, 2c + 1, ...
+    uint2 qf[NT == 1 ? OT : 1];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = t.r0 + nt * 8 + g, i = r / G;
+      const int64_t tok = int64_t(t.q_start) + i;
+      const bool in = i < t.q && tok < P.tokens;
+      const __half* src = P.query + (in ? (tok * P.num_heads + t.kvh * G + r % G) * HD : 0);
+#pragma unroll
+      for (int ks = 0; ks < OT; ++ks) {
+        const int s = ks / (E / 4), j = ks % (E / 4);
+        const int ch = C >= 8 ? 2 * c + (s & 1) + 8 * (s >> 1) : c;
+        const uint2 v = in ? *reinterpret_cast<const uint2*>(src + ch * E + 4 * j) : make_uint2(0, 0);
+        if constexpr (NT == 1) qf[ks] = v;
+        else *reinterpret_cast<uint2*>(q_s + ((nt * OT + ks) * 32 + lane) * 8) = v;
+      }
     }
-    if (tid < kTreeWords) bad_s[tid] = 0;
-    if (drafts && tid < NR) {
-      uint32_t bits[kTreeWords];
+    // ---- what the rows see of the drafts
+    if (drafts) {
+      if (lane < kTreeWords) bad_s[lane] = 0;
+      if (P.parents) {
+        // parents as bytes (255: a root), then every row's walk to its root
+        for (int i = lane; i < t.q; i += 32) {
+          const int up = int64_t(t.q_start) + i < P.tokens ? P.parents[t.q_start + i] : -1;
+          const bool ok = up >= -1 && up < i;
+          if (!ok) set_status(P.status, PA_STATUS_BIT_TREE);
+          par_s[i] = ok && up >= 0 ? uint8_t(up) : 255;
+        }
+        __syncwarp();
+        if (lane < NR) {
+          uint32_t* bits = mask_s + lane * kTreeWords;
 #pragma unroll
-      for (int w = 0; w < kTreeWords; ++w) bits[w] = 0;
-      const int i = (r0 + tid) / G;
-      if (P.parents && i < seq.q && int64_t(q_start) + i < P.tokens)
-        tree_ancestors(P, P.parents + q_start, i, bits);
-#pragma unroll
-      for (int w = 0; w < kTreeWords; ++w) mask_s[tid * kTreeWords + w] = bits[w];
+          for (int w = 0; w < kTreeWords; ++w) bits[w] = 0;
+          for (int i = (t.r0 + lane) / G; i < t.q; i = par_s[i]) {
+            bits[i >> 5] |= 1u << (i & 31);
+            if (par_s[i] == 255) break;
+          }
+        }
+      }
+      __syncwarp();
     }
-    int token[NT][2];  // of this lane's rows nt * 8 + 2 c + e
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) token[nt][e] = (r0 + nt * 8 + 2 * c + e) / G;
-    auto sees = [&](int row, int i, int a) {  // draft a from a row of draft i
-      return P.parents ? (mask_s[row * kTreeWords + (a >> 5)] >> (a & 31) & 1u) != 0 : a <= i;
+    auto sees = [&](int row, int a) {  // draft a from a row of the tile
+      return P.parents ? (mask_s[row * kTreeWords + (a >> 5)] >> (a & 31) & 1u) != 0
+                       : a <= (t.r0 + row) / G;
     };
-    __syncthreads();
 
     float m_run[NT][2], l_run[NT][2], o[OT][NT][4];
 #pragma unroll
@@ -228,46 +293,56 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       for (int k = 0; k < OT; ++k) o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
     }
 
-    for (int n = 0; n < nmine; ++n) {
+    for (int un = t.s0; un < t.s1; ++un, ++n) {
       cp_async_wait<Cfg::kStages - 1>();
       __syncwarp();
       uint8_t* kb = ring + (n % Cfg::kStages) * Cfg::kStage;
       uint8_t* vb = kb + Cfg::kV;
-      const int j0 = (s0 + warp + n * NW) * SUB;
+      const int j0 = un * SUB;
       const bool edge = j0 + SUB > prefix;
 
       // ---- S^T = K . Q^T
       float s[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
-        const uint8_t* row = kb + (mt * 16 + g) * RB;
 #pragma unroll
-        for (int sc = 0; sc < C / 4; ++sc) {
-          const int ch = tree_swz<C>(C >= 8 ? 2 * c + (sc & 1) + 8 * (sc >> 1) : c, g);
-          const uint4 xa = lds128(row + ch * 16), xb = lds128(row + 8 * RB + ch * 16);
-          const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa);
-          const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb);
+      for (int sc = 0; sc < C / 4; ++sc) {
+        const int ch = tree_swz<C>(C >= 8 ? 2 * c + (sc & 1) + 8 * (sc >> 1) : c, g);
+        uint4 xa[MT], xb[MT];
 #pragma unroll
-          for (int j = 0; j < E / 4; ++j) {
-            uint32_t a[4];
+        for (int mt = 0; mt < MT; ++mt) {
+          xa[mt] = lds128(kb + (mt * 16 + g) * RB + ch * 16);
+          xb[mt] = lds128(kb + (mt * 16 + 8 + g) * RB + ch * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+          const int ks = sc * (E / 4) + j;
+          uint32_t a[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[mt]);
+            const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[mt]);
             if constexpr (Q8) {
-              a[0] = e4m3x2_half2(wa[j]);
-              a[1] = e4m3x2_half2(wb[j]);
-              a[2] = e4m3x2_half2(wa[j] >> 16);
-              a[3] = e4m3x2_half2(wb[j] >> 16);
+              a[mt][0] = e4m3x2_half2(wa[j]);
+              a[mt][1] = e4m3x2_half2(wb[j]);
+              a[mt][2] = e4m3x2_half2(wa[j] >> 16);
+              a[mt][3] = e4m3x2_half2(wb[j] >> 16);
             } else {
-              a[0] = wa[2 * j];
-              a[1] = wb[2 * j];
-              a[2] = wa[2 * j + 1];
-              a[3] = wb[2 * j + 1];
+              a[mt][0] = wa[2 * j];
+              a[mt][1] = wb[2 * j];
+              a[mt][2] = wa[2 * j + 1];
+              a[mt][3] = wb[2 * j + 1];
             }
+          }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q = *reinterpret_cast<const uint2*>(q_s + ((nt * OT + sc * (E / 4) + j) * 32 + lane) * 8);
-              mma_16816(s[mt][nt], a, q.x, q.y);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 q;
+            if constexpr (NT == 1) q = qf[ks];
+            else q = *reinterpret_cast<const uint2*>(q_s + ((nt * OT + ks) * 32 + lane) * 8);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma_16816(s[mt][nt], a[mt], q.x, q.y);
           }
         }
       }
@@ -295,7 +370,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
               float& x = s[mt][nt][2 * hf + e];
               x = fmaf(x, f, add);
               if (edge) {
-                const bool in = key < prefix || (key < L && sees(nt * 8 + 2 * c + e, token[nt][e], key - prefix));
+                const bool in = key < prefix || (key < L && sees(nt * 8 + 2 * c + e, key - prefix));
                 if (!in) x = -INFINITY;
               }
             }
@@ -426,12 +501,11 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         }
       }
       __syncwarp();
-      issue(n + Cfg::kStages);
+      issue();
     }
-    cp_async_wait<0>();
-    if (u1 - u <= s1 - s0) launch_dependents();  // this CTA's last tile
+    if (u >= u1 && done + 1 == made) launch_dependents();  // this worker's last tile
 
-    // ---- the warps' states into shared memory, and merged
+    // ---- the end of a tile
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -442,75 +516,61 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         l += __shfl_xor_sync(FULL, l, 16);
         l_run[nt][e] = l;
       }
-    __syncthreads();  // every warp is done with its ring
-    float* o_s = reinterpret_cast<float*>(smem);
-    float2* ml_s = reinterpret_cast<float2*>(o_s + NW * NR * Cfg::kMergeStride);
-    constexpr int DL = HD / 8;  // dims of a lane's share, in runs of min(E, DL)
-    constexpr int RUN = E < DL ? E : DL;
+    constexpr int DL = HD / 8;             // dims of a lane's share of a row,
+    constexpr int RUN = E < DL ? E : DL;   // in runs of RUN next to one another
+    constexpr int KR = RUN / 2;            // m-tiles of a run
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int n = nt * 8 + 2 * c + e;
-        if (g == 0) ml_s[warp * NR + n] = make_float2(m_run[nt][e], l_run[nt][e]);
-        float* row = o_s + (warp * NR + n) * Cfg::kMergeStride;
+        const int row = nt * 8 + 2 * c + e, r = t.r0 + row, i = r / G;
+        const int64_t tok = int64_t(t.q_start) + i;
+        if (i >= t.q || tok >= P.tokens) continue;
+        if (drafts) {
+          // what was taken out of the product, for the rows that see it
+          for (int w = 0; w < kTreeWords; ++w) {
+            if (!bad_s[w]) continue;
+            for (int a = w * 32; a < t.q; ++a) {
+              const int key = prefix + a;
+              if ((a >> 5) % kTreeWords != w || !(bad_s[w] >> (a & 31) & 1) || key < t.s0 * SUB ||
+                  key >= t.s1 * SUB || !sees(row, a))
+                continue;
+              const int block = P.block_tables[int64_t(t.b) * P.max_blocks_per_seq + key / bs];
+              if (block < 0 || block >= P.num_blocks) continue;
+              const uint8_t* vr =
+                  P.value_cache + (int64_t(block) * bs + key % bs) * row_stride + int64_t(t.kvh) * RB;
 #pragma unroll
-        for (int k = 0; k < OT; ++k) {
-          const int run = 2 * k / RUN, d = (g + 8 * run) * RUN + 2 * k % RUN;
-          *reinterpret_cast<float2*>(row + d) = make_float2(o[k][nt][e], o[k][nt][2 + e]);
-        }
-      }
-    __syncthreads();
-    const bool whole = s0 == 0 && s1 == seq.units;
-    const int slot = 2 * int(blockIdx.x) + (u == u0 ? 0 : 1);
-    for (int at = tid; at < NR * (HD / 2); at += NW * 32) {
-      const int n = at / (HD / 2), d = at % (HD / 2) * 2;
-      const int r = r0 + n, i = r / G;
-      const int64_t t = int64_t(q_start) + i;
-      if (i >= seq.q || t >= P.tokens) continue;
-      float M = ml_s[n].x;
-#pragma unroll
-      for (int w = 1; w < NW; ++w) M = fmaxf(M, ml_s[w * NR + n].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-      float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float2 ml = ml_s[w * NR + n];
-        const float f = ex2(ml.x - ref);
-        const float2 v = *reinterpret_cast<const float2*>(o_s + (w * NR + n) * Cfg::kMergeStride + d);
-        sum = fmaf(ml.y, f, sum);
-        x = fmaf(v.x, f, x);
-        y = fmaf(v.y, f, y);
-      }
-      if (drafts) {
-        // what was taken out of the product, for the rows that see it
-        for (int w = 0; w < kTreeWords; ++w) {
-          if (!bad_s[w]) continue;
-          for (int a = w * 32; a < seq.q; ++a) {
-            if ((a >> 5) % kTreeWords != w || !(bad_s[w] >> (a & 31) & 1) || !sees(n, i, a)) continue;
-            const int key = prefix + a;
-            if (key < s0 * SUB || key >= s1 * SUB) continue;
-            const int block = table[key / bs];
-            if (block < 0 || block >= P.num_blocks) continue;
-            const uint8_t* vr = P.value_cache + (int64_t(block) * bs + key % bs) * row_stride + int64_t(kvh) * RB;
-            const float2 v = Q8 ? h2f2(e4m3x2_half2(*reinterpret_cast<const uint16_t*>(vr + d)))
-                                : h2f2(*reinterpret_cast<const uint32_t*>(vr + 2 * d));
-            if (!isfinite(v.x)) x += v.x;
-            if (!isfinite(v.y)) y += v.y;
+              for (int k = 0; k < OT; ++k) {
+                const int d = (g + 8 * (k / KR)) * RUN + k % KR * 2;
+                const float2 v = Q8 ? h2f2(e4m3x2_half2(*reinterpret_cast<const uint16_t*>(vr + d)))
+                                    : h2f2(*reinterpret_cast<const uint32_t*>(vr + 2 * d));
+                if (!isfinite(v.x)) o[k][nt][e] += v.x;
+                if (!isfinite(v.y)) o[k][nt][2 + e] += v.y;
+              }
+            }
           }
         }
+        if (t.slot < 0) {
+          const float l = l_run[nt][e];
+          __half* dst = P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD;
+#pragma unroll
+          for (int k0 = 0; k0 < OT; k0 += 4) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = pack_half2(o[k0 + k][nt][e] / l, o[k0 + k][nt][2 + e] / l);
+            *reinterpret_cast<uint4*>(dst + (g + 8 * (k0 / KR)) * RUN + k0 % KR * 2) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          const int64_t at = int64_t(t.slot) * NR + row;
+#pragma unroll
+          for (int k = 0; k < OT; k += 2)
+            *reinterpret_cast<float4*>(S.part_o + at * HD + (g + 8 * (k / KR)) * RUN + k % KR * 2) =
+                make_float4(o[k][nt][e], o[k][nt][2 + e], o[k + 1][nt][e], o[k + 1][nt][2 + e]);
+          if (g == 0) S.part_ml[at] = make_float2(m_run[nt][e], l_run[nt][e]);
+        }
       }
-      if (whole) {
-        __half2* dst = reinterpret_cast<__half2*>(P.out + (t * P.num_heads + kvh * G + r % G) * HD + d);
-        *dst = __floats2half2_rn(x / sum, y / sum);
-      } else {
-        const int64_t row = int64_t(slot) * NR + n;
-        *reinterpret_cast<float2*>(S.part_o + row * HD + d) = make_float2(x, y);
-        if (d == 0) S.part_ml[row] = make_float2(M, sum);
-      }
-    }
-    __syncthreads();  // the ring is free again
-    u += s1 - s0;
+    __syncwarp();
   }
 }
 

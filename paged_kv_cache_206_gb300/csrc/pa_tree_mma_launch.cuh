@@ -10,8 +10,8 @@ namespace pa {
 template <int HD, bool Q8, int NT>
 cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, cudaStream_t stream) {
   using Cfg = TreeMma<HD, Q8, NT>;
-  const int grid = sms * Cfg::kCtas;
-  const size_t rows = size_t(2) * grid * Cfg::kRows;
+  const int grid = sms * Cfg::kCtas, workers = grid * Cfg::kWarps;
+  const size_t rows = size_t(2) * workers * Cfg::kRows;
   const size_t o_off = PA_STATUS_BYTES, ml_off = align256(o_off + rows * HD * 4);
   if (need) {
     *need = align256(ml_off + rows * sizeof(float2));
@@ -20,14 +20,16 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   TreeSplit S;
   S.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o_off);
   S.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + ml_off);
-  S.min_units = Cfg::kWarps;
+  S.workers = workers;
+  // a partial result (kRows rows of fp32) should stay below the keys it stands for
+  S.min_units = Cfg::kLead + (NT + Cfg::kMT - 1) / Cfg::kMT;
   auto kern = tree_mma_kernel<HD, Q8, NT>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::bytes);
   if (e != cudaSuccess) return e;
   kern<<<unsigned(grid), Cfg::kWarps * 32, Cfg::bytes, stream>>>(P, S);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid), NT);
+  cfg.gridDim = dim3(unsigned(workers), NT);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -35,7 +37,7 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kSub, Cfg::kRows>, P, S, grid);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kSub, Cfg::kRows, Cfg::kLead>, P, S);
 }
 
 template <int HD, int MAX_NT>

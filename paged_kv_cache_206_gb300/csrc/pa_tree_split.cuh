@@ -1,15 +1,17 @@
-// How pa_tree_forward's kernels divide a batch: one line of units, cut into
-// equal pieces.
+// How pa_tree_forward's warp kernels divide a batch: one line, cut into equal
+// pieces.
 //
 // A row tile is up to NR rows of one (sequence, kv head): row r of the pair is
 // token r / G, head kvh * G + r % G. Every tile walks its sequence's keys in
-// units of UNIT keys, so sequence b has Hk * RT_b * NU_b units (RT_b row tiles,
-// NU_b = ceil(L_b / UNIT)); the units of the batch, in the order (b, kv head, row
-// tile, unit), form one line, of which CTA c of n takes the c-th n-th. A CTA
-// thus meets at most one tile that began before its piece, any number of whole
-// ones, and at most one that goes on behind it; the two incomplete ones leave
-// partial results (slots 2c and 2c + 1), which the combine kernel joins in key
-// order. The lengths are read on the device only, so a launch fits any.
+// units of UNIT keys, so sequence b has Hk * RT_b tiles of NU_b = ceil(L_b / UNIT)
+// units. On the line a tile takes LEAD + NU_b places, in the order (b, kv head,
+// row tile): LEAD stands for what a tile costs before its first and after
+// its last key. Worker c of n takes the c-th n-th of the line; a place of the lead
+// belongs to unit 0. A worker thus meets at most one tile that began before its
+// piece, any number of whole ones, and at most one that goes on behind it; the
+// two incomplete ones leave partial results (slots 2c and 2c + 1), which the combine
+// kernel joins in key order. The lengths are read on the device only, so a launch
+// fits any.
 #pragma once
 
 #include "pa_tree.cuh"
@@ -17,19 +19,21 @@
 namespace pa {
 
 struct TreeSplit {
-  float* part_o;   // [2 * CTAs][NR][hv], not yet divided by the sum
-  float2* part_ml; // [2 * CTAs][NR]: running maximum (base 2) and sum
-  int min_units;   // fewest units worth a CTA
+  float* part_o;    // [2 * workers][NR][hv], not yet divided by the sum
+  float2* part_ml;  // [2 * workers][NR]: running maximum (base 2) and sum
+  int workers;
+  int min_units;    // fewest places of the line worth a worker
 };
 
-template <int UNIT, int NR>
+template <int UNIT, int NR, int LEAD>
 struct TreeLine {
-  // Sequence b's tokens, row tiles and units per tile; a sequence whose lengths
-  // break a constraint has none.
+  // Sequence b's tokens, row tiles of a kv head and units of a tile; a sequence
+  // whose lengths break a constraint has none.
   struct Seq {
     int q, L, tiles, units;
+    __device__ __forceinline__ int places() const { return units + LEAD; }  // of a tile
     __device__ __forceinline__ int64_t total(const TreeParams& P) const {
-      return int64_t(P.kv_heads) * tiles * units;
+      return int64_t(P.kv_heads) * tiles * places();
     }
   };
   static __device__ __forceinline__ Seq load(const TreeParams& P, int b) {
@@ -45,7 +49,7 @@ struct TreeLine {
     return s;
   }
 
-  // Units of the whole batch (warp-collective).
+  // Places of the whole batch (warp-collective).
   static __device__ __forceinline__ int64_t total(const TreeParams& P, int lane) {
     int64_t n = 0;
     for (int b = lane; b < P.batch; b += 32) n += load(P, b).total(P);
@@ -54,7 +58,7 @@ struct TreeLine {
     return n;
   }
 
-  // The sequence that unit u of the line belongs to, the units and the tokens
+  // The sequence that place u of the line belongs to, the places and the tokens
   // before it (warp-collective; u below the total).
   static __device__ __forceinline__ int find(const TreeParams& P, int64_t u, int lane,
                                              int64_t& before, int& q_start) {
@@ -88,64 +92,79 @@ struct TreeLine {
     return -1;
   }
 
-  // CTAs that share the line, and where CTA c's piece begins.
-  static __device__ __forceinline__ int ctas(int64_t total, int grid, int min_units) {
+  // Workers that share the line, and where worker c's piece begins.
+  static __device__ __forceinline__ int active(int64_t total, int workers, int min_units) {
     const int64_t n = total / min_units;
-    return int(n < 1 ? 1 : n < grid ? n : grid);
+    return int(n < 1 ? 1 : n < workers ? n : workers);
   }
   static __device__ __forceinline__ int64_t begin(int64_t total, int c, int n) { return total * c / n; }
 };
 
-// Joins the partial results of the tiles that more than one CTA worked on. CTA
-// (c, y) takes the tile that piece c begins inside of, if c is the first piece
-// that does, and its rows [8 y, 8 y + 8), a warp a row. Launched as the
-// attention kernel's programmatic dependent.
-template <int HD, int UNIT, int NR>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, const TreeSplit S,
-                                                           int grid) {
-  using Line = TreeLine<UNIT, NR>;
-  constexpr int DPL = HD / 32;  // dims a lane holds: lane, lane + 32, ...
+// Joins the partial results of the tiles that more than one worker had keys of.
+// CTA (c, y) takes the tile that piece c begins inside of, if c is the first piece
+// that does, and its rows [8 y, 8 y + 8), a warp a row. Launched as the attention
+// kernel's programmatic dependent.
+template <int HD, int UNIT, int NR, int LEAD>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, const TreeSplit S) {
+  using Line = TreeLine<UNIT, NR, LEAD>;
+  constexpr int DPL = HD / 32;  // dims a lane holds, next to one another
+  constexpr int BATCH = 8;      // partial rows in flight
   const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int64_t total = Line::total(P, lane);
-  const int nact = Line::ctas(total, grid, S.min_units);
+  const int nact = Line::active(total, S.workers, S.min_units);
   const int c = blockIdx.x + 1;
   if (c >= nact) return;
-  const int64_t u = Line::begin(total, c, nact);
+  const int64_t u = Line::begin(total, c, nact), prev = Line::begin(total, c - 1, nact);
   int64_t before;
   int q_start;
   const int b = Line::find(P, u, lane, before, q_start);
   if (b < 0) return;
   const typename Line::Seq s = Line::load(P, b);
-  const int g = int((u - before) / s.units);
-  const int64_t g0 = before + int64_t(g) * s.units, g1 = g0 + s.units;
-  if (u == g0 || Line::begin(total, c - 1, nact) > g0) return;  // not inside a tile, or not its first
+  const int g = int((u - before) / s.places());
+  const int64_t g0 = before + int64_t(g) * s.places(), g1 = g0 + s.places();
+  if (u <= g0 + LEAD || prev > g0 + LEAD) return;  // not inside the keys, or not the first
   const int kvh = g / s.tiles, r = (g % s.tiles) * NR + n, i = r / P.group;
   const int64_t t = int64_t(q_start) + i;
   if (i >= s.q || t >= P.tokens) return;
-  // pieces c - 1 .. last hold a part of the tile
+  // workers c - 1 .. last hold a part of the tile
   int last = c;
   while (last + 1 < nact && Line::begin(total, last + 1, nact) < g1) ++last;
-  const int first_slot = 2 * (c - 1) + (Line::begin(total, c - 1, nact) == g0 ? 0 : 1);
+  const int parts = last - c + 2, first = 2 * (c - 1) + (prev >= g0 ? 0 : 1);
+  auto row_of = [&](int k) { return int64_t(k == 0 ? first : 2 * (c - 1 + k)) * NR + n; };
   grid_dependency_wait();
   float M = -INFINITY;
-  for (int k = c - 1 + lane; k <= last; k += 32)
-    M = fmaxf(M, S.part_ml[int64_t(k == c - 1 ? first_slot : 2 * k) * NR + n].x);
+  for (int k = lane; k < parts; k += 32) M = fmaxf(M, S.part_ml[row_of(k)].x);
   M = warp_max(M);
   if (M == -INFINITY) M = 0.f;  // no score above -inf: the sum below is 0
   float sum = 0.f, acc[DPL];
 #pragma unroll
   for (int k = 0; k < DPL; ++k) acc[k] = 0.f;
-  for (int k = c - 1; k <= last; ++k) {
-    const int64_t row = int64_t(k == c - 1 ? first_slot : 2 * k) * NR + n;
-    const float2 ml = S.part_ml[row];
-    const float w = ex2(ml.x - M);
-    sum += ml.y * w;
+  for (int k0 = 0; k0 < parts; k0 += BATCH) {
+    float2 ml[BATCH];
+    float x[BATCH][DPL];
 #pragma unroll
-    for (int d = 0; d < DPL; ++d) acc[d] += w * S.part_o[row * HD + d * 32 + lane];
+    for (int k = 0; k < BATCH; ++k) {
+      if (k0 + k >= parts) break;
+      const int64_t row = row_of(k0 + k);
+      ml[k] = S.part_ml[row];
+#pragma unroll
+      for (int d = 0; d < DPL; d += 2)
+        *reinterpret_cast<float2*>(&x[k][d]) =
+            *reinterpret_cast<const float2*>(S.part_o + row * HD + lane * DPL + d);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (k0 + k >= parts) break;
+      const float w = ex2(ml[k].x - M);
+      sum = fmaf(ml[k].y, w, sum);
+#pragma unroll
+      for (int d = 0; d < DPL; ++d) acc[d] = fmaf(w, x[k][d], acc[d]);
+    }
   }
-  __half* dst = P.out + (t * P.num_heads + kvh * P.group + r % P.group) * HD;
+  __half2* dst = reinterpret_cast<__half2*>(
+      P.out + (t * P.num_heads + kvh * P.group + r % P.group) * HD + lane * DPL);
 #pragma unroll
-  for (int d = 0; d < DPL; ++d) dst[d * 32 + lane] = __float2half_rn(acc[d] / sum);
+  for (int d = 0; d < DPL; d += 2) dst[d / 2] = __floats2half2_rn(acc[d] / sum, acc[d + 1] / sum);
 }
 
 }  // namespace pa

@@ -67,12 +67,13 @@ class Case:
     def run(self, stream=None):
         return self.step.run(*self.args, self.out, stream=stream)
 
-    def check(self):
+    def check(self, rows=slice(None)):
         want, bound = ref.tree_attention(self.query[:self.tokens], *self.real, *self.exp, self.batch,
                                          self.parents, self.scale)
         got = self.out.cpu().numpy().astype(np.float64)
-        assert (got[self.tokens:] == 7).all()
-        err = np.abs(got[:self.tokens] - want)
+        assert (got[self.tokens:] == 7).all()  # rows behind the last sequence
+        got, want, bound = got[:self.tokens][rows], want[rows], bound[rows]
+        err = np.abs(got - want)
         assert np.isfinite(got).all()
         assert (err <= bound).all(), (float((err / bound).max()), np.argwhere(err > bound)[:4])
 
@@ -171,8 +172,6 @@ def test_drafts_that_a_row_does_not_see_do_not_touch_it(torch, bits, shape, bad)
 
 def test_bad_parents_lengths_and_blocks(torch):
     c = Case(torch, 8, [4, 3], [40, 30], 8, 2, 128, 128, 16, "tree")
-    c.run()
-    good = c.out.clone()
     par = c.parents.copy()
     par[2], par[5] = 2, -7  # a draft that follows itself, and no draft at all: both roots
     c.args[4] = up(torch, par)
@@ -189,14 +188,17 @@ def test_bad_parents_lengths_and_blocks(torch):
     c.args[2] = up(torch, ctx)
     c.run()
     assert c.step.status() == (pa.PA_ERR_INVALID_ARG, pa.PA_STATUS_BIT_PLAN)
-    assert (c.out[:4] == 7).all() and torch.equal(c.out[4:], good[4:])
+    # the other sequence is right (the keys are split where the batch's lengths
+    # put it, so not bit for bit what it is in another batch)
+    assert (c.out[:4] == 7).all()
+    c.check(slice(4, 7))
     c = Case(torch, 8, [4, 3], [40, 30], 8, 2, 128, 128, 16, "tree")
     tables = c.batch.tables.copy()
     tables[0, 1] = c.batch.num_blocks
     c.args[1] = up(torch, tables)
     c.run()
     assert c.step.status() == (pa.PA_ERR_BLOCK_INDEX, pa.PA_STATUS_BIT_BLOCK_INDEX)
-    assert torch.equal(c.out[4:], good[4:])
+    c.check(slice(4, 7))
 
 
 def test_captured_and_replayed_with_other_lengths(torch):
