@@ -132,18 +132,27 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   uint8_t* ring = smem + Cfg::ring_off;
   const int worker = blockIdx.x * Cfg::kWarps + warp;
 
-  const int64_t total = Line::total(P, lane);
-  const int nact = Line::active(total, S.workers, S.min_units);
-  if (worker >= nact) return;
-  const int64_t u0 = Line::begin(total, worker, nact), u1 = Line::begin(total, worker + 1, nact);
   const int G = P.group, bs = P.block_size;
   const int64_t row_stride = int64_t(P.kv_heads) * RB;
 
   // ---- the stream of units: where it stands on the line, and in its tile
-  int64_t u = u0, before = 0;
-  int q_start = 0, b = 0, made = 0;  // tiles left for the arithmetic so far
-  if (u0 < u1) b = Line::find(P, u0, lane, before, q_start);
-  if (u0 >= u1 || b < 0) return;
+  int64_t u = 0, u1 = 0, before = 0, u0 = 0, total = 0;
+  int q_start = 0, b = -1, nact = 0, made = 0;  // tiles left for the arithmetic so far
+  {
+    const typename Line::Seq mine = Line::load(P, lane);
+    total = Line::total(P, lane, mine);
+    nact = Line::active(total, S.workers, S.min_units);
+    if (worker < nact) {
+      u = u0 = Line::begin(total, worker, nact);
+      u1 = Line::begin(total, worker + 1, nact);
+      if (u0 < u1) b = Line::find(P, u0, lane, mine, before, q_start);
+    }
+  }
+  bool noted = false;
+  if (b < 0) {
+    if (lane == 0) S.join[worker].parts = 0;
+    return;
+  }
   typename Line::Seq seq = Line::load(P, b);
   int kvh = 0, unit = 0, unit_end = 0, win0 = 0, cur = 0, next = 0;
   // Lane l holds the blocks of 16 keys each that the units to come need: MT a
@@ -169,7 +178,19 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       unit_end = max(p1 - Cfg::kLead, 0);
       if (unit == unit_end) continue;  // nothing but a lead: the next worker's
       kvh = tile / seq.tiles;
+      const bool goes_on = unit == 0 && unit_end < seq.units;
+      noted |= goes_on;
       if (lane == 0) {
+        if (goes_on) {
+          const int last = Line::last_before(total, before + int64_t(tile + 1) * seq.places(), nact);
+          TreeJoin& j = S.join[worker];
+          j.parts = last - worker + 1;
+          j.first_slot = 2 * worker + (first ? 0 : 1);
+          j.q_start = q_start;
+          j.q = seq.q;
+          j.kvh = kvh;
+          j.r0 = (tile % seq.tiles) * NR;
+        }
         TreeTile& t = tile_s[made % Cfg::kTiles];
         t.b = b;
         t.q_start = q_start;
@@ -503,7 +524,10 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       __syncwarp();
       issue();
     }
-    if (u >= u1 && done + 1 == made) launch_dependents();  // this worker's last tile
+    if (u >= u1 && done + 1 == made) {  // this worker's last tile
+      if (!noted && lane == 0) S.join[worker].parts = 0;
+      launch_dependents();
+    }
 
     // ---- the end of a tile
 #pragma unroll

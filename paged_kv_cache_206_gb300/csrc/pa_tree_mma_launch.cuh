@@ -13,13 +13,15 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   const int grid = sms * Cfg::kCtas, workers = grid * Cfg::kWarps;
   const size_t rows = size_t(2) * workers * Cfg::kRows;
   const size_t o_off = PA_STATUS_BYTES, ml_off = align256(o_off + rows * HD * 4);
+  const size_t join_off = align256(ml_off + rows * sizeof(float2));
   if (need) {
-    *need = align256(ml_off + rows * sizeof(float2));
+    *need = align256(join_off + workers * sizeof(TreeJoin));
     return cudaSuccess;
   }
   TreeSplit S;
   S.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o_off);
   S.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + ml_off);
+  S.join = reinterpret_cast<TreeJoin*>(static_cast<char*>(ws) + join_off);
   S.workers = workers;
   // a partial result (kRows rows of fp32) should stay below the keys it stands for
   S.min_units = Cfg::kLead + (NT + Cfg::kMT - 1) / Cfg::kMT;
@@ -37,7 +39,7 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kSub, Cfg::kRows, Cfg::kLead>, P, S);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kRows>, P, S);
 }
 
 template <int HD, int MAX_NT>

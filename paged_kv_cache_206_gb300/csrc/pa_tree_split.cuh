@@ -9,8 +9,9 @@
 // its last key. Worker c of n takes the c-th n-th of the line; a place of the lead
 // belongs to unit 0. A worker thus meets at most one tile that began before its
 // piece, any number of whole ones, and at most one that goes on behind it; the
-// two incomplete ones leave partial results (slots 2c and 2c + 1), which the combine
-// kernel joins in key order. The lengths are read on the device only, so a launch
+// two incomplete ones leave partial results (slots 2c and 2c + 1). The worker that has
+// a divided tile's first keys also leaves a note of it, by which the combine kernel
+// joins the parts in key order. The lengths are read on the device only, so a launch
 // fits any.
 #pragma once
 
@@ -18,9 +19,16 @@
 
 namespace pa {
 
+// A divided tile, noted by the worker that has its first keys: rows r0 .. of
+// (sequence tokens q_start ..+ q, kvh), in `parts` pieces, 0 for none.
+struct alignas(8) TreeJoin {
+  int parts, first_slot, q_start, q, kvh, r0;
+};
+
 struct TreeSplit {
   float* part_o;    // [2 * workers][NR][hv], not yet divided by the sum
   float2* part_ml;  // [2 * workers][NR]: running maximum (base 2) and sum
+  struct TreeJoin* join;  // [workers]
   int workers;
   int min_units;    // fewest places of the line worth a worker
 };
@@ -37,6 +45,7 @@ struct TreeLine {
     }
   };
   static __device__ __forceinline__ Seq load(const TreeParams& P, int b) {
+    if (b >= P.batch) return Seq{0, 0, 0, 0};
     Seq s;
     s.q = P.q_seqlens ? P.q_seqlens[b] : 1;
     s.L = P.context_lens[b];
@@ -49,10 +58,10 @@ struct TreeLine {
     return s;
   }
 
-  // Places of the whole batch (warp-collective).
-  static __device__ __forceinline__ int64_t total(const TreeParams& P, int lane) {
-    int64_t n = 0;
-    for (int b = lane; b < P.batch; b += 32) n += load(P, b).total(P);
+  // Places of the whole batch (warp-collective); `mine` is lane's load(P, lane).
+  static __device__ __forceinline__ int64_t total(const TreeParams& P, int lane, const Seq& mine) {
+    int64_t n = mine.total(P);
+    for (int b = lane + 32; b < P.batch; b += 32) n += load(P, b).total(P);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     return n;
@@ -60,13 +69,13 @@ struct TreeLine {
 
   // The sequence that place u of the line belongs to, the places and the tokens
   // before it (warp-collective; u below the total).
-  static __device__ __forceinline__ int find(const TreeParams& P, int64_t u, int lane,
+  static __device__ __forceinline__ int find(const TreeParams& P, int64_t u, int lane, const Seq& mine,
                                              int64_t& before, int& q_start) {
     before = 0;
     q_start = 0;
+    Seq s = mine;
     for (int b0 = 0; b0 < P.batch; b0 += 32) {
-      Seq s{0, 0, 0, 0};
-      if (b0 + lane < P.batch) s = load(P, b0 + lane);
+      if (b0) s = load(P, b0 + lane);
       const int64_t n = s.total(P);
       int64_t un = n;
       int tn = s.q;
@@ -98,40 +107,31 @@ struct TreeLine {
     return int(n < 1 ? 1 : n < workers ? n : workers);
   }
   static __device__ __forceinline__ int64_t begin(int64_t total, int c, int n) { return total * c / n; }
+  // The last worker whose piece begins before place u: total * k / n < u.
+  static __device__ __forceinline__ int last_before(int64_t total, int64_t u, int n) {
+    return int((u * n - 1) / total);
+  }
 };
 
-// Joins the partial results of the tiles that more than one worker had keys of.
-// CTA (c, y) takes the tile that piece c begins inside of, if c is the first piece
-// that does, and its rows [8 y, 8 y + 8), a warp a row. Launched as the attention
+// Joins the partial results of the divided tiles: CTA (c, y) the rows [8 y, 8 y + 8)
+// of the tile that worker c noted, a warp a row. Launched as the attention
 // kernel's programmatic dependent.
-template <int HD, int UNIT, int NR, int LEAD>
+template <int HD, int NR>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, const TreeSplit S) {
-  using Line = TreeLine<UNIT, NR, LEAD>;
   constexpr int DPL = HD / 32;  // dims a lane holds, next to one another
   constexpr int BATCH = 8;      // partial rows in flight
   const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int64_t total = Line::total(P, lane);
-  const int nact = Line::active(total, S.workers, S.min_units);
-  const int c = blockIdx.x + 1;
-  if (c >= nact) return;
-  const int64_t u = Line::begin(total, c, nact), prev = Line::begin(total, c - 1, nact);
-  int64_t before;
-  int q_start;
-  const int b = Line::find(P, u, lane, before, q_start);
-  if (b < 0) return;
-  const typename Line::Seq s = Line::load(P, b);
-  const int g = int((u - before) / s.places());
-  const int64_t g0 = before + int64_t(g) * s.places(), g1 = g0 + s.places();
-  if (u <= g0 + LEAD || prev > g0 + LEAD) return;  // not inside the keys, or not the first
-  const int kvh = g / s.tiles, r = (g % s.tiles) * NR + n, i = r / P.group;
-  const int64_t t = int64_t(q_start) + i;
-  if (i >= s.q || t >= P.tokens) return;
-  // workers c - 1 .. last hold a part of the tile
-  int last = c;
-  while (last + 1 < nact && Line::begin(total, last + 1, nact) < g1) ++last;
-  const int parts = last - c + 2, first = 2 * (c - 1) + (prev >= g0 ? 0 : 1);
-  auto row_of = [&](int k) { return int64_t(k == 0 ? first : 2 * (c - 1 + k)) * NR + n; };
   grid_dependency_wait();
+  const TreeJoin& t = S.join[blockIdx.x];
+  const int parts = t.parts;
+  if (parts == 0) return;
+  const int r = t.r0 + n, i = r / P.group;
+  const int64_t tok = int64_t(t.q_start) + i;
+  if (i >= t.q || tok >= P.tokens) return;
+  // part 0 is the noting worker's last tile, the others the next workers' first
+  auto row_of = [&](int k) {
+    return int64_t(k == 0 ? t.first_slot : 2 * (int(blockIdx.x) + k)) * NR + n;
+  };
   float M = -INFINITY;
   for (int k = lane; k < parts; k += 32) M = fmaxf(M, S.part_ml[row_of(k)].x);
   M = warp_max(M);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, c
     }
   }
   __half2* dst = reinterpret_cast<__half2*>(
-      P.out + (t * P.num_heads + kvh * P.group + r % P.group) * HD + lane * DPL);
+      P.out + (tok * P.num_heads + t.kvh * P.group + r % P.group) * HD + lane * DPL);
 #pragma unroll
   for (int d = 0; d < DPL; d += 2) dst[d / 2] = __floats2half2_rn(acc[d] / sum, acc[d + 1] / sum);
 }
