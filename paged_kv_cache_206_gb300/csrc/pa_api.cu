@@ -21,6 +21,7 @@
 #include "pa_prefill_tc.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_launch.h"
 #include "pa_plan_device.h"
 
 namespace pa {
@@ -30,20 +31,6 @@ cudaError_t launch_fma(const CUtensorMap&, const CUtensorMap&, const FwdParams&,
                        cudaStream_t);
 
 namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
 
 struct BoxGeom {
   int width;  // elements per row of one TMA box
@@ -112,7 +99,7 @@ MapCache& map_cache() {
 // The map for key k (fp16 elements; the row stride follows from the dims).
 bool cached_map(CUtensorMap* m, const MapKey& k, const cuuint64_t* strides) {
   if (map_cache().get(k, m)) return true;
-  auto enc = encode_fn();
+  auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {k.dims[0], k.dims[1], k.dims[2]};
   cuuint32_t box[3] = {k.box[0], k.box[1], k.box[2]};

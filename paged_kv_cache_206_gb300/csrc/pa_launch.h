@@ -1,6 +1,8 @@
 // Host-side launch helpers shared by the kernel launchers of libpa.so.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -8,6 +10,22 @@
 #include <unordered_map>
 
 namespace pa {
+
+// cuTensorMapEncodeTiled, through the runtime's entry-point query (the library
+// does not link the driver); null when there is none.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
 
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device) rather
 // than on every launch.

@@ -5,7 +5,7 @@
 #include <cmath>
 
 #include "pa_internal.h"
-#include "pa_tree_mma.cuh"
+#include "pa_tree_tc.cuh"
 
 namespace pa {
 
@@ -73,11 +73,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) tree_any_kernel(const TreePara
   for (int j = warp; j <= prefix + i; j += kAnyWarps) {
     if (P.parents && j >= prefix) {
       const int a = j - prefix;
-      uint32_t word = 0;
-#pragma unroll
-      for (int w = 0; w < kTreeWords; ++w)
-        if (a >> 5 == w) word = bits[w];
-      if (!(word >> (a & 31) & 1)) continue;
+      if (!(bits[a >> 5] >> (a & 31) & 1)) continue;
     }
     const int block = P.block_tables[int64_t(b) * P.max_blocks_per_seq + j / P.block_size];
     if (block < 0 || block >= P.num_blocks) {
@@ -155,14 +151,19 @@ pa_status check_tree(const pa_config* cfg) {
 }
 
 // The kernel for these head sizes and rows, if there is a faster one than
-// tree_any_kernel: the warp-level tensor instructions with the narrowest of
-// their 8-, 16- and 32-row tiles (16 at most for 256 dims) that holds a kv head's
-// rows, or several of the widest.
+// tree_any_kernel: for up to 32 rows of a kv head, and for 256 dims, the warp-level
+// tensor instructions with the narrowest of their 8-, 16- and 32-row tiles (16 at
+// most for 256 dims) that holds the rows, or several of the widest; beyond that
+// the tcgen05 tensor cores.
 bool tree_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws,
                 cudaStream_t stream, cudaError_t* e) {
   if (c.head_size_k != c.head_size_v) return false;
   const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  if (rows > 32 && (c.head_size_k == 64 || c.head_size_k == 128)) {
+    *e = tree_tc(P, c.head_size_k, q8, rows, c.num_sms, need, ws, stream);
+    return true;
+  }
   switch (c.head_size_k) {
     case 64: *e = tree_mma_64(P, q8, nt, c.num_sms, need, ws, stream); return true;
     case 128: *e = tree_mma_128(P, q8, nt, c.num_sms, need, ws, stream); return true;

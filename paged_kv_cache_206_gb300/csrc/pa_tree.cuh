@@ -62,15 +62,40 @@ __device__ __forceinline__ void tree_ancestors(const TreeParams& P, const int32_
 #pragma unroll
   for (int w = 0; w < kTreeWords; ++w) bits[w] = 0;
   while (true) {
-#pragma unroll
-    for (int w = 0; w < kTreeWords; ++w)
-      if (i >> 5 == w) bits[w] |= 1u << (i & 31);
+    bits[i >> 5] |= 1u << (i & 31);
     const int up = parents[i];
     if (up < 0 || up >= i) {
       if (up != -1) set_status(P.status, PA_STATUS_BIT_TREE);
       return;
     }
     i = up;
+  }
+}
+
+// Adds to one row's result what was taken out of its product: the non-finite
+// elements of the values of the drafts flagged in `bad` (draft a under bit a
+// modulo its size) that the row sees. `key0`, `key1` bound the keys that the result
+// is of; `seen` are the row's ancestor bits, or null for a chain, whose row is draft
+// `qi`. The result is fp16 (`out`) or an fp32 partial one (`part`, `stride`
+// apart); dims first, first + step, ... below `last`. Rare, hence not inlined.
+template <bool Q8>
+__device__ __noinline__ void tree_patch(const TreeParams& P, int b, int q, int prefix, int kvh, int qi,
+                                        const uint32_t* bad, const uint32_t* seen, int key0, int key1,
+                                        __half* out, float* part, int stride, int first, int step, int last) {
+  const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;
+  for (int a = max(key0 - prefix, 0); a < min(q, key1 - prefix); ++a) {
+    if (!(bad[(a >> 5) % kTreeWords] >> (a & 31) & 1)) continue;
+    if (seen ? !(seen[a >> 5] >> (a & 31) & 1) : a > qi) continue;
+    const int key = prefix + a, block = table[key / P.block_size];
+    if (block < 0 || block >= P.num_blocks) continue;
+    const int64_t row = ((int64_t(block) * P.block_size + key % P.block_size) * P.kv_heads + kvh) * P.hv;
+    for (int d = first; d < last; d += step) {
+      const float v = Q8 ? h2f2(e4m3x2_half2(P.value_cache[row + d])).x
+                         : __half2float(*reinterpret_cast<const __half*>(P.value_cache + 2 * (row + d)));
+      if (isfinite(v)) continue;
+      if (out) out[d] = __float2half_rn(__half2float(out[d]) + v);
+      else part[int64_t(d) * stride] += v;
+    }
   }
 }
 

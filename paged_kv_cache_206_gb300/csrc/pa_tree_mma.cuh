@@ -38,13 +38,6 @@
 
 namespace pa {
 
-// A tile of the line, as the key stream leaves it for the arithmetic.
-struct TreeTile {
-  int b, q_start, q, L, kvh, r0, s0, s1;  // units [s0, s1)
-  int slot;                               // of a partial result; -1: the whole tile
-  int pad[3];
-};
-
 template <int HD, bool Q8, int NT>
 struct TreeMma {
   static constexpr int kWarps = 4;
@@ -68,7 +61,9 @@ struct TreeMma {
   static constexpr uint32_t par_off = mask_off + kRows * kTreeWords * 4;
   static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
   static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
-  static constexpr uint32_t ring_off = (tile_off + kTiles * sizeof(TreeTile) + 127) & ~127u;
+  using Place = TreePlace<TreeWalk<kSub, kRows, kLead>>;
+  static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(TreeTile) + 7) & ~7u;
+  static constexpr uint32_t ring_off = (place_off + sizeof(Place) + 127) & ~127u;
   static constexpr int kFit = int((kBudget - ring_off) / kStage);
   static constexpr int kStages = kFit < 5 ? kFit : 5;
   static_assert(kStages >= 2 && kStages + 2 <= kTiles, "ring");
@@ -113,9 +108,8 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
 
 template <int HD, bool Q8, int NT>
 __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
-    tree_mma_kernel(const TreeParams P, const TreeSplit S) {
+    tree_mma_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
   using Cfg = TreeMma<HD, Q8, NT>;
-  using Line = TreeLine<Cfg::kSub, Cfg::kRows, Cfg::kLead>;
   constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows;
   constexpr int RB = Cfg::kRowBytes, C = Cfg::kChunks, E = Cfg::kElems;
   constexpr int OT = HD / 16;  // m-tiles of O^T, k-steps of S^T
@@ -136,84 +130,42 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   const int64_t row_stride = int64_t(P.kv_heads) * RB;
 
   // ---- the stream of units: where it stands on the line, and in its tile
-  int64_t u = 0, u1 = 0, before = 0, u0 = 0, total = 0;
-  int q_start = 0, b = -1, nact = 0, made = 0;  // tiles left for the arithmetic so far
-  {
-    const typename Line::Seq mine = Line::load(P, lane);
-    total = Line::total(P, lane, mine);
-    nact = Line::active(total, S.workers, S.min_units);
-    if (worker < nact) {
-      u = u0 = Line::begin(total, worker, nact);
-      u1 = Line::begin(total, worker + 1, nact);
-      if (u0 < u1) b = Line::find(P, u0, lane, mine, before, q_start);
-    }
-  }
-  bool noted = false;
-  if (b < 0) {
-    if (lane == 0) S.join[worker].parts = 0;
-    return;
-  }
-  typename Line::Seq seq = Line::load(P, b);
-  int kvh = 0, unit = 0, unit_end = 0, win0 = 0, cur = 0, next = 0;
+  typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
+  int made = 0;                             // tiles left for the arithmetic so far
+  if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
+  if (!tree_begin(P, S, place, worker, lane)) return;
+  int unit = 0, unit_end = 0, win0 = 0, cur = 0, next = 0, cut_L = 0, cut_b = 0, cut_kvh = 0;
   // Lane l holds the blocks of 16 keys each that the units to come need: MT a
   // unit, 32 / MT units a window, and the next window's.
   constexpr int WIN = 32 / MT;
   auto blocks_of = [&](int n0) {
     const int key = (n0 + lane / MT) * SUB + (lane % MT) * 16;
-    return n0 + lane / MT < unit_end && key < seq.L
-               ? P.block_tables[int64_t(b) * P.max_blocks_per_seq + key / bs] : 0;
+    return n0 + lane / MT < unit_end && key < cut_L
+               ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + key / bs] : 0;
   };
   auto next_tile = [&]() {
-    while (u < u1) {
-      while (u >= before + seq.total(P)) {
-        before += seq.total(P);
-        q_start += seq.q;
-        seq = Line::load(P, ++b);
-      }
-      const int tile = int((u - before) / seq.places()), p0 = int((u - before) % seq.places());
-      const int p1 = int(min(int64_t(seq.places()), p0 + (u1 - u)));
-      const bool first = u == u0;
-      u += p1 - p0;
-      unit = max(p0 - Cfg::kLead, 0);
-      unit_end = max(p1 - Cfg::kLead, 0);
-      if (unit == unit_end) continue;  // nothing but a lead: the next worker's
-      kvh = tile / seq.tiles;
-      const bool goes_on = unit == 0 && unit_end < seq.units;
-      noted |= goes_on;
-      if (lane == 0) {
-        if (goes_on) {
-          const int last = Line::last_before(total, before + int64_t(tile + 1) * seq.places(), nact);
-          TreeJoin& j = S.join[worker];
-          j.parts = last - worker + 1;
-          j.first_slot = 2 * worker + (first ? 0 : 1);
-          j.q_start = q_start;
-          j.q = seq.q;
-          j.kvh = kvh;
-          j.r0 = (tile % seq.tiles) * NR;
-        }
-        TreeTile& t = tile_s[made % Cfg::kTiles];
-        t.b = b;
-        t.q_start = q_start;
-        t.q = seq.q;
-        t.L = seq.L;
-        t.kvh = kvh;
-        t.r0 = (tile % seq.tiles) * NR;
-        t.s0 = unit;
-        t.s1 = unit_end;
-        t.slot = unit == 0 && unit_end == seq.units ? -1 : 2 * worker + (first ? 0 : 1);
-      }
-      ++made;
-      win0 = unit;
-      cur = blocks_of(unit);
-      next = blocks_of(unit + WIN);
-      return true;
+    if (!tree_next(P, place)) return false;
+    const TreeTile& t = place->tile;
+    if (lane == 0) {
+      tile_s[made % Cfg::kTiles] = t;
+      if (t.parts) tree_note(S, worker, t);
     }
-    return false;
+    ++made;
+    cut_L = t.L;
+    cut_b = t.b;
+    cut_kvh = t.kvh;
+    unit = t.s0;
+    unit_end = t.s1;
+    return true;
   };
   int issued = 0;
   auto issue = [&]() {
     if (unit < unit_end || next_tile()) {
-      if (unit >= win0 + WIN) {
+      if (unit == place->tile.s0) {
+        win0 = unit;
+        cur = blocks_of(unit);
+        next = blocks_of(unit + WIN);
+      } else if (unit >= win0 + WIN) {
         win0 += WIN;
         cur = next;
         next = blocks_of(win0 + WIN);
@@ -226,11 +178,11 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         const bool ok = block >= 0 && block < P.num_blocks;
         if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
         const int place = key % bs;
-        const int64_t base = ok && key < seq.L ? (int64_t(block) * bs + place) * row_stride + int64_t(kvh) * RB : 0;
+        const int64_t base = ok && key < cut_L ? (int64_t(block) * bs + place) * row_stride + int64_t(cut_kvh) * RB : 0;
 #pragma unroll
         for (int k = 0; k < C / 2; ++k) {
           const int at = lane + 32 * k, row = at / C, ch = at % C;
-          const bool in = ok && key + row < seq.L;
+          const bool in = ok && key + row < cut_L;
           const int64_t off = in ? base + row * row_stride + ch * 16 : 0;
           const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(ch, row) * 16;
           cp_async16(to, P.key_cache + off, in);
@@ -238,8 +190,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         }
         if constexpr (Q8) {
           if (lane < 2) {
-            const bool in = ok && key < seq.L;
-            const int64_t off = in ? (int64_t(block) * P.kv_heads + kvh) * bs + place : 0;
+            const bool in = ok && key < cut_L;
+            const int64_t off = in ? (int64_t(block) * P.kv_heads + cut_kvh) * bs + place : 0;
             cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + off, in);
           }
         }
@@ -524,10 +476,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       __syncwarp();
       issue();
     }
-    if (u >= u1 && done + 1 == made) {  // this worker's last tile
-      if (!noted && lane == 0) S.join[worker].parts = 0;
-      launch_dependents();
-    }
+    if (place->walk.u >= place->walk.u1 && done + 1 == made) launch_dependents();  // this worker's last tile
 
     // ---- the end of a tile
 #pragma unroll
@@ -550,38 +499,14 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         const int row = nt * 8 + 2 * c + e, r = t.r0 + row, i = r / G;
         const int64_t tok = int64_t(t.q_start) + i;
         if (i >= t.q || tok >= P.tokens) continue;
-        if (drafts) {
-          // what was taken out of the product, for the rows that see it
-          for (int w = 0; w < kTreeWords; ++w) {
-            if (!bad_s[w]) continue;
-            for (int a = w * 32; a < t.q; ++a) {
-              const int key = prefix + a;
-              if ((a >> 5) % kTreeWords != w || !(bad_s[w] >> (a & 31) & 1) || key < t.s0 * SUB ||
-                  key >= t.s1 * SUB || !sees(row, a))
-                continue;
-              const int block = P.block_tables[int64_t(t.b) * P.max_blocks_per_seq + key / bs];
-              if (block < 0 || block >= P.num_blocks) continue;
-              const uint8_t* vr =
-                  P.value_cache + (int64_t(block) * bs + key % bs) * row_stride + int64_t(t.kvh) * RB;
-#pragma unroll
-              for (int k = 0; k < OT; ++k) {
-                const int d = (g + 8 * (k / KR)) * RUN + k % KR * 2;
-                const float2 v = Q8 ? h2f2(e4m3x2_half2(*reinterpret_cast<const uint16_t*>(vr + d)))
-                                    : h2f2(*reinterpret_cast<const uint32_t*>(vr + 2 * d));
-                if (!isfinite(v.x)) o[k][nt][e] += v.x;
-                if (!isfinite(v.y)) o[k][nt][2 + e] += v.y;
-              }
-            }
-          }
-        }
         if (t.slot < 0) {
-          const float l = l_run[nt][e];
+          const float inv = 1.f / l_run[nt][e];
           __half* dst = P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD;
 #pragma unroll
           for (int k0 = 0; k0 < OT; k0 += 4) {
             uint32_t h[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = pack_half2(o[k0 + k][nt][e] / l, o[k0 + k][nt][2 + e] / l);
+            for (int k = 0; k < 4; ++k) h[k] = pack_half2(o[k0 + k][nt][e] * inv, o[k0 + k][nt][2 + e] * inv);
             *reinterpret_cast<uint4*>(dst + (g + 8 * (k0 / KR)) * RUN + k0 % KR * 2) =
                 make_uint4(h[0], h[1], h[2], h[3]);
           }
@@ -595,6 +520,22 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         }
       }
     __syncwarp();
+    if (drafts) {
+      uint32_t hit = 0;
+      for (int w = 0; w < kTreeWords; ++w) hit |= bad_s[w];
+      if (hit) {
+        for (int row = 0; row < NR; ++row) {
+          const int r = t.r0 + row, i = r / G;
+          const int64_t tok = int64_t(t.q_start) + i;
+          if (i >= t.q || tok >= P.tokens) continue;
+          tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, i, bad_s, P.parents ? mask_s + row * kTreeWords : nullptr,
+                         t.s0 * SUB, t.s1 * SUB,
+                         t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr,
+                         S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD, 1, lane, 32, HD);
+        }
+        __syncwarp();
+      }
+    }
   }
 }
 

@@ -33,6 +33,12 @@ struct TreeSplit {
   int min_units;    // fewest places of the line worth a worker
 };
 
+// a / b for a >= 0, b > 0: the 64-bit division takes several times the 32-bit one's time.
+__device__ __forceinline__ int64_t tree_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
+}
+
 template <int UNIT, int NR, int LEAD>
 struct TreeLine {
   // Sequence b's tokens, row tiles of a kv head and units of a tile; a sequence
@@ -103,15 +109,126 @@ struct TreeLine {
 
   // Workers that share the line, and where worker c's piece begins.
   static __device__ __forceinline__ int active(int64_t total, int workers, int min_units) {
-    const int64_t n = total / min_units;
+    const int64_t n = tree_div(total, min_units);
     return int(n < 1 ? 1 : n < workers ? n : workers);
   }
-  static __device__ __forceinline__ int64_t begin(int64_t total, int c, int n) { return total * c / n; }
+  static __device__ __forceinline__ int64_t begin(int64_t total, int c, int n) {
+    return tree_div(total * c, n);
+  }
   // The last worker whose piece begins before place u: total * k / n < u.
   static __device__ __forceinline__ int last_before(int64_t total, int64_t u, int n) {
-    return int((u * n - 1) / total);
+    return min(int(tree_div(u * n - 1, total)), n - 1);
   }
 };
+
+// The keys of one row tile that one worker has.
+struct TreeTile {
+  int b, q_start, q, L, kvh, r0;
+  int s0, s1;  // units [s0, s1)
+  int slot;    // of a partial result; -1: the whole tile
+  int parts;   // of a divided tile whose first keys are here, else 0
+};
+
+// One worker's way along the line (warp-collective, every lane the same).
+template <int UNIT, int NR, int LEAD>
+struct TreeWalk {
+  using Line = TreeLine<UNIT, NR, LEAD>;
+  int64_t u, u0, u1, before, total;
+  int q_start, b, nact, worker;
+  typename Line::Seq seq;
+
+  __device__ __forceinline__ bool begin(const TreeParams& P, const TreeSplit& S, int w, int lane) {
+    worker = w;
+    u = u0 = u1 = before = 0;
+    q_start = 0;
+    b = -1;
+    const typename Line::Seq mine = Line::load(P, lane);
+    total = Line::total(P, lane, mine);
+    nact = Line::active(total, S.workers, S.min_units);
+    if (worker < nact) {
+      u = u0 = Line::begin(total, worker, nact);
+      u1 = Line::begin(total, worker + 1, nact);
+      if (u0 < u1) b = Line::find(P, u0, lane, mine, before, q_start);
+    }
+    if (b < 0) {
+      u = u1;
+      return false;
+    }
+    seq = Line::load(P, b);
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const TreeParams& P, TreeTile& t) {
+    while (u < u1) {
+      while (u >= before + seq.total(P)) {
+        before += seq.total(P);
+        q_start += seq.q;
+        if (++b >= P.batch) {  // only if the lengths changed under the kernel
+          u = u1;
+          return false;
+        }
+        seq = Line::load(P, b);
+      }
+      const int tile = int(tree_div(u - before, seq.places()));
+      const int p0 = int(u - before - int64_t(tile) * seq.places());
+      const int p1 = int(min(int64_t(seq.places()), p0 + (u1 - u)));
+      const bool first = u == u0;
+      u += p1 - p0;
+      t.s0 = max(p0 - LEAD, 0);
+      t.s1 = max(p1 - LEAD, 0);
+      if (t.s0 == t.s1) continue;  // nothing but a lead: the next worker's
+      t.b = b;
+      t.q_start = q_start;
+      t.q = seq.q;
+      t.L = seq.L;
+      t.kvh = tile / seq.tiles;
+      t.r0 = (tile % seq.tiles) * NR;
+      t.slot = t.s0 == 0 && t.s1 == seq.units ? -1 : 2 * worker + (first ? 0 : 1);
+      t.parts = 0;
+      if (t.s0 == 0 && t.s1 < seq.units)
+        t.parts = Line::last_before(total, before + int64_t(tile + 1) * seq.places(), nact) - worker + 1;
+      return true;
+    }
+    return false;
+  }
+};
+
+// A warp's place on the line, in shared memory, and its steps along it as
+// functions of their own: they are rare, and inlined where they are called (with
+// their divisions) they pushed the kernels' loops out of the instruction cache.
+// All lanes hold and store the same values.
+template <class Walk>
+struct TreePlace {
+  Walk walk;
+  TreeTile tile;
+};
+
+template <class Walk>
+__device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S, TreePlace<Walk>* at, int worker,
+                                        int lane) {
+  Walk w;
+  const bool some = w.begin(P, S, worker, lane);
+  at->walk = w;
+  __syncwarp();
+  return some;
+}
+
+template <class Walk>
+__device__ __noinline__ bool tree_next(const TreeParams& P, TreePlace<Walk>* at) {
+  Walk w = at->walk;
+  TreeTile d;
+  const bool some = w.next(P, d);
+  __syncwarp();
+  if (some) at->tile = d;
+  at->walk = w;
+  __syncwarp();
+  return some;
+}
+
+// The note of a divided tile (parts = 0: none).
+__device__ __forceinline__ void tree_note(const TreeSplit& S, int worker, const TreeTile& t) {
+  S.join[worker] = TreeJoin{t.parts, t.slot, t.q_start, t.q, t.kvh, t.r0};
+}
 
 // Joins the partial results of the divided tiles: CTA (c, y) the rows [8 y, 8 y + 8)
 // of the tile that worker c noted, a warp a row. Launched as the attention
@@ -163,8 +280,49 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, c
   }
   __half2* dst = reinterpret_cast<__half2*>(
       P.out + (tok * P.num_heads + t.kvh * P.group + r % P.group) * HD + lane * DPL);
+  const float inv = 1.f / sum;
 #pragma unroll
-  for (int d = 0; d < DPL; d += 2) dst[d / 2] = __floats2half2_rn(acc[d] / sum, acc[d + 1] / sum);
+  for (int d = 0; d < DPL; d += 2) dst[d / 2] = __floats2half2_rn(acc[d] * inv, acc[d + 1] * inv);
+}
+
+// The same for wide row tiles, whose partial rows are stored by columns,
+// [slot][HD][NR], so that a kernel with a row per thread stores whole lines: CTA (c, y)
+// the rows [32 y, 32 y + 32), a lane a row, a warp HD / 8 columns.
+template <int HD, int NR>
+__global__ void __launch_bounds__(256) tree_combine_cols_kernel(const TreeParams P, const TreeSplit S) {
+  constexpr int COLS = HD / 8;
+  const int lane = threadIdx.x & 31, d0 = (threadIdx.x >> 5) * COLS, n = blockIdx.y * 32 + lane;
+  grid_dependency_wait();
+  const TreeJoin& t = S.join[blockIdx.x];
+  const int parts = t.parts;
+  if (parts == 0) return;
+  const int r = t.r0 + n, i = r / P.group;
+  const int64_t tok = int64_t(t.q_start) + i;
+  if (i >= t.q || tok >= P.tokens) return;
+  auto slot_of = [&](int k) { return int64_t(k == 0 ? t.first_slot : 2 * (int(blockIdx.x) + k)); };
+  float M = -INFINITY, sum = 0.f, acc[COLS];
+#pragma unroll
+  for (int d = 0; d < COLS; ++d) acc[d] = 0.f;
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, S.part_ml[slot_of(k) * NR + n].x);
+  if (M == -INFINITY) M = 0.f;  // no score above -inf: the sum below is 0
+  for (int k = 0; k < parts; ++k) {
+    const int64_t slot = slot_of(k);
+    const float2 ml = S.part_ml[slot * NR + n];
+    float x[COLS];
+#pragma unroll
+    for (int d = 0; d < COLS; ++d) x[d] = S.part_o[(slot * HD + d0 + d) * NR + n];
+    const float w = ex2(ml.x - M);
+    sum = fmaf(ml.y, w, sum);
+#pragma unroll
+    for (int d = 0; d < COLS; ++d) acc[d] = fmaf(w, x[d], acc[d]);
+  }
+  const float inv = 1.f / sum;
+  uint4* dst = reinterpret_cast<uint4*>(
+      P.out + (tok * P.num_heads + t.kvh * P.group + r % P.group) * HD + d0);
+#pragma unroll
+  for (int d = 0; d < COLS; d += 8)
+    dst[d / 8] = make_uint4(pack_half2(acc[d] * inv, acc[d + 1] * inv), pack_half2(acc[d + 2] * inv, acc[d + 3] * inv),
+                            pack_half2(acc[d + 4] * inv, acc[d + 5] * inv), pack_half2(acc[d + 6] * inv, acc[d + 7] * inv));
 }
 
 }  // namespace pa

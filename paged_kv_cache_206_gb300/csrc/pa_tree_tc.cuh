@@ -1,0 +1,839 @@
+// Tree attention on the tcgen05 tensor cores, for tiles of 128 or 256 rows (a
+// group of heads times many drafts) and heads of 64 or 128 dims, over the fp16 or
+// the 8-bit cache.
+//
+// One persistent CTA per SM, a worker of the line (pa_tree_split.cuh) with units of
+// 128 keys. Two chains of S = Q K^T -> softmax -> O += P V run against each other in
+// jobs of 64 keys: with up to 128 rows chain g takes half g of every key tile and
+// the two states are joined at the end (QT = 1), with more each has a query tile of
+// its own and takes both halves (QT = 2). A chain has two S buffers in TMEM, so that
+// the product of its next job runs under the softmax of this one; 64 scores of a
+// row fit in a thread's registers, so they are read from TMEM once. (Jobs of 128
+// keys with one S buffer per chain and the scores read twice took 4.6 us per 256 rows
+// x 128 keys, almost all of it latency.)
+//
+//   warp 0       keys' copies (TMA), for the 8-bit cache the values' too
+//   warp 1       issues every MMA: S_g's buffer s in TMEM columns 128 g + 64 s, O_g in
+//                [256 + 128 g, +HD); P_g (fp16) overwrites the front of its S, where
+//                O += P V takes it as its A operand from TMEM
+//   warp 2       values' copies of the fp16 cache
+//   warp 3       the query tile of every row tile (cp.async)
+//   warps 4-11   softmax, one row a thread: group g = chain g
+//   warps 12-15  8-bit cache only: codes to fp16 operands, each warp one of the four
+//                64-row parts (K, K, V, V) of a tile. The rows of a tile are
+//                brought to the tile's largest exponent (code * 2^(e_j - e_max), exact
+//                but for rows 2^15 times smaller than the tile's largest, whose
+//                low bits fall under fp16's 2^-24: an absolute 2^-25 of that
+//                unit), so the softmax sees one factor for K and one exponent for
+//                V per tile, as the fp16 cache's does.
+//
+// The reference maximum of a row moves only when a score passes it by 2^8; sums,
+// maxima and accumulators are fp32, the weights fp16. All roles walk the same
+// tiles of the line; rings and barriers run on across them, so the copies of the
+// next tile are under way while the last one's rows are written out. Every wait is
+// bounded; what was noted for the combine pass stands before the first of them.
+#pragma once
+
+#include "pa_prefill_tc.cuh"
+#include "pa_tree_mma.cuh"
+
+namespace pa {
+
+template <int HD, bool Q8, int QT>
+struct TreeTc {
+  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kTok = 128;
+  static constexpr int kRows = 128 * QT;
+  static constexpr int kLead = 3;
+  static constexpr int kHalves = HD / 64;
+  static constexpr uint32_t kHalf = 128 * 128;           // 64 dims of 128 fp16 rows
+  static constexpr uint32_t kTile = kHalf * kHalves;     // a K or V tile, a query tile
+  static constexpr int kKSlots = Q8 || QT == 2 ? 2 : 3;
+  static constexpr int kVSlots = Q8 && QT == 2 ? 1 : 2;
+  static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
+  static constexpr int kStages = Q8 ? 7 : 0;
+  static constexpr int kMeta = 4;                        // tiles whose exponents are held
+  static constexpr uint32_t q_off = 0;
+  static constexpr uint32_t k_off = q_off + QT * kTile;
+  static constexpr uint32_t v_off = k_off + kKSlots * kTile;
+  static constexpr uint32_t stage_off = v_off + kVSlots * kTile;
+  static constexpr uint32_t exps_off = stage_off + kStages * kStageBytes;  // [kMeta][2][128]
+  static constexpr uint32_t meta_off = exps_off + (Q8 ? kMeta * 256 : 0);  // [kMeta] int2
+  static constexpr uint32_t stat_off = meta_off + kMeta * 8;               // [2][2][128] float2
+  static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
+  static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [4][words]
+  static constexpr uint32_t bars_off = bad_off + 4 * kTreeWords * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 2 * kMeta + 18;
+  static constexpr uint32_t walk_off = bars_off + kBars * 8;  // a warp's place on the line
+  using Walk = TreeWalk<kTok, kRows, kLead>;
+  using Place = TreePlace<Walk>;
+  static constexpr uint32_t tmem_off = walk_off + (kThreads / 32 + 1) * sizeof(Place);
+  static constexpr uint32_t bytes = tmem_off + 16 + 1024;
+  static_assert(bytes <= kTcMaxSmem, "shared memory");
+};
+
+// Untiled copy of global memory into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Bounded wait of the whole warp for a phase of `bar`. Every lane polls, and the
+// loop's branch goes by a vote, so the warp stays converged: with one lane polling
+// for the others the compiler let that lane run apart from them for long after
+// the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
+// codes 11,000 to convert instead of 2,000).
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
+  return true;
+}
+
+// A value that is the same in every lane, said so in a way that the compiler
+// believes: tcgen05 instructions take their addresses and descriptors from
+// uniform registers, and for a value that it must take for divergent it emits a loop
+// over the lanes around each of them.
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uni_from(int x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
+
+// One lane of the warp, in a form that keeps what it issues uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
+// Barrier of the eight softmax warps: whether any thread's `pred` holds.
+__device__ __forceinline__ bool tree_softmax_bar(bool pred = false) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(uint32_t(pred))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t f) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int HD, bool Q8, int QT>
+__global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                   const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
+  using Cfg = TreeTc<HD, Q8, QT>;
+  constexpr int TOK = Cfg::kTok, H2 = Cfg::kHalves, KS = Cfg::kKSlots, VS = Cfg::kVSlots;
+  constexpr uint32_t kTmemCols = 512;
+  constexpr uint32_t kIdescQK = mma_idesc(128, 64, 0, 0);
+  constexpr uint32_t kIdescPV = mma_idesc(128, HD, 0, 1);
+  constexpr unsigned FULL = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  // (offset, not masked: the compiler keeps seeing shared memory behind the pointer)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = int(uni(tid >> 5));
+  uint8_t* q_s = smem + Cfg::q_off;
+  uint8_t* kring = smem + Cfg::k_off;
+  uint8_t* vring = smem + Cfg::v_off;
+  int2* meta = reinterpret_cast<int2*>(smem + Cfg::meta_off);
+  uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
+  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);
+  uint64_t* sempty = sfull + Cfg::kStages;
+  uint64_t* kfull = sempty + Cfg::kStages;
+  uint64_t* kempty = kfull + KS;
+  uint64_t* vfull = kempty + KS;
+  uint64_t* vempty = vfull + VS;
+  uint64_t* meta_full = vempty + VS;
+  uint64_t* exps_full = meta_full + Cfg::kMeta;
+  uint64_t* s_full = exps_full + Cfg::kMeta;  // [g][s] S written
+  uint64_t* p_full = s_full + 4;              // [g][s] P written, O_g rescaled
+  uint64_t* pv_done = s_full + 8;             // [g][s] O_g += P V complete
+  uint64_t* o_full = s_full + 12;             // [g] the row tile's last PV_g complete
+  uint64_t* q_full = s_full + 14;
+  uint64_t* q_empty = s_full + 15;            // the row tile's last QK complete
+  uint64_t* o_free = s_full + 16;             // both O read by the softmax warps
+  uint64_t* all_done = s_full + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
+  const int worker = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], 1);
+    }
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&kfull[i], Q8 ? 2 : 1);
+      mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&vfull[i], Q8 ? 2 : 1);
+      mbar_init(&vempty[i], 1);
+    }
+    for (int i = 0; i < Cfg::kMeta; ++i) {
+      mbar_init(&meta_full[i], 2);
+      mbar_init(&exps_full[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) mbar_init(&o_full[g], 1);
+    mbar_init(q_full, 32);
+    mbar_init(q_empty, 1);
+    mbar_init(o_free, 8);
+    mbar_init(all_done, 1);
+    fence_barrier_init();
+  }
+  if (tid < 4 * kTreeWords) bad_s[tid] = 0;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uni(*tmem_slot);
+  const uint32_t tmem_s = tmem, tmem_o = tmem + 256;
+  const int G = P.group, bs = P.block_size;
+
+  // Every warp's place on the line
+  typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::walk_off) + warp;
+  const TreeTile& t = place->tile;
+  tree_begin(P, S, place, worker, lane);
+  auto next_tile = [&]() { return tree_next(P, place); };
+  // Key tiles of a row tile: the keys past its last row's own position are no
+  // row's, so a tile of early rows (or a worker's share of one) may have fewer
+  // units than the line counts, or none.
+  auto key_tiles = [&](const TreeTile& w) {
+    const int last = min(w.q - 1, (w.r0 + Cfg::kRows - 1) / G);
+    const int units = (w.L - w.q + last + TOK) / TOK;
+    return max(0, min(w.s1, units) - w.s0);
+  };
+  // A chain's jobs among n key tiles; the key tile and the half of chain g's job m.
+  auto jobs = [](int n) { return QT == 2 ? 2 * n : n; };
+  auto tile_of = [](int m) { return QT == 2 ? m >> 1 : m; };
+  auto half_of = [](int g, int m) { return QT == 2 ? m & 1 : g; };
+  bool ok = true;
+
+  if (warp == 0 || (warp == 2 && !Q8)) {
+    // ================= copies =================
+    const int box = min(bs & -bs, 64), pieces = TOK / box;
+    const uint64_t pol = policy_evict_first();
+    int n = 0;    // key tiles so far
+    int iss = 0;  // and slots filled
+    int slot = 0, sphase = 0;  // of the 8-bit cache's next stage
+    while (ok && next_tile()) {
+      const int tiles = key_tiles(t);
+      const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
+      auto blocks_of = [&](int i) {  // lane l: the block of piece l of key tile i
+        const int key = (t.s0 + i) * TOK + lane * box;
+        return i < tiles && lane < pieces && key < t.L ? table[key / bs] : -1;
+      };
+      int next = blocks_of(0);
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        const int cur = next, j0 = (t.s0 + i) * TOK;
+        next = blocks_of(i + 1);
+        const bool there = cur >= 0 && cur < P.num_blocks;
+        if (lane < pieces && j0 + lane * box < t.L && !there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+        const unsigned valid = __ballot_sync(FULL, there);
+        const int64_t row = int64_t(cur) * bs + (j0 + lane * box) % bs;  // of this lane's piece
+        if constexpr (Q8) {
+          const int half = pieces / 2;
+          const int x = t.kvh * HD;
+          const int64_t eat = (int64_t(cur) * P.kv_heads + t.kvh) * bs + (j0 + lane * box) % bs;
+          uint64_t* efull = &exps_full[n % Cfg::kMeta];
+          const uint32_t ebytes = __popc(valid) * box * 2;
+#pragma unroll 1
+          for (int part = 0; part < 4; ++part) {
+            if (!tree_wait(&sempty[slot], sphase ^ 1)) {
+              ok = false;
+              break;
+            }
+            if (part == 0) {
+              if (lane == 0) {
+                if (ebytes) mbar_arrive_expect_tx(efull, ebytes); else mbar_arrive(efull);
+              }
+              __syncwarp();
+              if (there) {
+                uint8_t* e = smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + lane * box;
+                bulk_load(e, P.key_exps + eat, box, efull);
+                bulk_load(e + 128, P.value_exps + eat, box, efull);
+              }
+              __syncwarp();
+            }
+            const int p0 = (part & 1) * half;
+            const uint32_t bytes = __popc(valid >> p0 & ((1u << half) - 1)) * box * HD;
+            uint8_t* dst = smem + Cfg::stage_off + slot * Cfg::kStageBytes;
+            if (elect_one()) {
+              if (bytes) mbar_arrive_expect_tx(&sfull[slot], bytes); else mbar_arrive(&sfull[slot]);
+            }
+            for (int p = 0; p < half; ++p) {
+              const int y = uni_from(int(row), p0 + p);
+              if ((valid >> (p0 + p) & 1) && elect_one())
+                tma_load_2d(dst + p * box * HD, part < 2 ? &tmk : &tmv, &sfull[slot], x, y, pol);
+            }
+            __syncwarp();
+            ++iss;
+            if (++slot == Cfg::kStages) {
+              slot = 0;
+              sphase ^= 1;
+            }
+          }
+        } else {
+          const bool is_k = warp == 0;
+          const int nslots = is_k ? KS : VS;
+          slot = n % nslots;
+          uint64_t* full = is_k ? &kfull[slot] : &vfull[slot];
+          if (!tree_wait(is_k ? &kempty[slot] : &vempty[slot], ((n / nslots) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = __popc(valid) * box * 128 * H2;
+          if (lane == 0) {
+            if (bytes) mbar_arrive_expect_tx(full, bytes); else mbar_arrive(full);
+          }
+          __syncwarp();
+          uint8_t* dst = (is_k ? kring : vring) + slot * Cfg::kTile + lane * box * 128;
+          if (there)
+            for (int h = 0; h < H2; ++h)
+              tma_load_3d(dst + h * Cfg::kHalf, is_k ? &tmk : &tmv, full, 0, int(row), t.kvh * H2 + h, pol);
+          __syncwarp();
+          ++iss;
+        }
+      }
+    }
+    // copies still in flight land before the CTA's memory is given back
+    {
+      const int ns = Q8 ? Cfg::kStages : warp == 0 ? KS : VS;
+      uint64_t* fullb = Q8 ? sfull : warp == 0 ? kfull : vfull;
+      for (int i = iss > ns ? iss - ns : 0; i < iss; ++i) tree_wait(&fullb[i % ns], (i / ns) & 1);
+      if constexpr (Q8)
+        for (int i = max(0, n - Cfg::kMeta + 1); i < n; ++i)
+          tree_wait(&exps_full[i % Cfg::kMeta], (i / Cfg::kMeta) & 1);
+    }
+  } else if (warp == 1) {
+    // ================= MMA issuer =================
+    // Per row tile the first two S of both chains, then for the jobs m of both
+    // chains in turn O_g += P_g(m) V, S_g(m + 2): S_g(m + 2) overwrites P_g(m), which
+    // the tensor pipe, running one thread's operations in order, has then read.
+    // The whole warp waits and counts, one lane issues: what the instructions take
+    // from uniform registers then stays in them.
+    const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(kring), v_addr = smem_u32(vring);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!tree_wait(bar, parity)) ok = false;
+    };
+    int tile = 0;
+    uint32_t jp = 0;                             // a chain's jobs so far
+    int kslot = 0, kphase = 0, vslot = 0, vphase = 0;  // of the next K and V tile to read
+    while (ok && next_tile()) {
+      const int tiles = uni(key_tiles(t)), nj = jobs(tiles);
+      const int q_len = uni(t.q), prefix = uni(t.L) - q_len, s0 = uni(t.s0);
+      // S_g(m) into buffer b: keys of half hf of the K tile in kslot
+      auto qk = [&](int g, uint32_t b, int hf, bool tile_done, bool all_read) {
+        const uint32_t at = 2 * g + b, q0 = q_addr + (QT == 2 ? g : 0) * Cfg::kTile;
+        const uint32_t k0 = k_addr + kslot * Cfg::kTile + hf * 8192;
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < H2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma(tmem_s + at * 64, smem_desc(q0 + h * Cfg::kHalf + k * 32, 16, 1024),
+                     smem_desc(k0 + h * Cfg::kHalf + k * 32, 16, 1024), kIdescQK, (h | k) != 0);
+          tc_commit(&s_full[at]);
+          if (tile_done) tc_commit(&kempty[kslot]);  // its last reader
+          if (all_read) tc_commit(q_empty);          // the query tile may be replaced
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int g, uint32_t b, int hf, bool more, bool tile_done, bool last) {
+        const uint32_t at = 2 * g + b, v0 = v_addr + vslot * Cfg::kTile + hf * 8192;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_tmem_a(tmem_o + g * 128, tmem_s + at * 64 + k * 8,
+                          smem_desc(v0 + k * 2048, Cfg::kHalf, 1024), kIdescPV, k || more);
+          tc_commit(&pv_done[at]);
+          if (tile_done) tc_commit(&vempty[vslot]);
+          if (last) tc_commit(&o_full[g]);
+        }
+        __syncwarp();
+      };
+      // both chains' jobs m of S; K tiles are waited for and left in order
+      auto qk_both = [&](int m, int g) {
+        const int hf = half_of(g, m);
+        if (g == 0 && (QT == 1 || hf == 0)) wait(&kfull[kslot], kphase);
+        if (!ok) return;
+        tc_fence_after();
+        const bool done = g == 1 && (QT == 1 || hf == 1);
+        qk(g, (jp + m) & 1, hf, done, g == 1 && m + 1 == nj);
+        if (done && ++kslot == KS) {
+          kslot = 0;
+          kphase ^= 1;
+        }
+      };
+      wait(q_full, tile & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (tiles == 0 && elect_one()) tc_commit(q_empty);
+      __syncwarp();
+      if (QT == 1) {
+        // (job m of both chains reads K tile m)
+        for (int m = 0; m < 2 && m < nj && ok; ++m) {
+          qk_both(m, 0);
+          if (ok) qk_both(m, 1);
+        }
+      } else if (nj > 0) {
+        // (jobs 0 and 1 read K tile 0: chain 1's second is its last reader)
+        wait(&kfull[kslot], kphase);
+        if (ok) {
+          tc_fence_after();
+          qk(0, jp & 1, 0, false, false);
+          qk(0, (jp + 1) & 1, 1, false, false);
+          qk(1, jp & 1, 0, false, false);
+          qk(1, (jp + 1) & 1, 1, true, nj == 2);
+          if (++kslot == KS) {
+            kslot = 0;
+            kphase ^= 1;
+          }
+        }
+      }
+      // the last row tile's O has been read before the first PV overwrites it
+      if (tile > 0) wait(o_free, (tile - 1) & 1);
+      for (int m = 0; m < nj && ok; ++m) {
+        const uint32_t b = (jp + m) & 1, parity = (jp + m) >> 1 & 1;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int hf = half_of(g, m);
+          if (g == 0 && (QT == 1 || hf == 0)) {
+            wait(&vfull[vslot], vphase);
+            if constexpr (!Q8) {
+              // Rows behind the context may hold anything and become 0; non-finite
+              // elements of the drafts' rows leave the product
+              const int key0 = (s0 + tile_of(m)) * TOK;
+              if (ok && key0 + TOK > prefix) {
+                uint8_t* vb = vring + vslot * Cfg::kTile;
+                const int lo = max(prefix - key0, 0), hi = min(prefix + q_len - key0, TOK);  // drafts' rows
+                for (int at = lane; at < (TOK - hi) * 8 * H2; at += 32) {
+                  const int r = hi + at / (8 * H2), ch = at % (8 * H2);
+                  *reinterpret_cast<uint4*>(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                constexpr int B = 8;  // chunks a lane has in registers at a time
+                for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += 32 * B) {
+                  uint4 v[B];
+#pragma unroll
+                  for (int k = 0; k < B; ++k) {
+                    const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (r < hi) v[k] = lds128(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16);
+                  }
+#pragma unroll
+                  for (int k = 0; k < B; ++k) {
+                    bool hit = clear_nonfinite<false>(v[k].x);
+                    hit |= clear_nonfinite<false>(v[k].y);
+                    hit |= clear_nonfinite<false>(v[k].z);
+                    hit |= clear_nonfinite<false>(v[k].w);
+                    if (hit) {
+                      const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2), a = key0 + r - prefix;
+                      *reinterpret_cast<uint4*>(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16) = v[k];
+                      atomicOr(&bad_s[(tile & 3) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
+                    }
+                  }
+                }
+                fence_proxy_async();
+                __syncwarp();
+              }
+            }
+          }
+          if (ok) wait(&p_full[2 * g + b], parity);
+          if (!ok) break;
+          tc_fence_after();
+          const bool done = g == 1 && (QT == 1 || hf == 1);
+          pv(g, b, hf, m != 0, done, m + 1 == nj);
+          if (done && ++vslot == VS) {
+            vslot = 0;
+            vphase ^= 1;
+          }
+          if (m + 2 < nj) qk_both(m + 2, g);
+          if (!ok) break;
+        }
+      }
+      jp += nj;
+      ++tile;
+    }
+    if (elect_one()) tc_commit(all_done);
+    __syncwarp();
+  } else if (warp == 3) {
+    // ================= query tiles =================
+    int tile = 0;
+    if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
+    while (next_tile()) {
+      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy
+      const int ch = lane % CH;
+      const uint32_t base = smem_u32(q_s) + (ch >> 3) * Cfg::kHalf;
+#pragma unroll 1
+      for (int r0 = 0; r0 < Cfg::kRows; r0 += 32) {
+        // lane l finds row r0 + l of the query tensor
+        const int r = t.r0 + r0 + lane, i = r / G;
+        const int64_t tok = int64_t(t.q_start) + i;
+        const int from = i < t.q && tok < P.tokens ? int(tok * P.num_heads + t.kvh * G + r % G) : -1;
+#pragma unroll
+        for (int k = 0; k < 32 / RPI; ++k) {
+          const int row = r0 + k * RPI + lane / CH;
+          const int src = __shfl_sync(FULL, from, k * RPI + lane / CH);
+          cp_async16(base + (row >> 7) * Cfg::kTile + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                     P.query + int64_t(max(src, 0)) * HD + ch * 8, src >= 0);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(q_full);
+      if (tile == 0) {
+        // the note of a divided tile, before this warp's first wait
+        if (t.parts && lane == 0) tree_note(S, worker, t);
+        typename Cfg::Place* ahead = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::walk_off) + Cfg::kThreads / 32;
+        *ahead = *place;
+        __syncwarp();
+        while (tree_next(P, ahead))
+          if (ahead->tile.parts && lane == 0) tree_note(S, worker, ahead->tile);
+      }
+      ++tile;
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ================= softmax: group g (warps 4-7, 8-11) is chain g =================
+    const int g = (warp - 4) >> 2, quarter = warp & 3, m_lane = quarter * 32 + lane;
+    const int tr = (QT == 2 ? g * 128 : 0) + m_lane;  // row of the row tile
+    const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+    float2* stat = reinterpret_cast<float2*>(smem + Cfg::stat_off);
+    int tile = 0, n0 = 0, sj = 0, oc = 0;  // row tiles, key tiles, jobs, row tiles with keys
+    bool alive = true;  // agreed on by both groups, which meet at barriers
+    while (alive && next_tile()) {
+      const int tiles = key_tiles(t), nj = jobs(tiles);
+      const int prefix = t.L - t.q, r = t.r0 + tr, qi = r / G;
+      const int64_t tok = int64_t(t.q_start) + qi;
+      const bool row_ok = qi < t.q && tok < P.tokens;
+      const bool any_row = __any_sync(FULL, row_ok);
+      const bool drafts = (t.s0 + tiles) * TOK > prefix;
+      uint32_t bits[kTreeWords] = {};  // the drafts that this row sees (indexed: in local memory)
+      if (drafts && P.parents) {
+        uint8_t* par = smem + Cfg::par_off + (tile & 1) * PA_TREE_MAX_TOKENS;
+        for (int i = tid - 128; i < t.q; i += 256) {
+          const int up = int64_t(t.q_start) + i < P.tokens ? P.parents[t.q_start + i] : -1;
+          const bool fine = up >= -1 && up < i;
+          if (!fine) set_status(P.status, PA_STATUS_BIT_TREE);
+          par[i] = fine && up >= 0 ? uint8_t(up) : 255;
+        }
+        tree_softmax_bar();
+        if (row_ok) {
+          for (int i = qi;; i = par[i]) {
+            bits[i >> 5] |= 1u << (i & 31);
+            if (par[i] == 255) break;
+          }
+        }
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int m = 0; m < nj && ok; ++m, ++sj) {
+        const int i = tile_of(m), key0 = (t.s0 + i) * TOK + half_of(g, m) * 64, at = 2 * g + (sj & 1);
+        float F = P.scale_log2, ev = 0.f, unscale = 1.f;
+        if constexpr (Q8) {
+          const int k = (n0 + i) % Cfg::kMeta;
+          if (!tree_wait(&meta_full[k], ((n0 + i) / Cfg::kMeta) & 1)) { ok = false; break; }
+          const int2 e = meta[k];
+          F *= pow2(e.x);
+          ev = float(e.y);
+          unscale = pow2(-e.y);
+        }
+        if (!tree_wait(&s_full[at], (sj >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (any_row) {
+          const uint32_t sbuf = uni(tmem_s + at * 64 + lane_base);
+          float x[64];
+          tmem_ld32(sbuf, x);
+          tmem_ld32(sbuf + 32, x + 32);
+          const bool edge = key0 + 64 > prefix;
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int a0 = key0 + 32 * w - prefix;  // draft of the word's first column
+              uint32_t see = ~0u;                     // this row's columns
+              if (a0 > -32) {
+                if (P.parents) {
+                  // bits a0 .. a0 + 31 of (ones below 0, then the row's drafts)
+                  const int q = a0 >> 5, s = a0 & 31;
+                  const uint32_t lo = q < 0 ? ~0u : q < kTreeWords ? bits[q] : 0u;
+                  const uint32_t hi = q + 1 < kTreeWords ? bits[q + 1] : 0u;
+                  see = __funnelshift_r(lo, hi, s);
+                } else {
+                  const int n = qi - a0 + 1;  // columns up to the row's own
+                  see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[32 * w + k] = see >> k & 1 ? x[32 * w + k] : -INFINITY;
+            }
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), F, ev);
+          // move the reference only when a score passes it by more than 2^8
+          const bool grow = top > m_ref + kTcRescaleThreshold;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = ex2(m_ref - top);  // 0 on the first job that the row sees keys of
+            m_ref = top;
+            l *= alpha;
+          }
+          const float add = ev - (m_ref == -INFINITY ? 0.f : m_ref);
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float e0 = ex2(fmaf(x[32 * hf + 2 * k], F, add)), e1 = ex2(fmaf(x[32 * hf + 2 * k + 1], F, add));
+              sum[0] += e0;
+              sum[1] += e1;
+              pk[k] = pack_half2(e0, e1);
+            }
+            tmem_st16u(sbuf + hf * 16, pk);  // over scores that are in registers
+          }
+          l = fmaf(sum[0] + sum[1], unscale, l);
+          if (m > 0 && __any_sync(FULL, grow)) {
+            // O as the chain's job before left it
+            const int before = sj - 1;
+            if (!tree_wait(&pv_done[2 * g + (before & 1)], (before >> 1) & 1)) ok = false;
+            tc_fence_after();
+            const uint32_t o_mine = uni(tmem_o + g * 128 + lane_base);
+#pragma unroll 1
+            for (int cc = 0; cc < HD / 32; ++cc) {
+              float o[32];
+              tmem_ld32(o_mine + cc * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_st32(o_mine + cc * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[at]);
+      }
+      if (place->walk.u >= place->walk.u1) launch_dependents();  // the worker's last tile
+
+      // ---- the end of the row tile
+      float w[2] = {1.f, 0.f}, M = m_ref, sum = l;  // weights of O_0 and O_1 (QT = 2: of its own)
+      if constexpr (QT == 1) {
+        float2* st = stat + (tile & 1) * 256;
+        st[g * 128 + m_lane] = make_float2(m_ref, l);
+      }
+      alive = !tree_softmax_bar(!ok);
+      if constexpr (QT == 1) {
+        const float2* st = stat + (tile & 1) * 256;
+        const float2 a = st[m_lane], b = st[128 + m_lane];
+        M = fmaxf(a.x, b.x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        w[0] = ex2(a.x - ref);
+        w[1] = ex2(b.x - ref);
+        sum = a.y * w[0] + b.y * w[1];
+      }
+      if (tiles > 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if ((QT == 1 || k == g) && ok && !tree_wait(&o_full[k], oc & 1)) ok = false;
+        ++oc;
+      }
+      tc_fence_after();
+      const bool whole = t.slot < 0;
+      const float inv = whole ? 1.f / sum : 1.f;
+      const uint32_t* bad = bad_s + (tile & 3) * kTreeWords;
+      const int col0 = QT == 1 ? g * (HD / 2) : 0, cols = QT == 1 ? HD / 2 : HD;
+      bool any_bad = false;
+      if (drafts) {
+        uint32_t hit = 0;
+#pragma unroll
+        for (int k = 0; k < kTreeWords; ++k) hit |= bad[k];
+        any_bad = tree_softmax_bar(hit != 0);
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < cols / 16; ++cc) {
+        const int d0 = col0 + cc * 16;
+        float o[16], x[16];
+        const uint32_t from = uni(tmem_o + (QT == 2 ? g * 128 : 0) + d0 + lane_base);
+        if (tiles > 0) tmem_ld<16>(from, o);
+        if (QT == 1 && tiles > 0) tmem_ld<16>(from + 128, x);
+        tmem_wait_ld();
+        if (cc + 1 == cols / 16) {  // both O are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
+        if (!row_ok || !ok) continue;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          // (weight 0: a chain none of whose keys this row saw)
+          const float v = QT == 2 ? o[k] : (w[0] > 0.f ? o[k] * w[0] : 0.f) + (w[1] > 0.f ? x[k] * w[1] : 0.f);
+          o[k] = tiles > 0 ? v : 0.f;
+        }
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD + d0);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            dst[k] = make_uint4(pack_half2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                pack_half2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                pack_half2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                pack_half2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        } else {
+          float* dst = S.part_o + (int64_t(t.slot) * HD + d0) * Cfg::kRows + tr;  // by columns
+#pragma unroll
+          for (int k = 0; k < 16; ++k) dst[k * Cfg::kRows] = o[k];
+        }
+      }
+      if (!whole && row_ok && (QT == 2 || g == 0))
+        S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
+      // (this buffer's next row tile begins four tiles on, behind o_free)
+      if (any_bad) {
+        if (row_ok && alive)
+          tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK,
+                         whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr,
+                         S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr, Cfg::kRows, col0, 1, col0 + cols);
+        tree_softmax_bar();
+        if (tid - 128 < kTreeWords) bad_s[(tile & 3) * kTreeWords + tid - 128] = 0;
+      }
+      n0 += tiles;
+      ++tile;
+    }
+  } else if (warp >= 12) {
+    if constexpr (Q8) {
+    // ================= codes to fp16 operands =================
+    const int part = warp - 12, kv = part >> 1, ns = kv ? VS : KS;
+    constexpr int CH = HD / 8;      // 8-code chunks of a row: 16 bytes of operand
+    constexpr int RPI = 32 / CH;    // rows that the warp takes at a time
+    const int ch = lane % CH, r0 = lane / CH;
+    int n = 0, tile = 0;
+    while (ok && next_tile()) {
+      const int tiles = key_tiles(t), prefix = t.L - t.q;
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        const int key0 = (t.s0 + i) * TOK, st = n * 4 + part, slot = st % Cfg::kStages;
+        uint8_t* exps = smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + kv * 128;
+        ok = tree_wait(kv ? &vempty[n % ns] : &kempty[n % ns], ((n / ns) & 1) ^ 1) &&
+             tree_wait(&exps_full[n % Cfg::kMeta], (n / Cfg::kMeta) & 1);
+        if (!ok) break;
+        // the tile's largest exponent, over the keys of the context
+        const uint32_t e4 = *reinterpret_cast<const uint32_t*>(exps + lane * 4);
+        int top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (key0 + lane * 4 + k < t.L) top = max(top, int(e4 >> (8 * k) & 255));
+        top = __reduce_max_sync(FULL, top);
+        if ((part & 1) == 0 && lane == 0) {
+          int* m = reinterpret_cast<int*>(&meta[n % Cfg::kMeta]);
+          m[kv] = top - kExpBias;
+          mbar_arrive(&meta_full[n % Cfg::kMeta]);
+        }
+        if (!tree_wait(&sfull[slot], (st / Cfg::kStages) & 1)) { ok = false; break; }
+        uint8_t* src = smem + Cfg::stage_off + slot * Cfg::kStageBytes + lane * 8;
+        // this lane's rows, in the 64-dim half ch / 8 of the operand
+        uint8_t* dst = (kv ? vring + (n % VS) * Cfg::kTile : kring + (n % KS) * Cfg::kTile) + (ch >> 3) * Cfg::kHalf;
+        const int row0 = (part & 1) * 64 + r0;  // this lane's first row
+        if (key0 + TOK > prefix) {
+          // the tile reaches the drafts: rows behind the context become 0, and
+          // non-finite elements of the drafts' V rows leave the product
+          for (int k = 0; k < 64 / RPI; ++k) {
+            const int key = key0 + row0 + k * RPI, a = key - prefix;
+            uint2* p = reinterpret_cast<uint2*>(src + k * 256);
+            uint2 x = *p;
+            bool hit = key >= t.L;
+            if (hit) {
+              x = make_uint2(0, 0);
+              if (ch == 0) exps[row0 + k * RPI] = uint8_t(top);
+            } else if (kv && key >= prefix) {
+              hit = clear_nonfinite<true>(x.x);
+              hit |= clear_nonfinite<true>(x.y);
+              if (hit) atomicOr(&bad_s[(tile & 3) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
+            }
+            if (hit) *p = x;
+          }
+          __syncwarp();
+        }
+        // factors of rows lane and lane + 32 of the part: 2^-diff, in two steps (the
+        // second a rarity) where diff is past 14
+        uint32_t f1[2], f2[2];
+        bool deep = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + 32 * k + lane], more = max(diff, 14u) - 14u;
+          f1[k] = (15u - min(diff, 14u)) * 0x04000400u;
+          f2[k] = (more < 15 ? (15u - more) << 10 : more <= 24 ? 1u << (24 - more) : 0u) * 0x10001u;
+          deep |= more != 0;
+        }
+        deep = __any_sync(FULL, deep);
+        constexpr int B = 8;  // chunks in registers at a time
+#pragma unroll 1
+        for (int k0 = 0; k0 < 64 / RPI; k0 += B) {
+          uint2 x[B];
+#pragma unroll
+          for (int k = 0; k < B; ++k) x[k] = *reinterpret_cast<const uint2*>(src + (k0 + k) * 256);
+          const bool upper = k0 * RPI >= 32;  // (B * RPI divides 32)
+          const uint32_t fa = upper ? f1[1] : f1[0], fb = upper ? f2[1] : f2[0];
+#pragma unroll
+          for (int k = 0; k < B; ++k) {
+            const int rr = r0 + (k0 + k) * RPI, row = (part & 1) * 64 + rr;
+            const uint32_t f = __shfl_sync(FULL, fa, rr & 31);
+            uint32_t h[4] = {hmul2u(e4m3x2_half2(x[k].x), f), hmul2u(e4m3x2_half2(x[k].x >> 16), f),
+                             hmul2u(e4m3x2_half2(x[k].y), f), hmul2u(e4m3x2_half2(x[k].y >> 16), f)};
+            if (deep) {
+              const uint32_t fd = __shfl_sync(FULL, fb, rr & 31);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) h[j] = hmul2u(h[j], fd);
+            }
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sempty[slot]);
+          mbar_arrive(kv ? &vfull[n % VS] : &kfull[n % KS]);
+        }
+      }
+      ++tile;
+    }
+    }
+  }
+  if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_TIMEOUT);
+  // ---- teardown: every tcgen05 op has completed before TMEM is freed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(all_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+// Launches the kernel of a tile shape and its combine pass; with `need`, only
+// says how much workspace they take.
+cudaError_t tree_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
+                    void* ws, cudaStream_t s);
+
+}  // namespace pa
