@@ -3,18 +3,19 @@
 // the 8-bit cache.
 //
 // One persistent CTA per SM, a worker of the line (pa_tree_split.cuh) with units of
-// 128 keys. Two chains of S = Q K^T -> softmax -> O += P V run against each other in
-// jobs of 64 keys: with up to 128 rows chain g takes half g of every key tile and
-// the two states are joined at the end (QT = 1), with more each has a query tile of
-// its own and takes both halves (QT = 2). A chain has two S buffers in TMEM, so that
-// the product of its next job runs under the softmax of this one; 64 scores of a
-// row fit in a thread's registers, so they are read from TMEM once. (Jobs of 128
-// keys with one S buffer per chain and the scores read twice took 4.6 us per 256 rows
-// x 128 keys, almost all of it latency.)
+// 128 keys. Two chains of softmax and O += P V run against each other in jobs of 64
+// keys: with up to 128 rows chain g takes half g of every key tile, S = Q K^T of
+// two tiles being in TMEM, and the chains' states are joined at the end (QT = 1); with
+// more rows each chain has a query tile of its own and takes both halves of every
+// tile (QT = 2). The 64 scores of a row's job fit in a thread's registers, so they are
+// read from TMEM once. S is made for 128 keys at a time: an MMA of half the width
+// reads the query operand as often and took 500 cycles per 64 keys for the 64 it
+// computes. (Jobs of 128 keys, the scores read twice: 4.6 us per 256 rows x 128 keys.)
 //
 //   warp 0       keys' copies (TMA), for the 8-bit cache the values' too
-//   warp 1       issues every MMA: S_g's buffer s in TMEM columns 128 g + 64 s, O_g in
-//                [256 + 128 g, +HD); P_g (fp16) overwrites the front of its S, where
+//   warp 1       issues every MMA: S in TMEM columns [128 x, +128), x the key tile's
+//                parity (QT = 1) or the chain (QT = 2), O_g in [256 + 128 g, +HD); a
+//                job's P (fp16) overwrites the front of its 64 columns of S, where
 //                O += P V takes it as its A operand from TMEM
 //   warp 2       values' copies of the fp16 cache
 //   warp 3       the query tile of every row tile (cp.async)
@@ -63,8 +64,9 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [4][words]
   static constexpr uint32_t bars_off = bad_off + 4 * kTreeWords * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 2 * kMeta + 18;
-  static constexpr uint32_t walk_off = bars_off + kBars * 8;  // a warp's place on the line
+  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 2 * kMeta + 16;
+  static constexpr uint32_t fac_off = (bars_off + kBars * 8 + 15) & ~15u;     // [4][64] factors of rows
+  static constexpr uint32_t walk_off = fac_off + (Q8 ? 4 * 64 * 4 : 0);      // a warp's place on the line
   using Walk = TreeWalk<kTok, kRows, kLead>;
   using Place = TreePlace<Walk>;
   static constexpr uint32_t tmem_off = walk_off + (kThreads / 32 + 1) * sizeof(Place);
@@ -87,6 +89,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
 // codes 11,000 to convert instead of 2,000).
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
     if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
@@ -125,6 +128,42 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t f) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// An fp16 V tile [HD / 64][128 rows][128 B] before its product (one warp): rows
+// from `hi` become 0, and non-finite elements of rows [lo, hi), drafts row + a0,
+// become 0 and are flagged. Rare, hence not inlined.
+template <int H2>
+__device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, uint32_t* bad, int lane) {
+  constexpr uint32_t HALF = 128 * 128;
+  for (int at = lane; at < (128 - hi) * 8 * H2; at += 32) {
+    const int r = hi + at / (8 * H2), ch = at % (8 * H2);
+    *reinterpret_cast<uint4*>(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  constexpr int B = 8;  // chunks a lane has in registers at a time
+  for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += 32 * B) {
+    uint4 v[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (r < hi) v[k] = lds128(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      bool hit = clear_nonfinite<false>(v[k].x);
+      hit |= clear_nonfinite<false>(v[k].y);
+      hit |= clear_nonfinite<false>(v[k].z);
+      hit |= clear_nonfinite<false>(v[k].w);
+      if (hit) {
+        const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2), a = a0 + r;
+        *reinterpret_cast<uint4*>(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16) = v[k];
+        atomicOr(&bad[(a >> 5) % kTreeWords], 1u << (a & 31));
+      }
+    }
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
 template <int HD, bool Q8, int QT>
 __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -132,7 +171,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   using Cfg = TreeTc<HD, Q8, QT>;
   constexpr int TOK = Cfg::kTok, H2 = Cfg::kHalves, KS = Cfg::kKSlots, VS = Cfg::kVSlots;
   constexpr uint32_t kTmemCols = 512;
-  constexpr uint32_t kIdescQK = mma_idesc(128, 64, 0, 0);
+  constexpr uint32_t kIdescQK = mma_idesc(128, TOK, 0, 0);
   constexpr uint32_t kIdescPV = mma_idesc(128, HD, 0, 1);
   constexpr unsigned FULL = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
@@ -152,14 +191,15 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint64_t* vempty = vfull + VS;
   uint64_t* meta_full = vempty + VS;
   uint64_t* exps_full = meta_full + Cfg::kMeta;
-  uint64_t* s_full = exps_full + Cfg::kMeta;  // [g][s] S written
-  uint64_t* p_full = s_full + 4;              // [g][s] P written, O_g rescaled
-  uint64_t* pv_done = s_full + 8;             // [g][s] O_g += P V complete
-  uint64_t* o_full = s_full + 12;             // [g] the row tile's last PV_g complete
-  uint64_t* q_full = s_full + 14;
-  uint64_t* q_empty = s_full + 15;            // the row tile's last QK complete
-  uint64_t* o_free = s_full + 16;             // both O read by the softmax warps
-  uint64_t* all_done = s_full + 17;
+  // (of a job: [g][y], y the key tile's parity for QT = 1, its half for QT = 2)
+  uint64_t* s_full = exps_full + Cfg::kMeta;  // [x] S written
+  uint64_t* p_full = s_full + 2;              // [g][y] P written, O_g rescaled
+  uint64_t* pv_done = s_full + 6;             // [g][y] O_g += P V complete
+  uint64_t* o_full = s_full + 10;             // [g] the row tile's last PV_g complete
+  uint64_t* q_full = s_full + 12;
+  uint64_t* q_empty = s_full + 13;            // the row tile's last QK complete
+  uint64_t* o_free = s_full + 14;             // both O read by the softmax warps
+  uint64_t* all_done = s_full + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -181,11 +221,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       mbar_init(&exps_full[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    for (int g = 0; g < 2; ++g) mbar_init(&o_full[g], 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&o_full[g], 1);
+    }
     mbar_init(q_full, 32);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
@@ -219,10 +261,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int units = (w.L - w.q + last + TOK) / TOK;
     return max(0, min(w.s1, units) - w.s0);
   };
-  // A chain's jobs among n key tiles; the key tile and the half of chain g's job m.
-  auto jobs = [](int n) { return QT == 2 ? 2 * n : n; };
-  auto tile_of = [](int m) { return QT == 2 ? m >> 1 : m; };
-  auto half_of = [](int g, int m) { return QT == 2 ? m & 1 : g; };
+  // The phase of key tile n's S and jobs on their barriers.
+  auto phase_of = [](int n) { return QT == 2 ? n & 1 : n >> 1 & 1; };
   bool ok = true;
 
   if (warp == 0 || (warp == 2 && !Q8)) {
@@ -323,151 +363,124 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ================= MMA issuer =================
-    // Per row tile the first two S of both chains, then for the jobs m of both
-    // chains in turn O_g += P_g(m) V, S_g(m + 2): S_g(m + 2) overwrites P_g(m), which
-    // the tensor pipe, running one thread's operations in order, has then read.
+    // QT = 1: S(0) S(1), then per key tile n: O_0 += P_0(n) V, O_1 += P_1(n) V, S(n + 2).
+    // QT = 2: S_0(0) S_1(0), then per key tile n the halves' products in turn, and S_g(n + 1)
+    // behind O_g's second. An S overwrites the P of before, which the tensor pipe,
+    // running one thread's operations in order, has then read.
     // The whole warp waits and counts, one lane issues: what the instructions take
     // from uniform registers then stays in them.
-    const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(kring), v_addr = smem_u32(vring);
+    // Descriptors are a base and an offset in 16-byte units (the address field, in
+    // the low bits, does not overflow).
+    const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
+    const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!tree_wait(bar, parity)) ok = false;
     };
-    int tile = 0;
-    uint32_t jp = 0;                             // a chain's jobs so far
+    int tile = 0, n0 = 0;                              // row tiles and key tiles so far
     int kslot = 0, kphase = 0, vslot = 0, vphase = 0;  // of the next K and V tile to read
     while (ok && next_tile()) {
-      const int tiles = uni(key_tiles(t)), nj = jobs(tiles);
+      const int tiles = uni(key_tiles(t));
       const int q_len = uni(t.q), prefix = uni(t.L) - q_len, s0 = uni(t.s0);
-      // S_g(m) into buffer b: keys of half hf of the K tile in kslot
-      auto qk = [&](int g, uint32_t b, int hf, bool tile_done, bool all_read) {
-        const uint32_t at = 2 * g + b, q0 = q_addr + (QT == 2 ? g : 0) * Cfg::kTile;
-        const uint32_t k0 = k_addr + kslot * Cfg::kTile + hf * 8192;
+      // S into columns [128 x, +128): query tile g, the K tile in kslot
+      auto qk = [&](int x, int g, bool tile_done, bool all_read) {
+        const uint64_t a = dq + g * (Cfg::kTile >> 4), bk = dk + uint32_t(kslot * (Cfg::kTile >> 4));
+        const uint32_t s_col = tmem_s + x * 128;
+        tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < H2; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma(tmem_s + at * 64, smem_desc(q0 + h * Cfg::kHalf + k * 32, 16, 1024),
-                     smem_desc(k0 + h * Cfg::kHalf + k * 32, 16, 1024), kIdescQK, (h | k) != 0);
-          tc_commit(&s_full[at]);
+              tc_mma(s_col, a + ((h * Cfg::kHalf + k * 32) >> 4), bk + ((h * Cfg::kHalf + k * 32) >> 4), kIdescQK,
+                     (h | k) != 0);
+          tc_commit(&s_full[x]);
           if (tile_done) tc_commit(&kempty[kslot]);  // its last reader
           if (all_read) tc_commit(q_empty);          // the query tile may be replaced
         }
         __syncwarp();
-      };
-      auto pv = [&](int g, uint32_t b, int hf, bool more, bool tile_done, bool last) {
-        const uint32_t at = 2 * g + b, v0 = v_addr + vslot * Cfg::kTile + hf * 8192;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_tmem_a(tmem_o + g * 128, tmem_s + at * 64 + k * 8,
-                          smem_desc(v0 + k * 2048, Cfg::kHalf, 1024), kIdescPV, k || more);
-          tc_commit(&pv_done[at]);
-          if (tile_done) tc_commit(&vempty[vslot]);
-          if (last) tc_commit(&o_full[g]);
-        }
-        __syncwarp();
-      };
-      // both chains' jobs m of S; K tiles are waited for and left in order
-      auto qk_both = [&](int m, int g) {
-        const int hf = half_of(g, m);
-        if (g == 0 && (QT == 1 || hf == 0)) wait(&kfull[kslot], kphase);
-        if (!ok) return;
-        tc_fence_after();
-        const bool done = g == 1 && (QT == 1 || hf == 1);
-        qk(g, (jp + m) & 1, hf, done, g == 1 && m + 1 == nj);
-        if (done && ++kslot == KS) {
+        if (tile_done && ++kslot == KS) {
           kslot = 0;
           kphase ^= 1;
         }
       };
+      auto pv = [&](int g, int y, int hf, uint32_t p_col, bool more, bool tile_done, bool last) {
+        const uint64_t bv = dv + uint32_t(vslot * (Cfg::kTile >> 4) + hf * (8192 >> 4));
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_tmem_a(tmem_o + g * 128, p_col + k * 8, bv + (k * 2048 >> 4), kIdescPV, k || more);
+          tc_commit(&pv_done[2 * g + y]);
+          if (tile_done) tc_commit(&vempty[vslot]);
+          if (last) tc_commit(&o_full[g]);
+        }
+        __syncwarp();
+        if (tile_done && ++vslot == VS) {
+          vslot = 0;
+          vphase ^= 1;
+        }
+      };
       wait(q_full, tile & 1);
       if (!ok) break;
-      tc_fence_after();
-      if (tiles == 0 && elect_one()) tc_commit(q_empty);
-      __syncwarp();
+      if (tiles == 0) {
+        if (elect_one()) tc_commit(q_empty);
+        __syncwarp();
+      }
       if (QT == 1) {
-        // (job m of both chains reads K tile m)
-        for (int m = 0; m < 2 && m < nj && ok; ++m) {
-          qk_both(m, 0);
-          if (ok) qk_both(m, 1);
+        for (int i = 0; i < 2 && i < tiles && ok; ++i) {
+          wait(&kfull[kslot], kphase);
+          if (ok) qk((n0 + i) & 1, 0, true, i + 1 == tiles);
         }
-      } else if (nj > 0) {
-        // (jobs 0 and 1 read K tile 0: chain 1's second is its last reader)
+      } else if (tiles > 0) {
         wait(&kfull[kslot], kphase);
         if (ok) {
-          tc_fence_after();
-          qk(0, jp & 1, 0, false, false);
-          qk(0, (jp + 1) & 1, 1, false, false);
-          qk(1, jp & 1, 0, false, false);
-          qk(1, (jp + 1) & 1, 1, true, nj == 2);
-          if (++kslot == KS) {
-            kslot = 0;
-            kphase ^= 1;
-          }
+          qk(0, 0, false, false);
+          qk(1, 1, true, tiles == 1);
         }
       }
       // the last row tile's O has been read before the first PV overwrites it
       if (tile > 0) wait(o_free, (tile - 1) & 1);
-      for (int m = 0; m < nj && ok; ++m) {
-        const uint32_t b = (jp + m) & 1, parity = (jp + m) >> 1 & 1;
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int n = n0 + i, phase = phase_of(n);
+        const bool last = i + 1 == tiles;
+        wait(&vfull[vslot], vphase);
+        if constexpr (!Q8) {
+          // Rows behind the context may hold anything and become 0; non-finite
+          // elements of the drafts' rows leave the product
+          const int key0 = (s0 + i) * TOK;
+          if (ok && key0 + TOK > prefix)
+            clean_v_tile<H2>(vring + vslot * Cfg::kTile, max(prefix - key0, 0), min(prefix + q_len - key0, TOK), key0 - prefix,
+                    bad_s + (tile & 3) * kTreeWords, lane);
+        }
+        if constexpr (QT == 1) {
+          const uint32_t p_col = tmem_s + (n & 1) * 128;
+          if (ok) wait(&p_full[n & 1], phase);
+          if (!ok) break;
+          pv(0, n & 1, 0, p_col, i != 0, false, last);
+          wait(&p_full[2 + (n & 1)], phase);
+          if (!ok) break;
+          pv(1, n & 1, 1, p_col + 64, i != 0, true, last);
+          if (i + 2 < tiles) {
+            wait(&kfull[kslot], kphase);
+            if (!ok) break;
+            qk(n & 1, 0, true, i + 3 == tiles);
+          }
+        } else {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int hf = half_of(g, m);
-          if (g == 0 && (QT == 1 || hf == 0)) {
-            wait(&vfull[vslot], vphase);
-            if constexpr (!Q8) {
-              // Rows behind the context may hold anything and become 0; non-finite
-              // elements of the drafts' rows leave the product
-              const int key0 = (s0 + tile_of(m)) * TOK;
-              if (ok && key0 + TOK > prefix) {
-                uint8_t* vb = vring + vslot * Cfg::kTile;
-                const int lo = max(prefix - key0, 0), hi = min(prefix + q_len - key0, TOK);  // drafts' rows
-                for (int at = lane; at < (TOK - hi) * 8 * H2; at += 32) {
-                  const int r = hi + at / (8 * H2), ch = at % (8 * H2);
-                  *reinterpret_cast<uint4*>(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                constexpr int B = 8;  // chunks a lane has in registers at a time
-                for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += 32 * B) {
-                  uint4 v[B];
-#pragma unroll
-                  for (int k = 0; k < B; ++k) {
-                    const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (r < hi) v[k] = lds128(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16);
-                  }
-#pragma unroll
-                  for (int k = 0; k < B; ++k) {
-                    bool hit = clear_nonfinite<false>(v[k].x);
-                    hit |= clear_nonfinite<false>(v[k].y);
-                    hit |= clear_nonfinite<false>(v[k].z);
-                    hit |= clear_nonfinite<false>(v[k].w);
-                    if (hit) {
-                      const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2), a = key0 + r - prefix;
-                      *reinterpret_cast<uint4*>(vb + (ch >> 3) * Cfg::kHalf + r * 128 + (ch & 7) * 16) = v[k];
-                      atomicOr(&bad_s[(tile & 3) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
-                    }
-                  }
-                }
-                fence_proxy_async();
-                __syncwarp();
-              }
+          for (int j = 0; j < 4; ++j) {
+            const int hf = j >> 1, g = j & 1;
+            if (ok) wait(&p_full[2 * g + hf], phase);
+            if (!ok) break;
+            pv(g, hf, hf, tmem_s + g * 128 + hf * 64, i != 0 || hf, j == 3, last && hf == 1);
+            if (hf == 1 && !last) {
+              if (g == 0) wait(&kfull[kslot], kphase);
+              if (!ok) break;
+              qk(g, g, g == 1, g == 1 && i + 2 == tiles);
             }
           }
-          if (ok) wait(&p_full[2 * g + b], parity);
-          if (!ok) break;
-          tc_fence_after();
-          const bool done = g == 1 && (QT == 1 || hf == 1);
-          pv(g, b, hf, m != 0, done, m + 1 == nj);
-          if (done && ++vslot == VS) {
-            vslot = 0;
-            vphase ^= 1;
-          }
-          if (m + 2 < nj) qk_both(m + 2, g);
-          if (!ok) break;
         }
       }
-      jp += nj;
+      n0 += tiles;
       ++tile;
     }
     if (elect_one()) tc_commit(all_done);
@@ -519,10 +532,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int tr = (QT == 2 ? g * 128 : 0) + m_lane;  // row of the row tile
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     float2* stat = reinterpret_cast<float2*>(smem + Cfg::stat_off);
-    int tile = 0, n0 = 0, sj = 0, oc = 0;  // row tiles, key tiles, jobs, row tiles with keys
+    int tile = 0, n0 = 0, oc = 0;  // row tiles, key tiles, row tiles with keys
     bool alive = true;  // agreed on by both groups, which meet at barriers
     while (alive && next_tile()) {
-      const int tiles = key_tiles(t), nj = jobs(tiles);
+      const int tiles = key_tiles(t), nj = QT * tiles;
       const int prefix = t.L - t.q, r = t.r0 + tr, qi = r / G;
       const int64_t tok = int64_t(t.q_start) + qi;
       const bool row_ok = qi < t.q && tok < P.tokens;
@@ -546,21 +559,23 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
       }
       float m_ref = -INFINITY, l = 0.f;
-      for (int m = 0; m < nj && ok; ++m, ++sj) {
-        const int i = tile_of(m), key0 = (t.s0 + i) * TOK + half_of(g, m) * 64, at = 2 * g + (sj & 1);
+      for (int m = 0; m < nj && ok; ++m) {
+        const int i = QT == 2 ? m >> 1 : m, hf = QT == 2 ? m & 1 : g, n = n0 + i;
+        const int y = QT == 2 ? hf : n & 1, x_of_s = QT == 2 ? g : n & 1, phase = phase_of(n);
+        const int key0 = (t.s0 + i) * TOK + hf * 64;
         float F = P.scale_log2, ev = 0.f, unscale = 1.f;
         if constexpr (Q8) {
-          const int k = (n0 + i) % Cfg::kMeta;
-          if (!tree_wait(&meta_full[k], ((n0 + i) / Cfg::kMeta) & 1)) { ok = false; break; }
+          const int k = n % Cfg::kMeta;
+          if (!tree_wait(&meta_full[k], (n / Cfg::kMeta) & 1)) { ok = false; break; }
           const int2 e = meta[k];
           F *= pow2(e.x);
           ev = float(e.y);
           unscale = pow2(-e.y);
         }
-        if (!tree_wait(&s_full[at], (sj >> 1) & 1)) { ok = false; break; }
+        if (!tree_wait(&s_full[x_of_s], phase)) { ok = false; break; }
         tc_fence_after();
         if (any_row) {
-          const uint32_t sbuf = uni(tmem_s + at * 64 + lane_base);
+          const uint32_t sbuf = uni(tmem_s + x_of_s * 128 + hf * 64 + lane_base);
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
@@ -602,22 +617,22 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           const float add = ev - (m_ref == -INFINITY ? 0.f : m_ref);
           float sum[2] = {0.f, 0.f};
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int w = 0; w < 2; ++w) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float e0 = ex2(fmaf(x[32 * hf + 2 * k], F, add)), e1 = ex2(fmaf(x[32 * hf + 2 * k + 1], F, add));
+              const float e0 = ex2(fmaf(x[32 * w + 2 * k], F, add)), e1 = ex2(fmaf(x[32 * w + 2 * k + 1], F, add));
               sum[0] += e0;
               sum[1] += e1;
               pk[k] = pack_half2(e0, e1);
             }
-            tmem_st16u(sbuf + hf * 16, pk);  // over scores that are in registers
+            tmem_st16u(sbuf + w * 16, pk);  // over scores that are in registers
           }
           l = fmaf(sum[0] + sum[1], unscale, l);
           if (m > 0 && __any_sync(FULL, grow)) {
             // O as the chain's job before left it
-            const int before = sj - 1;
-            if (!tree_wait(&pv_done[2 * g + (before & 1)], (before >> 1) & 1)) ok = false;
+            const int nb = QT == 2 && hf ? n : n - 1, yb = QT == 2 ? hf ^ 1 : nb & 1;
+            if (!tree_wait(&pv_done[2 * g + yb], phase_of(nb))) ok = false;
             tc_fence_after();
             const uint32_t o_mine = uni(tmem_o + g * 128 + lane_base);
 #pragma unroll 1
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[at]);
+        if (lane == 0) mbar_arrive(&p_full[2 * g + y]);
       }
       if (place->walk.u >= place->walk.u1) launch_dependents();  // the worker's last tile
 
@@ -727,6 +742,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     constexpr int CH = HD / 8;      // 8-code chunks of a row: 16 bytes of operand
     constexpr int RPI = 32 / CH;    // rows that the warp takes at a time
     const int ch = lane % CH, r0 = lane / CH;
+    uint32_t* fac = reinterpret_cast<uint32_t*>(smem + Cfg::fac_off) + part * 64;
     int n = 0, tile = 0;
     while (ok && next_tile()) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
@@ -773,39 +789,44 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           }
           __syncwarp();
         }
-        // factors of rows lane and lane + 32 of the part: 2^-diff, in two steps (the
-        // second a rarity) where diff is past 14
-        uint32_t f1[2], f2[2];
+        // every row's factor 2^-diff, where diff is past 14 (a rarity) its first step
         bool deep = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + 32 * k + lane], more = max(diff, 14u) - 14u;
-          f1[k] = (15u - min(diff, 14u)) * 0x04000400u;
-          f2[k] = (more < 15 ? (15u - more) << 10 : more <= 24 ? 1u << (24 - more) : 0u) * 0x10001u;
-          deep |= more != 0;
+          const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + 32 * k + lane];
+          fac[32 * k + lane] = (15u - min(diff, 14u)) * 0x04000400u;
+          deep |= diff > 14;
         }
-        deep = __any_sync(FULL, deep);
+        __syncwarp();
         constexpr int B = 8;  // chunks in registers at a time
 #pragma unroll 1
         for (int k0 = 0; k0 < 64 / RPI; k0 += B) {
           uint2 x[B];
-#pragma unroll
-          for (int k = 0; k < B; ++k) x[k] = *reinterpret_cast<const uint2*>(src + (k0 + k) * 256);
-          const bool upper = k0 * RPI >= 32;  // (B * RPI divides 32)
-          const uint32_t fa = upper ? f1[1] : f1[0], fb = upper ? f2[1] : f2[0];
+          uint32_t f[B];
 #pragma unroll
           for (int k = 0; k < B; ++k) {
-            const int rr = r0 + (k0 + k) * RPI, row = (part & 1) * 64 + rr;
-            const uint32_t f = __shfl_sync(FULL, fa, rr & 31);
-            uint32_t h[4] = {hmul2u(e4m3x2_half2(x[k].x), f), hmul2u(e4m3x2_half2(x[k].x >> 16), f),
-                             hmul2u(e4m3x2_half2(x[k].y), f), hmul2u(e4m3x2_half2(x[k].y >> 16), f)};
-            if (deep) {
-              const uint32_t fd = __shfl_sync(FULL, fb, rr & 31);
+            x[k] = *reinterpret_cast<const uint2*>(src + (k0 + k) * 256);
+            f[k] = fac[r0 + (k0 + k) * RPI];
+          }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) h[j] = hmul2u(h[j], fd);
-            }
+          for (int k = 0; k < B; ++k) {
+            const int row = row0 + (k0 + k) * RPI;
             *reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+                make_uint4(hmul2u(e4m3x2_half2(x[k].x), f[k]), hmul2u(e4m3x2_half2(x[k].x >> 16), f[k]),
+                           hmul2u(e4m3x2_half2(x[k].y), f[k]), hmul2u(e4m3x2_half2(x[k].y >> 16), f[k]));
+          }
+        }
+        if (__any_sync(FULL, deep)) {
+          // the second step, for the rows that need it
+#pragma unroll 1
+          for (int k = 0; k < 64 / RPI; ++k) {
+            const int row = row0 + k * RPI;
+            const uint32_t diff = uint32_t(top) - exps[row], more = max(diff, 14u) - 14u;
+            if (more == 0) continue;
+            const uint32_t f2 = (more < 15 ? (15u - more) << 10 : more <= 24 ? 1u << (24 - more) : 0u) * 0x10001u;
+            uint4* p = reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const uint4 h = *p;
+            *p = make_uint4(hmul2u(h.x, f2), hmul2u(h.y, f2), hmul2u(h.z, f2), hmul2u(h.w, f2));
           }
         }
         fence_proxy_async();
