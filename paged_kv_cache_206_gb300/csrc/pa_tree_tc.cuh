@@ -12,13 +12,14 @@
 // reads the query operand as often and took 500 cycles per 64 keys for the 64 it
 // computes. (Jobs of 128 keys, the scores read twice: 4.6 us per 256 rows x 128 keys.)
 //
-//   warp 0       keys' copies (TMA), for the 8-bit cache the values' too
+//   warp 0       keys' copies (TMA)
 //   warp 1       issues every MMA: S in TMEM columns [128 x, +128), x the key tile's
 //                parity (QT = 1) or the chain (QT = 2), O_g in [256 + 128 g, +HD); a
 //                job's P (fp16) overwrites the front of its 64 columns of S, where
 //                O += P V takes it as its A operand from TMEM
-//   warp 2       values' copies of the fp16 cache
-//   warp 3       the query tile of every row tile (cp.async)
+//   warp 2       values' copies
+//   warp 3       finds the row tiles on the line and tells them to the others; loads
+//                their query tiles (cp.async)
 //   warps 4-11   softmax, one row a thread: group g = chain g
 //   warps 12-15  8-bit cache only: codes to fp16 operands, each warp one of the four
 //                64-row parts (K, K, V, V) of a tile. The rows of a tile are
@@ -32,7 +33,7 @@
 // maxima and accumulators are fp32, the weights fp16. All roles walk the same
 // tiles of the line; rings and barriers run on across them, so the copies of the
 // next tile are under way while the last one's rows are written out. Every wait is
-// bounded; what was noted for the combine pass stands before the first of them.
+// bounded.
 #pragma once
 
 #include "pa_prefill_tc.cuh"
@@ -52,8 +53,10 @@ struct TreeTc {
   static constexpr int kKSlots = Q8 || QT == 2 ? 2 : 3;
   static constexpr int kVSlots = Q8 && QT == 2 ? 1 : 2;
   static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
-  static constexpr int kStages = Q8 ? 7 : 0;
-  static constexpr int kMeta = 4;                        // tiles whose exponents are held
+  static constexpr int kKStages = Q8 ? 4 : 0, kVStages = Q8 ? 3 : 0, kStages = kKStages + kVStages;
+  static constexpr int kMeta = 4;                        // key tiles whose exponents are held
+  static constexpr int kAhead = 4;                       // row tiles told to the roles
+  static constexpr int kRoles = Q8 ? 15 : 11;            // warps that are told
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t k_off = q_off + QT * kTile;
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
@@ -64,12 +67,11 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [4][words]
   static constexpr uint32_t bars_off = bad_off + 4 * kTreeWords * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 2 * kMeta + 16;
-  static constexpr uint32_t fac_off = (bars_off + kBars * 8 + 15) & ~15u;     // [4][64] factors of rows
-  static constexpr uint32_t walk_off = fac_off + (Q8 ? 4 * 64 * 4 : 0);      // a warp's place on the line
+  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 3 * kMeta + 16 + 2 * kAhead;
+  static constexpr uint32_t fac_off = (bars_off + kBars * 8 + 15) & ~15u;  // [4][64] factors of rows
   using Walk = TreeWalk<kTok, kRows, kLead>;
-  using Place = TreePlace<Walk>;
-  static constexpr uint32_t tmem_off = walk_off + (kThreads / 32 + 1) * sizeof(Place);
+  static constexpr uint32_t tile_off = fac_off + (Q8 ? 4 * 64 * 4 : 0);    // [kAhead] row tiles
+  static constexpr uint32_t tmem_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
   static constexpr uint32_t bytes = tmem_off + 16 + 1024;
   static_assert(bytes <= kTcMaxSmem, "shared memory");
 };
@@ -190,9 +192,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint64_t* vfull = kempty + KS;
   uint64_t* vempty = vfull + VS;
   uint64_t* meta_full = vempty + VS;
-  uint64_t* exps_full = meta_full + Cfg::kMeta;
+  uint64_t* exps_full = meta_full + Cfg::kMeta;      // [K, V][kMeta]
+  uint64_t* tile_full = exps_full + 2 * Cfg::kMeta;  // a row tile told to the roles
+  uint64_t* tile_empty = tile_full + Cfg::kAhead;
   // (of a job: [g][y], y the key tile's parity for QT = 1, its half for QT = 2)
-  uint64_t* s_full = exps_full + Cfg::kMeta;  // [x] S written
+  uint64_t* s_full = tile_empty + Cfg::kAhead;  // [x] S written
   uint64_t* p_full = s_full + 2;              // [g][y] P written, O_g rescaled
   uint64_t* pv_done = s_full + 6;             // [g][y] O_g += P V complete
   uint64_t* o_full = s_full + 10;             // [g] the row tile's last PV_g complete
@@ -219,6 +223,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     for (int i = 0; i < Cfg::kMeta; ++i) {
       mbar_init(&meta_full[i], 2);
       mbar_init(&exps_full[i], 1);
+      mbar_init(&exps_full[Cfg::kMeta + i], 1);
+    }
+    for (int i = 0; i < Cfg::kAhead; ++i) {
+      mbar_init(&tile_full[i], 1);
+      mbar_init(&tile_empty[i], Cfg::kRoles);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&p_full[i], 4);
@@ -248,11 +257,19 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   const uint32_t tmem_s = tmem, tmem_o = tmem + 256;
   const int G = P.group, bs = P.block_size;
 
-  // Every warp's place on the line
-  typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::walk_off) + warp;
-  const TreeTile& t = place->tile;
-  tree_begin(P, S, place, worker, lane);
-  auto next_tile = [&]() { return tree_next(P, place); };
+  // The row tiles, as warp 3 finds them on the line, told to the other roles through
+  // a ring (one reading of the lengths for the whole CTA); q < 0 ends them.
+  TreeTile* told = reinterpret_cast<TreeTile*>(smem + Cfg::tile_off);
+  int heard = 0;  // row tiles begun
+  auto next_tile = [&](TreeTile& t) {
+    __syncwarp();
+    if (heard > 0 && lane == 0) mbar_arrive(&tile_empty[(heard - 1) % Cfg::kAhead]);
+    const int at = heard % Cfg::kAhead;
+    if (!tree_wait(&tile_full[at], (heard / Cfg::kAhead) & 1)) return false;
+    t = told[at];
+    ++heard;
+    return t.q >= 0;
+  };
   // Key tiles of a row tile: the keys past its last row's own position are no
   // row's, so a tile of early rows (or a worker's share of one) may have fewer
   // units than the line counts, or none.
@@ -265,14 +282,17 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   auto phase_of = [](int n) { return QT == 2 ? n & 1 : n >> 1 & 1; };
   bool ok = true;
 
-  if (warp == 0 || (warp == 2 && !Q8)) {
+  if (warp == 0 || warp == 2) {
     // ================= copies =================
     const int box = min(bs & -bs, 64), pieces = TOK / box;
     const uint64_t pol = policy_evict_first();
+    const bool is_k = warp == 0;
+    const CUtensorMap* map = is_k ? &tmk : &tmv;
     int n = 0;    // key tiles so far
     int iss = 0;  // and slots filled
     int slot = 0, sphase = 0;  // of the 8-bit cache's next stage
-    while (ok && next_tile()) {
+    TreeTile t;
+    while (ok && next_tile(t)) {
       const int tiles = key_tiles(t);
       const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
       auto blocks_of = [&](int i) {  // lane l: the block of piece l of key tile i
@@ -291,46 +311,45 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           const int half = pieces / 2;
           const int x = t.kvh * HD;
           const int64_t eat = (int64_t(cur) * P.kv_heads + t.kvh) * bs + (j0 + lane * box) % bs;
-          uint64_t* efull = &exps_full[n % Cfg::kMeta];
-          const uint32_t ebytes = __popc(valid) * box * 2;
+          uint64_t* efull = &exps_full[(is_k ? 0 : Cfg::kMeta) + n % Cfg::kMeta];
+          const uint32_t ebytes = __popc(valid) * box;
+          if (elect_one()) {
+            if (ebytes) mbar_arrive_expect_tx(efull, ebytes); else mbar_arrive(efull);
+          }
+          __syncwarp();
+          // (the slot's last reader was four tiles ago, before what the ring waits for)
+          bool wait_first = true;
 #pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
-            if (!tree_wait(&sempty[slot], sphase ^ 1)) {
+          for (int part = 0; part < 2; ++part) {
+            uint64_t* full = sfull + (is_k ? 0 : Cfg::kKStages) + slot;
+            if (!tree_wait(sempty + (is_k ? 0 : Cfg::kKStages) + slot, sphase ^ 1)) {
               ok = false;
               break;
             }
-            if (part == 0) {
-              if (lane == 0) {
-                if (ebytes) mbar_arrive_expect_tx(efull, ebytes); else mbar_arrive(efull);
-              }
-              __syncwarp();
-              if (there) {
-                uint8_t* e = smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + lane * box;
-                bulk_load(e, P.key_exps + eat, box, efull);
-                bulk_load(e + 128, P.value_exps + eat, box, efull);
-              }
-              __syncwarp();
-            }
-            const int p0 = (part & 1) * half;
+            if (wait_first && there)
+              bulk_load(smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + (is_k ? 0 : 128) + lane * box,
+                        (is_k ? P.key_exps : P.value_exps) + eat, box, efull);
+            wait_first = false;
+            __syncwarp();
+            const int p0 = part * half;
             const uint32_t bytes = __popc(valid >> p0 & ((1u << half) - 1)) * box * HD;
-            uint8_t* dst = smem + Cfg::stage_off + slot * Cfg::kStageBytes;
+            uint8_t* dst = smem + Cfg::stage_off + ((is_k ? 0 : Cfg::kKStages) + slot) * Cfg::kStageBytes;
             if (elect_one()) {
-              if (bytes) mbar_arrive_expect_tx(&sfull[slot], bytes); else mbar_arrive(&sfull[slot]);
+              if (bytes) mbar_arrive_expect_tx(full, bytes); else mbar_arrive(full);
             }
+            __syncwarp();
             for (int p = 0; p < half; ++p) {
               const int y = uni_from(int(row), p0 + p);
-              if ((valid >> (p0 + p) & 1) && elect_one())
-                tma_load_2d(dst + p * box * HD, part < 2 ? &tmk : &tmv, &sfull[slot], x, y, pol);
+              if ((valid >> (p0 + p) & 1) && elect_one()) tma_load_2d(dst + p * box * HD, map, full, x, y, pol);
             }
             __syncwarp();
             ++iss;
-            if (++slot == Cfg::kStages) {
+            if (++slot == (is_k ? Cfg::kKStages : Cfg::kVStages)) {
               slot = 0;
               sphase ^= 1;
             }
           }
         } else {
-          const bool is_k = warp == 0;
           const int nslots = is_k ? KS : VS;
           slot = n % nslots;
           uint64_t* full = is_k ? &kfull[slot] : &vfull[slot];
@@ -346,7 +365,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           uint8_t* dst = (is_k ? kring : vring) + slot * Cfg::kTile + lane * box * 128;
           if (there)
             for (int h = 0; h < H2; ++h)
-              tma_load_3d(dst + h * Cfg::kHalf, is_k ? &tmk : &tmv, full, 0, int(row), t.kvh * H2 + h, pol);
+              tma_load_3d(dst + h * Cfg::kHalf, map, full, 0, int(row), t.kvh * H2 + h, pol);
           __syncwarp();
           ++iss;
         }
@@ -354,12 +373,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     }
     // copies still in flight land before the CTA's memory is given back
     {
-      const int ns = Q8 ? Cfg::kStages : warp == 0 ? KS : VS;
-      uint64_t* fullb = Q8 ? sfull : warp == 0 ? kfull : vfull;
+      const int ns = Q8 ? (is_k ? Cfg::kKStages : Cfg::kVStages) : is_k ? KS : VS;
+      uint64_t* fullb = Q8 ? sfull + (is_k ? 0 : Cfg::kKStages) : is_k ? kfull : vfull;
       for (int i = iss > ns ? iss - ns : 0; i < iss; ++i) tree_wait(&fullb[i % ns], (i / ns) & 1);
       if constexpr (Q8)
         for (int i = max(0, n - Cfg::kMeta + 1); i < n; ++i)
-          tree_wait(&exps_full[i % Cfg::kMeta], (i / Cfg::kMeta) & 1);
+          tree_wait(&exps_full[(is_k ? 0 : Cfg::kMeta) + i % Cfg::kMeta], (i / Cfg::kMeta) & 1);
     }
   } else if (warp == 1) {
     // ================= MMA issuer =================
@@ -378,7 +397,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     };
     int tile = 0, n0 = 0;                              // row tiles and key tiles so far
     int kslot = 0, kphase = 0, vslot = 0, vphase = 0;  // of the next K and V tile to read
-    while (ok && next_tile()) {
+    TreeTile t;
+    while (ok && next_tile(t)) {
       const int tiles = uni(key_tiles(t));
       const int q_len = uni(t.q), prefix = uni(t.L) - q_len, s0 = uni(t.s0);
       // S into columns [128 x, +128): query tile g, the K tile in kslot
@@ -486,10 +506,28 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     if (elect_one()) tc_commit(all_done);
     __syncwarp();
   } else if (warp == 3) {
-    // ================= query tiles =================
+    // ================= row tiles and their queries =================
     int tile = 0;
     if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
-    while (next_tile()) {
+    typename Cfg::Walk walk;
+    TreeTile t;
+    walk.begin(P, S, worker, lane);
+    while (true) {
+      const bool some = walk.next(P, t);
+      if (!some) t.q = -1;
+      const int at = tile % Cfg::kAhead;
+      if (!tree_wait(&tile_empty[at], ((tile / Cfg::kAhead) & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        told[at] = t;
+        if (some && t.parts) tree_note(S, worker, t);
+        mbar_arrive(&tile_full[at]);
+      }
+      __syncwarp();
+      if (!some) break;
+      if (walk.u >= walk.u1) launch_dependents();  // the worker's last tile
       if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1)) {
         ok = false;
         break;
@@ -515,15 +553,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       cp_async_wait<0>();
       fence_proxy_async();
       mbar_arrive(q_full);
-      if (tile == 0) {
-        // the note of a divided tile, before this warp's first wait
-        if (t.parts && lane == 0) tree_note(S, worker, t);
-        typename Cfg::Place* ahead = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::walk_off) + Cfg::kThreads / 32;
-        *ahead = *place;
-        __syncwarp();
-        while (tree_next(P, ahead))
-          if (ahead->tile.parts && lane == 0) tree_note(S, worker, ahead->tile);
-      }
       ++tile;
     }
   } else if (warp >= 4 && warp < 12) {
@@ -534,7 +563,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     float2* stat = reinterpret_cast<float2*>(smem + Cfg::stat_off);
     int tile = 0, n0 = 0, oc = 0;  // row tiles, key tiles, row tiles with keys
     bool alive = true;  // agreed on by both groups, which meet at barriers
-    while (alive && next_tile()) {
+    TreeTile t;
+    while (alive && next_tile(t)) {
       const int tiles = key_tiles(t), nj = QT * tiles;
       const int prefix = t.L - t.q, r = t.r0 + tr, qi = r / G;
       const int64_t tok = int64_t(t.q_start) + qi;
@@ -651,7 +681,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * g + y]);
       }
-      if (place->walk.u >= place->walk.u1) launch_dependents();  // the worker's last tile
 
       // ---- the end of the row tile
       float w[2] = {1.f, 0.f}, M = m_ref, sum = l;  // weights of O_0 and O_1 (QT = 2: of its own)
@@ -744,13 +773,15 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int ch = lane % CH, r0 = lane / CH;
     uint32_t* fac = reinterpret_cast<uint32_t*>(smem + Cfg::fac_off) + part * 64;
     int n = 0, tile = 0;
-    while (ok && next_tile()) {
+    TreeTile t;
+    while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const int key0 = (t.s0 + i) * TOK, st = n * 4 + part, slot = st % Cfg::kStages;
+        const int key0 = (t.s0 + i) * TOK, st = n * 2 + (part & 1), nst = kv ? Cfg::kVStages : Cfg::kKStages;
+        const int slot = (kv ? Cfg::kKStages : 0) + st % nst;
         uint8_t* exps = smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + kv * 128;
         ok = tree_wait(kv ? &vempty[n % ns] : &kempty[n % ns], ((n / ns) & 1) ^ 1) &&
-             tree_wait(&exps_full[n % Cfg::kMeta], (n / Cfg::kMeta) & 1);
+             tree_wait(&exps_full[kv * Cfg::kMeta + n % Cfg::kMeta], (n / Cfg::kMeta) & 1);
         if (!ok) break;
         // the tile's largest exponent, over the keys of the context
         const uint32_t e4 = *reinterpret_cast<const uint32_t*>(exps + lane * 4);
@@ -764,7 +795,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           m[kv] = top - kExpBias;
           mbar_arrive(&meta_full[n % Cfg::kMeta]);
         }
-        if (!tree_wait(&sfull[slot], (st / Cfg::kStages) & 1)) { ok = false; break; }
+        if (!tree_wait(&sfull[slot], (st / nst) & 1)) { ok = false; break; }
         uint8_t* src = smem + Cfg::stage_off + slot * Cfg::kStageBytes + lane * 8;
         // this lane's rows, in the 64-dim half ch / 8 of the operand
         uint8_t* dst = (kv ? vring + (n % VS) * Cfg::kTile : kring + (n % KS) * Cfg::kTile) + (ch >> 3) * Cfg::kHalf;
