@@ -21,8 +21,8 @@
 //   warp 3       finds the row tiles on the line and tells them to the others; loads
 //                their query tiles (cp.async)
 //   warps 4-11   softmax, one row a thread: group g = chain g
-//   warps 12-15  8-bit cache only: codes to fp16 operands, each warp one of the four
-//                64-row parts (K, K, V, V) of a tile. The rows of a tile are
+//   warps 12-15  8-bit cache only: codes to fp16 operands, a warp for each of the
+//                four 64-row parts (K, K, V, V) of a tile. The rows of a tile are
 //                brought to the tile's largest exponent (code * 2^(e_j - e_max), exact
 //                but for rows 2^15 times smaller than the tile's largest, whose
 //                low bits fall under fp16's 2^-24: an absolute 2^-25 of that
@@ -43,7 +43,8 @@ namespace pa {
 
 template <int HD, bool Q8, int QT>
 struct TreeTc {
-  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
+  static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : 384;
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
   static constexpr int kLead = 3;
@@ -56,7 +57,7 @@ struct TreeTc {
   static constexpr int kKStages = Q8 ? 4 : 0, kVStages = Q8 ? 3 : 0, kStages = kKStages + kVStages;
   static constexpr int kMeta = 4;                        // key tiles whose exponents are held
   static constexpr int kAhead = 4;                       // row tiles told to the roles
-  static constexpr int kRoles = Q8 ? 15 : 11;            // warps that are told
+  static constexpr int kRoles = Q8 ? 11 + 4 * kConv : 11;            // warps that are told
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t k_off = q_off + QT * kTile;
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
@@ -68,9 +69,8 @@ struct TreeTc {
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [4][words]
   static constexpr uint32_t bars_off = bad_off + 4 * kTreeWords * 4;
   static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 3 * kMeta + 16 + 2 * kAhead;
-  static constexpr uint32_t fac_off = (bars_off + kBars * 8 + 15) & ~15u;  // [4][64] factors of rows
   using Walk = TreeWalk<kTok, kRows, kLead>;
-  static constexpr uint32_t tile_off = fac_off + (Q8 ? 4 * 64 * 4 : 0);    // [kAhead] row tiles
+  static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
   static constexpr uint32_t tmem_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
   static constexpr uint32_t bytes = tmem_off + 16 + 1024;
   static_assert(bytes <= kTcMaxSmem, "shared memory");
@@ -94,6 +94,15 @@ __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
+  return true;
+}
+
+// The same for three barriers at once.
+__device__ __forceinline__ bool tree_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c,
+                                           uint32_t pc) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(a, pa) & mbar_try_wait(b, pb) & mbar_try_wait(c, pc)))
     if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
   return true;
 }
@@ -210,14 +219,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < Cfg::kStages; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], 1);
+      mbar_init(&sempty[i], Cfg::kConv);
     }
     for (int i = 0; i < KS; ++i) {
-      mbar_init(&kfull[i], Q8 ? 2 : 1);
+      mbar_init(&kfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(&vfull[i], Q8 ? 2 : 1);
+      mbar_init(&vfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&vempty[i], 1);
     }
     for (int i = 0; i < Cfg::kMeta; ++i) {
@@ -767,43 +776,48 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   } else if (warp >= 12) {
     if constexpr (Q8) {
     // ================= codes to fp16 operands =================
-    const int part = warp - 12, kv = part >> 1, ns = kv ? VS : KS;
-    constexpr int CH = HD / 8;      // 8-code chunks of a row: 16 bytes of operand
-    constexpr int RPI = 32 / CH;    // rows that the warp takes at a time
-    const int ch = lane % CH, r0 = lane / CH;
-    uint32_t* fac = reinterpret_cast<uint32_t*>(smem + Cfg::fac_off) + part * 64;
-    int n = 0, tile = 0;
+    const int part = (warp - 12) / Cfg::kConv, sub = (warp - 12) % Cfg::kConv, kv = part >> 1;
+    constexpr int ROWS = 64 / Cfg::kConv;  // of this warp
+    constexpr int CH = HD / 8;             // 8-code chunks of a row: 16 bytes of operand
+    constexpr int RPI = 32 / CH;           // rows that the warp takes at a time
+    const int ch = lane % CH, row0 = (part & 1) * 64 + sub * ROWS + lane / CH;  // this lane's first row
+    uint64_t* full = kv ? vfull : kfull;
+    uint64_t* empty = kv ? vempty : kempty;
+    uint64_t* landed = sfull + (kv ? Cfg::kKStages : 0);
+    uint64_t* taken = sempty + (kv ? Cfg::kKStages : 0);
+    uint8_t* stage = smem + Cfg::stage_off + (kv ? Cfg::kKStages : 0) * Cfg::kStageBytes + sub * ROWS * HD + lane * 8;
+    // this lane's places in the operand: the 64-dim half ch / 8 of row0, row0 + RPI, ...
+    uint8_t* operand = (kv ? vring : kring) + (ch >> 3) * Cfg::kHalf + row0 * 128;
+    // (rings of this warp's tile: slots and phases counted, as a remainder takes long)
+    const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
+    int slot = 0, phase = 0, st = part & 1, sphase = 0, em = 0, ephase = 0, tile = 0;
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const int key0 = (t.s0 + i) * TOK, st = n * 2 + (part & 1), nst = kv ? Cfg::kVStages : Cfg::kKStages;
-        const int slot = (kv ? Cfg::kKStages : 0) + st % nst;
-        uint8_t* exps = smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + kv * 128;
-        ok = tree_wait(kv ? &vempty[n % ns] : &kempty[n % ns], ((n / ns) & 1) ^ 1) &&
-             tree_wait(&exps_full[kv * Cfg::kMeta + n % Cfg::kMeta], (n / Cfg::kMeta) & 1);
-        if (!ok) break;
+      for (int i = 0; i < tiles; ++i) {
+        const int key0 = (t.s0 + i) * TOK;
+        uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
+        if (!tree_wait3(&exps_full[kv * Cfg::kMeta + em], ephase, &landed[st], sphase, &empty[slot], phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* src = stage + st * Cfg::kStageBytes;
+        uint8_t* dst = operand + slot * Cfg::kTile;
         // the tile's largest exponent, over the keys of the context
         const uint32_t e4 = *reinterpret_cast<const uint32_t*>(exps + lane * 4);
-        int top = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (key0 + lane * 4 + k < t.L) top = max(top, int(e4 >> (8 * k) & 255));
+        const int left = t.L - key0 - lane * 4;  // of this lane's four
+        int top = max(max(left > 0 ? int(e4 & 255) : 0, left > 1 ? int(e4 >> 8 & 255) : 0),
+                      max(left > 2 ? int(e4 >> 16 & 255) : 0, left > 3 ? int(e4 >> 24) : 0));
         top = __reduce_max_sync(FULL, top);
-        if ((part & 1) == 0 && lane == 0) {
-          int* m = reinterpret_cast<int*>(&meta[n % Cfg::kMeta]);
-          m[kv] = top - kExpBias;
-          mbar_arrive(&meta_full[n % Cfg::kMeta]);
+        if ((part & 1) == 0 && sub == 0 && lane == 0) {
+          reinterpret_cast<int*>(&meta[em])[kv] = top - kExpBias;
+          mbar_arrive(&meta_full[em]);
         }
-        if (!tree_wait(&sfull[slot], (st / nst) & 1)) { ok = false; break; }
-        uint8_t* src = smem + Cfg::stage_off + slot * Cfg::kStageBytes + lane * 8;
-        // this lane's rows, in the 64-dim half ch / 8 of the operand
-        uint8_t* dst = (kv ? vring + (n % VS) * Cfg::kTile : kring + (n % KS) * Cfg::kTile) + (ch >> 3) * Cfg::kHalf;
-        const int row0 = (part & 1) * 64 + r0;  // this lane's first row
         if (key0 + TOK > prefix) {
           // the tile reaches the drafts: rows behind the context become 0, and
           // non-finite elements of the drafts' V rows leave the product
-          for (int k = 0; k < 64 / RPI; ++k) {
+#pragma unroll 1
+          for (int k = 0; k < ROWS / RPI; ++k) {
             const int key = key0 + row0 + k * RPI, a = key - prefix;
             uint2* p = reinterpret_cast<uint2*>(src + k * 256);
             uint2 x = *p;
@@ -820,29 +834,30 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           }
           __syncwarp();
         }
-        // every row's factor 2^-diff, where diff is past 14 (a rarity) its first step
+        // factors of the rows lane, lane + 32 of this warp: 2^-diff, where diff is past
+        // 14 (a rarity) its first step
+        uint32_t fac[ROWS / 32];
         bool deep = false;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + 32 * k + lane];
-          fac[32 * k + lane] = (15u - min(diff, 14u)) * 0x04000400u;
+        for (int k = 0; k < ROWS / 32; ++k) {
+          const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + sub * ROWS + 32 * k + lane];
+          fac[k] = (15u - min(diff, 14u)) * 0x04000400u;
           deep |= diff > 14;
         }
-        __syncwarp();
         constexpr int B = 8;  // chunks in registers at a time
-#pragma unroll 1
-        for (int k0 = 0; k0 < 64 / RPI; k0 += B) {
+#pragma unroll
+        for (int k0 = 0; k0 < ROWS / RPI; k0 += B) {
           uint2 x[B];
           uint32_t f[B];
 #pragma unroll
           for (int k = 0; k < B; ++k) {
             x[k] = *reinterpret_cast<const uint2*>(src + (k0 + k) * 256);
-            f[k] = fac[r0 + (k0 + k) * RPI];
+            f[k] = __shfl_sync(FULL, fac[(k0 + k) * RPI / 32], ((k0 + k) * RPI & 31) + lane / CH);
           }
 #pragma unroll
           for (int k = 0; k < B; ++k) {
-            const int row = row0 + (k0 + k) * RPI;
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+            const int rr = (k0 + k) * RPI;
+            *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ ((row0 + rr) & 7)) << 4)) =
                 make_uint4(hmul2u(e4m3x2_half2(x[k].x), f[k]), hmul2u(e4m3x2_half2(x[k].x >> 16), f[k]),
                            hmul2u(e4m3x2_half2(x[k].y), f[k]), hmul2u(e4m3x2_half2(x[k].y >> 16), f[k]));
           }
@@ -850,12 +865,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         if (__any_sync(FULL, deep)) {
           // the second step, for the rows that need it
 #pragma unroll 1
-          for (int k = 0; k < 64 / RPI; ++k) {
-            const int row = row0 + k * RPI;
-            const uint32_t diff = uint32_t(top) - exps[row], more = max(diff, 14u) - 14u;
+          for (int k = 0; k < ROWS / RPI; ++k) {
+            const int rr = k * RPI;
+            const uint32_t diff = uint32_t(top) - exps[row0 + rr], more = max(diff, 14u) - 14u;
             if (more == 0) continue;
             const uint32_t f2 = (more < 15 ? (15u - more) << 10 : more <= 24 ? 1u << (24 - more) : 0u) * 0x10001u;
-            uint4* p = reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            uint4* p = reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ ((row0 + rr) & 7)) << 4));
             const uint4 h = *p;
             *p = make_uint4(hmul2u(h.x, f2), hmul2u(h.y, f2), hmul2u(h.z, f2), hmul2u(h.w, f2));
           }
@@ -863,8 +878,20 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sempty[slot]);
-          mbar_arrive(kv ? &vfull[n % VS] : &kfull[n % KS]);
+          mbar_arrive(&taken[st]);
+          mbar_arrive(&full[slot]);
+        }
+        if (++slot == ns) {
+          slot = 0;
+          phase ^= 1;
+        }
+        if ((st += 2) >= nst) {
+          st -= nst;
+          sphase ^= 1;
+        }
+        if (++em == Cfg::kMeta) {
+          em = 0;
+          ephase ^= 1;
         }
       }
       ++tile;
