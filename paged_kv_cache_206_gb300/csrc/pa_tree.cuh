@@ -77,9 +77,9 @@ __device__ __forceinline__ void tree_ancestors(const TreeParams& P, const int32_
 // modulo its size) that the row sees. `key0`, `key1` bound the keys that the result
 // is of; `seen` are the row's ancestor bits, or null for a chain, whose row is draft
 // `qi`. The result is fp16 (`out`) or an fp32 partial one (`part`, `stride`
-// apart); dims first, first + step, ... below `last`.
+// apart); dims first, first + step, ... below `last`. Rare, hence not inlined.
 template <bool Q8>
-__device__ __forceinline__ void tree_patch(const TreeParams& P, int b, int q, int prefix, int kvh, int qi,
+__device__ __noinline__ void tree_patch(const TreeParams& P, int b, int q, int prefix, int kvh, int qi,
                                         const uint32_t* bad, const uint32_t* seen, int key0, int key1,
                                         __half* out, float* part, int stride, int first, int step, int last) {
   const int32_t* table = P.block_tables + int64_t(b) * P.max_blocks_per_seq;

@@ -13,13 +13,14 @@
 // computes. (Jobs of 128 keys, the scores read twice: 4.6 us per 256 rows x 128 keys.)
 //
 //   warp 0       keys' copies (TMA)
-//   warp 1       issues every MMA: S in TMEM columns [128 x, +128), x the key tile's
-//                parity (QT = 1) or the chain (QT = 2), O_g in [256 + 128 g, +HD); a
-//                job's P (fp16) overwrites the front of its 64 columns of S, where
-//                O += P V takes it as its A operand from TMEM
+//   warp 1       issues O_g += P_g V. O_g stands in TMEM columns [256 + 128 g, +HD)
 //   warp 2       values' copies
 //   warp 3       finds the row tiles on the line and tells them to the others; loads
-//                their query tiles (cp.async)
+//                their queries (cp.async); issues S = Q K^T into columns [128 x, +128), x
+//                the key tile's parity (QT = 1) or the chain (QT = 2). A job's P (fp16)
+//                overwrites the front of its 64 columns of S, where the other product
+//                takes it as its A operand from TMEM. (One warp issuing both products took
+//                2.7 us for a tile's 1,030 cycles of MMA: the waits of one stood before the other.)
 //   warps 4-11   softmax, one row a thread: group g = chain g
 //   warps 12-15  8-bit cache only: codes to fp16 operands, a warp for each of the
 //                four 64-row parts (K, K, V, V) of a tile. The rows of a tile are
@@ -55,23 +56,27 @@ struct TreeTc {
   static constexpr int kVSlots = Q8 && QT == 2 ? 1 : 2;
   static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
   static constexpr int kKStages = Q8 ? 4 : 0, kVStages = Q8 ? 3 : 0, kStages = kKStages + kVStages;
-  static constexpr int kMeta = 4;                        // key tiles whose exponents are held
+  // Key tiles whose exponents, and whose largest ones, are held; row tiles whose flags
+  // are. A widening warp is at most three tiles ahead of the softmax (the K and V
+  // rings' two, and one in registers), so a row tile or key tile eight on finds the place read.
+  static constexpr int kExps = 4, kMeta = 8, kBad = 8;
   static constexpr int kAhead = 4;                       // row tiles told to the roles
   static constexpr int kRoles = Q8 ? 11 + 4 * kConv : 11;            // warps that are told
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t k_off = q_off + QT * kTile;
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
   static constexpr uint32_t stage_off = v_off + kVSlots * kTile;
-  static constexpr uint32_t exps_off = stage_off + kStages * kStageBytes;  // [kMeta][2][128]
-  static constexpr uint32_t meta_off = exps_off + (Q8 ? kMeta * 256 : 0);  // [kMeta] int2
+  static constexpr uint32_t exps_off = stage_off + kStages * kStageBytes;  // [kExps][2][128]
+  static constexpr uint32_t meta_off = exps_off + (Q8 ? kExps * 256 : 0);  // [kMeta] int2
   static constexpr uint32_t stat_off = meta_off + kMeta * 8;               // [2][2][128] float2
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
-  static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [4][words]
-  static constexpr uint32_t bars_off = bad_off + 4 * kTreeWords * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + 3 * kMeta + 16 + 2 * kAhead;
-  using Walk = TreeWalk<kTok, kRows, kLead>;
+  static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
+  static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead;
+  using Place = TreePlace<TreeWalk<kTok, kRows, kLead>>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
-  static constexpr uint32_t tmem_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
+  static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
+  static constexpr uint32_t tmem_off = (place_off + sizeof(Place) + 15) & ~15u;
   static constexpr uint32_t bytes = tmem_off + 16 + 1024;
   static_assert(bytes <= kTcMaxSmem, "shared memory");
 };
@@ -91,20 +96,22 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
 // codes 11,000 to convert instead of 2,000).
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
-  return true;
+#pragma unroll 1
+  do {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
+  return false;
 }
 
-// The same for three barriers at once.
-__device__ __forceinline__ bool tree_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c,
-                                           uint32_t pc) {
+// The same for two barriers at once.
+__device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, mbar_try_wait(a, pa) & mbar_try_wait(b, pb) & mbar_try_wait(c, pc)))
-    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) return false;
-  return true;
+#pragma unroll 1
+  do {
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, pa) & mbar_try_wait(b, pb))) return true;
+  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
+  return false;
 }
 
 // A value that is the same in every lane, said so in a way that the compiler
@@ -124,6 +131,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // Barrier of the eight softmax warps: whether any thread's `pred` holds.
 __device__ __forceinline__ bool tree_softmax_bar(bool pred = false) {
+  __syncwarp();  // (the barrier wants the warp converged)
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
@@ -201,18 +209,17 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint64_t* vfull = kempty + KS;
   uint64_t* vempty = vfull + VS;
   uint64_t* meta_full = vempty + VS;
-  uint64_t* exps_full = meta_full + Cfg::kMeta;      // [K, V][kMeta]
-  uint64_t* tile_full = exps_full + 2 * Cfg::kMeta;  // a row tile told to the roles
+  uint64_t* exps_full = meta_full + Cfg::kMeta;      // [K, V][kExps]
+  uint64_t* tile_full = exps_full + 2 * Cfg::kExps;  // a row tile told to the roles
   uint64_t* tile_empty = tile_full + Cfg::kAhead;
   // (of a job: [g][y], y the key tile's parity for QT = 1, its half for QT = 2)
   uint64_t* s_full = tile_empty + Cfg::kAhead;  // [x] S written
   uint64_t* p_full = s_full + 2;              // [g][y] P written, O_g rescaled
   uint64_t* pv_done = s_full + 6;             // [g][y] O_g += P V complete
   uint64_t* o_full = s_full + 10;             // [g] the row tile's last PV_g complete
-  uint64_t* q_full = s_full + 12;
-  uint64_t* q_empty = s_full + 13;            // the row tile's last QK complete
-  uint64_t* o_free = s_full + 14;             // both O read by the softmax warps
-  uint64_t* all_done = s_full + 15;
+  uint64_t* q_empty = s_full + 12;            // the row tile's last S complete
+  uint64_t* o_free = s_full + 13;             // both O read by the softmax warps
+  uint64_t* all_done = s_full + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -229,11 +236,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       mbar_init(&vfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&vempty[i], 1);
     }
-    for (int i = 0; i < Cfg::kMeta; ++i) {
-      mbar_init(&meta_full[i], 2);
-      mbar_init(&exps_full[i], 1);
-      mbar_init(&exps_full[Cfg::kMeta + i], 1);
-    }
+    for (int i = 0; i < Cfg::kMeta; ++i) mbar_init(&meta_full[i], 2);
+    for (int i = 0; i < 2 * Cfg::kExps; ++i) mbar_init(&exps_full[i], 1);
     for (int i = 0; i < Cfg::kAhead; ++i) {
       mbar_init(&tile_full[i], 1);
       mbar_init(&tile_empty[i], Cfg::kRoles);
@@ -246,13 +250,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       mbar_init(&s_full[g], 1);
       mbar_init(&o_full[g], 1);
     }
-    mbar_init(q_full, 32);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
-    mbar_init(all_done, 1);
+    mbar_init(all_done, 2);
     fence_barrier_init();
   }
-  if (tid < 4 * kTreeWords) bad_s[tid] = 0;
+  if (tid < Cfg::kBad * kTreeWords) bad_s[tid] = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -292,146 +295,118 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0 || warp == 2) {
-    // ================= copies =================
-    const int box = min(bs & -bs, 64), pieces = TOK / box;
+    // ================= copies: keys (warp 0), values (warp 2) =================
+    // Lane l has piece l of every key tile, box keys that lie in one block: its place
+    // in the block table moves on by additions, and the next tile's entry is read
+    // before this one's slots are waited for.
+    const int box = min(bs & -bs, 64), pieces = TOK / box, step_b = TOK / bs, step_o = TOK % bs;
     const uint64_t pol = policy_evict_first();
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    int n = 0;    // key tiles so far
-    int iss = 0;  // and slots filled
-    int slot = 0, sphase = 0;  // of the 8-bit cache's next stage
+    const uint8_t* exps_of = is_k ? P.key_exps : P.value_exps;
+    // the ring: stages of 64 keys (8-bit cache) or tiles
+    const int nslots = Q8 ? (is_k ? Cfg::kKStages : Cfg::kVStages) : is_k ? KS : VS;
+    uint64_t* fulls = Q8 ? sfull + (is_k ? 0 : Cfg::kKStages) : is_k ? kfull : vfull;
+    uint64_t* empties = Q8 ? sempty + (is_k ? 0 : Cfg::kKStages) : is_k ? kempty : vempty;
+    uint8_t* ring = Q8 ? smem + Cfg::stage_off + (is_k ? 0 : Cfg::kKStages) * Cfg::kStageBytes : is_k ? kring : vring;
+    const int half = pieces / 2, part = lane >= half ? 1 : 0;
+    int n = 0, filled = 0;     // key tiles, and stages or tiles filled, so far
+    int slot = 0, phase = 0;   // of the next stage or tile
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t);
       const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
-      auto blocks_of = [&](int i) {  // lane l: the block of piece l of key tile i
-        const int key = (t.s0 + i) * TOK + lane * box;
-        return i < tiles && lane < pieces && key < t.L ? table[key / bs] : -1;
-      };
-      int next = blocks_of(0);
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const int cur = next, j0 = (t.s0 + i) * TOK;
-        next = blocks_of(i + 1);
-        const bool there = cur >= 0 && cur < P.num_blocks;
-        if (lane < pieces && j0 + lane * box < t.L && !there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+      int key = t.s0 * TOK + lane * box, blk = key / bs, off = key - blk * bs;
+      int id = tiles > 0 && lane < pieces && key < t.L ? table[blk] : -1;
+      for (int i = 0; i < tiles; ++i, ++n) {
+        const bool want = lane < pieces && key < t.L, there = want && id >= 0 && id < P.num_blocks;
+        if (want && !there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
         const unsigned valid = __ballot_sync(FULL, there);
-        const int64_t row = int64_t(cur) * bs + (j0 + lane * box) % bs;  // of this lane's piece
+        const int row = id * bs + off, id_now = id, off_now = off;
+        key += TOK;
+        blk += step_b;
+        off += step_o;
+        if (off >= bs) {
+          off -= bs;
+          ++blk;
+        }
+        id = i + 1 < tiles && lane < pieces && key < t.L ? table[blk] : -1;
         if constexpr (Q8) {
-          const int half = pieces / 2;
-          const int x = t.kvh * HD;
-          const int64_t eat = (int64_t(cur) * P.kv_heads + t.kvh) * bs + (j0 + lane * box) % bs;
-          uint64_t* efull = &exps_full[(is_k ? 0 : Cfg::kMeta) + n % Cfg::kMeta];
-          const uint32_t ebytes = __popc(valid) * box;
-          if (elect_one()) {
-            if (ebytes) mbar_arrive_expect_tx(efull, ebytes); else mbar_arrive(efull);
-          }
-          __syncwarp();
-          // (the slot's last reader was four tiles ago, before what the ring waits for)
-          bool wait_first = true;
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            uint64_t* full = sfull + (is_k ? 0 : Cfg::kKStages) + slot;
-            if (!tree_wait(sempty + (is_k ? 0 : Cfg::kKStages) + slot, sphase ^ 1)) {
+          const int slot1 = slot + 1 == nslots ? 0 : slot + 1, phase1 = slot1 == 0 ? phase ^ 1 : phase;
+          const int em = n % Cfg::kExps;
+          uint64_t* efull = &exps_full[(is_k ? 0 : Cfg::kExps) + em];
+          const int64_t eat = (int64_t(id_now) * P.kv_heads + t.kvh) * bs + off_now;
+          uint8_t* dst = ring + (part ? slot1 : slot) * Cfg::kStageBytes + (lane - part * half) * box * HD;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint64_t* full = &fulls[p ? slot1 : slot];
+            if (!tree_wait(&empties[p ? slot1 : slot], (p ? phase1 : phase) ^ 1)) {
               ok = false;
               break;
             }
-            if (wait_first && there)
-              bulk_load(smem + Cfg::exps_off + (n % Cfg::kMeta) * 256 + (is_k ? 0 : 128) + lane * box,
-                        (is_k ? P.key_exps : P.value_exps) + eat, box, efull);
-            wait_first = false;
-            __syncwarp();
-            const int p0 = part * half;
-            const uint32_t bytes = __popc(valid >> p0 & ((1u << half) - 1)) * box * HD;
-            uint8_t* dst = smem + Cfg::stage_off + ((is_k ? 0 : Cfg::kKStages) + slot) * Cfg::kStageBytes;
-            if (elect_one()) {
+            if (lane == 0) {
+              const uint32_t bytes = __popc(valid >> (p * half) & ((1u << half) - 1)) * box * HD;
               if (bytes) mbar_arrive_expect_tx(full, bytes); else mbar_arrive(full);
             }
-            __syncwarp();
-            for (int p = 0; p < half; ++p) {
-              const int y = uni_from(int(row), p0 + p);
-              if ((valid >> (p0 + p) & 1) && elect_one()) tma_load_2d(dst + p * box * HD, map, full, x, y, pol);
+            // (the exponents' slot was last read four tiles ago, before what was waited for)
+            if (p == 0 && lane == 1) {
+              const uint32_t bytes = __popc(valid) * box;
+              if (bytes) mbar_arrive_expect_tx(efull, bytes); else mbar_arrive(efull);
             }
             __syncwarp();
-            ++iss;
-            if (++slot == (is_k ? Cfg::kKStages : Cfg::kVStages)) {
-              slot = 0;
-              sphase ^= 1;
-            }
+            if (there && part == p) tma_load_2d(dst, map, full, t.kvh * HD, row, pol);
+            if (p == 0 && there)
+              bulk_load(smem + Cfg::exps_off + em * 256 + (is_k ? 0 : 128) + lane * box, exps_of + eat, box, efull);
+            __syncwarp();
+            ++filled;
           }
+          if (!ok) break;
+          slot = slot1 + 1 == nslots ? 0 : slot1 + 1;
+          phase = slot == 0 ? phase1 ^ 1 : phase1;
         } else {
-          const int nslots = is_k ? KS : VS;
-          slot = n % nslots;
-          uint64_t* full = is_k ? &kfull[slot] : &vfull[slot];
-          if (!tree_wait(is_k ? &kempty[slot] : &vempty[slot], ((n / nslots) & 1) ^ 1)) {
+          if (!tree_wait(&empties[slot], phase ^ 1)) {
             ok = false;
             break;
           }
-          const uint32_t bytes = __popc(valid) * box * 128 * H2;
+          uint64_t* full = &fulls[slot];
           if (lane == 0) {
+            const uint32_t bytes = __popc(valid) * box * 128 * H2;
             if (bytes) mbar_arrive_expect_tx(full, bytes); else mbar_arrive(full);
           }
           __syncwarp();
-          uint8_t* dst = (is_k ? kring : vring) + slot * Cfg::kTile + lane * box * 128;
           if (there)
             for (int h = 0; h < H2; ++h)
-              tma_load_3d(dst + h * Cfg::kHalf, map, full, 0, int(row), t.kvh * H2 + h, pol);
+              tma_load_3d(ring + slot * Cfg::kTile + h * Cfg::kHalf + lane * box * 128, map, full, 0, row,
+                          t.kvh * H2 + h, pol);
           __syncwarp();
-          ++iss;
+          ++filled;
+          if (++slot == nslots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
     }
     // copies still in flight land before the CTA's memory is given back
-    {
-      const int ns = Q8 ? (is_k ? Cfg::kKStages : Cfg::kVStages) : is_k ? KS : VS;
-      uint64_t* fullb = Q8 ? sfull + (is_k ? 0 : Cfg::kKStages) : is_k ? kfull : vfull;
-      for (int i = iss > ns ? iss - ns : 0; i < iss; ++i) tree_wait(&fullb[i % ns], (i / ns) & 1);
-      if constexpr (Q8)
-        for (int i = max(0, n - Cfg::kMeta + 1); i < n; ++i)
-          tree_wait(&exps_full[(is_k ? 0 : Cfg::kMeta) + i % Cfg::kMeta], (i / Cfg::kMeta) & 1);
+    for (int i = 0; i < nslots; ++i) {
+      const int times = filled / nslots + (i < filled % nslots ? 1 : 0);
+      if (times) tree_wait(&fulls[i], (times - 1) & 1);
     }
+    if constexpr (Q8)
+      for (int i = max(0, n - Cfg::kExps); i < n; ++i)
+        tree_wait(&exps_full[(is_k ? 0 : Cfg::kExps) + i % Cfg::kExps], (i / Cfg::kExps) & 1);
   } else if (warp == 1) {
-    // ================= MMA issuer =================
-    // QT = 1: S(0) S(1), then per key tile n: O_0 += P_0(n) V, O_1 += P_1(n) V, S(n + 2).
-    // QT = 2: S_0(0) S_1(0), then per key tile n the halves' products in turn, and S_g(n + 1)
-    // behind O_g's second. An S overwrites the P of before, which the tensor pipe,
-    // running one thread's operations in order, has then read.
+    // ================= O_g += P_g V =================
+    // Per key tile the two chains' products in turn (QT = 2: of its halves in turn).
     // The whole warp waits and counts, one lane issues: what the instructions take
-    // from uniform registers then stays in them.
-    // Descriptors are a base and an offset in 16-byte units (the address field, in
-    // the low bits, does not overflow).
-    const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
+    // from uniform registers then stays in them. Descriptors are a base and an offset in
+    // 16-byte units (the address field, in the low bits, does not overflow).
     const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!tree_wait(bar, parity)) ok = false;
-    };
-    int tile = 0, n0 = 0;                              // row tiles and key tiles so far
-    int kslot = 0, kphase = 0, vslot = 0, vphase = 0;  // of the next K and V tile to read
+    int tile = 0, n0 = 0, vslot = 0, vphase = 0;  // row tiles and key tiles so far; the next V tile
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = uni(key_tiles(t));
       const int q_len = uni(t.q), prefix = uni(t.L) - q_len, s0 = uni(t.s0);
-      // S into columns [128 x, +128): query tile g, the K tile in kslot
-      auto qk = [&](int x, int g, bool tile_done, bool all_read) {
-        const uint64_t a = dq + g * (Cfg::kTile >> 4), bk = dk + uint32_t(kslot * (Cfg::kTile >> 4));
-        const uint32_t s_col = tmem_s + x * 128;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int h = 0; h < H2; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma(s_col, a + ((h * Cfg::kHalf + k * 32) >> 4), bk + ((h * Cfg::kHalf + k * 32) >> 4), kIdescQK,
-                     (h | k) != 0);
-          tc_commit(&s_full[x]);
-          if (tile_done) tc_commit(&kempty[kslot]);  // its last reader
-          if (all_read) tc_commit(q_empty);          // the query tile may be replaced
-        }
-        __syncwarp();
-        if (tile_done && ++kslot == KS) {
-          kslot = 0;
-          kphase ^= 1;
-        }
-      };
       auto pv = [&](int g, int y, int hf, uint32_t p_col, bool more, bool tile_done, bool last) {
         const uint64_t bv = dv + uint32_t(vslot * (Cfg::kTile >> 4) + hf * (8192 >> 4));
         tc_fence_after();
@@ -444,69 +419,31 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           if (last) tc_commit(&o_full[g]);
         }
         __syncwarp();
-        if (tile_done && ++vslot == VS) {
-          vslot = 0;
-          vphase ^= 1;
-        }
       };
-      wait(q_full, tile & 1);
-      if (!ok) break;
-      if (tiles == 0) {
-        if (elect_one()) tc_commit(q_empty);
-        __syncwarp();
-      }
-      if (QT == 1) {
-        for (int i = 0; i < 2 && i < tiles && ok; ++i) {
-          wait(&kfull[kslot], kphase);
-          if (ok) qk((n0 + i) & 1, 0, true, i + 1 == tiles);
-        }
-      } else if (tiles > 0) {
-        wait(&kfull[kslot], kphase);
-        if (ok) {
-          qk(0, 0, false, false);
-          qk(1, 1, true, tiles == 1);
-        }
-      }
-      // the last row tile's O has been read before the first PV overwrites it
-      if (tile > 0) wait(o_free, (tile - 1) & 1);
+      // the last row tile's O has been read before the first product overwrites it
+      if (tile > 0 && !tree_wait(o_free, (tile - 1) & 1)) ok = false;
       for (int i = 0; i < tiles && ok; ++i) {
         const int n = n0 + i, phase = phase_of(n);
         const bool last = i + 1 == tiles;
-        wait(&vfull[vslot], vphase);
+        if (!tree_wait(&vfull[vslot], vphase)) { ok = false; break; }
         if constexpr (!Q8) {
           // Rows behind the context may hold anything and become 0; non-finite
           // elements of the drafts' rows leave the product
           const int key0 = (s0 + i) * TOK;
-          if (ok && key0 + TOK > prefix)
-            clean_v_tile<H2>(vring + vslot * Cfg::kTile, max(prefix - key0, 0), min(prefix + q_len - key0, TOK), key0 - prefix,
-                    bad_s + (tile & 3) * kTreeWords, lane);
+          if (key0 + TOK > prefix)
+            clean_v_tile<H2>(vring + vslot * Cfg::kTile, max(prefix - key0, 0), min(prefix + q_len - key0, TOK),
+                             key0 - prefix, bad_s + (tile % Cfg::kBad) * kTreeWords, lane);
         }
-        if constexpr (QT == 1) {
-          const uint32_t p_col = tmem_s + (n & 1) * 128;
-          if (ok) wait(&p_full[n & 1], phase);
-          if (!ok) break;
-          pv(0, n & 1, 0, p_col, i != 0, false, last);
-          wait(&p_full[2 + (n & 1)], phase);
-          if (!ok) break;
-          pv(1, n & 1, 1, p_col + 64, i != 0, true, last);
-          if (i + 2 < tiles) {
-            wait(&kfull[kslot], kphase);
-            if (!ok) break;
-            qk(n & 1, 0, true, i + 3 == tiles);
-          }
-        } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int hf = j >> 1, g = j & 1;
-            if (ok) wait(&p_full[2 * g + hf], phase);
-            if (!ok) break;
-            pv(g, hf, hf, tmem_s + g * 128 + hf * 64, i != 0 || hf, j == 3, last && hf == 1);
-            if (hf == 1 && !last) {
-              if (g == 0) wait(&kfull[kslot], kphase);
-              if (!ok) break;
-              qk(g, g, g == 1, g == 1 && i + 2 == tiles);
-            }
-          }
+        for (int j = 0; j < 2 * QT; ++j) {
+          const int g = j & 1, hf = QT == 2 ? j >> 1 : g, y = QT == 2 ? hf : n & 1;
+          if (!tree_wait(&p_full[2 * g + y], phase)) { ok = false; break; }
+          pv(g, y, hf, tmem_s + (QT == 2 ? g : n & 1) * 128 + hf * 64, i != 0 || (QT == 2 && hf), j == 2 * QT - 1,
+             last && (QT == 1 || hf));
+        }
+        if (++vslot == VS) {
+          vslot = 0;
+          vphase ^= 1;
         }
       }
       n0 += tiles;
@@ -515,28 +452,36 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     if (elect_one()) tc_commit(all_done);
     __syncwarp();
   } else if (warp == 3) {
-    // ================= row tiles and their queries =================
-    int tile = 0;
-    if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
-    typename Cfg::Walk walk;
-    TreeTile t;
-    walk.begin(P, S, worker, lane);
-    while (true) {
-      const bool some = walk.next(P, t);
-      if (!some) t.q = -1;
-      const int at = tile % Cfg::kAhead;
-      if (!tree_wait(&tile_empty[at], ((tile / Cfg::kAhead) & 1) ^ 1)) {
+    // ================= row tiles, their queries, S = Q K^T =================
+    const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
+    int told_n = 0, tile = 0, n = 0, kslot = 0, kphase = 0;  // tiles told, begun; key tiles; the next K tile
+    if (lane == 0) S.join[worker].parts = 0;                 // no divided tile yet
+    typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
+    TreeTile t, following;
+    tree_begin(P, S, place, worker, lane);
+    auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
+      const bool some = tree_next(P, place);
+      following = place->tile;
+      if (!some) following.q = -1;
+      const int at = told_n % Cfg::kAhead;
+      if (!tree_wait(&tile_empty[at], ((told_n / Cfg::kAhead) & 1) ^ 1)) {
         ok = false;
-        break;
+        return;
       }
       if (lane == 0) {
-        told[at] = t;
-        if (some && t.parts) tree_note(S, worker, t);
+        told[at] = following;
+        if (following.q >= 0 && following.parts) tree_note(S, worker, following);
         mbar_arrive(&tile_full[at]);
       }
       __syncwarp();
-      if (!some) break;
-      if (walk.u >= walk.u1) launch_dependents();  // the worker's last tile
+      ++told_n;
+      if (place->walk.u >= place->walk.u1) launch_dependents();  // the worker's last tile is known
+    };
+    tell();
+    while (ok && following.q >= 0) {
+      t = following;
+      const int tiles = uni(key_tiles(t));
+      // the queries, once the last row tile's S are complete
       if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1)) {
         ok = false;
         break;
@@ -559,11 +504,51 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
       }
       cp_async_commit();
+      tell();  // the next row tile, while the queries come
       cp_async_wait<0>();
       fence_proxy_async();
-      mbar_arrive(q_full);
+      __syncwarp();
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        if (!tree_wait(&kfull[kslot], kphase)) { ok = false; break; }
+        const bool last = i + 1 == tiles;
+        const uint64_t bk = dk + uint32_t(kslot * (Cfg::kTile >> 4));
+#pragma unroll
+        for (int g = 0; g < QT; ++g) {
+          // what stood in these columns, the P of two tiles ago (QT = 2: of the last),
+          // has been read
+          const int x = QT == 2 ? g : n & 1, nb = QT == 2 ? n - 1 : n - 2;
+          if (nb >= 0 && !tree_wait2(&pv_done[QT == 2 ? 2 * g : x], phase_of(nb), &pv_done[QT == 2 ? 2 * g + 1 : 2 + x],
+                                     phase_of(nb))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int h = 0; h < H2; ++h)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma(tmem_s + x * 128, dq + g * (Cfg::kTile >> 4) + ((h * Cfg::kHalf + k * 32) >> 4),
+                       bk + ((h * Cfg::kHalf + k * 32) >> 4), kIdescQK, (h | k) != 0);
+            tc_commit(&s_full[x]);
+            if (g == QT - 1) tc_commit(&kempty[kslot]);
+            if (g == QT - 1 && last) tc_commit(q_empty);  // the queries may be replaced
+          }
+          __syncwarp();
+        }
+        if (++kslot == KS) {
+          kslot = 0;
+          kphase ^= 1;
+        }
+      }
+      if (tiles == 0) {
+        if (elect_one()) tc_commit(q_empty);
+        __syncwarp();
+      }
       ++tile;
     }
+    if (elect_one()) tc_commit(all_done);
+    __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ================= softmax: group g (warps 4-7, 8-11) is chain g =================
     const int g = (warp - 4) >> 2, quarter = warp & 3, m_lane = quarter * 32 + lane;
@@ -614,6 +599,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         if (!tree_wait(&s_full[x_of_s], phase)) { ok = false; break; }
         tc_fence_after();
         if (any_row) {
+          __syncwarp();
           const uint32_t sbuf = uni(tmem_s + x_of_s * 128 + hf * 64 + lane_base);
           float x[64];
           tmem_ld32(sbuf, x);
@@ -655,6 +641,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           }
           const float add = ev - (m_ref == -INFINITY ? 0.f : m_ref);
           float sum[2] = {0.f, 0.f};
+          __syncwarp();  // (tcgen05.ld and .st want the warp converged)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             uint32_t pk[16];
@@ -684,6 +671,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
               tmem_st32(o_mine + cc * 32, o);
             }
           }
+          __syncwarp();
           tmem_wait_st();
         }
         tc_fence_before();
@@ -716,7 +704,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       tc_fence_after();
       const bool whole = t.slot < 0;
       const float inv = whole ? 1.f / sum : 1.f;
-      const uint32_t* bad = bad_s + (tile & 3) * kTreeWords;
+      const uint32_t* bad = bad_s + (tile % Cfg::kBad) * kTreeWords;
       const int col0 = QT == 1 ? g * (HD / 2) : 0, cols = QT == 1 ? HD / 2 : HD;
       bool any_bad = false;
       if (drafts) {
@@ -729,6 +717,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       for (int cc = 0; cc < cols / 16; ++cc) {
         const int d0 = col0 + cc * 16;
         float o[16], x[16];
+        __syncwarp();  // rows that there are not have left the rest of the loop out
         const uint32_t from = uni(tmem_o + (QT == 2 ? g * 128 : 0) + d0 + lane_base);
         if (tiles > 0) tmem_ld<16>(from, o);
         if (QT == 1 && tiles > 0) tmem_ld<16>(from + 128, x);
@@ -761,14 +750,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       }
       if (!whole && row_ok && (QT == 2 || g == 0))
         S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
-      // (this buffer's next row tile begins four tiles on, behind o_free)
       if (any_bad) {
         if (row_ok && alive)
           tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK,
                          whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr,
                          S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr, Cfg::kRows, col0, 1, col0 + cols);
         tree_softmax_bar();
-        if (tid - 128 < kTreeWords) bad_s[(tile & 3) * kTreeWords + tid - 128] = 0;
+        if (tid - 128 < kTreeWords) bad_s[(tile % Cfg::kBad) * kTreeWords + tid - 128] = 0;
       }
       n0 += tiles;
       ++tile;
@@ -790,14 +778,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     uint8_t* operand = (kv ? vring : kring) + (ch >> 3) * Cfg::kHalf + row0 * 128;
     // (rings of this warp's tile: slots and phases counted, as a remainder takes long)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
-    int slot = 0, phase = 0, st = part & 1, sphase = 0, em = 0, ephase = 0, tile = 0;
+    int slot = 0, phase = 0, st = part & 1, sphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       for (int i = 0; i < tiles; ++i) {
         const int key0 = (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
-        if (!tree_wait3(&exps_full[kv * Cfg::kMeta + em], ephase, &landed[st], sphase, &empty[slot], phase ^ 1)) {
+        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[st], sphase)) {
           ok = false;
           break;
         }
@@ -810,8 +798,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
                       max(left > 2 ? int(e4 >> 16 & 255) : 0, left > 3 ? int(e4 >> 24) : 0));
         top = __reduce_max_sync(FULL, top);
         if ((part & 1) == 0 && sub == 0 && lane == 0) {
-          reinterpret_cast<int*>(&meta[em])[kv] = top - kExpBias;
-          mbar_arrive(&meta_full[em]);
+          reinterpret_cast<int*>(&meta[mm])[kv] = top - kExpBias;
+          mbar_arrive(&meta_full[mm]);
         }
         if (key0 + TOK > prefix) {
           // the tile reaches the drafts: rows behind the context become 0, and
@@ -828,12 +816,19 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             } else if (kv && key >= prefix) {
               hit = clear_nonfinite<true>(x.x);
               hit |= clear_nonfinite<true>(x.y);
-              if (hit) atomicOr(&bad_s[(tile & 3) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
+              if (hit) atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
             }
             if (hit) *p = x;
           }
           __syncwarp();
         }
+        // all of the part into registers, so that its stage is free for the next copy
+        // while it is widened
+        uint2 x[ROWS / RPI];
+#pragma unroll
+        for (int k = 0; k < ROWS / RPI; ++k) x[k] = *reinterpret_cast<const uint2*>(src + k * 256);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[st]);
         // factors of the rows lane, lane + 32 of this warp: 2^-diff, where diff is past
         // 14 (a rarity) its first step
         uint32_t fac[ROWS / 32];
@@ -844,23 +839,17 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           fac[k] = (15u - min(diff, 14u)) * 0x04000400u;
           deep |= diff > 14;
         }
-        constexpr int B = 8;  // chunks in registers at a time
+        if (!tree_wait(&empty[slot], phase ^ 1)) {
+          ok = false;
+          break;
+        }
 #pragma unroll
-        for (int k0 = 0; k0 < ROWS / RPI; k0 += B) {
-          uint2 x[B];
-          uint32_t f[B];
-#pragma unroll
-          for (int k = 0; k < B; ++k) {
-            x[k] = *reinterpret_cast<const uint2*>(src + (k0 + k) * 256);
-            f[k] = __shfl_sync(FULL, fac[(k0 + k) * RPI / 32], ((k0 + k) * RPI & 31) + lane / CH);
-          }
-#pragma unroll
-          for (int k = 0; k < B; ++k) {
-            const int rr = (k0 + k) * RPI;
-            *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ ((row0 + rr) & 7)) << 4)) =
-                make_uint4(hmul2u(e4m3x2_half2(x[k].x), f[k]), hmul2u(e4m3x2_half2(x[k].x >> 16), f[k]),
-                           hmul2u(e4m3x2_half2(x[k].y), f[k]), hmul2u(e4m3x2_half2(x[k].y >> 16), f[k]));
-          }
+        for (int k = 0; k < ROWS / RPI; ++k) {
+          const int rr = k * RPI;
+          const uint32_t f = __shfl_sync(FULL, fac[rr / 32], (rr & 31) + lane / CH);
+          *reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ ((row0 + rr) & 7)) << 4)) =
+              make_uint4(hmul2u(e4m3x2_half2(x[k].x), f), hmul2u(e4m3x2_half2(x[k].x >> 16), f),
+                         hmul2u(e4m3x2_half2(x[k].y), f), hmul2u(e4m3x2_half2(x[k].y >> 16), f));
         }
         if (__any_sync(FULL, deep)) {
           // the second step, for the rows that need it
@@ -877,10 +866,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&taken[st]);
-          mbar_arrive(&full[slot]);
-        }
+        if (lane == 0) mbar_arrive(&full[slot]);
         if (++slot == ns) {
           slot = 0;
           phase ^= 1;
@@ -889,10 +875,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           st -= nst;
           sphase ^= 1;
         }
-        if (++em == Cfg::kMeta) {
+        if (++em == Cfg::kExps) {
           em = 0;
           ephase ^= 1;
         }
+        mm = (mm + 1) % Cfg::kMeta;
       }
       ++tile;
     }
@@ -900,11 +887,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   }
   if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_TIMEOUT);
   // ---- teardown: every tcgen05 op has completed before TMEM is freed
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) mbar_wait(all_done, 0);
-    __syncwarp();
+    tree_wait(all_done, 0);
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
