@@ -2,6 +2,7 @@
 // read back (pa_cache.h).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "pa_cache.h"
@@ -15,6 +16,11 @@ namespace {
 
 enum RowMode { kRotate, kWrite, kStore };
 
+// From this many warps on a group of lanes takes kRows rows at once: enough to
+// give each of 152 SMs 8.
+constexpr int64_t kManyWarps = 152 * 8;
+constexpr int kRows = 4;
+
 struct RowParams {
   const __half *query, *key, *value, *q_weight, *k_weight;
   const float* cos_sin;
@@ -25,8 +31,9 @@ struct RowParams {
   int64_t tokens, query_stride, key_stride, value_stride;
   int batch, heads, kv_heads, hk, hv, rot, interleaved, max_positions;
   int block_size, num_blocks, max_blocks_per_seq, max_rows;
-  int lanes;  // lanes of a row, a power of two
-  float eps;
+  int lane_shift;  // log2 of the lanes of a row
+  uint32_t q_slices, k_slices, slices;  // warps of a token: its queries', keys', all
+  float eps, inv_hk;
 };
 
 __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
@@ -34,48 +41,99 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
 }
 
 // Sequence and index in it of token t: the last sequence whose tokens begin at
-// or before t. Warp-collective; -1 past the last sequence.
+// or before t. Warp-collective, 128 sequences at a time; -1 past the last one.
 __device__ __forceinline__ int find_sequence(const RowParams& P, int64_t t, int lane, int& index) {
   if (!P.q_seqlens) {
     index = 0;
     return t < P.batch ? int(t) : -1;
   }
   int64_t before = 0;
-  for (int b0 = 0; b0 < P.batch; b0 += 32) {
-    const int n = b0 + lane < P.batch ? min(max(P.q_seqlens[b0 + lane], 0), P.max_rows) : 0;
-    int sum = n;
+  for (int b0 = 0; b0 < P.batch; b0 += 128) {
+    int n[4], own = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = b0 + 4 * lane + j;
+      n[j] = b < P.batch ? min(max(P.q_seqlens[b], 0), P.max_rows) : 0;
+    }
+    // a lane's four lengths may pass 2^31 together; the sums are 64 bits wide
+    int64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += n[j];
+    const int64_t mine = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += up;
     }
-    const bool mine = n > 0 && t >= before + sum - n && t < before + sum;
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    if (who) {
-      const int l = __ffs(who) - 1;
-      index = int(t - before) - __shfl_sync(0xffffffffu, sum - n, l);
-      return b0 + l;
+    int64_t at = before + sum - mine;
+    int who = -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (t >= at && t < at + n[j]) who = j, own = int(t - at);
+      at += n[j];
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, who >= 0);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      index = __shfl_sync(0xffffffffu, own, l);
+      return b0 + 4 * l + __shfl_sync(0xffffffffu, who, l);
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
   return -1;
 }
 
-// One warp per (token, slice of its head rows). A row's elements are 16-byte
-// chunks of 8; a lane holds chunks p and p + rot / 16 of the rotated part (so
-// that both members of every pair are its own, in either pairing), and two
-// neighbouring chunks of the rest.
-template <int MODE, int VPL>
+// One warp per (token, slice of its query, key or value heads), U rows to a
+// group of lanes. A row's elements are 16-byte chunks of 8; a lane holds chunk
+// pair p: chunks p and p + rot / 16 where they are rotated (so that both members
+// of every pair are its own, in either pairing), 2p and 2p + 1 behind the rotated
+// part, and p and p + dims / 16 of a row that is not rotated at all. What a row
+// is multiplied by but its own norm is the same for all rows of the warp: weight
+// times cosine and weight times sine, made once.
+template <int MODE, int VPL, int U, bool IL>
 __global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
   const int lane = threadIdx.x & 31;
-  const int per_warp = 32 / P.lanes, group = lane / P.lanes, gl = lane % P.lanes;
-  const int qrows = MODE == kWrite ? 0 : P.heads;
-  const int rows = qrows + P.kv_heads * (MODE == kRotate ? 1 : 2);
-  const int slices = (rows + per_warp - 1) / per_warp;
-  const int64_t task = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t t = task / slices;
+  const int lanes = 1 << P.lane_shift, per_warp = 32 >> P.lane_shift;
+  const int group = lane >> P.lane_shift, gl = lane & (lanes - 1);
+  const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const int64_t t = task / P.slices;
   if (t >= P.tokens) return;
-  const int row = int(task % slices) * per_warp + group;
+  const uint32_t slice = task - uint32_t(t) * P.slices;
+  const bool is_q = MODE != kWrite && slice < P.q_slices;
+  const bool is_v = MODE != kRotate && slice >= P.q_slices + P.k_slices;
+  const bool turned = MODE != kWrite && !is_v;  // normed and rotated
+  const int first = int(slice - (is_q ? 0 : is_v ? P.q_slices + P.k_slices : P.q_slices)) * U * per_warp;
+  const int left = (is_q ? P.heads : P.kv_heads) - first;  // rows from here on
+  const int dims = is_v ? P.hv : P.hk;
+  const int half = turned && P.rot ? P.rot / 16 : dims / 16;
+
+  const __half* src = is_q   ? P.query + t * P.query_stride
+                      : is_v ? P.value + t * P.value_stride
+                             : P.key + t * P.key_stride;
+  src += int64_t(first + group) * dims;
+  int at[VPL][2];
+  bool on[VPL], turn[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int p = gl + v * lanes;
+    on[v] = p < dims / 16;
+    turn[v] = turned && p < P.rot / 16;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) at[v][c] = p < half ? (p + c * half) * 8 : 16 * p + 8 * c;
+  }
+
+  // ---- the rows' elements: their loads do not wait for where the token goes
+  uint4 x[U][VPL][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        x[u][v][c] = make_uint4(0, 0, 0, 0);
+        if (on[v] && u * per_warp + group < left)
+          x[u][v][c] = *reinterpret_cast<const uint4*>(src + u * per_warp * dims + at[v][c]);
+      }
 
   // ---- where the token goes
   int64_t slot = -1;
@@ -102,158 +160,179 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
     if (pos < -1 || pos >= P.max_positions) report(P.status, PA_STATUS_BIT_POSITION);
     if (pos < 0 || pos >= P.max_positions) return;
   }
-  const bool is_q = row < qrows, is_k = !is_q && row < qrows + P.kv_heads;
-  const bool is_v = !is_q && !is_k && row < rows;
-  const int h = is_q ? row : is_k ? row - qrows : row - qrows - P.kv_heads;
-  const int dims = is_v ? P.hv : P.hk;
-  const __half* src = is_q   ? P.query + t * P.query_stride + int64_t(h) * P.hk
-                      : is_k ? P.key + t * P.key_stride + int64_t(h) * P.hk
-                      : is_v ? P.value + t * P.value_stride + int64_t(h) * P.hv
-                             : nullptr;
-  const __half* weight = is_q ? P.q_weight : is_k ? P.k_weight : nullptr;
-  const int rot = is_v || MODE == kWrite ? 0 : P.rot, half = rot / 16;
 
-  // ---- the row's elements
-  float y[VPL][2][8];
-  int at[VPL][2];
-  float sq = 0.f;
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    const int p = gl + v * P.lanes;
-    at[v][0] = p < half ? p * 8 : (rot / 8 + 2 * (p - half)) * 8;
-    at[v][1] = p < half ? (p + half) * 8 : at[v][0] + 8;
-    const bool on = src && p < dims / 16;
-    if (!on) at[v][0] = at[v][1] = -1;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (on) x = *reinterpret_cast<const uint4*>(src + at[v][c]);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = h2f2(w[j]);
-        y[v][c][2 * j] = f.x;
-        y[v][c][2 * j + 1] = f.y;
-        sq += f.x * f.x + f.y * f.y;
-      }
-    }
-  }
-  if constexpr (MODE != kWrite) {
-    for (int o = P.lanes >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const float inv = 1.0f / sqrtf(sq / float(P.hk) + P.eps);
+  // ---- the factors. Pair m of chunk pair v: elements m of both chunks, or
+  // (interleaved) 2m and 2m + 1 of the 16; ca, cb: the cosine times the weight
+  // of its first and second, sa, sb: the sine.
+  const auto chunk_of = [](int m, int second) { return IL ? m / 4 : second; };
+  const auto elem_of = [](int m, int second) { return IL ? 2 * (m % 4) + second : m; };
+  float ca[VPL][8], cb[VPL][8], sa[VPL][8], sb[VPL][8];
+  const __half* weight = is_q ? P.q_weight : P.k_weight;
+  if (turned) {
     const float* table = P.cos_sin + int64_t(pos) * P.rot;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      if (at[v][0] < 0) continue;
-      if (weight) {
+      float w[2][8];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(weight + at[v][c]);
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+      for (int c = 0; c < 2; ++c) {
+        uint4 g = make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u);  // ones
+        if (weight && on[v]) g = *reinterpret_cast<const uint4*>(weight + at[v][c]);
+        const uint32_t* h = reinterpret_cast<const uint32_t*>(&g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = h2f2(w[j]);
-            y[v][c][2 * j] *= inv * f.x;
-            y[v][c][2 * j + 1] *= inv * f.y;
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = h2f2(h[j]);
+          w[c][2 * j] = f.x;
+          w[c][2 * j + 1] = f.y;
         }
       }
-      if (at[v][0] < rot) {
-        if (P.interleaved) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float4 cs = *reinterpret_cast<const float4*>(table + at[v][c] / 2);
-            const float4 sn = *reinterpret_cast<const float4*>(table + rot / 2 + at[v][c] / 2);
-            const float* cc = reinterpret_cast<const float*>(&cs);
-            const float* ss = reinterpret_cast<const float*>(&sn);
+      for (int c = 0; c < 2; ++c) {
+        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (turn[v]) {
+          const float* from = table + (IL ? at[v][c] / 2 : at[v][0] + 4 * c);
+          cs = *reinterpret_cast<const float4*>(from);
+          sn = *reinterpret_cast<const float4*>(from + P.rot / 2);
+        }
+        const float* cc = reinterpret_cast<const float*>(&cs);
+        const float* ss = reinterpret_cast<const float*>(&sn);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = y[v][c][2 * j], b = y[v][c][2 * j + 1];
-              y[v][c][2 * j] = a * cc[j] - b * ss[j];
-              y[v][c][2 * j + 1] = b * cc[j] + a * ss[j];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j4 = 0; j4 < 2; ++j4) {
-            const float4 cs = *reinterpret_cast<const float4*>(table + at[v][0] + 4 * j4);
-            const float4 sn = *reinterpret_cast<const float4*>(table + rot / 2 + at[v][0] + 4 * j4);
-            const float* cc = reinterpret_cast<const float*>(&cs);
-            const float* ss = reinterpret_cast<const float*>(&sn);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = y[v][0][4 * j4 + j], b = y[v][1][4 * j4 + j];
-              y[v][0][4 * j4 + j] = a * cc[j] - b * ss[j];
-              y[v][1][4 * j4 + j] = b * cc[j] + a * ss[j];
-            }
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int m = 4 * c + j;
+          const float wa = w[chunk_of(m, 0)][elem_of(m, 0)], wb = w[chunk_of(m, 1)][elem_of(m, 1)];
+          ca[v][m] = wa * cc[j];
+          cb[v][m] = wb * cc[j];
+          sa[v][m] = wa * ss[j];
+          sb[v][m] = wb * ss[j];
         }
       }
     }
   }
 
-  // ---- fp16 rows: the queries, and the keys of a plain rotation
-  const bool dense = MODE != kWrite && (is_q || (MODE == kRotate && is_k));
-  if (dense) {
-    __half* dst = is_q ? P.q_out + (t * P.heads + h) * P.hk : P.k_out + (t * P.kv_heads + h) * P.hk;
+  __half* dense = is_q            ? P.q_out + (t * P.heads + first + group) * P.hk
+                  : MODE == kRotate ? P.k_out + (t * P.kv_heads + first + group) * P.hk
+                                    : nullptr;
+  const int64_t head0 = slot * P.kv_heads + first + group;
+  uint8_t* codes = is_v ? P.value_cache + head0 * dims : P.key_cache + head0 * dims;
+  uint8_t* exps = (is_v ? P.value_exps : P.key_exps) +
+                  (int64_t(block) * P.kv_heads + first + group) * P.block_size + place;
+
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u * per_warp >= left) break;
+    const bool row_on = u * per_warp + group < left;
+    float y[VPL][2][8], sq = 0.f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (at[v][c] < 0) continue;
-        const float* f = y[v][c];
-        *reinterpret_cast<uint4*>(dst + at[v][c]) =
-            make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]),
-                       pack_half2(f[6], f[7]));
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u][v][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = h2f2(w[j]);
+          y[v][c][2 * j] = f.x;
+          y[v][c][2 * j + 1] = f.y;
+        }
       }
-  }
-  if constexpr (MODE != kRotate) {
-    // ---- 8-bit rows: the exponent that the row's largest finite element
-    // needs, then the codes (scaling by a power of two is exact)
-    float top = 0.f;
+    if (turned) {
+      float inv = 1.f;
+      if (weight) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
+        for (int v = 0; v < VPL; ++v)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          top = fmaxf(top, isfinite(y[v][c][j]) ? fabsf(y[v][c][j]) : 0.f);
-    for (int o = P.lanes >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((is_k || is_v) && slot >= 0) {
-      const int e = row_exponent(top);
-      const float f = pow2(-e);
-      uint8_t* dst = is_k ? P.key_cache + (slot * P.kv_heads + h) * P.hk
-                          : P.value_cache + (slot * P.kv_heads + h) * P.hv;
+            for (int j = 0; j < 8; ++j) sq += y[v][c][j] * y[v][c][j];
+        for (int o = lanes >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        inv = rsqrtf(sq * P.inv_hk + P.eps);
+      }
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
+          float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
+          const float a = fa * inv, b = fb * inv;
+          // a sine of 0 is no reason to take in the other element's infinity
+          fa = turn[v] ? a * ca[v][m] - b * sb[v][m] : a * ca[v][m];
+          fb = turn[v] ? b * cb[v][m] + a * sa[v][m] : b * cb[v][m];
+        }
+    }
+
+    if (MODE == kRotate || is_q) {  // fp16 rows
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (at[v][c] < 0) continue;
-          const float* x = y[v][c];
-          const uint32_t lo = e4m3x2(x[0] * f, x[1] * f) | e4m3x2(x[2] * f, x[3] * f) << 16;
-          const uint32_t hi = e4m3x2(x[4] * f, x[5] * f) | e4m3x2(x[6] * f, x[7] * f) << 16;
-          *reinterpret_cast<uint2*>(dst + at[v][c]) = make_uint2(lo, hi);
+          const float* f = y[v][c];
+          if (on[v] && row_on)
+            *reinterpret_cast<uint4*>(dense + u * per_warp * dims + at[v][c]) =
+                make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]),
+                           pack_half2(f[6], f[7]));
         }
-      if (gl == 0) {
-        uint8_t* exps = is_k ? P.key_exps : P.value_exps;
-        exps[(int64_t(block) * P.kv_heads + h) * P.block_size + place] = uint8_t(e + kExpBias);
+    } else {
+      // 8-bit rows: the exponent that the row's largest finite element needs,
+      // then the codes (scaling by a power of two is exact). fmaxf leaves NaN
+      // out; an infinity, which is rare, is made one and left out so.
+      const auto largest = [&] {
+        float top = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[v][c][j]));
+        for (int o = lanes >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return top;
+      };
+      float top = largest();
+      if (__any_sync(0xffffffffu, isinf(top))) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (isinf(y[v][c][j])) y[v][c][j] = __uint_as_float(0x7fc00000u);
+        top = largest();
       }
+      const int e = row_exponent(top);
+      const float f = pow2(-e);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float* a = y[v][c];
+          const uint32_t lo = e4m3x2(a[0] * f, a[1] * f) | e4m3x2(a[2] * f, a[3] * f) << 16;
+          const uint32_t hi = e4m3x2(a[4] * f, a[5] * f) | e4m3x2(a[6] * f, a[7] * f) << 16;
+          if (on[v] && row_on && slot >= 0)
+            *reinterpret_cast<uint2*>(codes + u * per_warp * dims + at[v][c]) = make_uint2(lo, hi);
+        }
+      if (gl == 0 && row_on && slot >= 0)
+        exps[int64_t(u * per_warp) * P.block_size] = uint8_t(e + kExpBias);
     }
   }
 }
 
-template <int MODE>
+template <int MODE, bool IL>
 pa_status launch_rows(RowParams P, cudaStream_t stream) {
   if (P.tokens == 0) return PA_OK;
-  const int widest = (MODE == kRotate || P.hk > P.hv ? P.hk : P.hv) / 16;  // lanes' worth of chunk pairs
-  P.lanes = 1;
-  while (P.lanes < 32 && P.lanes < widest) P.lanes *= 2;
-  const int rows = (MODE == kWrite ? 0 : P.heads) + P.kv_heads * (MODE == kRotate ? 1 : 2);
-  const int64_t warps = P.tokens * cdiv(rows, 32 / P.lanes);
-  const int64_t grid = cdiv(warps, 8);
-  if (grid > INT32_MAX) return PA_ERR_INVALID_ARG;
-  if (widest <= 32) rows_kernel<MODE, 1><<<unsigned(grid), 256, 0, stream>>>(P);
-  else rows_kernel<MODE, 2><<<unsigned(grid), 256, 0, stream>>>(P);
+  const int widest = (MODE == kRotate || P.hk > P.hv ? P.hk : P.hv) / 16;  // chunk pairs of a row
+  while ((1 << P.lane_shift) < widest && P.lane_shift < 5) ++P.lane_shift;
+  P.inv_hk = 1.0f / float(P.hk);
+  const int per_warp = 32 >> P.lane_shift;
+  const auto slice = [&](int rows) {
+    P.q_slices = MODE == kWrite ? 0 : uint32_t(cdiv(P.heads, rows));
+    P.k_slices = uint32_t(cdiv(P.kv_heads, rows));
+    P.slices = P.q_slices + P.k_slices * (MODE == kRotate ? 1 : 2);
+    return P.tokens * P.slices;
+  };
+  const bool many = widest <= 32 && slice(kRows * per_warp) >= kManyWarps;
+  if (!many) slice(per_warp);
+  if (P.tokens > INT32_MAX || P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
+  const unsigned grid = unsigned(cdiv(P.tokens * P.slices, 8));
+  if (many) rows_kernel<MODE, 1, kRows, IL><<<grid, 256, 0, stream>>>(P);
+  else if (widest <= 32) rows_kernel<MODE, 1, 1, IL><<<grid, 256, 0, stream>>>(P);
+  else rows_kernel<MODE, 2, 1, IL><<<grid, 256, 0, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -266,64 +345,122 @@ struct ReadParams {
   uint32_t* status;
   int64_t out_rows;
   int batch, kv_heads, hk, hv, block_size, num_blocks, max_blocks_per_seq, max_rows;
+  int k_slices, v_slices;  // warps of a token's keys and of its values
+  int strip;               // tokens of a warp, at most 32
 };
 
-// A row's 16 codes to fp16: code * 2^e in fp32 (exact), rounded once.
-__device__ __forceinline__ void widen(const uint4& codes, float f, uint4& lo, uint4& hi) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&codes);
-  uint32_t o[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 a = h2f2(e4m3x2_half2(w[j])), b = h2f2(e4m3x2_half2(w[j] >> 16));
-    o[2 * j] = pack_half2(a.x * f, a.y * f);
-    o[2 * j + 1] = pack_half2(b.x * f, b.y * f);
-  }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+// 2^e in both halves, e in [-14, 15].
+__device__ __forceinline__ uint32_t half2_pow2(int e) {
+  const uint32_t h = uint32_t(e + 15) << 10;
+  return h | h << 16;
 }
 
-// One warp per cached token; its lanes stride over the token's key heads, then
-// its value heads (each contiguous in the cache and in the output).
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight codes times 2^(byte - 127), rounded once to fp16. Within [-14, 15] the
+// power is an fp16 and one product rounds once. Elsewhere the power is split:
+// the first product is exact (a code is a multiple of 2^-9, so that times 2^-14
+// it is one of 2^-23) or infinite as the result is, and the second rounds. Powers
+// past [-38, 30] give the zeros and infinities that these ends give.
+__device__ __forceinline__ uint4 widen(const uint2& codes, int byte) {
+  const int e = byte - kExpBias, near = min(max(e, -14), 15);
+  const uint32_t f = half2_pow2(near);
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = mul_half2(e4m3x2_half2((j < 2 ? codes.x : codes.y) >> (j % 2 ? 16 : 0)), f);
+  if (e != near) {
+    const __half2 g = __float2half2_rn(pow2(min(max(e - near, -24), 15)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = mul_half2(o[j], *reinterpret_cast<const uint32_t*>(&g));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One warp per (kStrip or fewer tokens of a sequence, 1 KB of their keys or of
+// their values): a token's heads are contiguous in the cache and in the output.
+// Lane l finds token l's place, so that a strip waits for one table lookup; then
+// R tokens are read at a time. A lane reads 8 codes and writes 16 bytes,
+// neighbouring lanes neighbouring ones.
+template <int R>
 __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
+  constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 31;
-  const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 5);
-  const int64_t all = int64_t(P.batch) * P.max_rows;
-  for (int64_t k = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); k < all; k += step) {
-    const int b = int(k / P.max_rows), i = int(k % P.max_rows);
+  const int slices = P.k_slices + P.v_slices;
+  for (int b = blockIdx.y; b < P.batch; b += gridDim.y) {
     const int start = P.starts ? P.starts[b] : 0, L = P.context_lens[b];
     if (start < 0 || L < start || int64_t(L) > int64_t(P.max_blocks_per_seq) * P.block_size ||
         L - start > P.max_rows) {
-      report(P.status, PA_STATUS_BIT_PLAN);
+      if (threadIdx.x == 0) report(P.status, PA_STATUS_BIT_PLAN);
       continue;
     }
-    const int pos = start + i;
-    if (pos >= L) continue;
-    const int64_t out = int64_t(P.out_starts[b]) + i;
-    const int block = P.block_tables[int64_t(b) * P.max_blocks_per_seq + pos / P.block_size];
-    const int place = pos % P.block_size;
-    if (out < 0 || out >= P.out_rows) {
-      report(P.status, PA_STATUS_BIT_WORKSPACE);
-      continue;
-    }
-    if (block < 0 || block >= P.num_blocks) {
-      report(P.status, PA_STATUS_BIT_BLOCK_INDEX);
-      continue;
-    }
-    const int64_t slot = int64_t(block) * P.block_size + place;
+    const int64_t out0 = P.out_starts[b], tasks = (int64_t(L - start) + P.strip - 1) / P.strip * slices;
+    for (int64_t k = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); k < tasks; k += int64_t(gridDim.x) * 8) {
+      const int64_t strip = k <= UINT32_MAX ? uint32_t(k) / uint32_t(slices) : k / slices;
+      const int slice = int(k - strip * slices), i0 = int(strip) * P.strip;
+      const int rows = min(P.strip, L - start - i0);
+      const bool kv = slice >= P.k_slices;
+      const int hd = kv ? P.hv : P.hk, width = P.kv_heads * hd, n = hd / 8;
+      const int c0 = (kv ? slice - P.k_slices : slice) * (32 * kUnroll) + lane;
+      const int chunks = (width / 8 - c0 + 31) / 32;  // of this lane in a row, from c0 on
+      const uint8_t* cache = (kv ? P.value_cache : P.key_cache) + c0 * 8;
+      __half* dst = (kv ? P.v_out : P.k_out) + (out0 + i0) * width + c0 * 8;
+
+      // token `lane` of the strip: its slot, and where its exponents begin
+      int slot = -1;
+      int64_t first = 0;
+      if (lane < rows) {
+        const int pos = start + i0 + lane;
+        const int64_t out = out0 + i0 + lane;
+        if (out < 0 || out >= P.out_rows) {
+          report(P.status, PA_STATUS_BIT_WORKSPACE);
+        } else {
+          const int page = pos / P.block_size, place = pos - page * P.block_size;
+          const int block = P.block_tables[int64_t(b) * P.max_blocks_per_seq + page];
+          if (block >= 0 && block < P.num_blocks) {
+            slot = block * P.block_size + place;
+            first = int64_t(block) * P.kv_heads * P.block_size + place;
+          } else {
+            report(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+          }
+        }
+      }
+      const uint8_t* exps[kUnroll];  // of the heads of this lane's chunks
+      int h = c0 / n, rest = c0 - h * n;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const int hd = kv ? P.hv : P.hk, width = P.kv_heads * hd;
-      const uint8_t* src = (kv ? P.value_cache : P.key_cache) + slot * width;
-      const uint8_t* exps =
-          (kv ? P.value_exps : P.key_exps) + int64_t(block) * P.kv_heads * P.block_size + place;
-      __half* dst = (kv ? P.v_out : P.k_out) + out * width;
-      for (int d = lane * 16; d < width; d += 512) {
-        const uint4 codes = *reinterpret_cast<const uint4*>(src + d);
-        const float f = pow2(int(exps[int64_t(d / hd) * P.block_size]) - kExpBias);
-        uint4 lo, hi;
-        widen(codes, f, lo, hi);
-        *reinterpret_cast<uint4*>(dst + d) = lo;
-        *reinterpret_cast<uint4*>(dst + d + 8) = hi;
+      for (int u = 0; u < kUnroll; ++u) {
+        exps[u] = (kv ? P.value_exps : P.key_exps) + int64_t(h) * P.block_size;
+        rest += 32 % n;
+        h += 32 / n;
+        if (rest >= n) rest -= n, ++h;
+      }
+
+      for (int r0 = 0; r0 < rows; r0 += R) {
+        uint2 codes[R][kUnroll];
+        int e[R][kUnroll];
+        bool row_on[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t s = __shfl_sync(0xffffffffu, slot, r0 + r);
+          const int64_t f = __shfl_sync(0xffffffffu, first, r0 + r);
+          row_on[r] = s >= 0 && r0 + r < rows;
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (row_on[r] && u < chunks) {
+              codes[r][u] = *reinterpret_cast<const uint2*>(cache + s * width + 256 * u);
+              e[r][u] = exps[u][f];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r, dst += width)
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (row_on[r] && u < chunks)
+              *reinterpret_cast<uint4*>(dst + 256 * u) = widen(codes[r][u], e[r][u]);
       }
     }
   }
@@ -436,7 +573,8 @@ extern "C" pa_status pa_qk_norm_rope(const pa_rotary* rot, int64_t tokens, const
   P.q_out = static_cast<__half*>(q_out);
   P.k_out = static_cast<__half*>(k_out);
   P.status = status;
-  return launch_rows<kRotate>(P, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return P.interleaved ? launch_rows<kRotate, true>(P, s) : launch_rows<kRotate, false>(P, s);
 }
 
 extern "C" pa_status pa_cache_write(const pa_cache_config* cfg, int64_t tokens, const void* key,
@@ -459,7 +597,7 @@ extern "C" pa_status pa_cache_write(const pa_cache_config* cfg, int64_t tokens, 
   P.key_stride = key_stride;
   P.value_stride = value_stride;
   P.status = status;
-  return launch_rows<kWrite>(P, static_cast<cudaStream_t>(stream));
+  return launch_rows<kWrite, false>(P, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" pa_status pa_cache_store(const pa_cache_config* cfg, const pa_rotary* rot, int64_t tokens,
@@ -494,7 +632,8 @@ extern "C" pa_status pa_cache_store(const pa_cache_config* cfg, const pa_rotary*
   P.value_stride = value_stride;
   P.q_out = static_cast<__half*>(q_out);
   P.status = status;
-  return launch_rows<kStore>(P, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return P.interleaved ? launch_rows<kStore, true>(P, s) : launch_rows<kStore, false>(P, s);
 }
 
 extern "C" pa_status pa_cache_read(const pa_cache_config* cfg, const void* key_cache,
@@ -532,8 +671,17 @@ extern "C" pa_status pa_cache_read(const pa_cache_config* cfg, const void* key_c
   P.num_blocks = cfg->num_blocks;
   P.max_blocks_per_seq = cfg->max_blocks_per_seq;
   P.max_rows = cfg->max_rows;
-  const int64_t warps = int64_t(cfg->batch) * cfg->max_rows;
-  const int64_t grid = cdiv(warps, 8) < 65536 ? cdiv(warps, 8) : 65536;
-  read_kernel<<<unsigned(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  P.k_slices = int(cdiv(int64_t(cfg->kv_heads) * cfg->head_size_k, 1024));
+  P.v_slices = int(cdiv(int64_t(cfg->kv_heads) * cfg->head_size_v, 1024));
+  const int64_t slices = int64_t(P.k_slices) + P.v_slices;
+  // a strip of tokens to a warp where that leaves warps enough
+  P.strip = 16;
+  while (P.strip > 1 && cdiv(cfg->max_rows, P.strip) * slices * cfg->batch < kManyWarps) P.strip /= 2;
+  const int64_t tasks = cdiv(cfg->max_rows, P.strip) * slices;
+  const dim3 grid(unsigned(std::min<int64_t>(cdiv(tasks, 8), 65536)),
+                  unsigned(std::min(cfg->batch, 65535)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (P.strip >= 4) read_kernel<4><<<grid, 256, 0, s>>>(P);
+  else read_kernel<1><<<grid, 256, 0, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

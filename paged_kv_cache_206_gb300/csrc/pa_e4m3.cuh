@@ -25,11 +25,10 @@ __device__ __forceinline__ int row_exponent(float a) {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// Two values to e4m3 (lo in the low byte): nearest even, NaN for a non-finite.
+// Two values to e4m3 (lo in the low byte): nearest even, NaN for NaN, the
+// largest finite code for an infinity.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
-  lo = isfinite(lo) ? lo : __uint_as_float(0x7fc00000u);
-  hi = isfinite(hi) ? hi : __uint_as_float(0x7fc00000u);
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }

@@ -30,6 +30,33 @@ class pa_cache_config(ctypes.Structure):
                                               "max_rows")]
 
 
+# A call first puts one question to its arguments, whether all are in order: a decode
+# loop pays for that alone. Where the answer is no, the checks behind it say what is wrong.
+
+_f16 = _i32 = _f32 = _stream = _device = None
+_configs: dict = {}  # configurations by their values
+
+
+def _start():
+    """torch's types and the calls that tell the current stream and device."""
+    global _f16, _i32, _f32, _stream, _device
+    import torch
+    _i32, _f32 = torch.int32, torch.float32
+    _stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _f16 = torch.float16
+
+
+def _config(kind, *values):
+    """A configuration's address; kept, as making one takes as long as the launch."""
+    key = (kind, values)
+    got = _configs.get(key)
+    if got is None:
+        if len(_configs) >= 4096:
+            _configs.clear()
+        got = _configs[key] = ctypes.byref(kind(*values))
+    return got
+
+
 def _refuse(where: str, what: str):
     raise PaError(PA_ERR_INVALID_ARG, f"{where}: {what}")
 
@@ -63,9 +90,8 @@ def _rows(where, name, t, dtype, device, tokens, heads, size):
     return st if tokens > 1 else heads * size
 
 
-def _launch(where, device, stream, call):
-    """``call(stream handle)`` with the tensors' device current."""
-    import torch
+def _target(where, device, stream):
+    """The stream's handle, and the device to make current (None: it is)."""
     if device.type != "cuda":
         _refuse(where, f"tensors must be on a CUDA device, got {device}")
     if stream is not None:
@@ -73,12 +99,19 @@ def _launch(where, device, stream, call):
             _refuse(where, f"the stream is on {stream.device}, the tensors on {device}")
         handle = stream.cuda_stream
     else:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
-        status = call(handle)
+        handle = _stream(device.index)
+    return handle, None if _device() == device.index else device
+
+
+def _launch(where, device, stream, call, *args):
+    """``call(*args, stream handle)`` with the tensors' device current."""
+    handle, other = _target(where, device, stream)
+    if other is None:
+        status = call(*args, handle)
     else:
-        with torch.cuda.device(device):
-            status = call(handle)
+        import torch
+        with torch.cuda.device(other):
+            status = call(*args, handle)
     if status:
         _check(status, where)
 
@@ -93,24 +126,47 @@ def _status_arg(where, status, device):
     return status.data_ptr()
 
 
-def _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, kv_heads, eps, interleaved,
-            device):
-    """Checks of the rotation's arguments; its config."""
-    f16, i32, f32, _, _ = _dtypes()
+def _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, device):
+    """Checks of the rotation's arguments."""
     tokens, heads, size = query.shape
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _dense(where, name, w, f16, device, (size,))
-    rot, limit = 0, 2**31 - 1
+            _dense(where, name, w, _f16, device, (size,))
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             _refuse(where, "cos_sin must be [max_positions, rotary_dim]")
-        _dense(where, "cos_sin", cos_sin, f32, device)
-        limit, rot = cos_sin.shape
+        _dense(where, "cos_sin", cos_sin, _f32, device)
     if positions is not None:
-        _dense(where, "positions", positions, i32, device, (tokens,))
-    _dense(where, "q_out", q_out, f16, device, (tokens, heads, size))
-    return pa_rotary(heads, kv_heads, size, rot, bool(interleaved), limit, eps)
+        _dense(where, "positions", positions, _i32, device, (tokens,))
+    _dense(where, "q_out", q_out, _f16, device, (tokens, heads, size))
+
+
+def _ok(t, dtype, at, shape):
+    """Whether a tensor (or None) is dense, of this type and shape, on device ``at``."""
+    return t is None or (t.dtype is dtype and t.get_device() == at and t.shape == shape
+                         and t.is_contiguous())
+
+
+def _rows_ok(t, at, tokens, heads, size):
+    """Whether [tokens, heads, size] fp16 rows have dense heads."""
+    return (t.dtype is _f16 and t.get_device() == at and t.shape == (tokens, heads, size)
+            and t.stride()[1:] == (size, 1))
+
+
+def _rotary_ok(at, tokens, heads, size, q_weight, k_weight, cos_sin, positions, q_out):
+    return (_ok(q_weight, _f16, at, (size,)) and _ok(k_weight, _f16, at, (size,))
+            and _ok(positions, _i32, at, (tokens,)) and _ok(q_out, _f16, at, (tokens, heads, size))
+            and (cos_sin is None or (cos_sin.dim() == 2 and _ok(cos_sin, _f32, at, cos_sin.shape))))
+
+
+def _row_stride(t, tokens, width):
+    return t.stride(0) if tokens > 1 else width
+
+
+def _rot_config(query, kv_heads, cos_sin, eps, interleaved):
+    limit, rot = (2**31 - 1, 0) if cos_sin is None else cos_sin.shape
+    _, heads, size = query.shape
+    return _config(pa_rotary, heads, kv_heads, size, rot, 1 if interleaved else 0, limit, eps)
 
 
 def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6,
@@ -121,23 +177,28 @@ def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k
     norm); ``cos_sin`` is fp32 [max_positions, rotary_dim] (None: no rotation);
     ``positions`` int32 [T], -1 for padding tokens, which are left out."""
     where = "pa_qk_norm_rope"
-    f16 = _dtypes()[0]
+    if _f16 is None:
+        _start()
     if query.dim() != 3 or key.dim() != 3 or positions is None:
         _refuse(where, "query and key must be [tokens, heads, head_size], with positions")
-    dev, tokens, size = query.device, query.shape[0], query.shape[2]
-    kv_heads = key.shape[1]
-    qs = _rows(where, "query", query, f16, dev, tokens, query.shape[1], size)
-    ks = _rows(where, "key", key, f16, dev, tokens, kv_heads, size)
-    rot = _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, kv_heads, eps,
-                  interleaved, dev)
-    _dense(where, "k_out", k_out, f16, dev, (tokens, kv_heads, size))
+    tokens, heads, size = query.shape
+    at, kv_heads = query.get_device(), key.shape[1]
+    if not (_rows_ok(query, at, tokens, heads, size) and _rows_ok(key, at, tokens, kv_heads, size)
+            and _ok(k_out, _f16, at, (tokens, kv_heads, size))
+            and _rotary_ok(at, tokens, heads, size, q_weight, k_weight, cos_sin, positions, q_out)):
+        dev = query.device
+        _rows(where, "query", query, _f16, dev, tokens, heads, size)
+        _rows(where, "key", key, _f16, dev, tokens, kv_heads, size)
+        _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, dev)
+        _dense(where, "k_out", k_out, _f16, dev, (tokens, kv_heads, size))
     if tokens == 0:
         return
-    st = _status_arg(where, status, dev)
-    lib = load_library()
-    _launch(where, dev, stream, lambda s: lib.pa_qk_norm_rope(
-        ctypes.byref(rot), tokens, query.data_ptr(), qs, key.data_ptr(), ks, _ptr(q_weight),
-        _ptr(k_weight), _ptr(cos_sin), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), st, s))
+    _launch(where, query.device, stream, load_library().pa_qk_norm_rope,
+            _rot_config(query, kv_heads, cos_sin, eps, interleaved), tokens, query.data_ptr(),
+            _row_stride(query, tokens, heads * size), key.data_ptr(),
+            _row_stride(key, tokens, kv_heads * size), _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+            positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+            _status_arg(where, status, query.device))
 
 
 def _cache_tensors(where, key, value, key_exps, value_exps):
@@ -155,6 +216,12 @@ def _cache_tensors(where, key, value, key_exps, value_exps):
     if key_exps is not None:
         _dense(where, "key_exps", key_exps, u8, key.device, (nb, hk, bs))
         _dense(where, "value_exps", value_exps, u8, key.device, (nb, hk, bs))
+
+
+def _batch_ok(at, block_tables, context_lens, q_seqlens):
+    shape = block_tables.shape
+    return (len(shape) == 2 and _ok(block_tables, _i32, at, shape)
+            and _ok(context_lens, _i32, at, shape[:1]) and _ok(q_seqlens, _i32, at, shape[:1]))
 
 
 def _batch_args(where, block_tables, context_lens, q_seqlens, device):
@@ -180,7 +247,12 @@ class QuantCache:
             _refuse("QuantCache", "an 8-bit cache has exponents")
         _cache_tensors("QuantCache", key, value, key_exps, value_exps)
         self.key, self.value, self.key_exps, self.value_exps = key, value, key_exps, value_exps
-        self.device = key.device
+        if _f16 is None:
+            _start()
+        self.device, self._at = key.device, key.get_device()
+        self._blocks, self._block_size, self._heads, self._hk = key.shape
+        self._hv = value.shape[3]
+        self._addresses = tuple(t.data_ptr() for t in (key, key_exps, value, value_exps))
 
     @classmethod
     def empty(cls, num_blocks, block_size, kv_heads, head_size_k, head_size_v=None, device="cuda"):
@@ -192,30 +264,33 @@ class QuantCache:
                 for _ in range(2)]
         return cls(*codes, *exps)
 
-    def _config(self, block_tables, max_rows):
-        nb, bs, heads, hk = self.key.shape
+    def _cfg(self, block_tables, max_rows):
         batch, cols = block_tables.shape
-        return pa_cache_config(batch, heads, hk, self.value.shape[3], bs, nb, cols, max_rows)
+        return _config(pa_cache_config, batch, self._heads, self._hk, self._hv, self._block_size,
+                       self._blocks, cols, max_rows)
 
     def write(self, key, value, block_tables, context_lens, q_seqlens=None, max_seqlen_q=None,
               status=None, stream=None) -> None:
         """Quantise the current tokens' ``key`` [T, Hk, hk] and ``value``
         [T, Hk, hv] (fp16) into the cache (pa_cache_write)."""
-        where, dev, f16 = "pa_cache_write", self.device, _dtypes()[0]
+        where, at, heads = "pa_cache_write", self._at, self._heads
         if key.dim() != 3:
             _refuse(where, "key must be [tokens, kv_heads, head_size]")
-        tokens, heads = key.shape[0], self.key.shape[2]
-        ks = _rows(where, "key", key, f16, dev, tokens, heads, self.key.shape[3])
-        vs = _rows(where, "value", value, f16, dev, tokens, heads, self.value.shape[3])
-        _batch_args(where, block_tables, context_lens, q_seqlens, dev)
+        tokens = key.shape[0]
+        if not (_rows_ok(key, at, tokens, heads, self._hk)
+                and _rows_ok(value, at, tokens, heads, self._hv)
+                and _batch_ok(at, block_tables, context_lens, q_seqlens)):
+            _rows(where, "key", key, _f16, self.device, tokens, heads, self._hk)
+            _rows(where, "value", value, _f16, self.device, tokens, heads, self._hv)
+            _batch_args(where, block_tables, context_lens, q_seqlens, self.device)
         if tokens == 0:
             return
-        cfg = self._config(block_tables, tokens if max_seqlen_q is None else max_seqlen_q)
-        st, lib = _status_arg(where, status, dev), load_library()
-        _launch(where, dev, stream, lambda s: lib.pa_cache_write(
-            ctypes.byref(cfg), tokens, key.data_ptr(), ks, value.data_ptr(), vs,
-            block_tables.data_ptr(), context_lens.data_ptr(), _ptr(q_seqlens), self.key.data_ptr(),
-            self.key_exps.data_ptr(), self.value.data_ptr(), self.value_exps.data_ptr(), st, s))
+        _launch(where, self.device, stream, load_library().pa_cache_write,
+                self._cfg(block_tables, tokens if max_seqlen_q is None else max_seqlen_q), tokens,
+                key.data_ptr(), _row_stride(key, tokens, heads * self._hk), value.data_ptr(),
+                _row_stride(value, tokens, heads * self._hv), block_tables.data_ptr(),
+                context_lens.data_ptr(), _ptr(q_seqlens), *self._addresses,
+                _status_arg(where, status, self.device))
 
     def store(self, query, key, value, q_weight, k_weight, cos_sin, positions, block_tables,
               context_lens, q_seqlens, max_seqlen_q, q_out, eps=1e-6, interleaved=False, status=None,
@@ -223,26 +298,31 @@ class QuantCache:
         """Norm and rotate ``query`` into ``q_out`` and ``key`` into the cache,
         with ``value``, in one pass (pa_cache_store). ``positions`` None takes
         the cache positions."""
-        where, dev, f16 = "pa_cache_store", self.device, _dtypes()[0]
+        where, at, heads = "pa_cache_store", self._at, self._heads
         if query.dim() != 3:
             _refuse(where, "query must be [tokens, heads, head_size]")
-        tokens, heads, size = query.shape[0], self.key.shape[2], self.key.shape[3]
-        qs = _rows(where, "query", query, f16, dev, tokens, query.shape[1], size)
-        ks = _rows(where, "key", key, f16, dev, tokens, heads, size)
-        vs = _rows(where, "value", value, f16, dev, tokens, heads, self.value.shape[3])
-        rot = _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, heads, eps,
-                      interleaved, dev)
-        _batch_args(where, block_tables, context_lens, q_seqlens, dev)
+        (tokens, qh, size), hk, hv = query.shape, self._hk, self._hv
+        if not (_rows_ok(query, at, tokens, qh, hk) and _rows_ok(key, at, tokens, heads, hk)
+                and _rows_ok(value, at, tokens, heads, hv)
+                and _rotary_ok(at, tokens, qh, hk, q_weight, k_weight, cos_sin, positions, q_out)
+                and _batch_ok(at, block_tables, context_lens, q_seqlens)):
+            dev = self.device
+            _rows(where, "query", query, _f16, dev, tokens, qh, hk)
+            _rows(where, "key", key, _f16, dev, tokens, heads, hk)
+            _rows(where, "value", value, _f16, dev, tokens, heads, hv)
+            _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, dev)
+            _batch_args(where, block_tables, context_lens, q_seqlens, dev)
         if tokens == 0:
             return
-        cfg = self._config(block_tables, tokens if max_seqlen_q is None else max_seqlen_q)
-        st, lib = _status_arg(where, status, dev), load_library()
-        _launch(where, dev, stream, lambda s: lib.pa_cache_store(
-            ctypes.byref(cfg), ctypes.byref(rot), tokens, query.data_ptr(), qs, key.data_ptr(), ks,
-            value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
-            block_tables.data_ptr(), context_lens.data_ptr(), _ptr(q_seqlens), self.key.data_ptr(),
-            self.key_exps.data_ptr(), self.value.data_ptr(), self.value_exps.data_ptr(),
-            q_out.data_ptr(), st, s))
+        _launch(where, self.device, stream, load_library().pa_cache_store,
+                self._cfg(block_tables, tokens if max_seqlen_q is None else max_seqlen_q),
+                _rot_config(query, heads, cos_sin, eps, interleaved), tokens, query.data_ptr(),
+                _row_stride(query, tokens, qh * hk), key.data_ptr(),
+                _row_stride(key, tokens, heads * hk), value.data_ptr(),
+                _row_stride(value, tokens, heads * hv), _ptr(q_weight), _ptr(k_weight),
+                _ptr(cos_sin), _ptr(positions), block_tables.data_ptr(), context_lens.data_ptr(),
+                _ptr(q_seqlens), *self._addresses, q_out.data_ptr(),
+                _status_arg(where, status, self.device))
 
     def read(self, block_tables, starts, context_lens, out_starts, max_rows, k_out, v_out,
              status=None, stream=None) -> None:
@@ -250,22 +330,22 @@ class QuantCache:
         sequence back as fp16 rows from row ``out_starts[b]`` of ``k_out``
         [rows, Hk, hk] and ``v_out`` [rows, Hk, hv]; ``max_rows`` is the most rows
         of one sequence (pa_cache_read)."""
-        where, dev = "pa_cache_read", self.device
-        f16, i32, _, _, _ = _dtypes()
-        rows, heads = k_out.shape[0], self.key.shape[2]
-        _dense(where, "k_out", k_out, f16, dev, (rows, heads, self.key.shape[3]))
-        _dense(where, "v_out", v_out, f16, dev, (rows, heads, self.value.shape[3]))
-        _batch_args(where, block_tables, context_lens, starts, dev)
-        _dense(where, "out_starts", out_starts, i32, dev, context_lens.shape)
+        where, at, rows = "pa_cache_read", self._at, k_out.shape[0]
+        if not (_ok(k_out, _f16, at, (rows, self._heads, self._hk))
+                and _ok(v_out, _f16, at, (rows, self._heads, self._hv))
+                and _batch_ok(at, block_tables, context_lens, starts)
+                and _ok(out_starts, _i32, at, context_lens.shape)):
+            dev = self.device
+            _dense(where, "k_out", k_out, _f16, dev, (rows, self._heads, self._hk))
+            _dense(where, "v_out", v_out, _f16, dev, (rows, self._heads, self._hv))
+            _batch_args(where, block_tables, context_lens, starts, dev)
+            _dense(where, "out_starts", out_starts, _i32, dev, context_lens.shape)
         if rows == 0:
             return
-        cfg = self._config(block_tables, max_rows)
-        st, lib = _status_arg(where, status, dev), load_library()
-        _launch(where, dev, stream, lambda s: lib.pa_cache_read(
-            ctypes.byref(cfg), self.key.data_ptr(), self.key_exps.data_ptr(), self.value.data_ptr(),
-            self.value_exps.data_ptr(), block_tables.data_ptr(), _ptr(starts),
-            context_lens.data_ptr(), out_starts.data_ptr(), rows, k_out.data_ptr(), v_out.data_ptr(),
-            st, s))
+        _launch(where, self.device, stream, load_library().pa_cache_read,
+                self._cfg(block_tables, max_rows), *self._addresses, block_tables.data_ptr(),
+                _ptr(starts), context_lens.data_ptr(), out_starts.data_ptr(), rows, k_out.data_ptr(),
+                v_out.data_ptr(), _status_arg(where, status, self.device))
 
 
 def pa_tree_workspace(cfg) -> int:
@@ -299,28 +379,34 @@ class TreeStep:
                                mask_type=PA_MASK_NONE, num_sms=sms, scale=scale)
         self.workspace = torch.zeros(pa_tree_workspace(self.cfg), dtype=torch.uint8,
                                      device=self.device)
+        if _f16 is None:
+            _start()
+        self._at = key.get_device()
+        self._shapes = (num_heads, hk), (num_heads, value.shape[3]), (batch, max_blocks_per_seq)
+        self._caches = tuple(_ptr(t) for t in (key, value, key_exps, value_exps))
+        self._space = ctypes.byref(self.cfg), self.workspace.data_ptr(), self.workspace.numel()
 
     def run(self, query, block_tables, context_lens, q_seqlens, parents, out, stream=None):
         """Attend ``query`` [T, H, hk] into ``out`` [T, H, hv]; ``parents`` int32 [T]
         or None (a chain). Returns ``out``."""
-        where, dev, cfg = "pa_tree_forward", self.device, self.cfg
-        f16, i32, _, _, _ = _dtypes()
-        tokens = query.shape[0]
-        _dense(where, "query", query, f16, dev, (tokens, cfg.num_heads, cfg.head_size_k))
-        _dense(where, "out", out, f16, dev, (tokens, cfg.num_heads, cfg.head_size_v))
-        _batch_args(where, block_tables, context_lens, q_seqlens, dev)
-        if block_tables.shape != (cfg.batch, cfg.max_blocks_per_seq):
-            _refuse(where, f"block_tables must be [{cfg.batch}, {cfg.max_blocks_per_seq}]")
-        if parents is not None:
-            _dense(where, "parents", parents, i32, dev, (tokens,))
+        where, at, tokens = "pa_tree_forward", self._at, query.shape[0]
+        (q, o, tables), (cfg, space, size) = self._shapes, self._space
+        if not (_ok(query, _f16, at, (tokens, *q)) and _ok(out, _f16, at, (tokens, *o))
+                and block_tables.shape == tables and _batch_ok(at, block_tables, context_lens, q_seqlens)
+                and _ok(parents, _i32, at, (tokens,))):
+            dev = self.device
+            _dense(where, "query", query, _f16, dev, (tokens, *q))
+            _dense(where, "out", out, _f16, dev, (tokens, *o))
+            _batch_args(where, block_tables, context_lens, q_seqlens, dev)
+            if block_tables.shape != tables:
+                _refuse(where, f"block_tables must be {list(tables)}")
+            if parents is not None:
+                _dense(where, "parents", parents, _i32, dev, (tokens,))
         if tokens == 0:
             return out
-        lib, ws = load_library(), self.workspace
-        _launch(where, dev, stream, lambda s: lib.pa_tree_forward(
-            ctypes.byref(cfg), tokens, query.data_ptr(), self.key.data_ptr(), self.value.data_ptr(),
-            _ptr(self.key_exps), _ptr(self.value_exps), block_tables.data_ptr(),
-            context_lens.data_ptr(), _ptr(q_seqlens), _ptr(parents), ws.data_ptr(), ws.numel(),
-            out.data_ptr(), s))
+        _launch(where, self.device, stream, load_library().pa_tree_forward, cfg, tokens,
+                query.data_ptr(), *self._caches, block_tables.data_ptr(), context_lens.data_ptr(),
+                _ptr(q_seqlens), _ptr(parents), space, size, out.data_ptr())
         return out
 
     def status(self, stream=None):
