@@ -16,10 +16,13 @@ namespace {
 
 enum RowMode { kRotate, kWrite, kStore };
 
-// From this many warps on a group of lanes takes kRows rows at once: enough to
-// give each of 152 SMs 8.
-constexpr int64_t kManyWarps = 152 * 8;
-constexpr int kRows = 4;
+// With kRows * kBatches rows to a group of lanes where that leaves 16 warps for
+// each of 152 SMs, kRows at once; with one row to it where there are fewer (one
+// token of 32 + 8 heads of 128 turned: 2.0 us so, 2.6 us with two rows; 8192
+// tokens: 34 us with 2 x 2, 43 us with one).
+constexpr int kRows = 2;
+constexpr int kBatches = 2;
+constexpr int64_t kManyWarps = 152 * 16;
 
 struct RowParams {
   const __half *query, *key, *value, *q_weight, *k_weight;
@@ -32,6 +35,7 @@ struct RowParams {
   int batch, heads, kv_heads, hk, hv, rot, interleaved, max_positions;
   int block_size, num_blocks, max_blocks_per_seq, max_rows;
   int lane_shift;  // log2 of the lanes of a row
+  int batches;     // of rows in a warp, at most
   uint32_t q_slices, k_slices, slices;  // warps of a token: its queries', keys', all
   float eps, inv_hk;
 };
@@ -42,43 +46,44 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
 
 // Sequence and index in it of token t: the last sequence whose tokens begin at
 // or before t. Warp-collective, 128 sequences at a time; -1 past the last one.
-__device__ __forceinline__ int find_sequence(const RowParams& P, int64_t t, int lane, int& index) {
+// The sums stop at the number of tokens, past which no token looks.
+__device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int lane, int& index) {
   if (!P.q_seqlens) {
     index = 0;
     return t < P.batch ? int(t) : -1;
   }
-  int64_t before = 0;
+  const uint32_t tokens = uint32_t(P.tokens);  // < 2^31: two of them fit in 32 bits
+  uint32_t before = 0;
   for (int b0 = 0; b0 < P.batch; b0 += 128) {
-    int n[4], own = 0;
+    uint32_t ends[4], sum = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int b = b0 + 4 * lane + j;
-      n[j] = b < P.batch ? min(max(P.q_seqlens[b], 0), P.max_rows) : 0;
+      const int n = b < P.batch ? min(max(P.q_seqlens[b], 0), P.max_rows) : 0;
+      ends[j] = sum = min(sum + min(uint32_t(n), tokens), tokens);
     }
-    // a lane's four lengths may pass 2^31 together; the sums are 64 bits wide
-    int64_t sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum += n[j];
-    const int64_t mine = sum;
+    uint32_t upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
+      const uint32_t up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = min(upto + up, tokens);
     }
-    int64_t at = before + sum - mine;
-    int who = -1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (t >= at && t < at + n[j]) who = j, own = int(t - at);
-      at += n[j];
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, who >= 0);
+    // the first lane whose sequences end behind the token holds it
+    const unsigned hit = __ballot_sync(0xffffffffu, t - before < upto);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      index = __shfl_sync(0xffffffffu, own, l);
-      return b0 + 4 * l + __shfl_sync(0xffffffffu, who, l);
+      uint32_t start = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 0) start = 0;
+      const uint32_t own = t - before - start;  // of lane l: below its `sum`
+      int j = 0;
+      uint32_t from = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (own >= ends[k]) j = k + 1, from = ends[k];
+      index = int(__shfl_sync(0xffffffffu, own - from, l));
+      return b0 + 4 * l + __shfl_sync(0xffffffffu, j, l);
     }
-    before += __shfl_sync(0xffffffffu, sum, 31);
+    before += __shfl_sync(0xffffffffu, upto, 31);  // at most t
   }
   return -1;
 }
@@ -91,7 +96,8 @@ __device__ __forceinline__ int find_sequence(const RowParams& P, int64_t t, int 
 // is multiplied by but its own norm is the same for all rows of the warp: weight
 // times cosine and weight times sine, made once.
 template <int MODE, int VPL, int U, bool IL>
-__global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
+__global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : 4) : 1)
+rows_kernel(const RowParams P) {
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << P.lane_shift, per_warp = 32 >> P.lane_shift;
   const int group = lane >> P.lane_shift, gl = lane & (lanes - 1);
@@ -102,8 +108,9 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
   const bool is_q = MODE != kWrite && slice < P.q_slices;
   const bool is_v = MODE != kRotate && slice >= P.q_slices + P.k_slices;
   const bool turned = MODE != kWrite && !is_v;  // normed and rotated
-  const int first = int(slice - (is_q ? 0 : is_v ? P.q_slices + P.k_slices : P.q_slices)) * U * per_warp;
-  const int left = (is_q ? P.heads : P.kv_heads) - first;  // rows from here on
+  const int step = U * per_warp;  // rows of a batch
+  const int first = int(slice - (is_q ? 0 : is_v ? P.q_slices + P.k_slices : P.q_slices)) * step * P.batches;
+  int left = min((is_q ? P.heads : P.kv_heads) - first, step * P.batches);  // rows to do
   const int dims = is_v ? P.hv : P.hk;
   const int half = turned && P.rot ? P.rot / 16 : dims / 16;
 
@@ -122,18 +129,22 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
     for (int c = 0; c < 2; ++c) at[v][c] = p < half ? (p + c * half) * 8 : 16 * p + 8 * c;
   }
 
-  // ---- the rows' elements: their loads do not wait for where the token goes
+  // ---- a batch's elements: the first loads do not wait for where the token goes
   uint4 x[U][VPL][2];
+  const auto load = [&] {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
+      for (int v = 0; v < VPL; ++v)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        x[u][v][c] = make_uint4(0, 0, 0, 0);
-        if (on[v] && u * per_warp + group < left)
-          x[u][v][c] = *reinterpret_cast<const uint4*>(src + u * per_warp * dims + at[v][c]);
-      }
+        for (int c = 0; c < 2; ++c) {
+          x[u][v][c] = make_uint4(0, 0, 0, 0);
+          if (on[v] && u * per_warp + group < left)
+            x[u][v][c] = *reinterpret_cast<const uint4*>(src + u * per_warp * dims + at[v][c]);
+        }
+    src += step * dims;
+  };
+  load();
 
   // ---- where the token goes
   int64_t slot = -1;
@@ -216,100 +227,163 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowParams P) {
   uint8_t* exps = (is_v ? P.value_exps : P.key_exps) +
                   (int64_t(block) * P.kv_heads + first + group) * P.block_size + place;
 
+#pragma unroll 1
+  for (;;) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (u * per_warp >= left) break;
-    const bool row_on = u * per_warp + group < left;
-    float y[VPL][2][8], sq = 0.f;
+    for (int u = 0; u < U; ++u) {
+      if (u * per_warp >= left) break;
+      const bool row_on = u * per_warp + group < left;
+      const int64_t row = u * per_warp;  // from the pointers on
+      if (MODE != kWrite && turned) {
+        float y[VPL][2][8], sq = 0.f, inv = 1.f;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
+        for (int v = 0; v < VPL; ++v)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u][v][c]);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u][v][c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = h2f2(w[j]);
-          y[v][c][2 * j] = f.x;
-          y[v][c][2 * j + 1] = f.y;
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = h2f2(w[j]);
+              y[v][c][2 * j] = f.x;
+              y[v][c][2 * j + 1] = f.y;
+              sq += f.x * f.x + f.y * f.y;
+            }
+          }
+        if (weight) {
+          for (int o = lanes >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+          inv = rsqrtf(sq * P.inv_hk + P.eps);
         }
-      }
-    if (turned) {
-      float inv = 1.f;
-      if (weight) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
+            float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
+            const float a = fa * inv, b = fb * inv;
+            // a sine of 0 is no reason to take in the other element's infinity
+            fa = turn[v] ? a * ca[v][m] - b * sb[v][m] : a * ca[v][m];
+            fb = turn[v] ? b * cb[v][m] + a * sa[v][m] : b * cb[v][m];
+          }
+        if (MODE == kRotate || is_q) {  // fp16 rows
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float* f = y[v][c];
+              if (on[v] && row_on)
+                *reinterpret_cast<uint4*>(dense + row * dims + at[v][c]) =
+                    make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
+                               pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+            }
+          continue;
+        }
+        // 8-bit rows: the exponent that the row's largest finite element needs,
+        // then the codes (scaling by a power of two is exact). fmaxf leaves NaN
+        // out; an infinity, which is rare, is made one and left out so.
+        const auto largest = [&] {
+          float top = 0.f;
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[v][c][j]));
+          for (int o = lanes >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          return top;
+        };
+        float top = largest();
+        if (__any_sync(0xffffffffu, isinf(top))) {
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (isinf(y[v][c][j])) y[v][c][j] = __uint_as_float(0x7fc00000u);
+          top = largest();
+        }
+        const int e = row_exponent(top);
+        const float f = pow2(-e);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float* a = y[v][c];
+            const uint32_t lo = e4m3x2(a[0] * f, a[1] * f) | e4m3x2(a[2] * f, a[3] * f) << 16;
+            const uint32_t hi = e4m3x2(a[4] * f, a[5] * f) | e4m3x2(a[6] * f, a[7] * f) << 16;
+            if (on[v] && row_on && slot >= 0)
+              *reinterpret_cast<uint2*>(codes + row * dims + at[v][c]) = make_uint2(lo, hi);
+          }
+        if (gl == 0 && row_on && slot >= 0) exps[row * P.block_size] = uint8_t(e + kExpBias);
+      } else if (MODE != kRotate) {
+        // Rows that are only quantised stay fp16, two elements to an
+        // instruction. Times 2^-e an element is exact or ends below 2^-14, and
+        // the least code is 2^-9: both give 0.
+        uint32_t y[VPL][2][4];
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq += y[v][c][j] * y[v][c][j];
-        for (int o = lanes >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        inv = rsqrtf(sq * P.inv_hk + P.eps);
-      }
+            for (int j = 0; j < 4; ++j) y[v][c][j] = reinterpret_cast<const uint32_t*>(&x[u][v][c])[j];
+        const auto largest = [&] {
+          uint32_t top = 0;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v)
+          for (int v = 0; v < VPL; ++v)
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
-          float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
-          const float a = fa * inv, b = fb * inv;
-          // a sine of 0 is no reason to take in the other element's infinity
-          fa = turn[v] ? a * ca[v][m] - b * sb[v][m] : a * ca[v][m];
-          fb = turn[v] ? b * cb[v][m] + a * sa[v][m] : b * cb[v][m];
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top = max_half2(top, y[v][c][j] & 0x7fff7fffu);
+          for (int o = lanes >> 1; o; o >>= 1)
+            top = max_half2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float2 f = h2f2(top);
+          return fmaxf(f.x, f.y);
+        };
+        float top = largest();
+        if (__any_sync(0xffffffffu, isinf(top))) {
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t& w = y[v][c][j];
+                if ((w & 0x7fffu) == 0x7c00u) w |= 0x200u;
+                if ((w >> 16 & 0x7fffu) == 0x7c00u) w |= 0x2000000u;
+              }
+          top = largest();
         }
+        const int e = row_exponent(top);  // in [-32, 8]; fp16 has the powers up to 15
+#pragma unroll 1
+        for (int more = -e; ; more -= 15) {
+          const uint32_t f = half2_pow2(min(max(more, -14), 15));
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[v][c][j] = mul_half2(y[v][c][j], f);
+          if (!__any_sync(0xffffffffu, more > 15)) break;
+          if (more < 15) more = 15;  // this row is done: 2^0 from here on
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t* a = y[v][c];
+            const uint32_t lo = half2_e4m3x2(a[0]) | half2_e4m3x2(a[1]) << 16;
+            const uint32_t hi = half2_e4m3x2(a[2]) | half2_e4m3x2(a[3]) << 16;
+            if (on[v] && row_on && slot >= 0)
+              *reinterpret_cast<uint2*>(codes + row * dims + at[v][c]) = make_uint2(lo, hi);
+          }
+        if (gl == 0 && row_on && slot >= 0) exps[row * P.block_size] = uint8_t(e + kExpBias);
+      }
     }
-
-    if (MODE == kRotate || is_q) {  // fp16 rows
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float* f = y[v][c];
-          if (on[v] && row_on)
-            *reinterpret_cast<uint4*>(dense + u * per_warp * dims + at[v][c]) =
-                make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]),
-                           pack_half2(f[6], f[7]));
-        }
-    } else {
-      // 8-bit rows: the exponent that the row's largest finite element needs,
-      // then the codes (scaling by a power of two is exact). fmaxf leaves NaN
-      // out; an infinity, which is rare, is made one and left out so.
-      const auto largest = [&] {
-        float top = 0.f;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[v][c][j]));
-        for (int o = lanes >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        return top;
-      };
-      float top = largest();
-      if (__any_sync(0xffffffffu, isinf(top))) {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (isinf(y[v][c][j])) y[v][c][j] = __uint_as_float(0x7fc00000u);
-        top = largest();
-      }
-      const int e = row_exponent(top);
-      const float f = pow2(-e);
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float* a = y[v][c];
-          const uint32_t lo = e4m3x2(a[0] * f, a[1] * f) | e4m3x2(a[2] * f, a[3] * f) << 16;
-          const uint32_t hi = e4m3x2(a[4] * f, a[5] * f) | e4m3x2(a[6] * f, a[7] * f) << 16;
-          if (on[v] && row_on && slot >= 0)
-            *reinterpret_cast<uint2*>(codes + u * per_warp * dims + at[v][c]) = make_uint2(lo, hi);
-        }
-      if (gl == 0 && row_on && slot >= 0)
-        exps[int64_t(u * per_warp) * P.block_size] = uint8_t(e + kExpBias);
-    }
+    if ((left -= step) <= 0) return;
+    load();
+    dense += int64_t(step) * dims;
+    codes += int64_t(step) * dims;
+    exps += int64_t(step) * P.block_size;
   }
 }
 
@@ -326,7 +400,8 @@ pa_status launch_rows(RowParams P, cudaStream_t stream) {
     P.slices = P.q_slices + P.k_slices * (MODE == kRotate ? 1 : 2);
     return P.tokens * P.slices;
   };
-  const bool many = widest <= 32 && slice(kRows * per_warp) >= kManyWarps;
+  const bool many = widest <= 32 && slice(per_warp * kRows * kBatches) >= kManyWarps;
+  P.batches = many ? kBatches : 1;
   if (!many) slice(per_warp);
   if (P.tokens > INT32_MAX || P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
   const unsigned grid = unsigned(cdiv(P.tokens * P.slices, 8));
@@ -349,18 +424,6 @@ struct ReadParams {
   int strip;               // tokens of a warp, at most 32
 };
 
-// 2^e in both halves, e in [-14, 15].
-__device__ __forceinline__ uint32_t half2_pow2(int e) {
-  const uint32_t h = uint32_t(e + 15) << 10;
-  return h | h << 16;
-}
-
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // Eight codes times 2^(byte - 127), rounded once to fp16. Within [-14, 15] the
 // power is an fp16 and one product rounds once. Elsewhere the power is split:
 // the first product is exact (a code is a multiple of 2^-9, so that times 2^-14
@@ -381,13 +444,12 @@ __device__ __forceinline__ uint4 widen(const uint2& codes, int byte) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One warp per (kStrip or fewer tokens of a sequence, 1 KB of their keys or of
+// One warp per (strip of tokens of a sequence, 1 KB of their keys or of
 // their values): a token's heads are contiguous in the cache and in the output.
-// Lane l finds token l's place, so that a strip waits for one table lookup; then
-// R tokens are read at a time. A lane reads 8 codes and writes 16 bytes,
+// Lane l finds token l's place, so that a strip waits for one table lookup. A
+// lane reads 8 codes and writes 16 bytes,
 // neighbouring lanes neighbouring ones.
-template <int R>
-__global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
+__global__ void __launch_bounds__(256, 5) read_kernel(const ReadParams P) {
   constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 31;
   const int slices = P.k_slices + P.v_slices;
@@ -439,28 +501,21 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
         if (rest >= n) rest -= n, ++h;
       }
 
-      for (int r0 = 0; r0 < rows; r0 += R) {
-        uint2 codes[R][kUnroll];
-        int e[R][kUnroll];
-        bool row_on[R];
+      for (int r = 0; r < rows; ++r, dst += width) {
+        const int64_t at = __shfl_sync(0xffffffffu, slot, r);
+        const int64_t f = __shfl_sync(0xffffffffu, first, r);
+        if (at < 0) continue;
+        uint2 codes[kUnroll];
+        int e[kUnroll];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int64_t s = __shfl_sync(0xffffffffu, slot, r0 + r);
-          const int64_t f = __shfl_sync(0xffffffffu, first, r0 + r);
-          row_on[r] = s >= 0 && r0 + r < rows;
+        for (int u = 0; u < kUnroll; ++u)
+          if (u < chunks) {
+            codes[u] = *reinterpret_cast<const uint2*>(cache + at * width + 256 * u);
+            e[u] = exps[u][f];
+          }
 #pragma unroll
-          for (int u = 0; u < kUnroll; ++u)
-            if (row_on[r] && u < chunks) {
-              codes[r][u] = *reinterpret_cast<const uint2*>(cache + s * width + 256 * u);
-              e[r][u] = exps[u][f];
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r, dst += width)
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u)
-            if (row_on[r] && u < chunks)
-              *reinterpret_cast<uint4*>(dst + 256 * u) = widen(codes[r][u], e[r][u]);
+        for (int u = 0; u < kUnroll; ++u)
+          if (u < chunks) *reinterpret_cast<uint4*>(dst + 256 * u) = widen(codes[u], e[u]);
       }
     }
   }
@@ -681,7 +736,6 @@ extern "C" pa_status pa_cache_read(const pa_cache_config* cfg, const void* key_c
   const dim3 grid(unsigned(std::min<int64_t>(cdiv(tasks, 8), 65536)),
                   unsigned(std::min(cfg->batch, 65535)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (P.strip >= 4) read_kernel<4><<<grid, 256, 0, s>>>(P);
-  else read_kernel<1><<<grid, 256, 0, s>>>(P);
+  read_kernel<<<grid, 256, 0, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -33,6 +33,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two fp16 values to e4m3, likewise.
+__device__ __forceinline__ uint32_t half2_e4m3x2(uint32_t a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+  return r;
+}
+
+// 2^e in both halves, e in [-14, 15].
+__device__ __forceinline__ uint32_t half2_pow2(int e) {
+  const uint32_t h = uint32_t(e + 15) << 10;
+  return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The larger of each half; the other one's where one is NaN.
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Two e4m3 codes (low 16 bits) to fp16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t codes) {
   uint32_t r;
