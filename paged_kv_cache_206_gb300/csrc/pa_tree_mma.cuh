@@ -47,7 +47,7 @@ struct TreeMma {
   static constexpr int kSub = kRowBytes <= 128 && NT == 1 ? 32 : 16;  // keys a warp takes at a time
   static constexpr int kMT = kSub / 16;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kLead = 2;
+  static constexpr int kLead = 3;
   static constexpr uint32_t kV = kSub * kRowBytes;  // V behind K in a stage
   static constexpr uint32_t kExps = 2 * kV;         // then 2 x 32 exponent bytes
   static constexpr uint32_t kStage = 2 * kV + (Q8 ? 64 : 0);
@@ -134,15 +134,11 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   int made = 0;                             // tiles left for the arithmetic so far
   if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
   if (!tree_begin(P, S, place, worker, lane)) return;
-  int unit = 0, unit_end = 0, win0 = 0, cur = 0, next = 0, cut_L = 0, cut_b = 0, cut_kvh = 0;
-  // Lane l holds the blocks of 16 keys each that the units to come need: MT a
+  int unit = 0, unit_end = 0, win0 = 0, cut_L = 0, cut_b = 0, cut_kvh = 0;
+  // Lane l holds the places of 16 keys each that the units to come need: MT a
   // unit, 32 / MT units a window, and the next window's.
   constexpr int WIN = 32 / MT;
-  auto blocks_of = [&](int n0) {
-    const int key = (n0 + lane / MT) * SUB + (lane % MT) * 16;
-    return n0 + lane / MT < unit_end && key < cut_L
-               ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + key / bs] : 0;
-  };
+  int block = 0, in_block = 0, next_block = 0, next_in = 0;
   auto next_tile = [&]() {
     if (!tree_next(P, place)) return false;
     const TreeTile& t = place->tile;
@@ -161,38 +157,47 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   int issued = 0;
   auto issue = [&]() {
     if (unit < unit_end || next_tile()) {
-      if (unit == place->tile.s0) {
-        win0 = unit;
-        cur = blocks_of(unit);
-        next = blocks_of(unit + WIN);
-      } else if (unit >= win0 + WIN) {
-        win0 += WIN;
-        cur = next;
-        next = blocks_of(win0 + WIN);
+      const bool fresh = unit == place->tile.s0;
+      if (fresh || unit >= win0 + WIN) {
+        win0 = fresh ? unit : win0 + WIN;
+#pragma unroll 1
+        for (int k = fresh ? 0 : 1; k < 2; ++k) {
+          block = next_block;
+          in_block = next_in;
+          const int at = win0 + k * WIN + lane / MT, key = at * SUB + (lane % MT) * 16, page = key / bs;
+          next_in = key - page * bs;
+          next_block = at < unit_end && key < cut_L ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
+        }
       }
       const uint32_t dst = smem_u32(ring + (issued % Cfg::kStages) * Cfg::kStage);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int block = __shfl_sync(FULL, cur, (unit - win0) * MT + m);
-        const int key = unit * SUB + m * 16;
-        const bool ok = block >= 0 && block < P.num_blocks;
-        if (!ok && lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
-        const int place = key % bs;
-        const int64_t base = ok && key < cut_L ? (int64_t(block) * bs + place) * row_stride + int64_t(cut_kvh) * RB : 0;
+        const int from = (unit - win0) * MT + m, key = unit * SUB + m * 16;
+        const int blk = __shfl_sync(FULL, block, from), in_blk = __shfl_sync(FULL, in_block, from);
+        int rows = max(cut_L - key, 0);  // of the 16 that are the sequence's
+        if (blk < 0 || blk >= P.num_blocks) {
+          rows = 0;
+          if (lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+        }
+        // 16 keys lie in one block: a row past the sequence's is not read, but may be pointed at
+        const int at_block = rows ? blk : 0, at_place = rows ? in_blk : 0;
+        constexpr int STEP = 32 / C;  // rows of a round of copies
+        const int row0 = lane / C;
+        const int64_t off = (int64_t(at_block) * bs + at_place + row0) * row_stride +
+                            int64_t(cut_kvh) * RB + lane % C * 16;
+        const uint8_t* kp = P.key_cache + off;
+        const uint8_t* vp = P.value_cache + off;
 #pragma unroll
         for (int k = 0; k < C / 2; ++k) {
-          const int at = lane + 32 * k, row = at / C, ch = at % C;
-          const bool in = ok && key + row < cut_L;
-          const int64_t off = in ? base + row * row_stride + ch * 16 : 0;
-          const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(ch, row) * 16;
-          cp_async16(to, P.key_cache + off, in);
-          cp_async16(to + Cfg::kV, P.value_cache + off, in);
+          const int row = row0 + k * STEP;
+          const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(lane % C, row) * 16;
+          cp_async16(to, kp + k * (STEP * row_stride), row < rows);
+          cp_async16(to + Cfg::kV, vp + k * (STEP * row_stride), row < rows);
         }
         if constexpr (Q8) {
           if (lane < 2) {
-            const bool in = ok && key < cut_L;
-            const int64_t off = in ? (int64_t(block) * P.kv_heads + cut_kvh) * bs + place : 0;
-            cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + off, in);
+            const int64_t e = (int64_t(at_block) * P.kv_heads + cut_kvh) * bs + at_place;
+            cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + e, rows > 0);
           }
         }
       }
@@ -342,12 +347,19 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
             for (int e = 0; e < 2; ++e) {
               float& x = s[mt][nt][2 * hf + e];
               x = fmaf(x, f, add);
-              if (edge) {
-                const bool in = key < prefix || (key < L && sees(nt * 8 + 2 * c + e, key - prefix));
-                if (!in) x = -INFINITY;
-              }
             }
         }
+      if (edge) {
+        uint32_t seen = 0;
+#pragma unroll 1
+        for (int k = 0; k < MT * NT * 4; ++k) {  // score k % 4 of s[k / 4 / NT][k / 4 % NT]
+          const int key = j0 + k / 4 / NT * 16 + (k >> 1 & 1) * 8 + g, row = k / 4 % NT * 8 + 2 * c + (k & 1);
+          if (key < prefix || (key < L && sees(row, key - prefix))) seen |= 1u << k;
+        }
+#pragma unroll
+        for (int k = 0; k < MT * NT * 4; ++k)
+          if (!(seen >> k & 1u)) s[k / 4 / NT][k / 4 % NT][k % 4] = -INFINITY;
+      }
       float alpha[NT][2];
       bool moved = false;
 #pragma unroll
@@ -388,6 +400,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       }
       if (edge) {
         // non-finite elements of the drafts' V rows leave the product
+#pragma unroll 1
         for (int at = lane; at < SUB * C; at += 32) {
           const int row = at / C, key = j0 + row;
           if (key < prefix || key >= L) continue;

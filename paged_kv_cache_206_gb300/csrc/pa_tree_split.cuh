@@ -64,47 +64,23 @@ struct TreeLine {
     return s;
   }
 
-  // Places of the whole batch (warp-collective); `mine` is lane's load(P, lane).
-  static __device__ __forceinline__ int64_t total(const TreeParams& P, int lane, const Seq& mine) {
-    int64_t n = mine.total(P);
-    for (int b = lane + 32; b < P.batch; b += 32) n += load(P, b).total(P);
+  // The places and tokens of 32 sequences up to this lane's, its own among them.
+  struct Sums {
+    int64_t places;
+    int tokens;
+  };
+  static __device__ __forceinline__ Sums scan(const TreeParams& P, int lane, const Seq& s) {
+    Sums u{s.total(P), s.q};
 #pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
-  }
-
-  // The sequence that place u of the line belongs to, the places and the tokens
-  // before it (warp-collective; u below the total).
-  static __device__ __forceinline__ int find(const TreeParams& P, int64_t u, int lane, const Seq& mine,
-                                             int64_t& before, int& q_start) {
-    before = 0;
-    q_start = 0;
-    Seq s = mine;
-    for (int b0 = 0; b0 < P.batch; b0 += 32) {
-      if (b0) s = load(P, b0 + lane);
-      const int64_t n = s.total(P);
-      int64_t un = n;
-      int tn = s.q;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t ua = __shfl_up_sync(0xffffffffu, un, o);
-        const int ta = __shfl_up_sync(0xffffffffu, tn, o);
-        if (lane >= o) {
-          un += ua;
-          tn += ta;
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, u.places, o);
+      const int ut = __shfl_up_sync(0xffffffffu, u.tokens, o);
+      if (lane >= o) {
+        u.places += up;
+        u.tokens += ut;
       }
-      const unsigned who = __ballot_sync(0xffffffffu, n > 0 && u < before + un);
-      if (who) {
-        const int l = __ffs(who) - 1;
-        before += __shfl_sync(0xffffffffu, un - n, l);
-        q_start += __shfl_sync(0xffffffffu, tn - s.q, l);
-        return b0 + l;
-      }
-      before += __shfl_sync(0xffffffffu, un, 31);
-      q_start += __shfl_sync(0xffffffffu, tn, 31);
     }
-    return -1;
+    return u;
   }
 
   // Workers that share the line, and where worker c's piece begins.
@@ -142,20 +118,44 @@ struct TreeWalk {
     u = u0 = u1 = before = 0;
     q_start = 0;
     b = -1;
-    const typename Line::Seq mine = Line::load(P, lane);
-    total = Line::total(P, lane, mine);
+    // the line's length: of the first 32 sequences (kept for the search) and the others
+    seq = Line::load(P, lane);
+    typename Line::Sums sums = Line::scan(P, lane, seq);
+    total = __shfl_sync(0xffffffffu, sums.places, 31);
+    if (P.batch > 32) {
+      int64_t rest = 0;
+      for (int k = lane + 32; k < P.batch; k += 32) rest += Line::load(P, k).total(P);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      total += rest;
+    }
     nact = Line::active(total, S.workers, S.min_units);
-    if (worker < nact) {
-      u = u0 = Line::begin(total, worker, nact);
-      u1 = Line::begin(total, worker + 1, nact);
-      if (u0 < u1) b = Line::find(P, u0, lane, mine, before, q_start);
+    if (worker >= nact) return false;
+    u = u0 = Line::begin(total, worker, nact);
+    u1 = Line::begin(total, worker + 1, nact);
+    // the sequence that place u0 belongs to
+    for (int b0 = 0; b0 < P.batch && u0 < u1; b0 += 32) {
+      if (b0) {
+        seq = Line::load(P, b0 + lane);
+        sums = Line::scan(P, lane, seq);
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, u0 - before < sums.places);
+      if (who) {
+        const int l = __ffs(who) - 1;
+        b = b0 + l;
+        before += __shfl_sync(0xffffffffu, sums.places - seq.total(P), l);
+        q_start += __shfl_sync(0xffffffffu, sums.tokens - seq.q, l);
+        seq.q = __shfl_sync(0xffffffffu, seq.q, l);
+        seq.L = __shfl_sync(0xffffffffu, seq.L, l);
+        seq.tiles = __shfl_sync(0xffffffffu, seq.tiles, l);
+        seq.units = __shfl_sync(0xffffffffu, seq.units, l);
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, sums.places, 31);
+      q_start += __shfl_sync(0xffffffffu, sums.tokens, 31);
     }
-    if (b < 0) {
-      u = u1;
-      return false;
-    }
-    seq = Line::load(P, b);
-    return true;
+    u = u1;
+    return false;
   }
 
   __device__ __forceinline__ bool next(const TreeParams& P, TreeTile& t) {
@@ -181,8 +181,8 @@ struct TreeWalk {
       t.q_start = q_start;
       t.q = seq.q;
       t.L = seq.L;
-      t.kvh = tile / seq.tiles;
-      t.r0 = (tile % seq.tiles) * NR;
+      t.kvh = seq.tiles == 1 ? tile : tile / seq.tiles;
+      t.r0 = (tile - t.kvh * seq.tiles) * NR;
       t.slot = t.s0 == 0 && t.s1 == seq.units ? -1 : 2 * worker + (first ? 0 : 1);
       t.parts = 0;
       if (t.s0 == 0 && t.s1 < seq.units)
@@ -232,16 +232,17 @@ __device__ __forceinline__ void tree_note(const TreeSplit& S, int worker, const 
 
 // Joins the partial results of the divided tiles: CTA (c, y) the rows [8 y, 8 y + 8)
 // of the tile that worker c noted, a warp a row. Launched as the attention
-// kernel's programmatic dependent.
+// kernel's programmatic dependent. The maxima and sums of 32 parts are read by a lane each,
+// and 16 parts' rows are on their way meanwhile: at 4096 keys of one decode step
+// a tile has 43 parts, and they come in three waits.
 template <int HD, int NR>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, const TreeSplit S) {
   constexpr int DPL = HD / 32;  // dims a lane holds, next to one another
-  constexpr int BATCH = 8;      // partial rows in flight
+  constexpr int BATCH = 8;  // partial rows in flight
   const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
   grid_dependency_wait();
-  const TreeJoin& t = S.join[blockIdx.x];
-  const int parts = t.parts;
-  if (parts == 0) return;
+  const TreeJoin t = S.join[blockIdx.x];
+  if (t.parts == 0) return;
   const int r = t.r0 + n, i = r / P.group;
   const int64_t tok = int64_t(t.q_start) + i;
   if (i >= t.q || tok >= P.tokens) return;
@@ -249,33 +250,40 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, c
   auto row_of = [&](int k) {
     return int64_t(k == 0 ? t.first_slot : 2 * (int(blockIdx.x) + k)) * NR + n;
   };
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, S.part_ml[row_of(k)].x);
-  M = warp_max(M);
-  if (M == -INFINITY) M = 0.f;  // no score above -inf: the sum below is 0
-  float sum = 0.f, acc[DPL];
+  float x[BATCH][DPL];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (k0 + k < t.parts)
+#pragma unroll
+        for (int d = 0; d < DPL; d += 2)
+          *reinterpret_cast<float2*>(&x[k][d]) =
+              *reinterpret_cast<const float2*>(S.part_o + row_of(k0 + k) * HD + lane * DPL + d);
+  };
+  float M = -INFINITY, sum = 0.f, w = 0.f, acc[DPL];
 #pragma unroll
   for (int k = 0; k < DPL; ++k) acc[k] = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += BATCH) {
-    float2 ml[BATCH];
-    float x[BATCH][DPL];
+#pragma unroll 1
+  for (int k0 = 0; k0 < t.parts; k0 += BATCH) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (k0 % 32 == 0 && k0 + lane < t.parts) ml = S.part_ml[row_of(k0 + lane)];
+    load(k0);
+    if (k0 % 32 == 0) {
+      const float top = fmaxf(M, warp_max(ml.x));
+      const float ref = top == -INFINITY ? 0.f : top;  // no score above -inf: weights of 0
+      const float alpha = ex2(M - ref);
+      M = top;
+      w = ex2(ml.x - ref);
+      sum = fmaf(sum, alpha, warp_sum(ml.y * w));
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (k0 + k >= parts) break;
-      const int64_t row = row_of(k0 + k);
-      ml[k] = S.part_ml[row];
-#pragma unroll
-      for (int d = 0; d < DPL; d += 2)
-        *reinterpret_cast<float2*>(&x[k][d]) =
-            *reinterpret_cast<const float2*>(S.part_o + row * HD + lane * DPL + d);
+      for (int d = 0; d < DPL; ++d) acc[d] *= alpha;
     }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      if (k0 + k >= parts) break;
-      const float w = ex2(ml[k].x - M);
-      sum = fmaf(ml[k].y, w, sum);
+      const float wk = __shfl_sync(0xffffffffu, w, k0 % 32 + k);
+      if (k0 + k < t.parts)
 #pragma unroll
-      for (int d = 0; d < DPL; ++d) acc[d] = fmaf(w, x[k][d], acc[d]);
+        for (int d = 0; d < DPL; ++d) acc[d] = fmaf(wk, x[k][d], acc[d]);
     }
   }
   __half2* dst = reinterpret_cast<__half2*>(
