@@ -58,6 +58,12 @@ struct TreeTc {
   static constexpr int kVSlots = Q8 && QT == 2 ? 1 : 2;
   static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
   static constexpr int kKStages = Q8 ? 4 : 0, kVStages = Q8 ? 3 : 0, kStages = kKStages + kVStages;
+  // Barriers of the parts that have landed: one for each part (rows 0.., rows 64..) of the even
+  // and of the odd key tiles, of K and of V, whatever stage a part is in. A barrier per stage would
+  // do for four stages; with three a stage serves the two parts' warps in turn, and a warp
+  // that asked for its turn while the other's copy was still in flight took the phase before
+  // that one for its own (parts may land in either order).
+  static constexpr int kLanded = Q8 ? 8 : 0;
   // Key tiles whose exponents, and whose largest ones, are held; row tiles whose flags
   // are. A widening warp is at most three tiles ahead of the softmax (the K and V
   // rings' two, and one in registers), so a row tile or key tile eight on finds the place read.
@@ -74,7 +80,7 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead;
+  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead;
   using Place = TreePlace<TreeWalk<kTok, kRows, kLead>>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
   static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
@@ -204,8 +210,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint8_t* vring = smem + Cfg::v_off;
   int2* meta = reinterpret_cast<int2*>(smem + Cfg::meta_off);
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
-  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);
-  uint64_t* sempty = sfull + Cfg::kStages;
+  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);  // [K, V][key tile parity][part]
+  uint64_t* sempty = sfull + Cfg::kLanded;  // [stage]
   uint64_t* kfull = sempty + Cfg::kStages;
   uint64_t* kempty = kfull + KS;
   uint64_t* vfull = kempty + KS;
@@ -226,10 +232,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   const int worker = blockIdx.x;
 
   if (tid == 0) {
-    for (int i = 0; i < Cfg::kStages; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], Cfg::kConv);
-    }
+    for (int i = 0; i < Cfg::kLanded; ++i) mbar_init(&sfull[i], 1);
+    for (int i = 0; i < Cfg::kStages; ++i) mbar_init(&sempty[i], Cfg::kConv);
     for (int i = 0; i < KS; ++i) {
       mbar_init(&kfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&kempty[i], 1);
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const uint8_t* exps_of = is_k ? P.key_exps : P.value_exps;
     // the ring: stages of 64 keys (8-bit cache) or tiles
     const int nslots = Q8 ? (is_k ? Cfg::kKStages : Cfg::kVStages) : is_k ? KS : VS;
-    uint64_t* fulls = Q8 ? sfull + (is_k ? 0 : Cfg::kKStages) : is_k ? kfull : vfull;
+    uint64_t* fulls = Q8 ? sfull + (is_k ? 0 : 4) : is_k ? kfull : vfull;
     uint64_t* empties = Q8 ? sempty + (is_k ? 0 : Cfg::kKStages) : is_k ? kempty : vempty;
     uint8_t* ring = Q8 ? smem + Cfg::stage_off + (is_k ? 0 : Cfg::kKStages) * Cfg::kStageBytes : is_k ? kring : vring;
     const int half = pieces / 2, part = lane >= half ? 1 : 0;
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           uint8_t* dst = ring + (part ? slot1 : slot) * Cfg::kStageBytes + (lane - part * half) * box * HD;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            uint64_t* full = &fulls[p ? slot1 : slot];
+            uint64_t* full = &fulls[2 * (n & 1) + p];
             if (!tree_wait(&empties[p ? slot1 : slot], (p ? phase1 : phase) ^ 1)) {
               ok = false;
               break;
@@ -390,8 +394,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       }
     }
     // copies still in flight land before the CTA's memory is given back
-    for (int i = 0; i < nslots; ++i) {
-      const int times = filled / nslots + (i < filled % nslots ? 1 : 0);
+    const int nfulls = Q8 ? 4 : nslots;
+    for (int i = 0; i < nfulls; ++i) {
+      const int times = filled / nfulls + (i < filled % nfulls ? 1 : 0);
       if (times) tree_wait(&fulls[i], (times - 1) & 1);
     }
     if constexpr (Q8)
@@ -773,21 +778,21 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int ch = lane % CH, row0 = (part & 1) * 64 + sub * ROWS + lane / CH;  // this lane's first row
     uint64_t* full = kv ? vfull : kfull;
     uint64_t* empty = kv ? vempty : kempty;
-    uint64_t* landed = sfull + (kv ? Cfg::kKStages : 0);
+    uint64_t* landed = sfull + (kv ? 4 : 0) + (part & 1);  // [2 * key tile parity]
     uint64_t* taken = sempty + (kv ? Cfg::kKStages : 0);
     uint8_t* stage = smem + Cfg::stage_off + (kv ? Cfg::kKStages : 0) * Cfg::kStageBytes + sub * ROWS * HD + lane * 8;
     // this lane's places in the operand: the 64-dim half ch / 8 of row0, row0 + RPI, ...
     uint8_t* operand = (kv ? vring : kring) + (ch >> 3) * Cfg::kHalf + row0 * 128;
     // (rings of this warp's tile: slots and phases counted, as a remainder takes long)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
-    int slot = 0, phase = 0, st = part & 1, sphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
+    int slot = 0, phase = 0, st = part & 1, done = 0, em = 0, ephase = 0, mm = 0, tile = 0;
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       for (int i = 0; i < tiles; ++i) {
         const int key0 = (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
-        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[st], sphase)) {
+        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[2 * (done & 1)], done >> 1 & 1)) {
           ok = false;
           break;
         }
@@ -873,10 +878,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           slot = 0;
           phase ^= 1;
         }
-        if ((st += 2) >= nst) {
-          st -= nst;
-          sphase ^= 1;
-        }
+        if ((st += 2) >= nst) st -= nst;
+        ++done;
         if (++em == Cfg::kExps) {
           em = 0;
           ephase ^= 1;
