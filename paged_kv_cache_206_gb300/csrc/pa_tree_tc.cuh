@@ -137,6 +137,29 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Two fp32 operations in one instruction, and the largest of three.
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Barrier of the eight softmax warps: whether any thread's `pred` holds.
 __device__ __forceinline__ bool tree_softmax_bar(bool pred = false) {
   __syncwarp();  // (the barrier wants the warp converged)
@@ -636,8 +659,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           }
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
-          const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), F, ev);
+          for (int k = 4; k < 64; k += 2) mx[k / 2 & 3] = max3(mx[k / 2 & 3], x[k], x[k + 1]);
+          const float top = fmaf(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])), F, ev);
           // move the reference only when a score passes it by more than 2^8
           const bool grow = top > m_ref + kTcRescaleThreshold;
           float alpha = 1.f;
@@ -647,21 +670,22 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             l *= alpha;
           }
           const float add = ev - (m_ref == -INFINITY ? 0.f : m_ref);
-          float sum[2] = {0.f, 0.f};
+          float2 sum = make_float2(0.f, 0.f);
+          const float2 f2 = make_float2(F, F), add2 = make_float2(add, add);
           __syncwarp();  // (tcgen05.ld and .st want the warp converged)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float e0 = ex2(fmaf(x[32 * w + 2 * k], F, add)), e1 = ex2(fmaf(x[32 * w + 2 * k + 1], F, add));
-              sum[0] += e0;
-              sum[1] += e1;
-              pk[k] = pack_half2(e0, e1);
+              float2 e = fma_pair(make_float2(x[32 * w + 2 * k], x[32 * w + 2 * k + 1]), f2, add2);
+              e = make_float2(ex2(e.x), ex2(e.y));
+              sum = add_pair(sum, e);
+              pk[k] = pack_half2(e.x, e.y);
             }
             tmem_st16u(sbuf + w * 16, pk);  // over scores that are in registers
           }
-          l = fmaf(sum[0] + sum[1], unscale, l);
+          l = fmaf(sum.x + sum.y, unscale, l);
           if (m > 0 && __any_sync(FULL, grow)) {
             // O as the chain's job before left it
             const int nb = QT == 2 && hf ? n : n - 1, yb = QT == 2 ? hf ^ 1 : nb & 1;
