@@ -145,22 +145,26 @@ __global__ void __launch_bounds__(kAnyWarps * 32) tree_any_kernel(const TreePara
 pa_status check_tree(const pa_config* cfg) {
   const pa_status st = validate_config(cfg);
   if (st != PA_OK) return st;
-  if (cfg->mask_type != PA_MASK_NONE || cfg->chunk_blocks != 0 || cfg->num_sms <= 0)
+  if (cfg->mask_type != PA_MASK_NONE || cfg->chunk_blocks != 0 || cfg->num_sms <= 0 ||
+      cfg->num_sms > 65535)
     return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
 
 // The kernel for these head sizes and rows, if there is a faster one than
-// tree_any_kernel: for up to 32 rows of a kv head, and for 256 dims, the warp-level
-// tensor instructions with the narrowest of their 8-, 16- and 32-row tiles (16 at
-// most for 256 dims) that holds the rows, or several of the widest; beyond that
-// the tcgen05 tensor cores.
+// tree_any_kernel: for up to 16 rows of a kv head, and for 256 dims, the warp-level
+// tensor instructions with the narrower of their 8- and 16-row tiles that holds the
+// rows, or several of the wider; beyond that the tcgen05 tensor cores. Of 64 sequences
+// of up to 4096 keys, 8 kv heads of 128 dims, 16 rows take 77 us (8 bits) and 88 us
+// (fp16) here and 92 and 83 us there; one sequence of 1024 keys 16 us here, 23 and 17 us
+// there. With 32 rows the warp-level instructions took 121 and 132 us (25 and 26 us for
+// the one sequence), the others take 94 and 87 us (23 and 17 us).
 bool tree_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws,
                 cudaStream_t stream, cudaError_t* e) {
   if (c.head_size_k != c.head_size_v) return false;
   const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  if (rows > 32 && (c.head_size_k == 64 || c.head_size_k == 128)) {
+  const int nt = rows <= 8 ? 1 : 2;
+  if (rows > 16 && (c.head_size_k == 64 || c.head_size_k == 128)) {
     *e = tree_tc(P, c.head_size_k, q8, rows, c.num_sms, need, ws, stream);
     return true;
   }

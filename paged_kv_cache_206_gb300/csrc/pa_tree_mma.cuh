@@ -1,4 +1,4 @@
-// Tree attention on the warp-level tensor instructions, for up to 32 rows (a
+// Tree attention on the warp-level tensor instructions, for up to 16 rows (a
 // group of heads times a few drafts) per tile and K and V heads of 64, 128 or 256
 // dims, over the fp16 or the 8-bit cache.
 //
@@ -51,7 +51,9 @@ struct TreeMma {
   static constexpr uint32_t kV = kSub * kRowBytes;  // V behind K in a stage
   static constexpr uint32_t kExps = 2 * kV;         // then 2 x 32 exponent bytes
   static constexpr uint32_t kStage = 2 * kV + (Q8 ? 64 : 0);
-  static constexpr int kCtas = kStage > 9000 ? 1 : 2;  // CTAs of an SM
+  // CTAs of an SM (with 3 for tiles of 8 rows, 64 decode steps of 1 to 4096 tokens in 8 bits took
+  // the same 56 us: the memory system, not the warps' latencies, bounds such a batch)
+  static constexpr int kCtas = kStage > 9000 ? 1 : 2;
   // a warp's shared memory: query fragments (tiles of 8 rows keep theirs in
   // registers), what the rows see, the parents, the tiles ahead, the ring
   static constexpr uint32_t kBudget = ((227 * 1024 - 1024 * kCtas) / kCtas / kWarps) & ~127u;

@@ -42,12 +42,9 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kRows>, P, S);
 }
 
-template <int HD, int MAX_NT>
+template <int HD>
 cudaError_t tree_mma_pick(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws,
                           cudaStream_t s) {
-  if constexpr (MAX_NT >= 4)
-    if (nt >= 4)
-      return q8 ? tree_mma_run<HD, true, 4>(P, sms, need, ws, s) : tree_mma_run<HD, false, 4>(P, sms, need, ws, s);
   if (nt >= 2)
     return q8 ? tree_mma_run<HD, true, 2>(P, sms, need, ws, s) : tree_mma_run<HD, false, 2>(P, sms, need, ws, s);
   return q8 ? tree_mma_run<HD, true, 1>(P, sms, need, ws, s) : tree_mma_run<HD, false, 1>(P, sms, need, ws, s);

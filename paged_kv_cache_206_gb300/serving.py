@@ -33,28 +33,33 @@ class pa_cache_config(ctypes.Structure):
 # A call first puts one question to its arguments, whether all are in order: a decode
 # loop pays for that alone. Where the answer is no, the checks behind it say what is wrong.
 
-_f16 = _i32 = _f32 = _stream = _device = None
-_configs: dict = {}  # configurations by their values
+_f16 = _i32 = _f32 = _stream = _device = _lib = None
 
 
 def _start():
-    """torch's types and the calls that tell the current stream and device."""
-    global _f16, _i32, _f32, _stream, _device
+    """torch's types, the calls that tell the current stream and device, the library."""
+    global _f16, _i32, _f32, _stream, _device, _lib
     import torch
     _i32, _f32 = torch.int32, torch.float32
-    _stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _lib = load_library()
     _f16 = torch.float16
 
 
-def _config(kind, *values):
-    """A configuration's address; kept, as making one takes as long as the launch."""
-    key = (kind, values)
-    got = _configs.get(key)
-    if got is None:
-        if len(_configs) >= 4096:
-            _configs.clear()
-        got = _configs[key] = ctypes.byref(kind(*values))
-    return got
+class _Configs(dict):
+    """Addresses of configurations by their values: making one takes as long as the launch."""
+
+    def __init__(self, kind):
+        self.kind = kind
+
+    def __missing__(self, values):
+        if len(self) >= 4096:
+            self.clear()
+        got = self[values] = ctypes.byref(self.kind(*values))
+        return got
+
+
+_rotations = _Configs(pa_rotary)
 
 
 def _refuse(where: str, what: str):
@@ -90,35 +95,27 @@ def _rows(where, name, t, dtype, device, tokens, heads, size):
     return st if tokens > 1 else heads * size
 
 
-def _target(where, device, stream):
-    """The stream's handle, and the device to make current (None: it is)."""
-    if device.type != "cuda":
-        _refuse(where, f"tensors must be on a CUDA device, got {device}")
-    if stream is not None:
-        if stream.device != device:
-            _refuse(where, f"the stream is on {stream.device}, the tensors on {device}")
+def _launch(where, at, stream, call, *args):
+    """``call(*args, stream handle)`` with device ``at`` (the tensors') current."""
+    if at < 0:
+        _refuse(where, "tensors must be on a CUDA device")
+    if stream is None:
+        handle = _stream(at)
+    elif stream.device.index == at:
         handle = stream.cuda_stream
     else:
-        handle = _stream(device.index)
-    return handle, None if _device() == device.index else device
-
-
-def _launch(where, device, stream, call, *args):
-    """``call(*args, stream handle)`` with the tensors' device current."""
-    handle, other = _target(where, device, stream)
-    if other is None:
+        _refuse(where, f"the stream is on {stream.device}, the tensors on cuda:{at}")
+    if _device() == at:
         status = call(*args, handle)
     else:
         import torch
-        with torch.cuda.device(other):
+        with torch.cuda.device(at):
             status = call(*args, handle)
     if status:
         _check(status, where)
 
 
 def _status_arg(where, status, device):
-    if status is None:
-        return None
     import torch
     if status.numel() < 1 or status.element_size() != 4 or status.device != device \
             or status.dtype not in (torch.int32, torch.uint32):
@@ -147,10 +144,13 @@ def _ok(t, dtype, at, shape):
                          and t.is_contiguous())
 
 
-def _rows_ok(t, at, tokens, heads, size):
-    """Whether [tokens, heads, size] fp16 rows have dense heads."""
-    return (t.dtype is _f16 and t.get_device() == at and t.shape == (tokens, heads, size)
-            and t.stride()[1:] == (size, 1))
+def _token_stride(t, at, tokens, heads, size):
+    """The token stride of fp16 rows [tokens, heads, size] with dense heads; None: they are not."""
+    if t.dtype is _f16 and t.get_device() == at and t.shape == (tokens, heads, size):
+        st, sh, sd = t.stride()
+        if sh == size and sd == 1:
+            return st if tokens > 1 else heads * size
+    return None
 
 
 def _rotary_ok(at, tokens, heads, size, q_weight, k_weight, cos_sin, positions, q_out):
@@ -159,14 +159,9 @@ def _rotary_ok(at, tokens, heads, size, q_weight, k_weight, cos_sin, positions, 
             and (cos_sin is None or (cos_sin.dim() == 2 and _ok(cos_sin, _f32, at, cos_sin.shape))))
 
 
-def _row_stride(t, tokens, width):
-    return t.stride(0) if tokens > 1 else width
-
-
-def _rot_config(query, kv_heads, cos_sin, eps, interleaved):
+def _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved):
     limit, rot = (2**31 - 1, 0) if cos_sin is None else cos_sin.shape
-    _, heads, size = query.shape
-    return _config(pa_rotary, heads, kv_heads, size, rot, 1 if interleaved else 0, limit, eps)
+    return _rotations[heads, kv_heads, size, rot, 1 if interleaved else 0, limit, eps]
 
 
 def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6,
@@ -183,22 +178,22 @@ def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k
         _refuse(where, "query and key must be [tokens, heads, head_size], with positions")
     tokens, heads, size = query.shape
     at, kv_heads = query.get_device(), key.shape[1]
-    if not (_rows_ok(query, at, tokens, heads, size) and _rows_ok(key, at, tokens, kv_heads, size)
-            and _ok(k_out, _f16, at, (tokens, kv_heads, size))
+    qs = _token_stride(query, at, tokens, heads, size)
+    ks = _token_stride(key, at, tokens, kv_heads, size)
+    if not (qs is not None and ks is not None and _ok(k_out, _f16, at, (tokens, kv_heads, size))
             and _rotary_ok(at, tokens, heads, size, q_weight, k_weight, cos_sin, positions, q_out)):
         dev = query.device
-        _rows(where, "query", query, _f16, dev, tokens, heads, size)
-        _rows(where, "key", key, _f16, dev, tokens, kv_heads, size)
+        qs = _rows(where, "query", query, _f16, dev, tokens, heads, size)
+        ks = _rows(where, "key", key, _f16, dev, tokens, kv_heads, size)
         _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, dev)
         _dense(where, "k_out", k_out, _f16, dev, (tokens, kv_heads, size))
     if tokens == 0:
         return
-    _launch(where, query.device, stream, load_library().pa_qk_norm_rope,
-            _rot_config(query, kv_heads, cos_sin, eps, interleaved), tokens, query.data_ptr(),
-            _row_stride(query, tokens, heads * size), key.data_ptr(),
-            _row_stride(key, tokens, kv_heads * size), _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+    _launch(where, at, stream, _lib.pa_qk_norm_rope,
+            _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved), tokens, query.data_ptr(),
+            qs, key.data_ptr(), ks, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
             positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            _status_arg(where, status, query.device))
+            None if status is None else _status_arg(where, status, query.device))
 
 
 def _cache_tensors(where, key, value, key_exps, value_exps):
@@ -253,6 +248,8 @@ class QuantCache:
         self._blocks, self._block_size, self._heads, self._hk = key.shape
         self._hv = value.shape[3]
         self._addresses = tuple(t.data_ptr() for t in (key, key_exps, value, value_exps))
+        self._configs = _Configs(lambda batch, cols, max_rows: pa_cache_config(
+            batch, self._heads, self._hk, self._hv, self._block_size, self._blocks, cols, max_rows))
 
     @classmethod
     def empty(cls, num_blocks, block_size, kv_heads, head_size_k, head_size_v=None, device="cuda"):
@@ -264,11 +261,6 @@ class QuantCache:
                 for _ in range(2)]
         return cls(*codes, *exps)
 
-    def _cfg(self, block_tables, max_rows):
-        batch, cols = block_tables.shape
-        return _config(pa_cache_config, batch, self._heads, self._hk, self._hv, self._block_size,
-                       self._blocks, cols, max_rows)
-
     def write(self, key, value, block_tables, context_lens, q_seqlens=None, max_seqlen_q=None,
               status=None, stream=None) -> None:
         """Quantise the current tokens' ``key`` [T, Hk, hk] and ``value``
@@ -277,20 +269,20 @@ class QuantCache:
         if key.dim() != 3:
             _refuse(where, "key must be [tokens, kv_heads, head_size]")
         tokens = key.shape[0]
-        if not (_rows_ok(key, at, tokens, heads, self._hk)
-                and _rows_ok(value, at, tokens, heads, self._hv)
+        ks = _token_stride(key, at, tokens, heads, self._hk)
+        vs = _token_stride(value, at, tokens, heads, self._hv)
+        if not (ks is not None and vs is not None
                 and _batch_ok(at, block_tables, context_lens, q_seqlens)):
-            _rows(where, "key", key, _f16, self.device, tokens, heads, self._hk)
-            _rows(where, "value", value, _f16, self.device, tokens, heads, self._hv)
+            ks = _rows(where, "key", key, _f16, self.device, tokens, heads, self._hk)
+            vs = _rows(where, "value", value, _f16, self.device, tokens, heads, self._hv)
             _batch_args(where, block_tables, context_lens, q_seqlens, self.device)
         if tokens == 0:
             return
-        _launch(where, self.device, stream, load_library().pa_cache_write,
-                self._cfg(block_tables, tokens if max_seqlen_q is None else max_seqlen_q), tokens,
-                key.data_ptr(), _row_stride(key, tokens, heads * self._hk), value.data_ptr(),
-                _row_stride(value, tokens, heads * self._hv), block_tables.data_ptr(),
+        _launch(where, at, stream, _lib.pa_cache_write,
+                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)],
+                tokens, key.data_ptr(), ks, value.data_ptr(), vs, block_tables.data_ptr(),
                 context_lens.data_ptr(), _ptr(q_seqlens), *self._addresses,
-                _status_arg(where, status, self.device))
+                None if status is None else _status_arg(where, status, self.device))
 
     def store(self, query, key, value, q_weight, k_weight, cos_sin, positions, block_tables,
               context_lens, q_seqlens, max_seqlen_q, q_out, eps=1e-6, interleaved=False, status=None,
@@ -302,27 +294,27 @@ class QuantCache:
         if query.dim() != 3:
             _refuse(where, "query must be [tokens, heads, head_size]")
         (tokens, qh, size), hk, hv = query.shape, self._hk, self._hv
-        if not (_rows_ok(query, at, tokens, qh, hk) and _rows_ok(key, at, tokens, heads, hk)
-                and _rows_ok(value, at, tokens, heads, hv)
+        qs = _token_stride(query, at, tokens, qh, hk)
+        ks = _token_stride(key, at, tokens, heads, hk)
+        vs = _token_stride(value, at, tokens, heads, hv)
+        if not (qs is not None and ks is not None and vs is not None
                 and _rotary_ok(at, tokens, qh, hk, q_weight, k_weight, cos_sin, positions, q_out)
                 and _batch_ok(at, block_tables, context_lens, q_seqlens)):
             dev = self.device
-            _rows(where, "query", query, _f16, dev, tokens, qh, hk)
-            _rows(where, "key", key, _f16, dev, tokens, heads, hk)
-            _rows(where, "value", value, _f16, dev, tokens, heads, hv)
+            qs = _rows(where, "query", query, _f16, dev, tokens, qh, hk)
+            ks = _rows(where, "key", key, _f16, dev, tokens, heads, hk)
+            vs = _rows(where, "value", value, _f16, dev, tokens, heads, hv)
             _rotary(where, query, q_weight, k_weight, cos_sin, positions, q_out, dev)
             _batch_args(where, block_tables, context_lens, q_seqlens, dev)
         if tokens == 0:
             return
-        _launch(where, self.device, stream, load_library().pa_cache_store,
-                self._cfg(block_tables, tokens if max_seqlen_q is None else max_seqlen_q),
-                _rot_config(query, heads, cos_sin, eps, interleaved), tokens, query.data_ptr(),
-                _row_stride(query, tokens, qh * hk), key.data_ptr(),
-                _row_stride(key, tokens, heads * hk), value.data_ptr(),
-                _row_stride(value, tokens, heads * hv), _ptr(q_weight), _ptr(k_weight),
+        _launch(where, at, stream, _lib.pa_cache_store,
+                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)],
+                _rot_config(qh, heads, hk, cos_sin, eps, interleaved), tokens, query.data_ptr(),
+                qs, key.data_ptr(), ks, value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight),
                 _ptr(cos_sin), _ptr(positions), block_tables.data_ptr(), context_lens.data_ptr(),
                 _ptr(q_seqlens), *self._addresses, q_out.data_ptr(),
-                _status_arg(where, status, self.device))
+                None if status is None else _status_arg(where, status, self.device))
 
     def read(self, block_tables, starts, context_lens, out_starts, max_rows, k_out, v_out,
              status=None, stream=None) -> None:
@@ -342,10 +334,10 @@ class QuantCache:
             _dense(where, "out_starts", out_starts, _i32, dev, context_lens.shape)
         if rows == 0:
             return
-        _launch(where, self.device, stream, load_library().pa_cache_read,
-                self._cfg(block_tables, max_rows), *self._addresses, block_tables.data_ptr(),
+        _launch(where, at, stream, _lib.pa_cache_read,
+                self._configs[(*block_tables.shape, max_rows)], *self._addresses, block_tables.data_ptr(),
                 _ptr(starts), context_lens.data_ptr(), out_starts.data_ptr(), rows, k_out.data_ptr(),
-                v_out.data_ptr(), _status_arg(where, status, self.device))
+                v_out.data_ptr(), None if status is None else _status_arg(where, status, self.device))
 
 
 def pa_tree_workspace(cfg) -> int:
@@ -404,7 +396,7 @@ class TreeStep:
                 _dense(where, "parents", parents, _i32, dev, (tokens,))
         if tokens == 0:
             return out
-        _launch(where, self.device, stream, load_library().pa_tree_forward, cfg, tokens,
+        _launch(where, at, stream, _lib.pa_tree_forward, cfg, tokens,
                 query.data_ptr(), *self._caches, block_tables.data_ptr(), context_lens.data_ptr(),
                 _ptr(q_seqlens), _ptr(parents), space, size, out.data_ptr())
         return out
