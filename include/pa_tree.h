@@ -14,6 +14,14 @@
  * out = softmax(scale * <q, K_j>) V_j over those, heads grouped as in pa.h.
  * Keys and values that a row does not attend have no effect on it, whatever
  * they hold (NaN and infinities included).
+ *
+ * Scores, softmax sums and outputs are accumulated in fp32; the weights are
+ * rounded to fp16 for their product with V. With more than 16 rows of a kv head
+ * (H / Hk * max_seqlen_q) and heads of 64 or 128 dims the 8-bit cache's rows are
+ * brought to the largest exponent among 128 keys in fp16, exact but for rows
+ * 2^15 times smaller than that. The same batch gives the same bits every time; a
+ * sequence in another batch may differ in its last bits, as the work is divided
+ * otherwise.
  */
 #ifndef PA_TREE_H
 #define PA_TREE_H
@@ -44,7 +52,7 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  * device only (so that it may be captured once and replayed as they change).
  *
  * cfg            as in pa.h, with mask_type = PA_MASK_NONE, chunk_blocks = 0 and
- *                num_sms > 0. With parents max_seqlen_q <= PA_TREE_MAX_TOKENS.
+ *                0 < num_sms <= 65535. With parents max_seqlen_q <= PA_TREE_MAX_TOKENS.
  * tokens         rows of query and out (sum q_b, or more: the rows behind the
  *                last sequence are neither read nor written)
  * query          device fp16 [tokens, H, hk], 16-byte aligned
@@ -63,7 +71,8 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  *                whose work overlaps on the GPU need a workspace each.
  * out            device fp16 [tokens, H, hv], 16-byte aligned
  *
- * A length that breaks a constraint (PA_STATUS_BIT_PLAN) leaves its sequence
+ * The lengths, the block tables and the parents must not change while the call's
+ * work runs. A length that breaks a constraint (PA_STATUS_BIT_PLAN) leaves its sequence
  * out; a block table entry outside [0, num_blocks) is never dereferenced and
  * makes the outputs of its sequence undefined (PA_STATUS_BIT_BLOCK_INDEX).
  */
