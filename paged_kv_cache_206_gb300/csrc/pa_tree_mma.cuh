@@ -26,7 +26,7 @@
 // them at the end to the rows that do see them.
 //
 // Every warp is a worker of its own (pa_tree_split.cuh): it streams the keys of
-// its piece of the line through a ring with cp.async, from one tile into the
+// its piece of the line through a ring of its own with TMA, from one tile into the
 // next without a pause, and keeps its rows' state in registers until a tile ends. There
 // is no block-wide barrier. (With a CTA as the worker, its four warps taking
 // turns at a tile's keys and merging in shared memory, the SMs stood idle 42 % of the
@@ -49,45 +49,63 @@ struct TreeMma {
   static constexpr int kRows = 8 * NT;
   static constexpr int kLead = 3;
   static constexpr uint32_t kV = kSub * kRowBytes;  // V behind K in a stage
-  static constexpr uint32_t kExps = 2 * kV;         // then 2 x 32 exponent bytes
-  static constexpr uint32_t kStage = 2 * kV + (Q8 ? 64 : 0);
+  static constexpr uint32_t kStage = 2 * kV;
+  static_assert(kV % 1024 == 0, "swizzled boxes begin on 1024 bytes");
   // CTAs of an SM (with 3 for tiles of 8 rows, 64 decode steps of 1 to 4096 tokens in 8 bits took
   // the same 56 us: the memory system, not the warps' latencies, bounds such a batch)
   static constexpr int kCtas = kStage > 9000 ? 1 : 2;
-  // a warp's shared memory: query fragments (tiles of 8 rows keep theirs in
-  // registers), what the rows see, the parents, the tiles ahead, the ring
-  static constexpr uint32_t kBudget = ((227 * 1024 - 1024 * kCtas) / kCtas / kWarps) & ~127u;
-  static constexpr int kTiles = 8;
-  static constexpr uint32_t q_off = 0;
+  // a warp's shared memory: the ring, query fragments (tiles of 8 rows keep theirs in
+  // registers), what the rows see, the parents, the tiles ahead, the exponents, barriers
+  static constexpr uint32_t kBudget = ((227 * 1024 - 2048 * kCtas) / kCtas / kWarps) & ~1023u;
+  static constexpr int kTiles = 8, kMaxStages = 5;
+  static constexpr uint32_t q_off = 0;  // from the ring's end on
   static constexpr uint32_t mask_off = q_off + (NT > 1 ? kRows * HD * 2 : 0);
   static constexpr uint32_t par_off = mask_off + kRows * kTreeWords * 4;
   static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
   static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
   using Place = TreePlace<TreeWalk<kSub, kRows, kLead>>;
   static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(TreeTile) + 7) & ~7u;
-  static constexpr uint32_t ring_off = (place_off + sizeof(Place) + 127) & ~127u;
-  static constexpr int kFit = int((kBudget - ring_off) / kStage);
-  static constexpr int kStages = kFit < 5 ? kFit : 5;
+  static constexpr uint32_t exps_off = (place_off + sizeof(Place) + 15) & ~15u;  // [stage][K, V][32]
+  static constexpr uint32_t bars_off = exps_off + (Q8 ? kMaxStages * 64 : 0);
+  static constexpr uint32_t kRest = bars_off + kMaxStages * 8;
+  static constexpr int kFit = int((kBudget - kRest) / kStage);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2 && kStages + 2 <= kTiles, "ring");
-  static constexpr uint32_t warp_bytes = (ring_off + kStages * kStage + 127) & ~127u;
-  static constexpr uint32_t bytes = kWarps * warp_bytes;
+  static constexpr uint32_t warp_bytes = (kStages * kStage + kRest + 1023) & ~1023u;
+  static constexpr uint32_t bytes = kWarps * warp_bytes + 1024;
   static_assert((bytes + 1024) * kCtas <= 228 * 1024, "shared memory");
 };
 
-// The chunk's place in its row: rows of a line or more spread over all banks.
-template <int CHUNKS>
-__device__ __forceinline__ int tree_swz(int chunk, int row) {
-  return CHUNKS >= 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+// Byte of chunk `chunk` of row `row` in a K or V stage, as the copies leave it: 128-byte
+// parts of the rows, [part][row][128 bytes], or rows of 64 bytes, the chunk XORed with
+// the row (the copies' swizzle), which spreads equal chunks of 8 rows over all banks.
+template <int CHUNKS, int SUB>
+__device__ __forceinline__ uint32_t tree_at(int chunk, int row) {
+  return CHUNKS >= 8 ? (chunk >> 3) * (SUB * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)
+                     : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  const uint32_t n = ok ? 16 : 0;  // 0: the 16 bytes are zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// Untiled copy of global memory into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+
+// Bounded wait of the whole warp for a phase of `bar`. Every lane polls, and the
+// loop's branch goes by a vote, so the warp stays converged: with one lane polling
+// for the others the compiler let that lane run apart from them for long after
+// the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
+// codes 11,000 to convert instead of 2,000).
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+#pragma unroll 1
+  do {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
+  return false;
 }
 
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -110,31 +128,39 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
 
 template <int HD, bool Q8, int NT>
 __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
-    tree_mma_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
+    tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                    const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S, int box) {
   using Cfg = TreeMma<HD, Q8, NT>;
   constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows;
   constexpr int RB = Cfg::kRowBytes, C = Cfg::kChunks, E = Cfg::kElems;
+  constexpr int RPB = RB < 128 ? RB : 128;  // bytes of a row that lie together
   constexpr int OT = HD / 16;  // m-tiles of O^T, k-steps of S^T
   constexpr unsigned FULL = 0xffffffffu;
-  extern __shared__ __align__(128) uint8_t smem_all[];
+  extern __shared__ uint8_t smem_all[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  uint8_t* smem = smem_all + warp * Cfg::warp_bytes;
+  uint8_t* ring = smem_all + (-smem_u32(smem_all) & 1023u) + warp * Cfg::warp_bytes;
+  uint8_t* smem = ring + Cfg::kStages * Cfg::kStage;
   uint8_t* q_s = smem + Cfg::q_off;
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + Cfg::mask_off);
   uint8_t* par_s = smem + Cfg::par_off;
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
   TreeTile* tile_s = reinterpret_cast<TreeTile*>(smem + Cfg::tile_off);
-  uint8_t* ring = smem + Cfg::ring_off;
+  uint8_t* exps_s = smem + Cfg::exps_off;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);  // [stage] landed
   const int worker = blockIdx.x * Cfg::kWarps + warp;
 
   const int G = P.group, bs = P.block_size;
-  const int64_t row_stride = int64_t(P.kv_heads) * RB;
 
   // ---- the stream of units: where it stands on the line, and in its tile
   typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
   int made = 0;                             // tiles left for the arithmetic so far
-  if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
+  if (lane == 0) {
+    S.join[worker].parts = 0;  // no divided tile yet
+    for (int k = 0; k < Cfg::kStages; ++k) mbar_init(&full[k], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
   if (!tree_begin(P, S, place, worker, lane)) return;
   int unit = 0, unit_end = 0, win0 = 0, cut_L = 0, cut_b = 0, cut_kvh = 0;
   // Lane l holds the places of 16 keys each that the units to come need: MT a
@@ -156,62 +182,65 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     unit_end = t.s1;
     return true;
   };
-  int issued = 0;
+  // The next unit's copies: boxes of `box` keys, which lie in one block. Rows behind the
+  // context come with the last box and are dealt with where the drafts are.
+  const uint64_t pol = policy_evict_first();
+  int issued = 0, to = 0;  // units so far, the next one's stage
   auto issue = [&]() {
-    if (unit < unit_end || next_tile()) {
-      const bool fresh = unit == place->tile.s0;
-      if (fresh || unit >= win0 + WIN) {
-        win0 = fresh ? unit : win0 + WIN;
+    if (unit >= unit_end && !next_tile()) return;
+    const bool fresh = unit == place->tile.s0;
+    if (fresh || unit >= win0 + WIN) {
+      win0 = fresh ? unit : win0 + WIN;
 #pragma unroll 1
-        for (int k = fresh ? 0 : 1; k < 2; ++k) {
-          block = next_block;
-          in_block = next_in;
-          const int at = win0 + k * WIN + lane / MT, key = at * SUB + (lane % MT) * 16, page = key / bs;
-          next_in = key - page * bs;
-          next_block = at < unit_end && key < cut_L ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
-        }
+      for (int k = fresh ? 0 : 1; k < 2; ++k) {
+        block = next_block;
+        in_block = next_in;
+        const int at = win0 + k * WIN + lane / MT, key = at * SUB + (lane % MT) * 16, page = key / bs;
+        next_in = key - page * bs;
+        next_block = at < unit_end && key < cut_L ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
       }
-      const uint32_t dst = smem_u32(ring + (issued % Cfg::kStages) * Cfg::kStage);
+    }
+    int blk[MT], in_blk[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      blk[m] = __shfl_sync(FULL, block, (unit - win0) * MT + m);
+      in_blk[m] = __shfl_sync(FULL, in_block, (unit - win0) * MT + m);
+    }
+    if (lane == 0) {
+      bool go[MT];
+      uint32_t n = 0;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int from = (unit - win0) * MT + m, key = unit * SUB + m * 16;
-        const int blk = __shfl_sync(FULL, block, from), in_blk = __shfl_sync(FULL, in_block, from);
-        int rows = max(cut_L - key, 0);  // of the 16 that are the sequence's
-        if (blk < 0 || blk >= P.num_blocks) {
-          rows = 0;
-          if (lane == 0) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
-        }
-        // 16 keys lie in one block: a row past the sequence's is not read, but may be pointed at
-        const int at_block = rows ? blk : 0, at_place = rows ? in_blk : 0;
-        constexpr int STEP = 32 / C;  // rows of a round of copies
-        const int row0 = lane / C;
-        const int64_t off = (int64_t(at_block) * bs + at_place + row0) * row_stride +
-                            int64_t(cut_kvh) * RB + lane % C * 16;
-        const uint8_t* kp = P.key_cache + off;
-        const uint8_t* vp = P.value_cache + off;
+        const bool there = blk[m] >= 0 && blk[m] < P.num_blocks, mine = m * 16 % box == 0 && unit * SUB + m * 16 < cut_L;
+        if (!there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
+        go[m] = there && mine;
+        n += go[m] ? 1 : 0;
+      }
+      if (n) mbar_arrive_expect_tx(&full[to], n * box * (2 * RB + (Q8 ? 2 : 0)));
+      else mbar_arrive(&full[to]);
+      uint8_t* dst = ring + to * Cfg::kStage;
 #pragma unroll
-        for (int k = 0; k < C / 2; ++k) {
-          const int row = row0 + k * STEP;
-          const uint32_t to = dst + (m * 16 + row) * RB + tree_swz<C>(lane % C, row) * 16;
-          cp_async16(to, kp + k * (STEP * row_stride), row < rows);
-          cp_async16(to + Cfg::kV, vp + k * (STEP * row_stride), row < rows);
-        }
+      for (int m = 0; m < MT; ++m) {
+        if (!go[m]) continue;
+        const int row = blk[m] * bs + in_blk[m], part = cut_kvh * (RB > 128 ? RB / 128 : 1);
+        tma_load_3d(dst + m * 16 * RB, &tmk, &full[to], 0, row, part, pol);
+        tma_load_3d(dst + Cfg::kV + m * 16 * RB, &tmv, &full[to], 0, row, part, pol);
         if constexpr (Q8) {
-          if (lane < 2) {
-            const int64_t e = (int64_t(at_block) * P.kv_heads + cut_kvh) * bs + at_place;
-            cp_async16(dst + Cfg::kExps + lane * 32 + m * 16, (lane ? P.value_exps : P.key_exps) + e, rows > 0);
-          }
+          const int64_t e = (int64_t(blk[m]) * P.kv_heads + cut_kvh) * bs + in_blk[m];
+          bulk_load(exps_s + to * 64 + m * 16, P.key_exps + e, box, &full[to]);
+          bulk_load(exps_s + to * 64 + 32 + m * 16, P.value_exps + e, box, &full[to]);
         }
       }
-      ++unit;
     }
+    __syncwarp();
+    ++unit;
     ++issued;
-    cp_async_commit();
+    if (++to == Cfg::kStages) to = 0;
   };
 #pragma unroll 1
   for (int n = 0; n < Cfg::kStages; ++n) issue();
 
-  int n = 0;  // units done
+  int n = 0, stage = 0, phase = 0;  // units done, the next one's stage
   for (int done = 0; done < made; ++done) {
     __syncwarp();
     const TreeTile t = tile_s[done % Cfg::kTiles];
@@ -274,10 +303,19 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     }
 
     for (int un = t.s0; un < t.s1; ++un, ++n) {
-      cp_async_wait<Cfg::kStages - 1>();
-      __syncwarp();
-      uint8_t* kb = ring + (n % Cfg::kStages) * Cfg::kStage;
+      if (!tree_wait(&full[stage], phase)) {
+        // the copies in flight land before the CTA's memory is given back
+        if (lane == 0) set_status(P.status, PA_STATUS_BIT_TIMEOUT);
+        for (++n; n < issued; ++n) {
+          if (++stage == Cfg::kStages) stage = 0, phase ^= 1;
+          tree_wait(&full[stage], phase);
+        }
+        return;
+      }
+      uint8_t* kb = ring + stage * Cfg::kStage;
       uint8_t* vb = kb + Cfg::kV;
+      const uint8_t* ex = exps_s + stage * 64;
+      if (++stage == Cfg::kStages) stage = 0, phase ^= 1;
       const int j0 = un * SUB;
       const bool edge = j0 + SUB > prefix;
 
@@ -289,12 +327,12 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
 #pragma unroll
       for (int sc = 0; sc < C / 4; ++sc) {
-        const int ch = tree_swz<C>(C >= 8 ? 2 * c + (sc & 1) + 8 * (sc >> 1) : c, g);
+        const uint8_t* kc = kb + tree_at<C, SUB>(C >= 8 ? 2 * c + (sc & 1) + 8 * (sc >> 1) : c, g);
         uint4 xa[MT], xb[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          xa[mt] = lds128(kb + (mt * 16 + g) * RB + ch * 16);
-          xb[mt] = lds128(kb + (mt * 16 + 8 + g) * RB + ch * 16);
+          xa[mt] = lds128(kc + mt * 16 * RPB);
+          xb[mt] = lds128(kc + (mt * 16 + 8) * RPB);
         }
 #pragma unroll
         for (int j = 0; j < E / 4; ++j) {
@@ -337,7 +375,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           float f = P.scale_log2, add = 0.f;
           unscale[mt][hf] = 1.f;
           if constexpr (Q8) {
-            int ke = kb[Cfg::kExps + kk], ve = kb[Cfg::kExps + 32 + kk];
+            int ke = ex[kk], ve = ex[32 + kk];
             if (edge && key >= L) ke = ve = kExpBias;  // exponents behind the context: anything
             f *= pow2(ke - kExpBias);
             add = float(ve - kExpBias);
@@ -401,12 +439,17 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           }
       }
       if (edge) {
-        // non-finite elements of the drafts' V rows leave the product
+        // V rows behind the context hold anything and become 0, and non-finite elements of
+        // the drafts' leave the product
 #pragma unroll 1
         for (int at = lane; at < SUB * C; at += 32) {
           const int row = at / C, key = j0 + row;
-          if (key < prefix || key >= L) continue;
-          uint4* p = reinterpret_cast<uint4*>(vb + row * RB + (at % C) * 16);
+          if (key < prefix) continue;
+          uint4* p = reinterpret_cast<uint4*>(vb + tree_at<C, SUB>(at % C, row));
+          if (key >= L) {
+            *p = make_uint4(0, 0, 0, 0);
+            continue;
+          }
           uint4 v = *p;
           bool hit = clear_nonfinite<Q8>(v.x);
           hit |= clear_nonfinite<Q8>(v.y);
@@ -418,6 +461,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
             atomicOr(&bad_s[(a >> 5) % kTreeWords], 1u << (a & 31));
           }
         }
+        fence_proxy_async();  // before the stage's next copy
         __syncwarp();
       }
 
@@ -431,13 +475,13 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           pb[nt][1] = movmatrix_t(pack_half2(s[mt][nt][2], s[mt][nt][3]));
         }
         // this lane's keys 2c, 2c + 1, 2c + 8, 2c + 9 (rows mt * 16 + ...)
-        const uint8_t* v0 = vb + (mt * 16 + 2 * c) * RB;
+        const uint8_t* v0 = vb + (mt * 16 + 2 * c) * RPB;
         if constexpr (C >= 8) {
 #pragma unroll
           for (int uu = 0; uu < C / 8; ++uu) {
-            const int even = ((g + 8 * uu) ^ (2 * c)) * 16, odd = ((g + 8 * uu) ^ (2 * c + 1)) * 16;
-            const uint4 x0 = lds128(v0 + even), x1 = lds128(v0 + RB + odd);
-            const uint4 x2 = lds128(v0 + 8 * RB + even), x3 = lds128(v0 + 9 * RB + odd);
+            const int even = uu * SUB * 128 + (g ^ (2 * c)) * 16, odd = uu * SUB * 128 + (g ^ (2 * c + 1)) * 16;
+            const uint4 x0 = lds128(v0 + even), x1 = lds128(v0 + RPB + odd);
+            const uint4 x2 = lds128(v0 + 8 * RPB + even), x3 = lds128(v0 + 9 * RPB + odd);
             const uint32_t *w0 = reinterpret_cast<const uint32_t*>(&x0), *w1 = reinterpret_cast<const uint32_t*>(&x1);
             const uint32_t *w2 = reinterpret_cast<const uint32_t*>(&x2), *w3 = reinterpret_cast<const uint32_t*>(&x3);
 #pragma unroll
@@ -468,7 +512,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int row = 2 * c + (k & 1) + 8 * (k >> 1);
-            x[k] = *reinterpret_cast<const uint2*>(vb + (mt * 16 + row) * RB + tree_swz<C>(g >> 1, row) * 16 + (g & 1) * 8);
+            x[k] = *reinterpret_cast<const uint2*>(vb + tree_at<C, SUB>(g >> 1, mt * 16 + row) + (g & 1) * 8);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {

@@ -89,30 +89,17 @@ struct TreeTc {
   static_assert(bytes <= kTcMaxSmem, "shared memory");
 };
 
-// Untiled copy of global memory into shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  const uint32_t n = ok ? 16 : 0;  // 0: the 16 bytes are zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Bounded wait of the whole warp for a phase of `bar`. Every lane polls, and the
-// loop's branch goes by a vote, so the warp stays converged: with one lane polling
-// for the others the compiler let that lane run apart from them for long after
-// the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
-// codes 11,000 to convert instead of 2,000).
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-#pragma unroll 1
-  do {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
-  return false;
-}
-
-// The same for two barriers at once.
+// tree_wait for two barriers at once.
 __device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
   const long long t0 = clock64();
 #pragma unroll 1
