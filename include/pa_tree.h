@@ -69,7 +69,7 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  * workspace      device, >= pa_tree_workspace's bytes, 256-byte aligned; its
  *                status word zero before the first call, as in pa.h. Calls
  *                whose work overlaps on the GPU need a workspace each.
- * out            device fp16 [tokens, H, hv], 16-byte aligned
+ * out            device fp16 [tokens, H, hv], 16-byte aligned, not the query
  *
  * The lengths, the block tables and the parents must not change while the call's
  * work runs. A length that breaks a constraint (PA_STATUS_BIT_PLAN) leaves its sequence

@@ -155,7 +155,7 @@ pa_status check_tree(const pa_config* cfg) {
 // tree_any_kernel: for up to 16 rows of a kv head, and for 256 dims, the warp-level
 // tensor instructions with the narrower of their 8- and 16-row tiles that holds the
 // rows, or several of the wider; beyond that the tcgen05 tensor cores. Of 64 sequences
-// of up to 4096 keys, 8 kv heads of 128 dims, 16 rows take 77 us (8 bits) and 88 us
+// of up to 4096 keys, 8 kv heads of 128 dims, 16 rows take 59 us (8 bits) and 83 us
 // (fp16) here and 92 and 83 us there; one sequence of 1024 keys 16 us here, 23 and 17 us
 // there. With 32 rows the warp-level instructions took 121 and 132 us (25 and 26 us for
 // the one sequence), the others take 94 and 87 us (23 and 17 us).
@@ -221,6 +221,7 @@ extern "C" pa_status pa_tree_forward(const pa_config* cfg, int64_t tokens, const
   if (workspace_bytes < need) return PA_ERR_BUFFER_TOO_SMALL;
   if (tokens * c.num_heads > INT32_MAX) return PA_ERR_INVALID_ARG;
   if (tokens == 0) return PA_OK;
+  if (out == query) return PA_ERR_INVALID_ARG;  // a tile in parts reads its rows after others wrote theirs
   TreeParams P{};
   P.query = static_cast<const __half*>(query);
   P.key_cache = static_cast<const uint8_t*>(key_cache);

@@ -28,7 +28,8 @@
 // Every warp is a worker of its own (pa_tree_split.cuh): it streams the keys of
 // its piece of the line through a ring of its own with TMA, from one tile into the
 // next without a pause, and keeps its rows' state in registers until a tile ends. There
-// is no block-wide barrier. (With a CTA as the worker, its four warps taking
+// is no block-wide barrier. (Copied with cp.async, 16 bytes a lane, the 64 decode steps below took
+// 57 us in 8 bits and the copies alone 47; with TMA they take 50. With a CTA as the worker, its four warps taking
 // turns at a tile's keys and merging in shared memory, the SMs stood idle 42 % of the
 // time at 64 decode steps of 1 to 4096 tokens: every tile end drained four rings.)
 #pragma once
@@ -44,15 +45,18 @@ struct TreeMma {
   static constexpr int kRowBytes = HD * (Q8 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
   static constexpr int kElems = Q8 ? 16 : 8;      // elements of a chunk
-  static constexpr int kSub = kRowBytes <= 128 && NT == 1 ? 32 : 16;  // keys a warp takes at a time
+  // keys a warp takes at a time, 4 KB of K (16 rows over 8 bits of 128 dims: 60 us with 32, 77 with 16)
+  static constexpr int kSub = kRowBytes <= 128 ? 32 : 16;
   static constexpr int kMT = kSub / 16;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kLead = 3;
+  // what a tile costs besides its keys, in units; measured, 64 sequences of up to 4096 keys and one
+  // of 4096 (8 rows of 128 dims, 8 bits): 54.4 and 15.2 us at 3, 55.3 and 15.8 at 2, 54.8 and 17.2 at 5;
+  // 16 rows: 60 us at 3, 59 at 4 and 58 at 6, but 22, 23 and 25 us for 8 sequences of 2048
+  static constexpr int kLead = NT == 1 ? 3 : 4;
   static constexpr uint32_t kV = kSub * kRowBytes;  // V behind K in a stage
   static constexpr uint32_t kStage = 2 * kV;
   static_assert(kV % 1024 == 0, "swizzled boxes begin on 1024 bytes");
-  // CTAs of an SM (with 3 for tiles of 8 rows, 64 decode steps of 1 to 4096 tokens in 8 bits took
-  // the same 56 us: the memory system, not the warps' latencies, bounds such a batch)
+  // CTAs of an SM (3 for tiles of 8 rows, which registers and shared memory would allow, measured the same)
   static constexpr int kCtas = kStage > 9000 ? 1 : 2;
   // a warp's shared memory: the ring, query fragments (tiles of 8 rows keep theirs in
   // registers), what the rows see, the parents, the tiles ahead, the exponents, barriers

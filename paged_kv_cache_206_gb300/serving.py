@@ -351,7 +351,8 @@ class TreeStep:
     """Attention of drafted tokens (a tree, a chain, or one token per sequence)
     over a paged cache (pa_tree_forward). Holds the configuration and a
     workspace; a step's launches do not depend on the lengths, so :meth:`run`
-    may be captured in a CUDA graph. ``key_exps`` and ``value_exps`` select the
+    may be captured in a CUDA graph. Steps that overlap on the GPU need a TreeStep
+    each; keep it until its work is done. ``key_exps`` and ``value_exps`` select the
     8-bit cache of :class:`QuantCache`, None the fp16 one."""
 
     def __init__(self, key, value, key_exps=None, value_exps=None, *, batch, num_heads,
@@ -371,6 +372,8 @@ class TreeStep:
                                mask_type=PA_MASK_NONE, num_sms=sms, scale=scale)
         self.workspace = torch.zeros(pa_tree_workspace(self.cfg), dtype=torch.uint8,
                                      device=self.device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()  # zeroed before any stream's step
         if _f16 is None:
             _start()
         self._at = key.get_device()

@@ -363,3 +363,72 @@ def test_long_contexts_again_and_again(torch, bits, drafts):
     for i in range(45):
         step, args, out = states[i % 3][:3]
         assert torch.equal(step.run(*args, out), first[i % 3]), i
+
+
+def speculation(torch, seed, bs=32, drafts=5):
+    """Inputs of a step: store the drafts into an 8-bit cache, then attend them."""
+    B, H, Hk, d = 6, 8, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    q = rng.integers(1, drafts + 1, B).astype(np.int32)
+    ctx = (q + rng.integers(1, 700, B)).astype(np.int32)
+    cols = int(-(-ctx.max() // bs))
+    T = int(q.sum())
+    cache = pa.QuantCache.empty(B * cols, bs, Hk, d)
+    old = [torch.randn((int(ctx.sum()), Hk, d), generator=g, device="cuda").half() for _ in range(2)]
+    tables = up(torch, np.arange(B * cols, dtype=np.int32).reshape(B, cols))
+    cache.write(*old, tables, up(torch, ctx), up(torch, ctx), int(ctx.max()))
+    x = torch.randn((T, H + 2 * Hk, d), generator=g, device="cuda").half()
+    cs = torch.randn((2048, d), generator=g, device="cuda")
+    step = pa.TreeStep(cache.key, cache.value, cache.key_exps, cache.value_exps, batch=B, num_heads=H,
+                       max_seqlen_q=drafts, max_blocks_per_seq=cols)
+    qr, out = (torch.empty((T, H, d), dtype=torch.float16, device="cuda") for _ in range(2))
+    lens, qlens, parents = up(torch, ctx), up(torch, q), up(torch, ref.trees(rng, q, "tree"))
+
+    def run(stream=None):
+        cache.store(x[:, :H], x[:, H:H + Hk], x[:, H + Hk:], None, None, cs, None, tables, lens, qlens,
+                    drafts, qr, stream=stream)
+        step.run(qr, tables, lens, qlens, parents, out, stream=stream)
+        return out
+    run.x = x
+    torch.cuda.synchronize()
+    return run
+
+
+def test_two_streams_at_once(torch):
+    """Two steps with a workspace each, at work side by side on streams of their own,
+    give what they give alone."""
+    runs = [speculation(torch, s) for s in (1, 2)]
+    alone = [r().clone() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(25):
+        for r, s in zip(runs, streams):
+            got = r(stream=s)
+    torch.cuda.synchronize()
+    for r, want in zip(runs, alone):
+        with torch.cuda.stream(streams[0]):
+            got = r()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_store_and_tree_captured_and_replayed(torch):
+    """A captured step replayed on other queries, keys and values, next to the same
+    step run eagerly."""
+    run, s = speculation(torch, 3), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run()
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = run()
+        for n in range(3):
+            run.x.copy_(torch.randn(run.x.shape, device="cuda").half())
+            g.replay()
+            s.synchronize()
+            got = out.clone()
+            out.fill_(0)
+            want = run().clone()
+            s.synchronize()
+            assert torch.equal(got, want) and bool(got.isfinite().all()), n

@@ -213,3 +213,29 @@ def test_binding_refuses_what_the_library_cannot_see():
                dict(q_out=q[:4]), dict(k_out=q), dict(key=k[:4]), dict(query=q[0])):
         refused(pa.pa_qk_norm_rope, **{**args, **kw})
     refused(pa.TreeStep, c.key, c.value, batch=5, num_heads=4, max_seqlen_q=1, max_blocks_per_seq=2)
+
+
+def test_tree_refuses_its_query_as_output_and_too_many_sms(lib):
+    def call(cfg, out):
+        return lib.pa_tree_forward(ctypes.byref(cfg), 1, FAKE, FAKE, OTHER, None, None, FAKE, FAKE, FAKE,
+                                   FAKE, FAKE, 1 << 30, out, None)
+    assert call(tree_cfg(), FAKE) == pa.PA_ERR_INVALID_ARG
+    assert call(tree_cfg(num_sms=65536), OTHER) == pa.PA_ERR_INVALID_ARG
+    need = ctypes.c_size_t()
+    assert lib.pa_tree_workspace(ctypes.byref(tree_cfg(num_sms=65535)), ctypes.byref(need)) == pa.PA_OK
+
+
+def test_tensors_off_the_gpu_are_refused():
+    f16 = torch.float16
+    cache = pa.QuantCache.empty(2, 16, 2, 64, device="cpu")
+    rows, ints = torch.zeros((1, 2, 64), dtype=f16), torch.ones(1, dtype=torch.int32)
+    table = torch.zeros((1, 1), dtype=torch.int32)
+    out = torch.zeros((1, 2, 64), dtype=f16)
+    for call in (lambda: cache.write(rows, rows, table, ints),
+                 lambda: cache.store(rows, rows, rows, None, None, None, None, table, ints, None, 1, out),
+                 lambda: cache.read(table, None, ints, torch.zeros_like(ints), 1, out, rows),
+                 lambda: pa.pa_qk_norm_rope(rows, rows, None, None, None, ints, out, torch.zeros_like(out)),
+                 lambda: pa.TreeStep(cache.key, cache.value, cache.key_exps, cache.value_exps, batch=1,
+                                     num_heads=2, max_seqlen_q=1, max_blocks_per_seq=1)):
+        with pytest.raises(pa.PaError, match="CUDA device"):
+            call()
