@@ -16,6 +16,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
+CALL = os.path.join(BUILD, "pa_call.so")  # the Python module of csrc/pa_call.c
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -55,6 +57,20 @@ def _stamp(cc: str) -> str:
     return hashlib.sha256(text.encode()).hexdigest()[:16]
 
 
+def _build_call(force: bool) -> None:
+    """The module through which serving.py calls the library (host code only)."""
+    src = os.path.join(CSRC, "pa_call.c")
+    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= os.path.getmtime(src):
+        return
+    tmp = CALL + f".tmp{os.getpid()}"
+    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-Wall", "-std=c11", "-shared", "-fPIC",
+                        f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on pa_call.c:\n{r.stderr}")
+    os.replace(tmp, CALL)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     """Compile what is stale and link; returns the library path."""
     os.makedirs(os.path.join(BUILD, "obj"), exist_ok=True)
@@ -63,6 +79,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     stamp = _stamp(cc)
     if not os.path.exists(stamp_path) or open(stamp_path).read().strip() != stamp:
         force = True  # objects (if any) from another machine, compiler or flag set
+    _build_call(force)
     hdr = _headers_mtime()
     objs, todo = [], []
     for src in sources():

@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
   int made = 0;                             // tiles left for the arithmetic so far
   if (lane == 0) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
     S.join[worker].parts = 0;  // no divided tile yet
     for (int k = 0; k < Cfg::kStages; ++k) mbar_init(&full[k], 1);
     fence_barrier_init();

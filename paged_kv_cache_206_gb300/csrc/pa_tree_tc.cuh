@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   const int worker = blockIdx.x;
 
   if (tid == 0) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
     for (int i = 0; i < Cfg::kLanded; ++i) mbar_init(&sfull[i], 1);
     for (int i = 0; i < Cfg::kStages; ++i) mbar_init(&sempty[i], Cfg::kConv);
     for (int i = 0; i < KS; ++i) {

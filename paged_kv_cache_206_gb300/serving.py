@@ -9,6 +9,7 @@ on the tensors' device, on ``stream`` or that device's current stream.
 from __future__ import annotations
 
 import ctypes
+import os
 
 from . import (PA_ERR_INVALID_ARG, PA_MASK_NONE, PaError, _check, load_library, make_config,
                pa_status_read)
@@ -33,21 +34,38 @@ class pa_cache_config(ctypes.Structure):
 # A call first puts one question to its arguments, whether all are in order: a decode
 # loop pays for that alone. Where the answer is no, the checks behind it say what is wrong.
 
-_f16 = _i32 = _f32 = _stream = _device = _lib = None
+_f16 = _i32 = _f32 = _stream = _device = _call = None
+_rope = _write = _store = _read = _tree = None  # addresses of the library's functions
 
 
 def _start():
-    """torch's types, the calls that tell the current stream and device, the library."""
-    global _f16, _i32, _f32, _stream, _device, _lib
+    """torch's types, the calls that tell the current stream and device, the library's
+    functions and what calls them."""
+    global _f16, _i32, _f32, _stream, _device, _call, _rope, _write, _store, _read, _tree
+    import importlib.util
+
     import torch
+
+    from .build_lib import CALL
     _i32, _f32 = torch.int32, torch.float32
     _stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _lib = load_library()
+    lib = load_library()
+    _rope, _write, _store, _read, _tree = (
+        ctypes.cast(f, ctypes.c_void_p).value
+        for f in (lib.pa_qk_norm_rope, lib.pa_cache_write, lib.pa_cache_store, lib.pa_cache_read,
+                  lib.pa_tree_forward))
+    if not os.path.exists(CALL):
+        raise RuntimeError(f"{CALL} is missing: run paged_kv_cache_206_gb300.build_lib.build()")
+    spec = importlib.util.spec_from_file_location("pa_call", CALL)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _call = module.call
     _f16 = torch.float16
 
 
 class _Configs(dict):
-    """Addresses of configurations by their values: making one takes as long as the launch."""
+    """Configurations, each with its address, by their values: making one takes as long as
+    the launch."""
 
     def __init__(self, kind):
         self.kind = kind
@@ -55,7 +73,8 @@ class _Configs(dict):
     def __missing__(self, values):
         if len(self) >= 4096:
             self.clear()
-        got = self[values] = ctypes.byref(self.kind(*values))
+        struct = self.kind(*values)
+        got = self[values] = ctypes.addressof(struct), struct
         return got
 
 
@@ -95,8 +114,8 @@ def _rows(where, name, t, dtype, device, tokens, heads, size):
     return st if tokens > 1 else heads * size
 
 
-def _launch(where, at, stream, call, *args):
-    """``call(*args, stream handle)`` with device ``at`` (the tensors') current."""
+def _launch(where, at, stream, function, *args):
+    """``function(*args, stream handle)`` with device ``at`` (the tensors') current."""
     if at < 0:
         _refuse(where, "tensors must be on a CUDA device")
     if stream is None:
@@ -106,11 +125,11 @@ def _launch(where, at, stream, call, *args):
     else:
         _refuse(where, f"the stream is on {stream.device}, the tensors on cuda:{at}")
     if _device() == at:
-        status = call(*args, handle)
+        status = _call(function, *args, handle)
     else:
         import torch
         with torch.cuda.device(at):
-            status = call(*args, handle)
+            status = _call(function, *args, handle)
     if status:
         _check(status, where)
 
@@ -189,9 +208,9 @@ def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k
         _dense(where, "k_out", k_out, _f16, dev, (tokens, kv_heads, size))
     if tokens == 0:
         return
-    _launch(where, at, stream, _lib.pa_qk_norm_rope,
-            _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved), tokens, query.data_ptr(),
-            qs, key.data_ptr(), ks, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+    _launch(where, at, stream, _rope,
+            _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved)[0], tokens,
+            query.data_ptr(), qs, key.data_ptr(), ks, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
             positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
             None if status is None else _status_arg(where, status, query.device))
 
@@ -278,8 +297,8 @@ class QuantCache:
             _batch_args(where, block_tables, context_lens, q_seqlens, self.device)
         if tokens == 0:
             return
-        _launch(where, at, stream, _lib.pa_cache_write,
-                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)],
+        _launch(where, at, stream, _write,
+                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)][0],
                 tokens, key.data_ptr(), ks, value.data_ptr(), vs, block_tables.data_ptr(),
                 context_lens.data_ptr(), _ptr(q_seqlens), *self._addresses,
                 None if status is None else _status_arg(where, status, self.device))
@@ -308,9 +327,9 @@ class QuantCache:
             _batch_args(where, block_tables, context_lens, q_seqlens, dev)
         if tokens == 0:
             return
-        _launch(where, at, stream, _lib.pa_cache_store,
-                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)],
-                _rot_config(qh, heads, hk, cos_sin, eps, interleaved), tokens, query.data_ptr(),
+        _launch(where, at, stream, _store,
+                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)][0],
+                _rot_config(qh, heads, hk, cos_sin, eps, interleaved)[0], tokens, query.data_ptr(),
                 qs, key.data_ptr(), ks, value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight),
                 _ptr(cos_sin), _ptr(positions), block_tables.data_ptr(), context_lens.data_ptr(),
                 _ptr(q_seqlens), *self._addresses, q_out.data_ptr(),
@@ -334,10 +353,11 @@ class QuantCache:
             _dense(where, "out_starts", out_starts, _i32, dev, context_lens.shape)
         if rows == 0:
             return
-        _launch(where, at, stream, _lib.pa_cache_read,
-                self._configs[(*block_tables.shape, max_rows)], *self._addresses, block_tables.data_ptr(),
-                _ptr(starts), context_lens.data_ptr(), out_starts.data_ptr(), rows, k_out.data_ptr(),
-                v_out.data_ptr(), None if status is None else _status_arg(where, status, self.device))
+        _launch(where, at, stream, _read,
+                self._configs[(*block_tables.shape, max_rows)][0], *self._addresses,
+                block_tables.data_ptr(), _ptr(starts), context_lens.data_ptr(), out_starts.data_ptr(),
+                rows, k_out.data_ptr(), v_out.data_ptr(),
+                None if status is None else _status_arg(where, status, self.device))
 
 
 def pa_tree_workspace(cfg) -> int:
@@ -379,7 +399,7 @@ class TreeStep:
         self._at = key.get_device()
         self._shapes = (num_heads, hk), (num_heads, value.shape[3]), (batch, max_blocks_per_seq)
         self._caches = tuple(_ptr(t) for t in (key, value, key_exps, value_exps))
-        self._space = ctypes.byref(self.cfg), self.workspace.data_ptr(), self.workspace.numel()
+        self._space = ctypes.addressof(self.cfg), self.workspace.data_ptr(), self.workspace.numel()
 
     def run(self, query, block_tables, context_lens, q_seqlens, parents, out, stream=None):
         """Attend ``query`` [T, H, hk] into ``out`` [T, H, hv]; ``parents`` int32 [T]
@@ -399,7 +419,7 @@ class TreeStep:
                 _dense(where, "parents", parents, _i32, dev, (tokens,))
         if tokens == 0:
             return out
-        _launch(where, at, stream, _lib.pa_tree_forward, cfg, tokens,
+        _launch(where, at, stream, _tree, cfg, tokens,
                 query.data_ptr(), *self._caches, block_tables.data_ptr(), context_lens.data_ptr(),
                 _ptr(q_seqlens), _ptr(parents), space, size, out.data_ptr())
         return out
