@@ -358,8 +358,7 @@ pa_status pa_status_clear(void* workspace, void* stream);
 
 /* Wait for stream, read the status word into *bits (may be NULL) and map it to
  * PA_OK, PA_ERR_TIMEOUT, PA_ERR_BLOCK_INDEX, PA_ERR_BUFFER_TOO_SMALL or
- * PA_ERR_INVALID_ARG (PA_STATUS_BIT_PLAN, and the bits of pa_cache.h and
- * pa_tree.h). */
+ * PA_ERR_INVALID_ARG (PA_STATUS_BIT_PLAN). */
 pa_status pa_status_read(const void* workspace, void* stream, uint32_t* bits);
 
 /* Static description of a status code. */

@@ -22,7 +22,8 @@
  * Conventions are those of pa.h: every function returns a pa_status, is
  * asynchronous on the caller's stream, allocates nothing, and returns host-side
  * errors before anything is enqueued. `status` is a device uint32 or NULL; the
- * kernels only OR bits into it (pa_status_read takes its address):
+ * kernels only OR bits into it (pa_status_read takes its address; it returns
+ * PA_ERR_INVALID_ARG for the PLAN and POSITION bits):
  *   PA_STATUS_BIT_BLOCK_INDEX  a block table entry outside [0, num_blocks); the
  *                              tokens of that block are neither stored nor read
  *   PA_STATUS_BIT_PLAN         a length breaks a constraint; that sequence (or

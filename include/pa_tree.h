@@ -36,7 +36,8 @@ extern "C" {
 #endif
 
 /* A parent that is not -1 or an earlier token of its sequence: the token is
- * taken as a root and the bit is set in the status word. */
+ * taken as a root and the bit is set in the status word (pa_status_read returns
+ * PA_ERR_INVALID_ARG). */
 #define PA_STATUS_BIT_TREE 32u
 /* Most current tokens of a sequence when parents are given. */
 #define PA_TREE_MAX_TOKENS 256
