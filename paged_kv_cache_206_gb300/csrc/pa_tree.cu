@@ -1,5 +1,5 @@
 // Attention for drafted tokens over a paged cache (pa_tree.h): the C entry, the
-// choice of the kernel, and the kernel for any head sizes.
+// choice of the kernel, and the kernel for the largest heads.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -39,8 +39,11 @@ __device__ __forceinline__ void load8(const uint8_t* row, int d, float (&x)[8]) 
   }
 }
 
-// One CTA per (token, head); warp w takes the keys w, w + 4, ..., a lane holds
-// 8-dim chunks lane, lane + 32, ... of the row. Softmax and sums in fp32.
+// Heads of more than 256 dims. One CTA per (token, head); warp w takes the keys w, w + 4,
+// ..., a lane holds 8-dim chunks lane, lane + 32, ... of the row. Softmax and sums in fp32.
+// Bound by the latency of a key after another, and the heads of a group read the
+// same keys each: 2.4 ms for 64 decode steps of up to 4096 keys of 8 kv heads, whatever
+// their size.
 template <bool Q8>
 __global__ void __launch_bounds__(kAnyWarps * 32) tree_any_kernel(const TreeParams P) {
   __shared__ float o_s[kAnyWarps][PA_MAX_HEAD_SIZE];
@@ -152,28 +155,30 @@ pa_status check_tree(const pa_config* cfg) {
 }
 
 // The kernel for these head sizes and rows, if there is a faster one than
-// tree_any_kernel: for up to 16 rows of a kv head, and for 256 dims, the warp-level
-// tensor instructions with the narrower of their 8- and 16-row tiles that holds the
-// rows, or several of the wider; beyond that the tcgen05 tensor cores. Of 64 sequences
-// of up to 4096 keys, 8 kv heads of 128 dims, 16 rows take 59 us (8 bits) and 83 us
-// (fp16) here and 92 and 83 us there; one sequence of 1024 keys 16 us here, 23 and 17 us
-// there. With 32 rows the warp-level instructions took 121 and 132 us (25 and 26 us for
-// the one sequence), the others take 94 and 87 us (23 and 17 us).
+// tree_any_kernel: for up to 16 rows of a kv head the warp-level tensor instructions
+// with the narrower of their 8- and 16-row tiles that holds the rows, and the least
+// of 64, 128 and 256 dims that hold a head; for more rows of 64 or 128 dims the tcgen05
+// tensor cores, of other sizes several of the 16-row tiles. Of 64 sequences of up to
+// 4096 keys, 8 kv heads of 128 dims, 16 rows take 59 us (8 bits) and 83 us (fp16) here and
+// 92 and 83 us there; one sequence of 1024 keys 16 us here, 23 and 17 us there. With
+// 32 rows the warp-level instructions took 121 and 132 us (25 and 26 us for the one
+// sequence), the others take 94 and 87 us (23 and 17 us).
 bool tree_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws,
                 cudaStream_t stream, cudaError_t* e) {
-  if (c.head_size_k != c.head_size_v) return false;
+  const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;
   const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
   const int nt = rows <= 8 ? 1 : 2;
-  if (rows > 16 && (c.head_size_k == 64 || c.head_size_k == 128)) {
-    *e = tree_tc(P, c.head_size_k, q8, rows, c.num_sms, need, ws, stream);
-    return true;
-  }
-  switch (c.head_size_k) {
-    case 64: *e = tree_mma_64(P, q8, nt, c.num_sms, need, ws, stream); return true;
-    case 128: *e = tree_mma_128(P, q8, nt, c.num_sms, need, ws, stream); return true;
-    case 256: *e = tree_mma_256(P, q8, nt, c.num_sms, need, ws, stream); return true;
-  }
-  return false;
+  if (rows > 16 && c.head_size_k == c.head_size_v && (hd == 64 || hd == 128))
+    *e = tree_tc(P, hd, q8, rows, c.num_sms, need, ws, stream);
+  else if (hd <= 64)
+    *e = tree_mma_64(P, q8, nt, c.num_sms, need, ws, stream);
+  else if (hd <= 128)
+    *e = tree_mma_128(P, q8, nt, c.num_sms, need, ws, stream);
+  else if (hd <= 256)
+    *e = tree_mma_256(P, q8, nt, c.num_sms, need, ws, stream);
+  else
+    return false;
+  return true;
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

@@ -1,6 +1,7 @@
 // Tree attention on the warp-level tensor instructions, for up to 16 rows (a
-// group of heads times a few drafts) per tile and K and V heads of 64, 128 or 256
-// dims, over the fp16 or the 8-bit cache.
+// group of heads times a few drafts) per tile and K and V heads of up to 64, 128 or 256
+// dims (the copies fill what a head is short of that with zeros, which add nothing to
+// a score; such dims of the output are not written), over the fp16 or the 8-bit cache.
 //
 // A warp takes SUB keys at a time, with the keys on the M side of m16n8k16:
 //   S^T[16 keys x 8 rows] = K . Q^T        online softmax in base 2
@@ -228,9 +229,13 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (!go[m]) continue;
-        const int row = blk[m] * bs + in_blk[m], part = cut_kvh * (RB > 128 ? RB / 128 : 1);
-        tma_load_3d(dst + m * 16 * RB, &tmk, &full[to], 0, row, part, pol);
-        tma_load_3d(dst + Cfg::kV + m * 16 * RB, &tmv, &full[to], 0, row, part, pol);
+        const int row = blk[m] * bs + in_blk[m];
+#pragma unroll
+        for (int part = 0; part < (RB + 127) / 128; ++part) {
+          uint8_t* at = dst + part * SUB * 128 + m * 16 * RPB;
+          tma_load_3d(at, &tmk, &full[to], part * 128, cut_kvh, row, pol);
+          tma_load_3d(at + Cfg::kV, &tmv, &full[to], part * 128, cut_kvh, row, pol);
+        }
         if constexpr (Q8) {
           const int64_t e = (int64_t(blk[m]) * P.kv_heads + cut_kvh) * bs + in_blk[m];
           bulk_load(exps_s + to * 64 + m * 16, P.key_exps + e, box, &full[to]);
@@ -260,12 +265,13 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       const int r = t.r0 + nt * 8 + g, i = r / G;
       const int64_t tok = int64_t(t.q_start) + i;
       const bool in = i < t.q && tok < P.tokens;
-      const __half* src = P.query + (in ? (tok * P.num_heads + t.kvh * G + r % G) * HD : 0);
+      const __half* src = P.query + (in ? (tok * P.num_heads + t.kvh * G + r % G) * P.hk : 0);
 #pragma unroll
       for (int ks = 0; ks < OT; ++ks) {
         const int s = ks / (E / 4), j = ks % (E / 4);
         const int ch = C >= 8 ? 2 * c + (s & 1) + 8 * (s >> 1) : c;
-        const uint2 v = in ? *reinterpret_cast<const uint2*>(src + ch * E + 4 * j) : make_uint2(0, 0);
+        const bool some = in && ch * E + 4 * j < P.hk;
+          const uint2 v = some ? *reinterpret_cast<const uint2*>(src + ch * E + 4 * j) : make_uint2(0, 0);
         if constexpr (NT == 1) qf[ks] = v;
         else *reinterpret_cast<uint2*>(q_s + ((nt * OT + ks) * 32 + lane) * 8) = v;
       }
@@ -566,14 +572,14 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
         if (i >= t.q || tok >= P.tokens) continue;
         if (t.slot < 0) {
           const float inv = 1.f / l_run[nt][e];
-          __half* dst = P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD;
+          __half* dst = P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv;
 #pragma unroll
           for (int k0 = 0; k0 < OT; k0 += 4) {
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[k] = pack_half2(o[k0 + k][nt][e] * inv, o[k0 + k][nt][2 + e] * inv);
-            *reinterpret_cast<uint4*>(dst + (g + 8 * (k0 / KR)) * RUN + k0 % KR * 2) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+            const int d = (g + 8 * (k0 / KR)) * RUN + k0 % KR * 2;
+            if (d < P.hv) *reinterpret_cast<uint4*>(dst + d) = make_uint4(h[0], h[1], h[2], h[3]);
           }
         } else {
           const int64_t at = int64_t(t.slot) * NR + row;
@@ -595,8 +601,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           if (i >= t.q || tok >= P.tokens) continue;
           tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, i, bad_s, P.parents ? mask_s + row * kTreeWords : nullptr,
                          t.s0 * SUB, t.s1 * SUB,
-                         t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr,
-                         S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD, 1, lane, 32, HD);
+                         t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv : nullptr,
+                         S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD, 1, lane, 32, P.hv);
         }
         __syncwarp();
       }

@@ -1,4 +1,4 @@
-// The warp-level tree attention kernels for heads of 128 dims (pa_tree_mma.cuh).
+// The warp-level tree attention kernels for heads of up to 128 dims (pa_tree_mma.cuh).
 #include "pa_tree_mma_launch.cuh"
 
 namespace pa {

@@ -7,16 +7,15 @@
 
 namespace pa {
 
-// A cache as (bytes of a 128-byte part of a row, or of a row of 64; token rows; parts of all kv
-// heads), a box being `box` tokens of one head, whole rows, swizzled.
-inline bool tree_rows_map(CUtensorMap* m, const void* base, const TreeParams& P, int row_bytes, int box) {
+// A cache as (bytes of a row, kv heads, token rows), a box being up to 128 bytes of
+// `box` tokens of one head, swizzled, zeros behind a row's end.
+inline bool tree_rows_map(CUtensorMap* m, const void* base, const TreeParams& P, int row_bytes, int part, int box) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
-  const int part = row_bytes < 128 ? row_bytes : 128, parts = row_bytes / part;
-  const cuuint64_t dims[3] = {cuuint64_t(part), cuuint64_t(P.num_blocks) * P.block_size,
-                              cuuint64_t(P.kv_heads) * parts};
-  const cuuint64_t strides[2] = {cuuint64_t(P.kv_heads) * row_bytes, cuuint64_t(part)};
-  const cuuint32_t b[3] = {cuuint32_t(part), cuuint32_t(box), cuuint32_t(parts)}, es[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {cuuint64_t(row_bytes), cuuint64_t(P.kv_heads),
+                              cuuint64_t(P.num_blocks) * P.block_size};
+  const cuuint64_t strides[2] = {cuuint64_t(row_bytes), cuuint64_t(P.kv_heads) * row_bytes};
+  const cuuint32_t b[3] = {cuuint32_t(part), 1, cuuint32_t(box)}, es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, b, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, part == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -45,8 +44,9 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   if (e != cudaSuccess) return e;
   const int low = P.block_size & -P.block_size, box = low < Cfg::kSub ? low : Cfg::kSub;
   CUtensorMap tmk, tmv;
-  if (!tree_rows_map(&tmk, P.key_cache, P, Cfg::kRowBytes, box) ||
-      !tree_rows_map(&tmv, P.value_cache, P, Cfg::kRowBytes, box))
+  const int part = Cfg::kRowBytes < 128 ? Cfg::kRowBytes : 128, elem = Q8 ? 1 : 2;
+  if (!tree_rows_map(&tmk, P.key_cache, P, P.hk * elem, part, box) ||
+      !tree_rows_map(&tmv, P.value_cache, P, P.hv * elem, part, box))
     return cudaErrorInvalidValue;
   kern<<<unsigned(grid), Cfg::kWarps * 32, Cfg::bytes, stream>>>(tmk, tmv, P, S, box);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

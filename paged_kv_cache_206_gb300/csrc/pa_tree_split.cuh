@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams P, c
         for (int d = 0; d < DPL; ++d) acc[d] = fmaf(wk, x[k][d], acc[d]);
     }
   }
+  if (lane * DPL >= P.hv) return;
   __half2* dst = reinterpret_cast<__half2*>(
-      P.out + (tok * P.num_heads + t.kvh * P.group + r % P.group) * HD + lane * DPL);
+      P.out + (tok * P.num_heads + t.kvh * P.group + r % P.group) * P.hv + lane * DPL);
   const float inv = 1.f / sum;
 #pragma unroll
   for (int d = 0; d < DPL; d += 2) dst[d / 2] = __floats2half2_rn(acc[d] * inv, acc[d + 1] * inv);

@@ -432,3 +432,17 @@ def test_store_and_tree_captured_and_replayed(torch):
             want = run().clone()
             s.synchronize()
             assert torch.equal(got, want) and bool(got.isfinite().all()), n
+
+
+@pytest.mark.parametrize("sizes", [(16, 16), (32, 48), (80, 80), (96, 96), (112, 64), (64, 112), (144, 144),
+                                   (192, 128), (240, 256), (272, 256)], ids=str)
+@pytest.mark.parametrize("bits", [8, 16])
+def test_head_sizes_between_the_tiles(torch, bits, sizes):
+    """Heads that fill no tile's dims, unlike ones, in tiles of 8 and 16 rows and several of them;
+    what lies next to a head's row (its neighbours' rows and NaN) does not reach it."""
+    for q, ctx, H, Hk, bs in (([1, 1, 1], [1, 33, 700], 8, 2, 16), ([5, 0, 3], [90, 40, 1300], 6, 3, 48),
+                              ([13], [777], 12, 3, 128)):
+        c = Case(torch, bits, q, ctx, H, Hk, *sizes, bs, "tree", behind=1)
+        c.run()
+        c.check()
+        assert c.step.status() == (pa.PA_OK, 0)
