@@ -95,8 +95,16 @@ __device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int
 // part, and p and p + dims / 16 of a row that is not rotated at all. What a row
 // is multiplied by but its own norm is the same for all rows of the warp: weight
 // times cosine and weight times sine, made once.
+//
+// Bytes bound these rows, and come close: 8192 tokens of 32 + 8 heads of 128 are turned in
+// 32.5 us (25.3 at the copy rate; issue slots 66 % full), and 2 x 32 heads of as many
+// written to 8 bits in 37 (29.6; conversions and maxima keep the ALU 64 % busy). The store
+// of 8 prompts of 1 to 2048 tokens, 48 heads, takes 47 us for 24 us of bytes: it makes
+// the factors, looks the token up and quantises. Registers are held to what lets 32 (store:
+// 24, write: 40) warps an SM have loads in flight; a warp that loaded the next token's
+// rows ahead at half the warps was slower (39 us for the 8192 tokens).
 template <int MODE, int VPL, int U, bool IL>
-__global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : 4) : 1)
+__global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : MODE == kStore ? 3 : 4) : 1)
 rows_kernel(const RowParams P) {
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << P.lane_shift, per_warp = 32 >> P.lane_shift;
@@ -250,7 +258,9 @@ rows_kernel(const RowParams P) {
             }
           }
         if (weight) {
-          for (int o = lanes >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+          #pragma unroll
+          for (int o = 16; o; o >>= 1)
+            if (o < lanes) sq += __shfl_xor_sync(0xffffffffu, sq, o);
           inv = rsqrtf(sq * P.inv_hk + P.eps);
         }
 #pragma unroll
@@ -261,8 +271,12 @@ rows_kernel(const RowParams P) {
             float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
             const float a = fa * inv, b = fb * inv;
             // a sine of 0 is no reason to take in the other element's infinity
-            fa = turn[v] ? a * ca[v][m] - b * sb[v][m] : a * ca[v][m];
-            fb = turn[v] ? b * cb[v][m] + a * sa[v][m] : b * cb[v][m];
+            fa = a * ca[v][m];
+            fb = b * cb[v][m];
+            if (turn[v]) {
+              fa -= b * sb[v][m];
+              fb += a * sa[v][m];
+            }
           }
         if (MODE == kRotate || is_q) {  // fp16 rows
 #pragma unroll
@@ -447,8 +461,10 @@ __device__ __forceinline__ uint4 widen(const uint2& codes, int byte) {
 // One warp per (strip of tokens of a sequence, 1 KB of their keys or of
 // their values): a token's heads are contiguous in the cache and in the output.
 // Lane l finds token l's place, so that a strip waits for one table lookup. A
-// lane reads 8 codes and writes 16 bytes,
-// neighbouring lanes neighbouring ones.
+// lane reads 8 codes and writes 16 bytes, neighbouring lanes neighbouring ones.
+// 32 sequences of 64 to 8192 tokens, 8 + 8 heads of 128, come back in 146 us, 6.1 TB/s of
+// reads and writes (90 % of a copy), with a token at a time and 40 warps an SM; with
+// four tokens at a time and 16 warps it took 190.
 __global__ void __launch_bounds__(256, 5) read_kernel(const ReadParams P) {
   constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 31;

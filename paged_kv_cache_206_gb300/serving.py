@@ -264,11 +264,13 @@ class QuantCache:
         if _f16 is None:
             _start()
         self.device, self._at = key.device, key.get_device()
-        self._blocks, self._block_size, self._heads, self._hk = key.shape
-        self._hv = value.shape[3]
+        nb, bs, heads, hk = key.shape
+        hv = value.shape[3]
+        self._heads, self._hk, self._hv = heads, hk, hv
         self._addresses = tuple(t.data_ptr() for t in (key, key_exps, value, value_exps))
+        # (no reference to self: the caches are freed as soon as the last name of them is)
         self._configs = _Configs(lambda batch, cols, max_rows: pa_cache_config(
-            batch, self._heads, self._hk, self._hv, self._block_size, self._blocks, cols, max_rows))
+            batch, heads, hk, hv, bs, nb, cols, max_rows))
 
     @classmethod
     def empty(cls, num_blocks, block_size, kv_heads, head_size_k, head_size_v=None, device="cuda"):

@@ -239,3 +239,12 @@ def test_tensors_off_the_gpu_are_refused():
                                      num_heads=2, max_seqlen_q=1, max_blocks_per_seq=1)):
         with pytest.raises(pa.PaError, match="CUDA device"):
             call()
+
+
+def test_a_cache_is_freed_with_its_last_name():
+    import weakref
+    cache = pa.QuantCache.empty(2, 16, 2, 64, device="cpu")
+    cache._configs[1, 1, 1]
+    codes = weakref.ref(cache.key)
+    del cache
+    assert codes() is None
