@@ -48,9 +48,10 @@ struct TreeTc {
   static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : 384;
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
-  // what a row tile costs next to its key tiles: measured least at 3 for the fp16 cache (trees of
-  // 64: 75 us; 80 at 1, 77 at 5) and at 8 for the 8-bit one (trees of 16: 94; 104 at 3, 95 at 5)
-  static constexpr int kLead = Q8 ? 8 : 3;
+  // What a row tile costs next to its key tiles, in these, measured at 32 trees over 64 to 8192
+  // keys, heads of 128: trees of 16 in 8 bits 90 us at 3, 83 at 5, 85 at 8, 88 at 12; of 64 in fp16
+  // 129, 128, 129 and 132 (and 16 of those 75, 77 and 80).
+  static constexpr int kLead = Q8 ? 6 : 4;
   static constexpr int kHalves = HD / 64;
   static constexpr uint32_t kHalf = 128 * 128;           // 64 dims of 128 fp16 rows
   static constexpr uint32_t kTile = kHalf * kHalves;     // a K or V tile, a query tile
