@@ -56,19 +56,23 @@ struct TreeTc {
   static constexpr uint32_t kHalf = 128 * 128;           // 64 dims of 128 fp16 rows
   static constexpr uint32_t kTile = kHalf * kHalves;     // a K or V tile, a query tile
   static constexpr int kKSlots = Q8 || QT == 2 ? 2 : 3;
-  static constexpr int kVSlots = Q8 && QT == 2 ? 1 : 2;
+  static constexpr int kVSlots = Q8 ? 1 : 2;
   static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
-  static constexpr int kKStages = Q8 ? 4 : 0, kVStages = Q8 ? 3 : 0, kStages = kKStages + kVStages;
-  // Barriers of the parts that have landed: one for each part (rows 0.., rows 64..) of the even
-  // and of the odd key tiles, of K and of V, whatever stage a part is in. A barrier per stage would
-  // do for four stages; with three a stage serves the two parts' warps in turn, and a warp
-  // that asked for its turn while the other's copy was still in flight took the phase before
-  // that one for its own (parts may land in either order).
-  static constexpr int kLanded = Q8 ? 8 : 0;
+  // Stages for the codes rather than a second V operand (trees of 16: 88.5 us, 92.3 with two V
+  // slots and 4 + 3 stages, 107 with one K slot and 7 + 8)
+  static constexpr int kKStages = Q8 ? (QT == 1 ? 5 : 4) : 0, kVStages = Q8 ? (QT == 1 ? 6 : 3) : 0;
+  static constexpr int kStages = kKStages + kVStages;
+  // Barriers of the parts that have landed: of each part (rows 0.., rows 64..) of as many key tiles
+  // as have parts in the ring, whatever stage a part is in. A barrier per stage would do for
+  // an even number of stages; with an odd one a stage serves the two parts' warps in turn, and a
+  // warp that asked for its turn while the other's copy was still in flight took the phase
+  // before that one for its own (parts may land in either order).
+  static constexpr int kKRounds = (kKStages + 1) / 2, kVRounds = (kVStages + 1) / 2;
+  static constexpr int kLanded = 2 * (kKRounds + kVRounds);
   // Key tiles whose exponents, and whose largest ones, are held; row tiles whose flags
   // are. A widening warp is at most three tiles ahead of the softmax (the K and V
   // rings' two, and one in registers), so a row tile or key tile eight on finds the place read.
-  static constexpr int kExps = 4, kMeta = 8, kBad = 8;
+  static constexpr int kExps = 8, kMeta = 8, kBad = 8;
   static constexpr int kAhead = 4;                       // row tiles told to the roles
   static constexpr int kRoles = Q8 ? 11 + 4 * kConv : 11;            // warps that are told
   static constexpr uint32_t q_off = 0;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint8_t* vring = smem + Cfg::v_off;
   int2* meta = reinterpret_cast<int2*>(smem + Cfg::meta_off);
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
-  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);  // [K, V][key tile parity][part]
+  uint64_t* sfull = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);  // [K, V][round][part]
   uint64_t* sempty = sfull + Cfg::kLanded;  // [stage]
   uint64_t* kfull = sempty + Cfg::kStages;
   uint64_t* kempty = kfull + KS;
@@ -325,12 +329,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const uint8_t* exps_of = is_k ? P.key_exps : P.value_exps;
     // the ring: stages of 64 keys (8-bit cache) or tiles
     const int nslots = Q8 ? (is_k ? Cfg::kKStages : Cfg::kVStages) : is_k ? KS : VS;
-    uint64_t* fulls = Q8 ? sfull + (is_k ? 0 : 4) : is_k ? kfull : vfull;
+    uint64_t* fulls = Q8 ? sfull + (is_k ? 0 : 2 * Cfg::kKRounds) : is_k ? kfull : vfull;
+    const int rounds = is_k ? Cfg::kKRounds : Cfg::kVRounds;
     uint64_t* empties = Q8 ? sempty + (is_k ? 0 : Cfg::kKStages) : is_k ? kempty : vempty;
     uint8_t* ring = Q8 ? smem + Cfg::stage_off + (is_k ? 0 : Cfg::kKStages) * Cfg::kStageBytes : is_k ? kring : vring;
     const int half = pieces / 2, part = lane >= half ? 1 : 0;
     int n = 0, filled = 0;     // key tiles, and stages or tiles filled, so far
     int slot = 0, phase = 0;   // of the next stage or tile
+    int round = 0;             // of the next key tile's barriers
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t);
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           uint8_t* dst = ring + (part ? slot1 : slot) * Cfg::kStageBytes + (lane - part * half) * box * HD;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            uint64_t* full = &fulls[2 * (n & 1) + p];
+            uint64_t* full = &fulls[2 * round + p];
             if (!tree_wait(&empties[p ? slot1 : slot], (p ? phase1 : phase) ^ 1)) {
               ok = false;
               break;
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
               const uint32_t bytes = __popc(valid >> (p * half) & ((1u << half) - 1)) * box * HD;
               if (bytes) mbar_arrive_expect_tx(full, bytes); else mbar_arrive(full);
             }
-            // (the exponents' slot was last read four tiles ago, before what was waited for)
+            // (the exponents' slot was last read kExps tiles ago, long before what was waited for)
             if (p == 0 && lane == 1) {
               const uint32_t bytes = __popc(valid) * box;
               if (bytes) mbar_arrive_expect_tx(efull, bytes); else mbar_arrive(efull);
@@ -380,6 +386,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             ++filled;
           }
           if (!ok) break;
+          if (++round == rounds) round = 0;
           slot = slot1 + 1 == nslots ? 0 : slot1 + 1;
           phase = slot == 0 ? phase1 ^ 1 : phase1;
         } else {
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       }
     }
     // copies still in flight land before the CTA's memory is given back
-    const int nfulls = Q8 ? 4 : nslots;
+    const int nfulls = Q8 ? 2 * rounds : nslots;
     for (int i = 0; i < nfulls; ++i) {
       const int times = filled / nfulls + (i < filled % nfulls ? 1 : 0);
       if (times) tree_wait(&fulls[i], (times - 1) & 1);
@@ -792,21 +799,22 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int ch = lane % CH, row0 = (part & 1) * 64 + sub * ROWS + lane / CH;  // this lane's first row
     uint64_t* full = kv ? vfull : kfull;
     uint64_t* empty = kv ? vempty : kempty;
-    uint64_t* landed = sfull + (kv ? 4 : 0) + (part & 1);  // [2 * key tile parity]
+    uint64_t* landed = sfull + (kv ? 2 * Cfg::kKRounds : 0) + (part & 1);  // [2 * round]
+    const int rounds = kv ? Cfg::kVRounds : Cfg::kKRounds;
     uint64_t* taken = sempty + (kv ? Cfg::kKStages : 0);
     uint8_t* stage = smem + Cfg::stage_off + (kv ? Cfg::kKStages : 0) * Cfg::kStageBytes + sub * ROWS * HD + lane * 8;
     // this lane's places in the operand: the 64-dim half ch / 8 of row0, row0 + RPI, ...
     uint8_t* operand = (kv ? vring : kring) + (ch >> 3) * Cfg::kHalf + row0 * 128;
     // (rings of this warp's tile: slots and phases counted, as a remainder takes long)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
-    int slot = 0, phase = 0, st = part & 1, done = 0, em = 0, ephase = 0, mm = 0, tile = 0;
+    int slot = 0, phase = 0, st = part & 1, round = 0, lphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
     TreeTile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       for (int i = 0; i < tiles; ++i) {
         const int key0 = (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
-        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[2 * (done & 1)], done >> 1 & 1)) {
+        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[2 * round], lphase)) {
           ok = false;
           break;
         }
@@ -893,7 +901,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           phase ^= 1;
         }
         if ((st += 2) >= nst) st -= nst;
-        ++done;
+        if (++round == rounds) {
+          round = 0;
+          lphase ^= 1;
+        }
         if (++em == Cfg::kExps) {
           em = 0;
           ephase ^= 1;
