@@ -183,6 +183,11 @@ rows_kernel(const RowParams P) {
   // ---- the factors. Pair m of chunk pair v: elements m of both chunks, or
   // (interleaved) 2m and 2m + 1 of the 16; ca, cb: the cosine times the weight
   // of its first and second, sa, sb: the sine.
+  // Keys on their way to 8 bits are rounded coarsely, and an error in the last place of fp32 that
+  // moves one over a border costs a whole step; so they are made closer: an element times
+  // its weight is exact in fp32 (11 bits times 11), the sum of two products is taken with the
+  // error of one of them (Kahan), and ca, cb are the weights, sa, sb cosine and sine.
+  const bool exact = MODE == kStore && !is_q;
   const auto chunk_of = [](int m, int second) { return IL ? m / 4 : second; };
   const auto elem_of = [](int m, int second) { return IL ? 2 * (m % 4) + second : m; };
   float ca[VPL][8], cb[VPL][8], sa[VPL][8], sb[VPL][8];
@@ -218,10 +223,10 @@ rows_kernel(const RowParams P) {
         for (int j = 0; j < 4; ++j) {
           const int m = 4 * c + j;
           const float wa = w[chunk_of(m, 0)][elem_of(m, 0)], wb = w[chunk_of(m, 1)][elem_of(m, 1)];
-          ca[v][m] = wa * cc[j];
-          cb[v][m] = wb * cc[j];
-          sa[v][m] = wa * ss[j];
-          sb[v][m] = wb * ss[j];
+          ca[v][m] = exact ? wa : wa * cc[j];
+          cb[v][m] = exact ? wb : wb * cc[j];
+          sa[v][m] = exact ? cc[j] : wa * ss[j];
+          sb[v][m] = exact ? ss[j] : wb * ss[j];
         }
       }
     }
@@ -261,7 +266,12 @@ rows_kernel(const RowParams P) {
           #pragma unroll
           for (int o = 16; o; o >>= 1)
             if (o < lanes) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-          inv = rsqrtf(sq * P.inv_hk + P.eps);
+          // one step of Newton's method takes rsqrtf's two units of error to one (a row with an
+          // infinity has inv = 0, where the step's residual is NaN)
+          const float mean = sq * P.inv_hk + P.eps;
+          inv = rsqrtf(mean);
+          const float rest = fmaf(-mean * inv, inv, 1.f);
+          if (rest == rest) inv = fmaf(0.5f * inv, rest, inv);
         }
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
@@ -269,6 +279,19 @@ rows_kernel(const RowParams P) {
           for (int m = 0; m < 8; ++m) {
             float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
             float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
+            if (exact) {
+              const float a = fa * ca[v][m], b = fb * cb[v][m];
+              fa = a;
+              fb = b;
+              if (turn[v]) {
+                const float bs = b * sb[v][m], as = a * sb[v][m];
+                fa = fmaf(a, sa[v][m], -bs) + fmaf(-b, sb[v][m], bs);
+                fb = fmaf(b, sa[v][m], as) + fmaf(a, sb[v][m], -as);
+              }
+              fa *= inv;
+              fb *= inv;
+              continue;
+            }
             const float a = fa * inv, b = fb * inv;
             // a sine of 0 is no reason to take in the other element's infinity
             fa = a * ca[v][m];
