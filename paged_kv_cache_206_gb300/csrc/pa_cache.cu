@@ -100,11 +100,11 @@ __device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int
 // 32.5 us (25.3 at the copy rate; issue slots 66 % full), and 2 x 32 heads of as many
 // written to 8 bits in 37 (29.6; conversions and maxima keep the ALU 64 % busy). The store
 // of 8 prompts of 1 to 2048 tokens, 48 heads, takes 47 us for 24 us of bytes: it makes
-// the factors, looks the token up and quantises. Registers are held to what lets 32 (store:
-// 24, write: 40) warps an SM have loads in flight; a warp that loaded the next token's
-// rows ahead at half the warps was slower (39 us for the 8192 tokens).
+// the factors, looks the token up and quantises. Registers are held to what lets 32 warps an
+// SM (40 in the write) have loads in flight; a warp that loaded the next token's rows
+// ahead, at half the warps, was slower (39 us for the 8192 tokens).
 template <int MODE, int VPL, int U, bool IL>
-__global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : MODE == kStore ? 3 : 4) : 1)
+__global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : 4) : 1)
 rows_kernel(const RowParams P) {
   const int lane = threadIdx.x & 31;
   const int lanes = 1 << P.lane_shift, per_warp = 32 >> P.lane_shift;
@@ -273,13 +273,13 @@ rows_kernel(const RowParams P) {
           const float rest = fmaf(-mean * inv, inv, 1.f);
           if (rest == rest) inv = fmaf(0.5f * inv, rest, inv);
         }
+        if (exact) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
+          for (int v = 0; v < VPL; ++v)
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
-            float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
-            if (exact) {
+            for (int m = 0; m < 8; ++m) {
+              float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
+              float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
               const float a = fa * ca[v][m], b = fb * cb[v][m];
               fa = a;
               fb = b;
@@ -290,17 +290,24 @@ rows_kernel(const RowParams P) {
               }
               fa *= inv;
               fb *= inv;
-              continue;
             }
-            const float a = fa * inv, b = fb * inv;
-            // a sine of 0 is no reason to take in the other element's infinity
-            fa = a * ca[v][m];
-            fb = b * cb[v][m];
-            if (turn[v]) {
-              fa -= b * sb[v][m];
-              fb += a * sa[v][m];
+        } else {
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              float& fa = y[v][chunk_of(m, 0)][elem_of(m, 0)];
+              float& fb = y[v][chunk_of(m, 1)][elem_of(m, 1)];
+              const float a = fa * inv, b = fb * inv;
+              // a sine of 0 is no reason to take in the other element's infinity
+              fa = a * ca[v][m];
+              fb = b * cb[v][m];
+              if (turn[v]) {
+                fa -= b * sb[v][m];
+                fb += a * sa[v][m];
+              }
             }
-          }
+        }
         if (MODE == kRotate || is_q) {  // fp16 rows
 #pragma unroll
           for (int v = 0; v < VPL; ++v)
