@@ -65,7 +65,8 @@ def _start():
 
 class _Configs(dict):
     """Configurations, each with its address, by their values: making one takes as long as
-    the launch."""
+    the launch. A call keeps the pair by a name of its own until it returns: another thread
+    may clear the dictionary meanwhile, and the address alone keeps nothing alive."""
 
     def __init__(self, kind):
         self.kind = kind
@@ -208,8 +209,8 @@ def pa_qk_norm_rope(query, key, q_weight, k_weight, cos_sin, positions, q_out, k
         _dense(where, "k_out", k_out, _f16, dev, (tokens, kv_heads, size))
     if tokens == 0:
         return
-    _launch(where, at, stream, _rope,
-            _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved)[0], tokens,
+    rotation = _rot_config(heads, kv_heads, size, cos_sin, eps, interleaved)
+    _launch(where, at, stream, _rope, rotation[0], tokens,
             query.data_ptr(), qs, key.data_ptr(), ks, _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
             positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
             None if status is None else _status_arg(where, status, query.device))
@@ -299,8 +300,8 @@ class QuantCache:
             _batch_args(where, block_tables, context_lens, q_seqlens, self.device)
         if tokens == 0:
             return
-        _launch(where, at, stream, _write,
-                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)][0],
+        config = self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)]
+        _launch(where, at, stream, _write, config[0],
                 tokens, key.data_ptr(), ks, value.data_ptr(), vs, block_tables.data_ptr(),
                 context_lens.data_ptr(), _ptr(q_seqlens), *self._addresses,
                 None if status is None else _status_arg(where, status, self.device))
@@ -329,9 +330,9 @@ class QuantCache:
             _batch_args(where, block_tables, context_lens, q_seqlens, dev)
         if tokens == 0:
             return
-        _launch(where, at, stream, _store,
-                self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)][0],
-                _rot_config(qh, heads, hk, cos_sin, eps, interleaved)[0], tokens, query.data_ptr(),
+        config = self._configs[(*block_tables.shape, tokens if max_seqlen_q is None else max_seqlen_q)]
+        rotation = _rot_config(qh, heads, hk, cos_sin, eps, interleaved)
+        _launch(where, at, stream, _store, config[0], rotation[0], tokens, query.data_ptr(),
                 qs, key.data_ptr(), ks, value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight),
                 _ptr(cos_sin), _ptr(positions), block_tables.data_ptr(), context_lens.data_ptr(),
                 _ptr(q_seqlens), *self._addresses, q_out.data_ptr(),
@@ -355,8 +356,8 @@ class QuantCache:
             _dense(where, "out_starts", out_starts, _i32, dev, context_lens.shape)
         if rows == 0:
             return
-        _launch(where, at, stream, _read,
-                self._configs[(*block_tables.shape, max_rows)][0], *self._addresses,
+        config = self._configs[(*block_tables.shape, max_rows)]
+        _launch(where, at, stream, _read, config[0], *self._addresses,
                 block_tables.data_ptr(), _ptr(starts), context_lens.data_ptr(), out_starts.data_ptr(),
                 rows, k_out.data_ptr(), v_out.data_ptr(),
                 None if status is None else _status_arg(where, status, self.device))

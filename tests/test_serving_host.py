@@ -248,3 +248,37 @@ def test_a_cache_is_freed_with_its_last_name():
     codes = weakref.ref(cache.key)
     del cache
     assert codes() is None
+
+
+@pytest.mark.parametrize("call", ["rotate", "write", "store", "read"])
+def test_a_configuration_lives_as_long_as_its_call(monkeypatch, call):
+    """While the C side has a configuration's address, another thread's new
+    configurations may clear the dictionary that holds it."""
+    import weakref
+
+    from paged_kv_cache_206_gb300 import serving
+    cache = pa.QuantCache.empty(2, 16, 2, 64, device="cpu")
+    rows, ints = torch.zeros((1, 2, 64), dtype=torch.float16), torch.ones(1, dtype=torch.int32)
+    table, out = torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2, 64), dtype=torch.float16)
+    serving._rotations.clear()
+    calls = []
+
+    def launch(where, at, stream, function, *args):
+        held = [c for d in (cache._configs, serving._rotations) for c in d.values()]
+        used = [weakref.ref(c) for a, c in held if a in args]
+        del held
+        cache._configs.clear()
+        serving._rotations.clear()
+        calls.append(len(used))
+        assert all(c() is not None for c in used)
+
+    monkeypatch.setattr(serving, "_launch", launch)
+    if call == "rotate":
+        pa.pa_qk_norm_rope(rows, rows, None, None, None, ints, out, out.clone())
+    elif call == "write":
+        cache.write(rows, rows, table, ints)
+    elif call == "store":
+        cache.store(rows, rows, rows, None, None, None, None, table, ints, None, 1, out)
+    else:
+        cache.read(table, None, ints, torch.zeros_like(ints), 1, out, rows)
+    assert calls == [2 if call == "store" else 1]
