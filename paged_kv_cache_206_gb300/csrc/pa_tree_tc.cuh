@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             }
             if (hit) *p = x;
           }
+          fence_proxy_async();  // before the stage's next copy, which may begin once it is given back
           __syncwarp();
         }
         // all of the part into registers, so that its stage is free for the next copy

@@ -446,3 +446,40 @@ def test_head_sizes_between_the_tiles(torch, bits, sizes):
         c.run()
         c.check()
         assert c.step.status() == (pa.PA_OK, 0)
+
+
+@pytest.mark.parametrize("drafts,lo,hi", [(16, 0, 300), (5, 0, 40), (64, 100, 700)])
+def test_many_ends_of_contexts_in_turn(torch, drafts, lo, hi):
+    """Hundreds of short contexts, so that a stage whose rows behind the context were cleared (they
+    hold NaN, and some drafts' values do) is filled again at once: every run gives the same bits, and
+    the rows of every tenth sequence that see no NaN are attention in 64 bits."""
+    rng = np.random.default_rng(drafts)
+    B = 200
+    q = rng.integers(max(1, drafts // 2), drafts + 1, B)
+    ctx = q + rng.integers(lo, hi, B)
+    nan = []
+
+    def poison(case, x):
+        if len(case.real) == 0:
+            return
+        for b in range(0, B, 3):
+            i = int(q[b]) - 1  # the last draft, which none but itself sees
+            blk, off = case.batch.slots(b, int(ctx[b]) - 1, int(ctx[b]))
+            x[blk[0], off[0], :, 5] = np.nan
+            nan.append(int(case.batch.starts[b]) + i)
+
+    c = Case(torch, 8, q, ctx, 32, 2, 128, 128, 16, "tree", poison=poison)
+    c.run()
+    first = c.out.clone()
+    assert c.step.status() == (pa.PA_OK, 0)
+    for _ in range(20):
+        assert torch.equal(c.run().view(torch.int16), first.view(torch.int16))
+    got = c.out.cpu().numpy()
+    assert np.isnan(got[nan][:, :, 5]).all()
+    some = ref.Batch(c.batch.tables[::10], c.batch.ctx[::10], c.batch.q[::10], 16, c.batch.num_blocks)
+    at = np.concatenate([t + np.arange(n) for t, n in zip(c.batch.starts[::10], some.q)])
+    for v in c.real:
+        v[np.isnan(v)] = 0  # behind the contexts, and the drafts that only `nan` sees
+    want, bound = ref.tree_attention(c.query[at], *c.real, *c.exp, some, c.parents[at], c.scale)
+    ok = ~np.isin(at, nan)
+    assert ok.any() and (np.abs(got[at].astype(np.float64) - want)[ok] <= bound[ok]).all()
