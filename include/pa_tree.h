@@ -74,7 +74,8 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  *
  * The lengths, the block tables and the parents must not change while the call's
  * work runs. A length that breaks a constraint (PA_STATUS_BIT_PLAN) leaves its sequence
- * out; a block table entry outside [0, num_blocks) is never dereferenced and
+ * out; the other sequences' rows lie where the stated lengths put them (a negative one
+ * counts as 0). A block table entry outside [0, num_blocks) is never dereferenced and
  * makes the outputs of its sequence undefined (PA_STATUS_BIT_BLOCK_INDEX).
  */
 pa_status pa_tree_forward(const pa_config* cfg, int64_t tokens, const void* query,

@@ -46,7 +46,9 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
 
 // Sequence and index in it of token t: the last sequence whose tokens begin at
 // or before t. Warp-collective, 128 sequences at a time; -1 past the last one.
-// The sums stop at the number of tokens, past which no token looks.
+// Every sequence counts with the length it states (a negative one with 0), whether it
+// is valid or not: the rows lie as the lengths say. The sums stop at the number
+// of tokens, past which no token looks.
 __device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int lane, int& index) {
   if (!P.q_seqlens) {
     index = 0;
@@ -59,7 +61,7 @@ __device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int b = b0 + 4 * lane + j;
-      const int n = b < P.batch ? min(max(P.q_seqlens[b], 0), P.max_rows) : 0;
+      const int n = b < P.batch ? max(P.q_seqlens[b], 0) : 0;
       ends[j] = sum = min(sum + min(uint32_t(n), tokens), tokens);
     }
     uint32_t upto = sum;

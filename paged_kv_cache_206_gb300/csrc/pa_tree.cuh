@@ -23,34 +23,41 @@ struct TreeParams {
   float scale_log2;  // scale * log2(e)
 };
 
-// Whether sequence b's lengths keep the constraints.
+// Whether a sequence's lengths keep the constraints.
 __device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int L) {
-  return q >= 0 && q <= P.max_q && L >= q &&
+  return q >= 0 && q <= P.max_q && q <= P.tokens && L >= q &&
          int64_t(L) <= int64_t(P.max_blocks_per_seq) * P.block_size;
 }
 
+// a + b tokens, at most all of them: where the rows of a sequence begin is a sum of the
+// lengths before it, which may be any.
+__device__ __forceinline__ int tree_tokens(const TreeParams& P, int a, int b) {
+  return int(min(uint32_t(a) + uint32_t(b), uint32_t(P.tokens)));
+}
+
 // Sequence and index in it of token t (warp-collective); -1 past the last one.
-// A length out of range counts as its nearest valid one here, so that the
-// rows of the other sequences do not depend on the launch's shape.
+// Every sequence counts with the length it states (a negative one with 0), whether
+// it is valid or not: the rows lie as the lengths say.
 __device__ __forceinline__ int tree_sequence(const TreeParams& P, int64_t t, int lane, int& index) {
   index = 0;
   if (!P.q_seqlens) return t < P.batch ? int(t) : -1;
-  int64_t before = 0;
+  int before = 0;
   for (int b0 = 0; b0 < P.batch; b0 += 32) {
-    const int n = b0 + lane < P.batch ? min(max(P.q_seqlens[b0 + lane], 0), P.max_q) : 0;
-    int sum = n;
+    int upto = b0 + lane < P.batch ? tree_tokens(P, 0, max(P.q_seqlens[b0 + lane], 0)) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
+      const int up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = tree_tokens(P, upto, up);
     }
-    const unsigned who = __ballot_sync(0xffffffffu, n > 0 && t >= before + sum - n && t < before + sum);
+    // the first lane whose sequence ends behind the token holds it
+    const unsigned who = __ballot_sync(0xffffffffu, t - before < upto);
     if (who) {
       const int l = __ffs(who) - 1;
-      index = int(t - before) - __shfl_sync(0xffffffffu, sum - n, l);
+      const int start = __shfl_sync(0xffffffffu, upto, l > 0 ? l - 1 : 0);
+      index = int(t - before) - (l > 0 ? start : 0);
       return b0 + l;
     }
-    before += __shfl_sync(0xffffffffu, sum, 31);
+    before += __shfl_sync(0xffffffffu, upto, 31);  // at most t
   }
   return -1;
 }

@@ -42,7 +42,8 @@ __device__ __forceinline__ int64_t tree_div(int64_t a, int64_t b) {
 template <int UNIT, int NR, int LEAD>
 struct TreeLine {
   // Sequence b's tokens, row tiles of a kv head and units of a tile; a sequence
-  // whose lengths break a constraint has none.
+  // whose lengths break a constraint has no tiles, but as many tokens as it states (at
+  // most all that there are): the rows of the next one lie behind them.
   struct Seq {
     int q, L, tiles, units;
     __device__ __forceinline__ int places() const { return units + LEAD; }  // of a tile
@@ -57,14 +58,15 @@ struct TreeLine {
     s.L = P.context_lens[b];
     const bool ok = tree_lengths_ok(P, s.q, s.L);
     if (!ok) set_status(P.status, PA_STATUS_BIT_PLAN);
-    s.q = min(max(s.q, 0), P.max_q);
+    s.q = tree_tokens(P, 0, max(s.q, 0));
     const bool some = ok && s.q > 0;
-    s.tiles = some ? (s.q * P.group + NR - 1) / NR : 0;
-    s.units = some ? (s.L + UNIT - 1) / UNIT : 0;
+    s.tiles = some ? (s.q * P.group - 1) / NR + 1 : 0;
+    s.units = some ? (s.L - 1) / UNIT + 1 : 0;
     return s;
   }
 
-  // The places and tokens of 32 sequences up to this lane's, its own among them.
+  // The places and tokens of 32 sequences up to this lane's, its own among them (the
+  // tokens stop at all that there are).
   struct Sums {
     int64_t places;
     int tokens;
@@ -77,7 +79,7 @@ struct TreeLine {
       const int ut = __shfl_up_sync(0xffffffffu, u.tokens, o);
       if (lane >= o) {
         u.places += up;
-        u.tokens += ut;
+        u.tokens = tree_tokens(P, u.tokens, ut);
       }
     }
     return u;
@@ -144,7 +146,8 @@ struct TreeWalk {
         const int l = __ffs(who) - 1;
         b = b0 + l;
         before += __shfl_sync(0xffffffffu, sums.places - seq.total(P), l);
-        q_start += __shfl_sync(0xffffffffu, sums.tokens - seq.q, l);
+        const int ahead = __shfl_sync(0xffffffffu, sums.tokens, l > 0 ? l - 1 : 0);
+        if (l > 0) q_start = tree_tokens(P, q_start, ahead);
         seq.q = __shfl_sync(0xffffffffu, seq.q, l);
         seq.L = __shfl_sync(0xffffffffu, seq.L, l);
         seq.tiles = __shfl_sync(0xffffffffu, seq.tiles, l);
@@ -152,7 +155,7 @@ struct TreeWalk {
         return true;
       }
       before += __shfl_sync(0xffffffffu, sums.places, 31);
-      q_start += __shfl_sync(0xffffffffu, sums.tokens, 31);
+      q_start = tree_tokens(P, q_start, __shfl_sync(0xffffffffu, sums.tokens, 31));
     }
     u = u1;
     return false;
@@ -162,7 +165,7 @@ struct TreeWalk {
     while (u < u1) {
       while (u >= before + seq.total(P)) {
         before += seq.total(P);
-        q_start += seq.q;
+        q_start = tree_tokens(P, q_start, seq.q);
         if (++b >= P.batch) {  // only if the lengths changed under the kernel
           u = u1;
           return false;
