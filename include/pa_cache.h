@@ -29,7 +29,8 @@
  *   PA_STATUS_BIT_PLAN         a length breaks a constraint; that sequence (or
  *                              the rows past `tokens`) is left out. The other
  *                              sequences' rows lie where the stated lengths put
- *                              them (a negative one counts as 0)
+ *                              them (a negative one counts as 0). A call of
+ *                              no tokens looks at none
  *   PA_STATUS_BIT_POSITION     a position outside [-1, max_positions); that
  *                              token is left out
  *   PA_STATUS_BIT_WORKSPACE    an output row outside [0, out_rows); left out

@@ -55,7 +55,8 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  * cfg            as in pa.h, with mask_type = PA_MASK_NONE, chunk_blocks = 0 and
  *                0 < num_sms <= 65535. With parents max_seqlen_q <= PA_TREE_MAX_TOKENS.
  * tokens         rows of query and out (sum q_b, or more: the rows behind the
- *                last sequence are neither read nor written)
+ *                last sequence are neither read nor written; with fewer the rows
+ *                past them are left out, and PA_STATUS_BIT_PLAN says so)
  * query          device fp16 [tokens, H, hk], 16-byte aligned
  * key_cache, value_cache  fp16 as in pa.h, or e4m3 codes as in pa_cache.h; two
  *                different caches

@@ -90,6 +90,22 @@ __device__ __forceinline__ int find_sequence(const RowParams& P, uint32_t t, int
   return -1;
 }
 
+// What no token's warp can see of the lengths: that one is negative or past its bound, or
+// that they are more than the tokens (one warp, where there is a status to tell).
+__device__ __noinline__ void check_lengths(const RowParams& P, int lane) {
+  const uint32_t over = uint32_t(P.tokens) + 1;  // < 2^30: two of them fit in 32 bits
+  uint32_t sum = 0;
+  bool bad = false;
+  for (int b = lane; b < P.batch; b += 32) {
+    const int q = P.q_seqlens ? P.q_seqlens[b] : 1;
+    bad |= q < 0 || q > P.max_rows;
+    sum = min(sum + min(uint32_t(max(q, 0)), over), over);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum = min(sum + __shfl_xor_sync(0xffffffffu, sum, o), over);
+  if (bad || sum == over) report(P.status, PA_STATUS_BIT_PLAN);
+}
+
 // One warp per (token, slice of its query, key or value heads), U rows to a
 // group of lanes. A row's elements are 16-byte chunks of 8; a lane holds chunk
 // pair p: chunks p and p + rot / 16 where they are rotated (so that both members
@@ -113,7 +129,10 @@ rows_kernel(const RowParams P) {
   const int group = lane >> P.lane_shift, gl = lane & (lanes - 1);
   const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5);
   const int64_t t = task / P.slices;
-  if (t >= P.tokens) return;
+  if (t >= P.tokens) {
+    if (MODE != kRotate && P.status && task == uint32_t(P.tokens) * P.slices) check_lengths(P, lane);
+    return;
+  }
   const uint32_t slice = task - uint32_t(t) * P.slices;
   const bool is_q = MODE != kWrite && slice < P.q_slices;
   const bool is_v = MODE != kRotate && slice >= P.q_slices + P.k_slices;
@@ -450,7 +469,8 @@ pa_status launch_rows(RowParams P, cudaStream_t stream) {
   P.batches = many ? kBatches : 1;
   if (!many) slice(per_warp);
   if (P.tokens > INT32_MAX || P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
-  const unsigned grid = unsigned(cdiv(P.tokens * P.slices, 8));
+  const int check = MODE != kRotate && P.status ? 1 : 0;  // a warp for the lengths
+  const unsigned grid = unsigned(cdiv(P.tokens * P.slices + check, 8));
   if (many) rows_kernel<MODE, 1, kRows, IL><<<grid, 256, 0, stream>>>(P);
   else if (widest <= 32) rows_kernel<MODE, 1, 1, IL><<<grid, 256, 0, stream>>>(P);
   else rows_kernel<MODE, 2, 1, IL><<<grid, 256, 0, stream>>>(P);

@@ -39,6 +39,19 @@ __device__ __forceinline__ void load8(const uint8_t* row, int d, float (&x)[8]) 
   }
 }
 
+// The lengths of sequences that no token of the call may belong to (one warp).
+__device__ __noinline__ void tree_check_lengths(const TreeParams& P, int lane) {
+  int64_t sum = 0;
+  for (int b = lane; b < P.batch; b += 32) {
+    const int q = P.q_seqlens ? P.q_seqlens[b] : 1;
+    if (!tree_lengths_ok(P, q, P.context_lens[b])) set_status(P.status, PA_STATUS_BIT_PLAN);
+    sum += max(q, 0);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (sum > P.tokens) set_status(P.status, PA_STATUS_BIT_PLAN);
+}
+
 // Heads of more than 256 dims. One CTA per (token, head); warp w takes the keys w, w + 4,
 // ..., a lane holds 8-dim chunks lane, lane + 32, ... of the row. Softmax and sums in fp32.
 // Bound by the latency of a key after another, and the heads of a group read the
@@ -52,6 +65,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) tree_any_kernel(const TreePara
   const int64_t t = blockIdx.x / P.num_heads;
   const int h = int(blockIdx.x % P.num_heads), kvh = h / P.group;
   int i;
+  if (blockIdx.x == 0 && warp == 0) tree_check_lengths(P, lane);
   const int b = tree_sequence(P, t, lane, i);
   if (b < 0) return;
   const int q = P.q_seqlens ? P.q_seqlens[b] : 1, L = P.context_lens[b];

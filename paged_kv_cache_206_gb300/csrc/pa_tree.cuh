@@ -29,6 +29,11 @@ __device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int 
          int64_t(L) <= int64_t(P.max_blocks_per_seq) * P.block_size;
 }
 
+// Whether the tokens end before sequence rows begun at q_start do (the rows past them are left out).
+__device__ __forceinline__ bool tree_rows_missing(const TreeParams& P, int q_start, int q) {
+  return P.tokens - q_start < q;
+}
+
 // a + b tokens, at most all of them: where the rows of a sequence begin is a sum of the
 // lengths before it, which may be any.
 __device__ __forceinline__ int tree_tokens(const TreeParams& P, int a, int b) {

@@ -180,6 +180,7 @@ struct TreeWalk {
       t.s0 = max(p0 - LEAD, 0);
       t.s1 = max(p1 - LEAD, 0);
       if (t.s0 == t.s1) continue;  // nothing but a lead: the next worker's
+      if (tree_rows_missing(P, q_start, seq.q)) set_status(P.status, PA_STATUS_BIT_PLAN);
       t.b = b;
       t.q_start = q_start;
       t.q = seq.q;

@@ -102,3 +102,59 @@ def test_lengths_whose_sum_passes_32_bits(torch, shape):
     want, want_e = expected_cache(good, x[:5], d, Hk)
     assert ref.same_codes(cache.key.view(torch.uint8).cpu().numpy(), want)
     np.testing.assert_array_equal(cache.key_exps.cpu().numpy(), want_e)
+
+
+@pytest.mark.parametrize("call", ["write", "store"])
+@pytest.mark.parametrize("fault", ["negative", "more than the tokens", "no lengths"])
+def test_the_cache_reports_lengths_that_no_token_belongs_to(torch, call, fault):
+    rng = np.random.default_rng(7)
+    q = [1] * 5 if fault == "no lengths" else [2, 1, 3, 2, 1]
+    batch = ref.make_batch(rng, q, [n + 20 for n in q], 16)
+    stated, T, stored = batch.q.copy(), int(batch.q.sum()), np.array(q)
+    if fault == "negative":
+        stated[1], stored[1] = -3, 0
+        T -= 1
+    else:
+        T -= 2  # the last sequence and a token of the one before it, or two sequences
+        stored = np.array([1, 1, 1, 0, 0]) if fault == "no lengths" else np.array([2, 1, 3, 1, 0])
+    k, v, xq = rows(rng, T, 2, 64), rows(rng, T, 2, 64), rows(rng, T, 4, 64)
+    c = empty_cache(torch, batch.num_blocks, 16, 2, 64, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = (up(torch, batch.tables), up(torch, batch.ctx),
+            None if fault == "no lengths" else up(torch, stated), 3)
+    if call == "write":
+        c.write(up(torch, k), up(torch, v), *lens, status=status)
+    else:
+        c.store(up(torch, xq), up(torch, k), up(torch, v), None, None, None, None, *lens,
+                torch.zeros((T, 4, 64), dtype=torch.float16, device="cuda"), status=status)
+    assert status.item() == pa.PA_STATUS_BIT_PLAN
+    # the stored tokens of a sequence are its first ones
+    ctx = batch.ctx - np.array(q) + stored if fault != "negative" else batch.ctx
+    good = ref.Batch(batch.tables, ctx, stored, 16, batch.num_blocks)
+    want, want_e = expected_cache(good, k, 64, 2)
+    assert ref.same_codes(c.key.view(torch.uint8).cpu().numpy(), want)
+    np.testing.assert_array_equal(c.key_exps.cpu().numpy(), want_e)
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 64), (32, 4, 128), (2, 1, 272)], ids=str)
+@pytest.mark.parametrize("fault", ["negative", "more than the tokens", "context"])
+def test_the_attention_reports_lengths_that_no_token_belongs_to(torch, shape, fault):
+    H, Hk, d = shape
+    q = [2, 0, 3, 2, 1]
+    c = Case(torch, 8, q, [n + 20 for n in q], H, Hk, d, d, 16, "tree")
+    stated, ctx, rows_in = c.batch.q.copy(), c.batch.ctx.copy(), c.tokens
+    if fault == "negative":
+        stated[1] = -1
+    elif fault == "context":
+        ctx[1] = -1  # of a sequence without tokens
+    else:
+        rows_in -= 2
+    c.args[0], c.args[2], c.args[3] = c.args[0][:rows_in], up(torch, ctx), up(torch, stated)
+    c.args[4], out = c.args[4][:rows_in].contiguous(), c.out
+    c.out = out[:rows_in]
+    c.run()
+    assert c.step.status() == (pa.PA_ERR_INVALID_ARG, pa.PA_STATUS_BIT_PLAN)
+    assert (out[rows_in:] == 7).all()
+    want, bound = ref.tree_attention(c.query, *c.real, *c.exp, c.batch, c.parents, c.scale)
+    got = out.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want)[:rows_in] <= bound[:rows_in]).all()
