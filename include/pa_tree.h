@@ -13,7 +13,8 @@
  *   without parents  every current token before it (a chain)
  * out = softmax(scale * <q, K_j>) V_j over those, heads grouped as in pa.h.
  * Keys and values that a row does not attend have no effect on it, whatever
- * they hold (NaN and infinities included).
+ * they hold (NaN and infinities included). A slot of the 8-bit cache that nothing
+ * was written into (zero codes, zero exponent byte) is a row of zeros.
  *
  * Scores, softmax sums and outputs are accumulated in fp32; the weights are
  * rounded to fp16 for their product with V. With more than 16 rows of a kv head

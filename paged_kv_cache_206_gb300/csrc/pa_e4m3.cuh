@@ -12,6 +12,12 @@ namespace pa {
 constexpr int kExpMin = -32;   // least exponent a row is held with
 constexpr int kExpBias = 127;  // of the exponent byte
 
+// The attention folds 2^e of a V row into its weight and takes it out of the sum again, a product
+// of up to 2^31 keys' 2^-e. Bytes below this one (2^-64; writing a row makes none, a slot that was
+// never written holds 0) count as it there: what they stand for, 448 * 2^-64 and less, is
+// nothing beside fp16's least number, 2^-24, and sums of 2^64 stay far from fp32's end.
+constexpr int kExpLeastByte = 63;
+
 // e: the least integer >= kExpMin with a <= 448 * 2^e, a >= 0 finite.
 // 448 = 1.75 * 2^8, so e = k - 8 for a = m * 2^k with m <= 1.75, else k - 7
 // (zero and subnormal a have k = -127 here and end at kExpMin).

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           float f = P.scale_log2, add = 0.f;
           unscale[mt][hf] = 1.f;
           if constexpr (Q8) {
-            int ke = ex[kk], ve = ex[32 + kk];
+            int ke = ex[kk], ve = max(int(ex[32 + kk]), kExpLeastByte);
             if (edge && key >= L) ke = ve = kExpBias;  // exponents behind the context: anything
             f *= pow2(ke - kExpBias);
             add = float(ve - kExpBias);

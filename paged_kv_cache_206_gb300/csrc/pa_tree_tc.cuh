@@ -37,6 +37,8 @@
 // bounded.
 #pragma once
 
+#include <cfloat>
+
 #include "pa_prefill_tc.cuh"
 #include "pa_tree_mma.cuh"
 
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           const int k = n % Cfg::kMeta;
           if (!tree_wait(&meta_full[k], (n / Cfg::kMeta) & 1)) { ok = false; break; }
           const int2 e = meta[k];
-          F *= pow2(e.x);
+          F = fmaxf(F * pow2(e.x), FLT_MIN);  // (0 times the -inf of a masked score is NaN)
           ev = float(e.y);
           unscale = pow2(-e.y);
         }
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         const int left = t.L - key0 - lane * 4;  // of this lane's four
         int top = max(max(left > 0 ? int(e4 & 255) : 0, left > 1 ? int(e4 >> 8 & 255) : 0),
                       max(left > 2 ? int(e4 >> 16 & 255) : 0, left > 3 ? int(e4 >> 24) : 0));
-        top = __reduce_max_sync(FULL, top);
+        top = max(__reduce_max_sync(FULL, top), kExpLeastByte);
         if ((part & 1) == 0 && sub == 0 && lane == 0) {
           reinterpret_cast<int*>(&meta[mm])[kv] = top - kExpBias;
           mbar_arrive(&meta_full[mm]);

@@ -483,3 +483,40 @@ def test_many_ends_of_contexts_in_turn(torch, drafts, lo, hi):
     want, bound = ref.tree_attention(c.query[at], *c.real, *c.exp, some, c.parents[at], c.scale)
     ok = ~np.isin(at, nan)
     assert ok.any() and (np.abs(got[at].astype(np.float64) - want)[ok] <= bound[ok]).all()
+
+
+# rows of a kv head: the kernels of up to 16, of up to 128 and of more; heads above 256 dims
+UNWRITTEN = [(8, 2, 64, 2), (16, 2, 128, 1), (16, 1, 128, 8), (16, 1, 64, 20), (4, 2, 272, 3)]
+
+
+@pytest.mark.parametrize("shape", UNWRITTEN, ids=str)
+def test_an_empty_cache_gives_zeros(torch, shape):
+    """A warm-up over a cache that nothing was written into."""
+    H, Hk, d, q = shape
+    c = Case(torch, 8, [q, 1], [300, 1], H, Hk, d, d, 16, "tree")
+    e = pa.QuantCache.empty(c.batch.num_blocks, 16, Hk, d)
+    c.step = pa.TreeStep(e.key, e.value, e.key_exps, e.value_exps, batch=2, num_heads=H, max_seqlen_q=q,
+                         max_blocks_per_seq=c.batch.tables.shape[1])
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0) and bool((c.out == 0).all())
+
+
+@pytest.mark.parametrize("shape", UNWRITTEN, ids=str)
+@pytest.mark.parametrize("scale", [0.0, 1e-30])
+def test_slots_that_were_never_written_are_zero_rows(torch, shape, scale):
+    """Zero codes under zero exponent bytes amid a context, in all of a key tile, in all of a
+    sequence, and in the values alone: keys of score 0 and values of 0."""
+    H, Hk, d, q = shape
+    c = Case(torch, 8, [q, q, 1, q], [400, 290, 9, 140 + q], H, Hk, d, d, 16, "tree", scale=scale)
+    for n, (codes, exps) in enumerate(c.dev):
+        for b, lo, hi in ((0, 3, 90), (0, 200, 201), (1, 0, 140), (2, 0, 9), (3, 20, 140 + q)):
+            if (b, n) == (3, 0):
+                continue
+            blk, off = c.batch.slots(b, lo, hi)
+            codes.view(torch.uint8)[blk, off] = 0
+            exps.transpose(1, 2)[blk, off] = 0
+            c.real[n][blk, off] = 0
+            c.exp[n].transpose(0, 2, 1)[blk, off] = -127
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    c.check()
