@@ -851,7 +851,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             }
             if (hit) *p = x;
           }
-          fence_proxy_async();  // before the stage's next copy, which may begin once it is given back
           __syncwarp();
         }
         // all of the part into registers, so that its stage is free for the next copy
@@ -859,6 +858,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         uint2 x[ROWS / RPI];
 #pragma unroll
         for (int k = 0; k < ROWS / RPI; ++k) x[k] = *reinterpret_cast<const uint2*>(src + k * 256);
+        // The stage's next copy comes by another proxy, so it does not queue behind these loads (nor
+        // behind the stores above) as an ordinary store would: without the fence their last
+        // rows were at times the next copy's, where the softmax warps' stores at the end of a
+        // row tile held the loads up.
+        fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&taken[st]);
         // factors of the rows lane, lane + 32 of this warp: 2^-diff, where diff is past
