@@ -473,7 +473,6 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
             atomicOr(&bad_s[(a >> 5) % kTreeWords], 1u << (a & 31));
           }
         }
-        fence_proxy_async();  // before the stage's next copy
         __syncwarp();
       }
 
@@ -544,6 +543,9 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           }
         }
       }
+      // the stage's next copy comes by another proxy and waits neither for the loads nor for the
+      // stores of this one by itself
+      fence_proxy_async();
       __syncwarp();
       issue();
     }

@@ -485,15 +485,16 @@ def test_many_ends_of_contexts_in_turn(torch, drafts, lo, hi):
     assert ok.any() and (np.abs(got[at].astype(np.float64) - want)[ok] <= bound[ok]).all()
 
 
-@pytest.mark.parametrize("bits,H,drafts,lo,hi", [(8, 32, 64, 100, 700), (8, 32, 8, 100, 700), (8, 16, 32, 600, 1400),
-                                                 (16, 32, 64, 100, 700), (8, 8, 4, 100, 700), (16, 8, 4, 100, 700),
-                                                 (8, 8, 1, 1, 900)], ids=str)
-def test_many_row_tiles_again_and_again(torch, bits, H, drafts, lo, hi):
+@pytest.mark.parametrize("bits,H,drafts,lo,hi,d", [
+    (8, 32, 64, 100, 700, 128), (8, 32, 8, 100, 700, 128), (8, 16, 32, 600, 1400, 128), (16, 32, 64, 100, 700, 128),
+    (8, 8, 4, 100, 700, 128), (16, 8, 4, 100, 700, 128), (8, 8, 1, 1, 900, 128), (8, 8, 4, 50, 300, 64),
+    (16, 8, 2, 50, 300, 64), (8, 8, 4, 50, 300, 256), (16, 8, 2, 50, 300, 256), (8, 12, 5, 50, 300, 96)])
+def test_many_row_tiles_again_and_again(torch, bits, H, drafts, lo, hi, d):
     """Rings that never run empty while row tiles end, so that every stage is filled again as soon as
     it is given back: three hundred runs give the same bits."""
     rng = np.random.default_rng(drafts + H)
     q = rng.integers(max(1, drafts // 2), drafts + 1, 200)
-    c = Case(torch, bits, q, q + rng.integers(lo, hi, 200), H, 2, 128, 128, 16, "tree")
+    c = Case(torch, bits, q, q + rng.integers(lo, hi, 200), H, 2, d, d, 16, "tree")
     first = c.run().clone().view(torch.int16)
     differ = torch.zeros((), dtype=torch.int64, device="cuda")
     for _ in range(300):
