@@ -16,11 +16,9 @@
  * they hold (NaN and infinities included). A slot of the 8-bit cache that nothing
  * was written into (zero codes, zero exponent byte) is a row of zeros.
  *
- * Scores, softmax sums and outputs are accumulated in fp32; the weights are
- * rounded to fp16 for their product with V. With more than 16 rows of a kv head
- * (H / Hk * max_seqlen_q) and heads of 64 or 128 dims the 8-bit cache's rows are
- * brought to the largest exponent among 128 keys in fp16, exact but for rows
- * 2^15 times smaller than that. The same batch gives the same bits every time; a
+ * Scores, softmax sums and outputs are accumulated in fp32, the 8-bit cache's codes and
+ * exponents enter them exactly; the weights are rounded to fp16 for their product
+ * with V. The same batch gives the same bits every time; a
  * sequence in another batch may differ in its last bits, as the work is divided
  * otherwise.
  */

@@ -24,14 +24,18 @@
 //   warps 4-11   softmax, one row a thread: group g = chain g
 //   warps 12-15  8-bit cache only: codes to fp16 operands, a warp for each of the
 //                four 64-row parts (K, K, V, V) of a tile. The rows of a tile are
-//                brought to the tile's largest exponent (code * 2^(e_j - e_max), exact
-//                but for rows 2^15 times smaller than the tile's largest, whose
-//                low bits fall under fp16's 2^-24: an absolute 2^-25 of that
-//                unit), so the softmax sees one factor for K and one exponent for
-//                V per tile, as the fp16 cache's does.
+//                brought to the tile's largest exponent (code * 2^(e_j - e_max),
+//                exact), so the softmax sees one factor for K and one exponent for
+//                V per tile, as the fp16 cache's does. A row whose exponent lies
+//                further below (kSpreadK, kSpreadV), as one row may be large that
+//                others do not even attend, is brought down by that much only, and
+//                the softmax applies the rest to the key's score and weight
+//                (tree_apart), exactly, as the warp-level kernel always does.
 //
 // The reference maximum of a row moves only when a score passes it by 2^8; sums,
-// maxima and accumulators are fp32, the weights fp16. All roles walk the same
+// maxima and accumulators are fp32, the weights fp16. Over the 8-bit cache the weights
+// stand 2^kLift above that: a tile's exponent may be kSpreadV above that of every V row
+// that a row attends, and its weights keep their 11 bits all the same. All roles walk the same
 // tiles of the line; rings and barriers run on across them, so the copies of the
 // next tile are under way while the last one's rows are written out. Every wait is
 // bounded.
@@ -72,9 +76,13 @@ struct TreeTc {
   static constexpr int kKRounds = (kKStages + 1) / 2, kVRounds = (kVStages + 1) / 2;
   static constexpr int kLanded = 2 * (kKRounds + kVRounds);
   // Key tiles whose exponents, and whose largest ones, are held; row tiles whose flags
-  // are. A widening warp is at most three tiles ahead of the softmax (the K and V
-  // rings' two, and one in registers), so a row tile or key tile eight on finds the place read.
+  // are. While the softmax has a key tile n before it, the products S reach n + 1, the K slots n + 3,
+  // the widening warps' registers n + 4 (whose exponents they have told) and the K stages the first
+  // half of n + 7 (the V ones n + 4), so a row tile or key tile eight on finds the place read.
   static constexpr int kExps = 8, kMeta = 8, kBad = 8;
+  // How far below the tile's largest exponent a row is brought up to it: a code (a multiple of
+  // 2^-9) times 2^-14 is still exact in fp16, and weights may stand 2^7 higher (2^(8 + 7) < 65504).
+  static constexpr int kSpreadK = 14, kSpreadV = 7, kLift = Q8 ? kSpreadV : 0;
   static constexpr int kAhead = 4;                       // row tiles told to the roles
   static constexpr int kRoles = Q8 ? 11 + 4 * kConv : 11;            // warps that are told
   static constexpr uint32_t q_off = 0;
@@ -82,7 +90,8 @@ struct TreeTc {
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
   static constexpr uint32_t stage_off = v_off + kVSlots * kTile;
   static constexpr uint32_t exps_off = stage_off + kStages * kStageBytes;  // [kExps][2][128]
-  static constexpr uint32_t meta_off = exps_off + (Q8 ? kExps * 256 : 0);  // [kMeta] int2
+  // [kMeta] int2: the exponent bytes of K and V, and bit 8: there are rows further below than that
+  static constexpr uint32_t meta_off = exps_off + (Q8 ? kExps * 256 : 0);
   static constexpr uint32_t stat_off = meta_off + kMeta * 8;               // [2][2][128] float2
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
@@ -206,6 +215,64 @@ __device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, u
   }
   fence_proxy_async();
   __syncwarp();
+}
+
+// Which of 32 columns a row attends, the first one being draft a0 (negative: prefix) of its sequence:
+// of `seen`, its bits, or of a chain, whose row is draft `qi`.
+__device__ __forceinline__ uint32_t tree_attends(const uint32_t* seen, int qi, int a0) {
+  if (a0 <= -32) return ~0u;
+  if (!seen) {
+    const int n = qi - a0 + 1;  // columns up to the row's own
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+  }
+  // bits a0 .. a0 + 31 of (ones below 0, then the row's drafts)
+  const int q = a0 >> 5;
+  const uint32_t lo = q < 0 ? ~0u : q < kTreeWords ? seen[q] : 0u;
+  const uint32_t hi = q + 1 < kTreeWords ? seen[q + 1] : 0u;
+  return __funnelshift_r(lo, hi, a0 & 31);
+}
+
+// The scores of a job some of whose keys lie further below the tile's exponents than they were
+// brought up to, 64 columns of S in TMEM, become base-2 exponents of weights in place: s_j + v_j, with
+// s_j = S_j * scale * 2^k_j and k_j, v_j what is left of the exponents in `exps` (V's 128 bytes behind
+// K's). `left` columns lie in the context, the first is draft a0. *own: the largest s_j that
+// the row attends and the sum of 2^(s_j - it). Rare, hence not inlined and a loop of 16 columns.
+template <int SPREAD_K, int SPREAD_V>
+__device__ __noinline__ void tree_apart(uint32_t sbuf, const uint8_t* exps, int2 tile, float scale_log2, int left,
+                                        const uint32_t* seen, int qi, int a0, float2* own) {
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    float s[16], most = top;
+    uint32_t x[16];
+    __syncwarp();
+    tmem_ld<16>(sbuf + c, s);
+    tmem_wait_ld();
+    const uint32_t bits = tree_attends(seen, qi, a0 + (c & 32)) >> (c & 16);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      int k = (tile.x & 255) - kExpBias, v = (tile.y & 255) - kExpBias;
+      if (c + j < left) {  // (exponents behind the context: anything)
+        k = min(k, max(int(exps[c + j]), kExpLeastByte) - kExpBias + SPREAD_K);
+        v = min(v, max(int(exps[c + j + 128]), kExpLeastByte) - kExpBias + SPREAD_V);
+      }
+      s[j] *= fmaxf(scale_log2 * pow2(k), FLT_MIN);
+      x[j] = __float_as_uint(s[j] + float(v));
+      if (!(bits >> j & 1)) s[j] = -INFINITY;
+      most = fmaxf(most, s[j]);
+    }
+    const float ref = most == -INFINITY ? 0.f : most;
+    float add = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) add += ex2(s[j] - ref);
+    sum = fmaf(sum, ex2(top - ref), add);
+    top = most;
+    __syncwarp();
+    tmem_st16u(sbuf + c, x);
+  }
+  __syncwarp();
+  tmem_wait_st();
+  *own = make_float2(top, sum);
 }
 
 template <int HD, bool Q8, int QT>
@@ -617,19 +684,30 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         const int y = QT == 2 ? hf : n & 1, x_of_s = QT == 2 ? g : n & 1, phase = phase_of(n);
         const int key0 = (t.s0 + i) * TOK + hf * 64;
         float F = P.scale_log2, ev = 0.f, unscale = 1.f;
+        int2 e = make_int2(0, 0);
         if constexpr (Q8) {
           const int k = n % Cfg::kMeta;
           if (!tree_wait(&meta_full[k], (n / Cfg::kMeta) & 1)) { ok = false; break; }
-          const int2 e = meta[k];
-          F = fmaxf(F * pow2(e.x), FLT_MIN);  // (0 times the -inf of a masked score is NaN)
-          ev = float(e.y);
-          unscale = pow2(-e.y);
+          e = meta[k];
+          F = fmaxf(F * pow2((e.x & 255) - kExpBias), FLT_MIN);  // (0 times the -inf of a masked score is NaN)
+          ev = float((e.y & 255) - kExpBias);
+          unscale = pow2(kExpBias - (e.y & 255));
         }
         if (!tree_wait(&s_full[x_of_s], phase)) { ok = false; break; }
         tc_fence_after();
         if (any_row) {
           __syncwarp();
           const uint32_t sbuf = uni(tmem_s + x_of_s * 128 + hf * 64 + lane_base);
+          float2 own;  // of keys with exponents of their own: the largest score, the sum
+          if (Q8 && ((e.x | e.y) & 256)) {
+            const int em = n % Cfg::kExps, ph = (n / Cfg::kExps) & 1;
+            if (!tree_wait2(&exps_full[em], ph, &exps_full[Cfg::kExps + em], ph)) ok = false;
+            tree_apart<Cfg::kSpreadK, Cfg::kSpreadV>(sbuf, smem + Cfg::exps_off + em * 256 + hf * 64, e, P.scale_log2,
+                                                     t.L - key0, P.parents ? bits : nullptr, qi, key0 - prefix, &own);
+            F = 1.f;
+            ev = unscale = 0.f;
+            __syncwarp();
+          }
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
@@ -638,20 +716,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           if (edge) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const int a0 = key0 + 32 * w - prefix;  // draft of the word's first column
-              uint32_t see = ~0u;                     // this row's columns
-              if (a0 > -32) {
-                if (P.parents) {
-                  // bits a0 .. a0 + 31 of (ones below 0, then the row's drafts)
-                  const int q = a0 >> 5, s = a0 & 31;
-                  const uint32_t lo = q < 0 ? ~0u : q < kTreeWords ? bits[q] : 0u;
-                  const uint32_t hi = q + 1 < kTreeWords ? bits[q + 1] : 0u;
-                  see = __funnelshift_r(lo, hi, s);
-                } else {
-                  const int n = qi - a0 + 1;  // columns up to the row's own
-                  see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
-                }
-              }
+              const uint32_t see = tree_attends(P.parents ? bits : nullptr, qi, key0 + 32 * w - prefix);
 #pragma unroll
               for (int k = 0; k < 32; ++k) x[32 * w + k] = see >> k & 1 ? x[32 * w + k] : -INFINITY;
             }
@@ -661,11 +726,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           for (int k = 4; k < 64; k += 2) mx[k / 2 & 3] = max3(mx[k / 2 & 3], x[k], x[k + 1]);
           const float top = fmaf(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])), F, ev);
           // move the reference only when a score passes it by more than 2^8
-          const bool grow = top > m_ref + kTcRescaleThreshold;
+          const bool grow = top > m_ref + (kTcRescaleThreshold + Cfg::kLift);
           float alpha = 1.f;
           if (grow) {
-            alpha = ex2(m_ref - top);  // 0 on the first job that the row sees keys of
-            m_ref = top;
+            alpha = ex2(m_ref - (top - Cfg::kLift));  // 0 on the first job that the row sees keys of
+            m_ref = top - Cfg::kLift;
             l *= alpha;
           }
           const float add = ev - (m_ref == -INFINITY ? 0.f : m_ref);
@@ -685,6 +750,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
             tmem_st16u(sbuf + w * 16, pk);  // over scores that are in registers
           }
           l = fmaf(sum.x + sum.y, unscale, l);
+          if (Q8 && ((e.x | e.y) & 256) && m_ref != -INFINITY) l = fmaf(own.y, ex2(own.x - m_ref), l);
           if (m > 0 && __any_sync(FULL, grow)) {
             // O as the chain's job before left it
             const int nb = QT == 2 && hf ? n : n - 1, yb = QT == 2 ? hf ^ 1 : nb & 1;
@@ -811,27 +877,44 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
     int slot = 0, phase = 0, st = part & 1, round = 0, lphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
     TreeTile t;
+    // The largest exponent of the tile in slot `es`, `keys` of whose rows are the context's; of each kind
+    // the first part's warp tells the softmax, and whether some lie far below it.
+    auto look = [&](int keys, int es, int ph, int m, int& top) {
+      if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph)) return false;
+      const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
+      const int left = keys - lane * 4;  // of this lane's four
+      int low = 255;
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = int(e4 >> (8 * j) & 255);
+        top = max(top, left > j ? e : 0);
+        low = min(low, left > j ? e : 255);
+      }
+      top = max(__reduce_max_sync(FULL, top), kExpLeastByte);
+      low = __reduce_min_sync(FULL, low);
+      if ((part & 1) == 0 && sub == 0 && lane == 0) {
+        reinterpret_cast<int*>(&meta[m])[kv] = top | (top - low > (kv ? Cfg::kSpreadV : Cfg::kSpreadK) ? 256 : 0);
+        mbar_arrive(&meta_full[m]);
+      }
+      return true;
+    };
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
+      int top = 0;
+      if (tiles > 0 && !look(t.L - t.s0 * TOK, em, ephase, mm, top)) {
+        ok = false;
+        break;
+      }
       for (int i = 0; i < tiles; ++i) {
         const int key0 = (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
-        if (!tree_wait2(&exps_full[kv * Cfg::kExps + em], ephase, &landed[2 * round], lphase)) {
+        if (!tree_wait(&landed[2 * round], lphase)) {
           ok = false;
           break;
         }
         uint8_t* src = stage + st * Cfg::kStageBytes;
         uint8_t* dst = operand + slot * Cfg::kTile;
-        // the tile's largest exponent, over the keys of the context
-        const uint32_t e4 = *reinterpret_cast<const uint32_t*>(exps + lane * 4);
-        const int left = t.L - key0 - lane * 4;  // of this lane's four
-        int top = max(max(left > 0 ? int(e4 & 255) : 0, left > 1 ? int(e4 >> 8 & 255) : 0),
-                      max(left > 2 ? int(e4 >> 16 & 255) : 0, left > 3 ? int(e4 >> 24) : 0));
-        top = max(__reduce_max_sync(FULL, top), kExpLeastByte);
-        if ((part & 1) == 0 && sub == 0 && lane == 0) {
-          reinterpret_cast<int*>(&meta[mm])[kv] = top - kExpBias;
-          mbar_arrive(&meta_full[mm]);
-        }
         if (key0 + TOK > prefix) {
           // the tile reaches the drafts: rows behind the context become 0, and
           // non-finite elements of the drafts' V rows leave the product
@@ -865,15 +948,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&taken[st]);
-        // factors of the rows lane, lane + 32 of this warp: 2^-diff, where diff is past
-        // 14 (a rarity) its first step
+        // factors of the rows lane, lane + 32 of this warp: 2^-diff, as far down as goes
         uint32_t fac[ROWS / 32];
-        bool deep = false;
 #pragma unroll
         for (int k = 0; k < ROWS / 32; ++k) {
           const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + sub * ROWS + 32 * k + lane];
-          fac[k] = (15u - min(diff, 14u)) * 0x04000400u;
-          deep |= diff > 14;
+          fac[k] = (15u - min(diff, uint32_t(kv ? Cfg::kSpreadV : Cfg::kSpreadK))) * 0x04000400u;
         }
         if (!tree_wait(&empty[slot], phase ^ 1)) {
           ok = false;
@@ -887,18 +967,16 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
               make_uint4(hmul2u(e4m3x2_half2(x[k].x), f), hmul2u(e4m3x2_half2(x[k].x >> 16), f),
                          hmul2u(e4m3x2_half2(x[k].y), f), hmul2u(e4m3x2_half2(x[k].y >> 16), f));
         }
-        if (__any_sync(FULL, deep)) {
-          // the second step, for the rows that need it
-#pragma unroll 1
-          for (int k = 0; k < ROWS / RPI; ++k) {
-            const int rr = k * RPI;
-            const uint32_t diff = uint32_t(top) - exps[row0 + rr], more = max(diff, 14u) - 14u;
-            if (more == 0) continue;
-            const uint32_t f2 = (more < 15 ? (15u - more) << 10 : more <= 24 ? 1u << (24 - more) : 0u) * 0x10001u;
-            uint4* p = reinterpret_cast<uint4*>(dst + rr * 128 + (((ch & 7) ^ ((row0 + rr) & 7)) << 4));
-            const uint4 h = *p;
-            *p = make_uint4(hmul2u(h.x, f2), hmul2u(h.y, f2), hmul2u(h.z, f2), hmul2u(h.w, f2));
-          }
+        mm = (mm + 1) % Cfg::kMeta;
+        if (++em == Cfg::kExps) {
+          em = 0;
+          ephase ^= 1;
+        }
+        // the next tile's exponents now, or its softmax would wait for them (trees of 16: 93.8 us so, 103
+        // at the tile's own turn, 98 before the wait for the place, 97 behind the hand-over)
+        if (i + 1 < tiles && !look(t.L - key0 - TOK, em, ephase, mm, top)) {
+          ok = false;
+          break;
         }
         fence_proxy_async();
         __syncwarp();
@@ -912,11 +990,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           round = 0;
           lphase ^= 1;
         }
-        if (++em == Cfg::kExps) {
-          em = 0;
-          ephase ^= 1;
-        }
-        mm = (mm + 1) % Cfg::kMeta;
       }
       ++tile;
     }

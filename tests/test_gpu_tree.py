@@ -538,3 +538,69 @@ def test_slots_that_were_never_written_are_zero_rows(torch, shape, scale):
     c.run()
     assert c.step.status() == (pa.PA_OK, 0)
     c.check()
+
+
+# q, ctx, H, Hk, dims, block, kind: few rows of a kv head, up to 128, more; heads above 256 dims
+SPREAD = [
+    ([3, 2], [290, 40], 8, 2, 128, 16, "tree"),
+    ([9, 12], [50, 300], 16, 2, 128, 16, "tree"),
+    ([20, 7, 1], [150, 263, 128], 8, 4, 64, 48, "tree"),
+    ([12], [520], 8, 1, 128, 64, "chain"),
+    ([30, 9], [31, 400], 16, 2, 128, 32, "tree"),
+    ([200], [700], 2, 1, 64, 128, "chain"),
+    ([5], [200], 4, 2, 272, 16, "tree"),
+]
+
+
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("big", ["key", "value", "both"])
+def test_large_drafts_that_a_row_does_not_see_take_nothing_from_it(torch, bits, case, big):
+    """One draft's key or value is of fp16's largest size among small ones: the rows that do not
+    attend it are as exact as without it."""
+    q, ctx, H, Hk, d, bs, kind = case
+
+    def poison(case, x):
+        which = ("key", "value")[len(case.real)]
+        if which == "value":
+            x *= np.float16(2.0**-9)
+        if big not in (which, "both"):
+            return
+        for b, n in enumerate(q):
+            blk, off = case.batch.slots(b, ctx[b] - n + n // 2, ctx[b] - n + n // 2 + 1)
+            x[blk[0], off[0]] = np.where(x[blk[0], off[0]] < 0, -65504, 65504)
+
+    c = Case(torch, bits, q, ctx, H, Hk, d, d, bs, kind, poison=poison)
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    seen = np.zeros(c.tokens, bool)  # the rows that do attend it: their scores are no fp32 sums to bound
+    for b, n in enumerate(q):
+        t0 = int(c.batch.starts[b])
+        seen[t0:t0 + n] = ref.sees(n, None if c.parents is None else c.parents[t0:t0 + n])[:, n // 2]
+    if max(q) > 2:
+        assert not seen.all()
+    c.check(slice(None) if big == "value" else ~seen)
+
+
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+@pytest.mark.parametrize("spread", [(0, 7), (0, 8), (0, 14), (0, 15), (-14, 13), (-24, 16)], ids=str)
+@pytest.mark.parametrize("which", ["key", "value", "both"])
+def test_rows_of_many_magnitudes_in_a_key_tile(torch, case, spread, which):
+    """Exponents as far apart as a key tile's common one reaches, one further, and as far as
+    fp16 goes, with zero rows among the widest."""
+    q, ctx, H, Hk, d, bs, kind = case
+    lo, hi = spread
+
+    def poison(case, x):
+        if which not in (("key", "value")[len(case.real)], "both"):
+            return
+        rng = np.random.default_rng(99)
+        e = rng.integers(lo, hi, x.shape[:3] + (1,))
+        x[:] = (rng.uniform(0.5, 0.99, x.shape) * 2.0**e * rng.choice([-1, 1], x.shape)).astype(np.float16)
+        if lo < -20:
+            x[rng.random(x.shape[:3]) < 0.1] = 0
+
+    c = Case(torch, 8, q, ctx, H, Hk, d, d, bs, kind, poison=poison, scale=2.0 ** -(hi + 3))
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    c.check()
