@@ -652,7 +652,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     float2* stat = reinterpret_cast<float2*>(smem + Cfg::stat_off);
     int tile = 0, n0 = 0, oc = 0;  // row tiles, key tiles, row tiles with keys
-    bool alive = true;  // agreed on by both groups, which meet at barriers
+    // Agreed on by both groups, which meet at barriers: that every warp has seen the next row tile told
+    // too (next_tile does not wait here), as one whose wait ran out would leave the others at one.
+    if (!tree_wait(&tile_full[0], 0)) ok = false;
+    bool alive = !tree_softmax_bar(!ok);
     TreeTile t;
     while (alive && next_tile(t)) {
       const int tiles = key_tiles(t), nj = QT * tiles;
@@ -781,6 +784,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         float2* st = stat + (tile & 1) * 256;
         st[g * 128 + m_lane] = make_float2(m_ref, l);
       }
+      if (!tree_wait(&tile_full[heard % Cfg::kAhead], (heard / Cfg::kAhead) & 1)) ok = false;
       alive = !tree_softmax_bar(!ok);
       if constexpr (QT == 1) {
         const float2* st = stat + (tile & 1) * 256;
