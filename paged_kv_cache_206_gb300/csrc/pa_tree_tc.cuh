@@ -488,9 +488,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       const int times = filled / nfulls + (i < filled % nfulls ? 1 : 0);
       if (times) tree_wait(&fulls[i], (times - 1) & 1);
     }
-    if constexpr (Q8)
-      for (int i = max(0, n - Cfg::kExps); i < n; ++i)
+    if constexpr (Q8) {
+      // (a tile's exponents come with its first part, which the second may not have followed)
+      const int with_exps = (filled + 1) / 2;
+      for (int i = max(0, with_exps - Cfg::kExps); i < with_exps; ++i)
         tree_wait(&exps_full[(is_k ? 0 : Cfg::kExps) + i % Cfg::kExps], (i / Cfg::kExps) & 1);
+    }
   } else if (warp == 1) {
     // ================= O_g += P_g V =================
     // Per key tile the two chains' products in turn (QT = 2: of its halves in turn).
