@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
 
     for (int un = t.s0; un < t.s1; ++un, ++n) {
       if (!tree_wait(&full[stage], phase)) {
-        // the copies in flight land before the CTA's memory is given back
+        // the copies in flight, this one among them, land before the CTA's memory is given back
         if (lane == 0) set_status(P.status, PA_STATUS_BIT_TIMEOUT);
-        for (++n; n < issued; ++n) {
-          if (++stage == Cfg::kStages) stage = 0, phase ^= 1;
+        for (; n < issued; ++n) {
           tree_wait(&full[stage], phase);
+          if (++stage == Cfg::kStages) stage = 0, phase ^= 1;
         }
         return;
       }
