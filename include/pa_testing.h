@@ -21,13 +21,14 @@ extern "C" {
 
 /*
  * pa_testing_set_wait_limit -- the cycle limit of the decode kernels' waits
- * (the CUDA-core, mma.sync and 64-row tcgen05 kernels), for every later
- * pa_forward / pa_forward_device_plan / pa_forward_noalloc call of the
+ * (the CUDA-core, mma.sync and 64-row tcgen05 kernels) and of the tree
+ * attention's, for every later pa_forward / pa_forward_device_plan /
+ * pa_forward_noalloc / pa_tree_forward call of the
  * process; 0 restores the default (about two seconds). Under a lowered limit
  * the CUDA-core and mma.sync kernels poll their copies without suspending, so
  * a copy that has not landed within the limit makes the wait run out; the
- * tcgen05 kernel keeps its suspending polls, so there a wait runs out when it
- * outlasts one suspension and the limit (its waits on other roles do). The
+ * tcgen05 kernels keep their suspending polls, so there a wait runs out when it
+ * outlasts one suspension and the limit (their waits on other roles do). The
  * waits a CTA makes for its own copies and tensor-core operations before it
  * exits keep the default whatever this is, and the prefill kernels always use
  * the default. Returns PA_ERR_INVALID_ARG for a negative value.

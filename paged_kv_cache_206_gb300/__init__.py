@@ -254,8 +254,8 @@ def hbm_read_probe(buf, ctas_per_sm: int, sink, stream=None) -> None:
 
 
 def testing_set_wait_limit(cycles: int) -> None:
-    """Test hook (pa_testing_set_wait_limit): the cycle limit of the decode
-    kernels' waits on other roles for later launches; 0 restores the default."""
+    """Test hook (pa_testing_set_wait_limit): the cycle limit of the decode and
+    tree kernels' waits on other roles for later launches; 0 restores the default."""
     _check(load_library().pa_testing_set_wait_limit(int(cycles)), "pa_testing_set_wait_limit")
 
 

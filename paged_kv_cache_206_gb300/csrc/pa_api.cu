@@ -172,11 +172,16 @@ bool query_map(CUtensorMap* m, const void* query, const pa_config& c, int blocks
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Cycle limit of the decode kernels' waits on other roles (0: the default);
+// Cycle limit of the decode and tree kernels' waits on other roles (0: the default);
 // set only through pa_testing_set_wait_limit.
 std::atomic<long long> g_wait_limit{0};
 
 }  // namespace
+
+long long wait_limit() {
+  const long long cycles = g_wait_limit.load(std::memory_order_relaxed);
+  return cycles > 0 ? cycles : kWaitLimitCycles;
+}
 
 pa_status check_forward(const pa_config* cfg, const void* query, const void* key_cache,
                         const void* value_cache, const int32_t* block_tables,
@@ -262,8 +267,7 @@ pa_status forward_impl(const pa_config* cfg, const void* query, const void* key_
   P.mask_kv = int64_t(c.max_blocks_per_seq) * c.block_size;
   const float scale = c.scale > 0.f ? c.scale : 1.0f / std::sqrt(float(hk));
   P.scale_log2 = scale * kLog2e;
-  const long long wlim = g_wait_limit.load(std::memory_order_relaxed);
-  P.wait_limit = wlim > 0 ? wlim : kWaitLimitCycles;
+  P.wait_limit = wait_limit();
 
   cudaError_t err;
   if (TR <= PA_FMA_MAX_ROWS) {

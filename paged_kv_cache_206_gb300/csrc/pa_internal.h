@@ -15,6 +15,9 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // (head sizes multiple of 16, supported mask types).
 pa_status validate_config(const pa_config* cfg);
 
+// Cycle limit of the kernels' waits on other roles (pa_testing_set_wait_limit).
+long long wait_limit();
+
 inline int64_t max_q(const pa_config& c) { return c.max_seqlen_q > 0 ? c.max_seqlen_q : 1; }
 
 // Tokens per TMA box of a kernel with `tile`-token key tiles (a power of two):

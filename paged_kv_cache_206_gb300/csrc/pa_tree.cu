@@ -2,6 +2,7 @@
 // choice of the kernel, and the kernel for the largest heads.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "pa_internal.h"
@@ -265,6 +266,7 @@ extern "C" pa_status pa_tree_forward(const pa_config* cfg, int64_t tokens, const
   P.max_blocks_per_seq = c.max_blocks_per_seq;
   P.max_q = int(max_q(c));
   P.scale_log2 = (c.scale > 0.f ? c.scale : 1.0f / std::sqrt(float(c.head_size_k))) * kLog2e;
+  P.wait_limit = uint32_t(std::min<long long>(wait_limit(), kTreeWaitLimit));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   cudaError_t e = cudaSuccess;
   if (tree_tiles(c, P, key_exps != nullptr, nullptr, workspace, stream, &e))

@@ -8,6 +8,8 @@
 
 namespace pa {
 
+// Cycles of a wait that has no other limit, about a second and a half: the 32-bit clock tells it.
+constexpr uint32_t kTreeWaitLimit = 3u << 30;
 constexpr int kTreeWords = PA_TREE_MAX_TOKENS / 32;  // ancestor bits of one draft
 
 struct TreeParams {
@@ -21,6 +23,7 @@ struct TreeParams {
   int batch, num_heads, kv_heads, group, hk, hv, block_size, num_blocks, max_blocks_per_seq;
   int max_q;
   float scale_log2;  // scale * log2(e)
+  uint32_t wait_limit;  // cycles a wait on another role's progress may take
 };
 
 // Whether a sequence's lengths keep the constraints.

@@ -104,12 +104,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // for the others the compiler let that lane run apart from them for long after
 // the wait, and every shuffle of the code behind it took some 300 cycles (a tile of
 // codes 11,000 to convert instead of 2,000).
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, uint32_t limit = kTreeWaitLimit) {
+  const uint32_t t0 = clock();
 #pragma unroll 1
   do {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
+  } while (__all_sync(0xffffffffu, uint32_t(clock()) - t0 <= limit));
+  return false;
+}
+
+// The same for a copy of the warp's own under a lowered limit (tests): its polls do not suspend, so
+// that the limit decides. Not inlined: no other call reaches it.
+inline __device__ __noinline__ bool tree_wait_lowered(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  const uint32_t t0 = clock();
+#pragma unroll 1
+  do {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  } while (__all_sync(0xffffffffu, uint32_t(clock()) - t0 <= limit));
   return false;
 }
 
@@ -315,7 +326,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     }
 
     for (int un = t.s0; un < t.s1; ++un, ++n) {
-      if (!tree_wait(&full[stage], phase)) {
+      if (!(P.wait_limit == kTreeWaitLimit ? tree_wait(&full[stage], phase)
+                                             : tree_wait_lowered(&full[stage], phase, P.wait_limit))) {
         // the copies in flight, this one among them, land before the CTA's memory is given back
         if (lane == 0) set_status(P.status, PA_STATUS_BIT_TIMEOUT);
         for (; n < issued; ++n) {

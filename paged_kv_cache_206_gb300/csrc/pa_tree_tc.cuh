@@ -116,12 +116,12 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // tree_wait for two barriers at once.
-__device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
-  const long long t0 = clock64();
+__device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint32_t limit) {
+  const uint32_t t0 = clock();
 #pragma unroll 1
   do {
     if (__all_sync(0xffffffffu, mbar_try_wait(a, pa) & mbar_try_wait(b, pb))) return true;
-  } while (__all_sync(0xffffffffu, clock64() - t0 <= kWaitLimitCycles));
+  } while (__all_sync(0xffffffffu, uint32_t(clock()) - t0 <= limit));
   return false;
 }
 
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     __syncwarp();
     if (heard > 0 && lane == 0) mbar_arrive(&tile_empty[(heard - 1) % Cfg::kAhead]);
     const int at = heard % Cfg::kAhead;
-    if (!tree_wait(&tile_full[at], (heard / Cfg::kAhead) & 1)) return false;
+    if (!tree_wait(&tile_full[at], (heard / Cfg::kAhead) & 1, P.wait_limit)) return false;
     t = told[at];
     ++heard;
     return t.q >= 0;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             uint64_t* full = &fulls[2 * round + p];
-            if (!tree_wait(&empties[p ? slot1 : slot], (p ? phase1 : phase) ^ 1)) {
+            if (!tree_wait(&empties[p ? slot1 : slot], (p ? phase1 : phase) ^ 1, P.wait_limit)) {
               ok = false;
               break;
             }
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           slot = slot1 + 1 == nslots ? 0 : slot1 + 1;
           phase = slot == 0 ? phase1 ^ 1 : phase1;
         } else {
-          if (!tree_wait(&empties[slot], phase ^ 1)) {
+          if (!tree_wait(&empties[slot], phase ^ 1, P.wait_limit)) {
             ok = false;
             break;
           }
@@ -520,11 +520,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         __syncwarp();
       };
       // the last row tile's O has been read before the first product overwrites it
-      if (tile > 0 && !tree_wait(o_free, (tile - 1) & 1)) ok = false;
+      if (tile > 0 && !tree_wait(o_free, (tile - 1) & 1, P.wait_limit)) ok = false;
       for (int i = 0; i < tiles && ok; ++i) {
         const int n = n0 + i, phase = phase_of(n);
         const bool last = i + 1 == tiles;
-        if (!tree_wait(&vfull[vslot], vphase)) { ok = false; break; }
+        if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) { ok = false; break; }
         if constexpr (!Q8) {
           // Rows behind the context may hold anything and become 0; non-finite
           // elements of the drafts' rows leave the product
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 2 * QT; ++j) {
           const int g = j & 1, hf = QT == 2 ? j >> 1 : g, y = QT == 2 ? hf : n & 1;
-          if (!tree_wait(&p_full[2 * g + y], phase)) { ok = false; break; }
+          if (!tree_wait(&p_full[2 * g + y], phase, P.wait_limit)) { ok = false; break; }
           pv(g, y, hf, tmem_s + (QT == 2 ? g : n & 1) * 128 + hf * 64, i != 0 || (QT == 2 && hf), j == 2 * QT - 1,
              last && (QT == 1 || hf));
         }
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       following = place->tile;
       if (!some) following.q = -1;
       const int at = told_n % Cfg::kAhead;
-      if (!tree_wait(&tile_empty[at], ((told_n / Cfg::kAhead) & 1) ^ 1)) {
+      if (!tree_wait(&tile_empty[at], ((told_n / Cfg::kAhead) & 1) ^ 1, P.wait_limit)) {
         ok = false;
         return;
       }
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       t = following;
       const int tiles = uni(key_tiles(t));
       // the queries, once the last row tile's S are complete
-      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1)) {
+      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit)) {
         ok = false;
         break;
       }
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       fence_proxy_async();
       __syncwarp();
       for (int i = 0; i < tiles && ok; ++i, ++n) {
-        if (!tree_wait(&kfull[kslot], kphase)) { ok = false; break; }
+        if (!tree_wait(&kfull[kslot], kphase, P.wait_limit)) { ok = false; break; }
         const bool last = i + 1 == tiles;
         const uint64_t bk = dk + uint32_t(kslot * (Cfg::kTile >> 4));
 #pragma unroll
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           // has been read
           const int x = QT == 2 ? g : n & 1, nb = QT == 2 ? n - 1 : n - 2;
           if (nb >= 0 && !tree_wait2(&pv_done[QT == 2 ? 2 * g : x], phase_of(nb), &pv_done[QT == 2 ? 2 * g + 1 : 2 + x],
-                                     phase_of(nb))) {
+                                     phase_of(nb), P.wait_limit)) {
             ok = false;
             break;
           }
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     int tile = 0, n0 = 0, oc = 0;  // row tiles, key tiles, row tiles with keys
     // Agreed on by both groups, which meet at barriers: that every warp has seen the next row tile told
     // too (next_tile does not wait here), as one whose wait ran out would leave the others at one.
-    if (!tree_wait(&tile_full[0], 0)) ok = false;
+    if (!tree_wait(&tile_full[0], 0, P.wait_limit)) ok = false;
     bool alive = !tree_softmax_bar(!ok);
     TreeTile t;
     while (alive && next_tile(t)) {
@@ -693,13 +693,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         int2 e = make_int2(0, 0);
         if constexpr (Q8) {
           const int k = n % Cfg::kMeta;
-          if (!tree_wait(&meta_full[k], (n / Cfg::kMeta) & 1)) { ok = false; break; }
+          if (!tree_wait(&meta_full[k], (n / Cfg::kMeta) & 1, P.wait_limit)) { ok = false; break; }
           e = meta[k];
           F = fmaxf(F * pow2((e.x & 255) - kExpBias), FLT_MIN);  // (0 times the -inf of a masked score is NaN)
           ev = float((e.y & 255) - kExpBias);
           unscale = pow2(kExpBias - (e.y & 255));
         }
-        if (!tree_wait(&s_full[x_of_s], phase)) { ok = false; break; }
+        if (!tree_wait(&s_full[x_of_s], phase, P.wait_limit)) { ok = false; break; }
         tc_fence_after();
         if (any_row) {
           __syncwarp();
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           float2 own;  // of keys with exponents of their own: the largest score, the sum
           if (Q8 && ((e.x | e.y) & 256)) {
             const int em = n % Cfg::kExps, ph = (n / Cfg::kExps) & 1;
-            if (!tree_wait2(&exps_full[em], ph, &exps_full[Cfg::kExps + em], ph)) ok = false;
+            if (!tree_wait2(&exps_full[em], ph, &exps_full[Cfg::kExps + em], ph, P.wait_limit)) ok = false;
             tree_apart<Cfg::kSpreadK, Cfg::kSpreadV>(sbuf, smem + Cfg::exps_off + em * 256 + hf * 64, e, P.scale_log2,
                                                      t.L - key0, P.parents ? bits : nullptr, qi, key0 - prefix, &own);
             F = 1.f;
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           if (m > 0 && __any_sync(FULL, grow)) {
             // O as the chain's job before left it
             const int nb = QT == 2 && hf ? n : n - 1, yb = QT == 2 ? hf ^ 1 : nb & 1;
-            if (!tree_wait(&pv_done[2 * g + yb], phase_of(nb))) ok = false;
+            if (!tree_wait(&pv_done[2 * g + yb], phase_of(nb), P.wait_limit)) ok = false;
             tc_fence_after();
             const uint32_t o_mine = uni(tmem_o + g * 128 + lane_base);
 #pragma unroll 1
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         float2* st = stat + (tile & 1) * 256;
         st[g * 128 + m_lane] = make_float2(m_ref, l);
       }
-      if (!tree_wait(&tile_full[heard % Cfg::kAhead], (heard / Cfg::kAhead) & 1)) ok = false;
+      if (!tree_wait(&tile_full[heard % Cfg::kAhead], (heard / Cfg::kAhead) & 1, P.wait_limit)) ok = false;
       alive = !tree_softmax_bar(!ok);
       if constexpr (QT == 1) {
         const float2* st = stat + (tile & 1) * 256;
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       if (tiles > 0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if ((QT == 1 || k == g) && ok && !tree_wait(&o_full[k], oc & 1)) ok = false;
+          if ((QT == 1 || k == g) && ok && !tree_wait(&o_full[k], oc & 1, P.wait_limit)) ok = false;
         ++oc;
       }
       tc_fence_after();
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     // The largest exponent of the tile in slot `es`, `keys` of whose rows are the context's; of each kind
     // the first part's warp tells the softmax, and whether some lie far below it.
     auto look = [&](int keys, int es, int ph, int m, int& top) {
-      if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph)) return false;
+      if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
       const int left = keys - lane * 4;  // of this lane's four
       int low = 255;
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       for (int i = 0; i < tiles; ++i) {
         const int key0 = (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
-        if (!tree_wait(&landed[2 * round], lphase)) {
+        if (!tree_wait(&landed[2 * round], lphase, P.wait_limit)) {
           ok = false;
           break;
         }
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           const uint32_t diff = uint32_t(top) - exps[(part & 1) * 64 + sub * ROWS + 32 * k + lane];
           fac[k] = (15u - min(diff, uint32_t(kv ? Cfg::kSpreadV : Cfg::kSpreadK))) * 0x04000400u;
         }
-        if (!tree_wait(&empty[slot], phase ^ 1)) {
+        if (!tree_wait(&empty[slot], phase ^ 1, P.wait_limit)) {
           ok = false;
           break;
         }
