@@ -7,6 +7,11 @@ stamp (machine, compiler version, flags) matches the one the objects were made
 with; objects from another machine or compiler are never reused. The CUDA runtime
 is linked statically and the driver is reached through the runtime's
 entry-point query, so the library loads on a machine without a GPU.
+
+The Python module of ``csrc/pa_call.c``, through which serving.py calls the library,
+is built next to it for the interpreter that runs the build (its file name has the
+interpreter's tag, as any extension module's). Where Python's headers are missing it
+is left out, and the serving calls go through ctypes.
 """
 from __future__ import annotations
 
@@ -25,7 +30,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
-CALL = os.path.join(BUILD, "pa_call.so")  # the Python module of csrc/pa_call.c
+# the Python module of csrc/pa_call.c, as this interpreter names its extension modules
+CALL = os.path.join(BUILD, "pa_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -58,13 +64,20 @@ def _stamp(cc: str) -> str:
 
 
 def _build_call(force: bool) -> None:
-    """The module through which serving.py calls the library (host code only)."""
+    """The module through which serving.py calls the library (host code only);
+    none where this Python has no headers."""
     src = os.path.join(CSRC, "pa_call.c")
+    headers = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers, "Python.h")):
+        if os.path.exists(CALL):
+            os.remove(CALL)  # of another machine's, or of older sources
+        print(f"pa_call.c is left out ({headers} has no Python.h): serving calls go through ctypes")
+        return
     if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= os.path.getmtime(src):
         return
     tmp = CALL + f".tmp{os.getpid()}"
     r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-Wall", "-std=c11", "-shared", "-fPIC",
-                        f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp],
+                        f"-I{headers}", src, "-o", tmp],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on pa_call.c:\n{r.stderr}")
@@ -79,7 +92,6 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     stamp = _stamp(cc)
     if not os.path.exists(stamp_path) or open(stamp_path).read().strip() != stamp:
         force = True  # objects (if any) from another machine, compiler or flag set
-    _build_call(force)
     hdr = _headers_mtime()
     objs, todo = [], []
     for src in sources():
@@ -116,6 +128,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         os.replace(tmp, LIB)
         with open(stamp_path, "w") as f:
             f.write(stamp + "\n")
+    _build_call(force)
     return LIB
 
 

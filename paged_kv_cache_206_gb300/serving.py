@@ -54,13 +54,20 @@ def _start():
         ctypes.cast(f, ctypes.c_void_p).value
         for f in (lib.pa_qk_norm_rope, lib.pa_cache_write, lib.pa_cache_store, lib.pa_cache_read,
                   lib.pa_tree_forward))
-    if not os.path.exists(CALL):
-        raise RuntimeError(f"{CALL} is missing: run paged_kv_cache_206_gb300.build_lib.build()")
-    spec = importlib.util.spec_from_file_location("pa_call", CALL)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    _call = module.call
+    if os.path.exists(CALL):
+        spec = importlib.util.spec_from_file_location("pa_call", CALL)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _call = module.call
+    else:  # built without Python's headers
+        _call = _ctypes_call
     _f16 = torch.float16
+
+
+def _ctypes_call(address, *args):
+    """What csrc/pa_call.c does, 3 to 5 us slower."""
+    words = [None if a is None else a & (2**64 - 1) for a in args]
+    return ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * len(args))(address)(*words)
 
 
 class _Configs(dict):

@@ -282,3 +282,40 @@ def test_a_configuration_lives_as_long_as_its_call(monkeypatch, call):
     else:
         cache.read(table, None, ints, torch.zeros_like(ints), 1, out, rows)
     assert calls == [2 if call == "store" else 1]
+
+
+def test_the_build_does_without_pythons_headers(monkeypatch, tmp_path, lib):
+    """The library is built (and a module of other sources taken away) where there is no Python.h."""
+    called = tmp_path / "pa_call.so"
+    called.write_bytes(b"")
+    monkeypatch.setattr(build_lib, "CALL", str(called))
+    monkeypatch.setattr(build_lib.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build_lib.build() == build_lib.LIB
+    assert not called.exists()
+
+
+def test_the_module_is_named_for_its_interpreter():
+    import sysconfig
+    assert build_lib.CALL.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+@pytest.mark.parametrize("module", [True, False])
+def test_calls_with_and_without_the_module(monkeypatch, lib, module):
+    """Both ways reach the library with every argument in its place."""
+    from paged_kv_cache_206_gb300 import serving
+    monkeypatch.setattr(serving, "_f16", None)
+    if not module:
+        monkeypatch.setattr(build_lib, "CALL", "/nonexistent")
+    serving._start()
+    assert (serving._call is serving._ctypes_call) == (not module)
+    config = cache()
+
+    def read(rows, k_out, v_out):
+        return serving._call(serving._read, ctypes.addressof(config), FAKE.value, FAKE.value, OTHER.value,
+                             OTHER.value, FAKE.value, None, FAKE.value, FAKE.value, rows, k_out, v_out, None, 0)
+    assert read(0, FAKE.value, OTHER.value) == pa.PA_OK
+    assert read(-1, FAKE.value, OTHER.value) == pa.PA_ERR_INVALID_ARG
+    assert read(0, FAKE.value, FAKE.value) == pa.PA_ERR_INVALID_ARG
+    assert read(0, FAKE.value, BAD.value) == pa.PA_ERR_INVALID_ARG
+    monkeypatch.undo()
+    serving._start()
