@@ -455,6 +455,7 @@ rows_kernel(const RowParams P) {
 template <int MODE, bool IL>
 pa_status launch_rows(RowParams P, cudaStream_t stream) {
   if (P.tokens == 0) return PA_OK;
+  if (P.tokens > INT32_MAX) return PA_ERR_INVALID_ARG;  // (before it is multiplied)
   const int widest = (MODE == kRotate || P.hk > P.hv ? P.hk : P.hv) / 16;  // chunk pairs of a row
   while ((1 << P.lane_shift) < widest && P.lane_shift < 5) ++P.lane_shift;
   P.inv_hk = 1.0f / float(P.hk);
@@ -468,7 +469,7 @@ pa_status launch_rows(RowParams P, cudaStream_t stream) {
   const bool many = widest <= 32 && slice(per_warp * kRows * kBatches) >= kManyWarps;
   P.batches = many ? kBatches : 1;
   if (!many) slice(per_warp);
-  if (P.tokens > INT32_MAX || P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
+  if (P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
   const int check = MODE != kRotate && P.status ? 1 : 0;  // a warp for the lengths
   const unsigned grid = unsigned(cdiv(P.tokens * P.slices + check, 8));
   if (many) rows_kernel<MODE, 1, kRows, IL><<<grid, 256, 0, stream>>>(P);

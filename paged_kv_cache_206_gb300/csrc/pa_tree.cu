@@ -239,7 +239,7 @@ extern "C" pa_status pa_tree_forward(const pa_config* cfg, int64_t tokens, const
       !aligned(workspace, 256))
     return PA_ERR_INVALID_ARG;
   if (workspace_bytes < need) return PA_ERR_BUFFER_TOO_SMALL;
-  if (tokens * c.num_heads > INT32_MAX) return PA_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX / c.num_heads) return PA_ERR_INVALID_ARG;
   if (tokens == 0) return PA_OK;
   if (out == query) return PA_ERR_INVALID_ARG;  // a tile in parts reads its rows after others wrote theirs
   TreeParams P{};

@@ -319,3 +319,17 @@ def test_calls_with_and_without_the_module(monkeypatch, lib, module):
     assert read(0, FAKE.value, BAD.value) == pa.PA_ERR_INVALID_ARG
     monkeypatch.undo()
     serving._start()
+
+
+@pytest.mark.parametrize("tokens", [2**31, 2**58, 2**60, 2**61, 2**62, 2**63 - 1])
+def test_numbers_of_tokens_whose_products_pass_64_bits_are_refused(lib, tokens):
+    """Before anything is launched: on a machine without a GPU a launch would be PA_ERR_CUDA."""
+    assert call_rotate(lib, tokens=tokens) == pa.PA_ERR_INVALID_ARG
+    assert call_rotate(lib, rotary(num_heads=8, kv_heads=8), tokens=tokens, qs=512, ks=512) == pa.PA_ERR_INVALID_ARG
+    assert call_write(lib, tokens=tokens) == pa.PA_ERR_INVALID_ARG
+    assert call_write(lib, store=rotary(), tokens=tokens) == pa.PA_ERR_INVALID_ARG
+    for heads in (8, 32):
+        for d in (64, 128, 272):
+            cfg = tree_cfg(num_heads=heads, head_size_k=d)
+            assert lib.pa_tree_forward(ctypes.byref(cfg), tokens, FAKE, FAKE, OTHER, None, None, FAKE, FAKE, FAKE,
+                                       FAKE, FAKE, 1 << 40, OTHER, None) == pa.PA_ERR_INVALID_ARG
