@@ -174,10 +174,10 @@ pa_status check_tree(const pa_config* cfg) {
 // with the narrower of their 8- and 16-row tiles that holds the rows, and the least
 // of 64, 128 and 256 dims that hold a head; for more rows of 64 or 128 dims the tcgen05
 // tensor cores, of other sizes several of the 16-row tiles. Of 64 sequences of up to
-// 4096 keys, 8 kv heads of 128 dims, 16 rows take 59 us (8 bits) and 83 us (fp16) here and
-// 92 and 83 us there; one sequence of 1024 keys 16 us here, 23 and 17 us there. With
-// 32 rows the warp-level instructions took 121 and 132 us (25 and 26 us for the one
-// sequence), the others take 94 and 87 us (23 and 17 us).
+// 4096 keys, 8 kv heads of 128 dims, 16 rows take 60 us (8 bits) and 89 us (fp16) here and
+// 91 and 84 us there; one sequence of 1024 keys 19 and 18 us here, 21 and 16 us there. With
+// 32 rows the warp-level instructions take 104 and 164 us (20 and 18 us for the one
+// sequence), the others 93 and 86 us (22 and 16 us).
 bool tree_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws,
                 cudaStream_t stream, cudaError_t* e) {
   const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;

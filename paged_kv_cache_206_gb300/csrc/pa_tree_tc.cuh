@@ -55,8 +55,8 @@ struct TreeTc {
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
   // What a row tile costs next to its key tiles, in these, measured at 32 trees over 64 to 8192
-  // keys, heads of 128: trees of 16 in 8 bits 90 us at 3, 83 at 5, 85 at 8, 88 at 12; of 64 in fp16
-  // 129, 128, 129 and 132 (and 16 of those 75, 77 and 80).
+  // keys, heads of 128: trees of 5 to 16 in 8 bits 108 us at 3, 97 at 5, 95 at 6, 96 at 8, 99 at 12; of
+  // 64 in fp16 144 at 3, 135 at 4, 132 at 5, 136 at 8 (and 16 of those 75, 76, 77 and 81).
   static constexpr int kLead = Q8 ? 6 : 4;
   static constexpr int kHalves = HD / 64;
   static constexpr uint32_t kHalf = 128 * 128;           // 64 dims of 128 fp16 rows
@@ -64,8 +64,8 @@ struct TreeTc {
   static constexpr int kKSlots = Q8 || QT == 2 ? 2 : 3;
   static constexpr int kVSlots = Q8 ? 1 : 2;
   static constexpr uint32_t kStageBytes = 64 * HD;       // 64 rows of codes
-  // Stages for the codes rather than a second V operand (trees of 16: 88.5 us, 92.3 with two V
-  // slots and 4 + 3 stages, 107 with one K slot and 7 + 8)
+  // Stages for the codes rather than a second V operand (trees of 16, when this was chosen: 88.5 us, 92.3
+  // with two V slots and 4 + 3 stages, 107 with one K slot and 7 + 8)
   static constexpr int kKStages = Q8 ? (QT == 1 ? 5 : 4) : 0, kVStages = Q8 ? (QT == 1 ? 6 : 3) : 0;
   static constexpr int kStages = kKStages + kVStages;
   // Barriers of the parts that have landed: of each part (rows 0.., rows 64..) of as many key tiles
