@@ -185,3 +185,43 @@ def test_caches_past_32_bit_offsets(torch, bits):
         torch.cuda.empty_cache()
     for small, far in zip(*kinds):
         assert torch.equal(small, far) and bool(small.isfinite().all())
+
+
+def test_two_threads_at_once(torch):
+    """A thread that attends and one that reads the same 8-bit cache back, each on a stream of its own and
+    with configurations that change from call to call."""
+    import threading
+
+    from paged_kv_cache_206_gb300 import serving
+    c = Case(torch, 8, [4] * 6, [500, 30, 900, 4, 77, 260], 8, 2, 128, 128, 16, "tree")
+    (k, ke), (v, ve) = c.dev
+    cache = pa.QuantCache(k, v, ke, ve)
+    n = int(c.batch.ctx.sum())
+    at = up(torch, (np.cumsum(c.batch.ctx) - c.batch.ctx).astype(np.int32))
+    kv = [torch.zeros((n, 2, 128), dtype=torch.float16, device="cuda") for _ in range(2)]
+    want = c.run().clone()
+    cache.read(c.args[1], None, c.args[2], at, 900, *kv)
+    held = [t.clone() for t in kv]
+    torch.cuda.synchronize()
+    wrong, streams = [], [torch.cuda.Stream() for _ in range(2)]
+
+    def attend():
+        with torch.cuda.stream(streams[0]):
+            for _ in range(300):
+                if not torch.equal(c.run(), want):
+                    wrong.append("attention")
+
+    def read():
+        with torch.cuda.stream(streams[1]):
+            for i in range(300):
+                cache.read(c.args[1], None, c.args[2], at, 900 + i, *kv)
+                cache._configs.clear()
+                serving._rotations.clear()
+                if not all(torch.equal(a, b) for a, b in zip(kv, held)):
+                    wrong.append("read")
+    threads = [threading.Thread(target=f) for f in (attend, read)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
