@@ -99,14 +99,13 @@ MapCache& map_cache() {
 // The map for key k (fp16 elements; the row stride follows from the dims).
 bool cached_map(CUtensorMap* m, const MapKey& k, const cuuint64_t* strides) {
   if (map_cache().get(k, m)) return true;
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
   cuuint64_t dims[3] = {k.dims[0], k.dims[1], k.dims[2]};
   cuuint32_t box[3] = {k.box[0], k.box[1], k.box[2]};
   cuuint32_t es[3] = {1, 1, 1};
-  if (enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cuuint32_t(k.rank), const_cast<void*>(k.base), dims,
-          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CUtensorMapSwizzle(k.swizzle),
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  if (!encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cuuint32_t(k.rank),
+                         const_cast<void*>(k.base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CUtensorMapSwizzle(k.swizzle),
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE))
     return false;
   map_cache().put(k, *m);
   return true;

@@ -27,6 +27,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// Encodes a tensor map (the arguments are cuTensorMapEncodeTiled's). The driver wants a current
+// context, and a thread that has made no runtime call yet has none: cudaSetDevice binds its device's.
+template <class... Args>
+inline bool encode_tensor_map(Args... args) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  CUresult r = encode(args...);
+  int device = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess &&
+      cudaSetDevice(device) == cudaSuccess)
+    r = encode(args...);
+  return r == CUDA_SUCCESS;
+}
+
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device) rather
 // than on every launch.
 inline cudaError_t ensure_smem_attr(const void* kern, int bytes) {

@@ -10,15 +10,13 @@ namespace pa {
 // A cache as (bytes of a row, kv heads, token rows), a box being up to 128 bytes of
 // `box` tokens of one head, swizzled, zeros behind a row's end.
 inline bool tree_rows_map(CUtensorMap* m, const void* base, const TreeParams& P, int row_bytes, int part, int box) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
   const cuuint64_t dims[3] = {cuuint64_t(row_bytes), cuuint64_t(P.kv_heads),
                               cuuint64_t(P.num_blocks) * P.block_size};
   const cuuint64_t strides[2] = {cuuint64_t(row_bytes), cuuint64_t(P.kv_heads) * row_bytes};
   const cuuint32_t b[3] = {cuuint32_t(part), 1, cuuint32_t(box)}, es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, b, es,
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, b, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, part == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int HD, bool Q8, int NT>

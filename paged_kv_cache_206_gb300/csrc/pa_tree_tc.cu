@@ -13,23 +13,21 @@ namespace {
 // being `box` tokens of one block with the 128-byte swizzle; the 8-bit cache as
 // (bytes of a row, token rows), a box being `box` tokens of one head.
 bool tree_map(CUtensorMap* m, const void* base, const TreeParams& P, bool q8, int box) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
   const cuuint64_t rows = cuuint64_t(P.num_blocks) * P.block_size;
   const cuuint32_t es[3] = {1, 1, 1};
   if (q8) {
     const cuuint64_t dims[2] = {cuuint64_t(P.kv_heads) * P.hk, rows}, strides[1] = {dims[0]};
     const cuuint32_t b[2] = {cuuint32_t(P.hk), cuuint32_t(box)};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, b, es,
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, b, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   const cuuint64_t dims[3] = {64, rows, cuuint64_t(P.kv_heads) * (P.hk / 64)};
   const cuuint64_t strides[2] = {cuuint64_t(P.kv_heads) * P.hk * 2, 128};
   const cuuint32_t b[3] = {64, cuuint32_t(box), 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, b, es,
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, b, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int HD, bool Q8, int QT>

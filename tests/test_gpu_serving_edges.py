@@ -219,9 +219,42 @@ def test_two_threads_at_once(torch):
                 serving._rotations.clear()
                 if not all(torch.equal(a, b) for a, b in zip(kv, held)):
                     wrong.append("read")
-    threads = [threading.Thread(target=f) for f in (attend, read)]
+    def kept(f):
+        try:
+            f()
+        except Exception as e:  # a thread's own exception ends no test
+            wrong.append(e)
+    threads = [threading.Thread(target=kept, args=(f,)) for f in (attend, read)]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
-    assert not wrong
+    assert not wrong, wrong
+
+
+@pytest.mark.parametrize("call", [(8, 2, 64, 2), (8, 2, 256, 2), (16, 1, 128, 6), (4, 2, 272, 2), "forward"], ids=str)
+def test_a_threads_first_cuda_call(torch, call):
+    """In a thread that has called nothing of CUDA before."""
+    import threading
+    if call == "forward":
+        from paged_kv_cache_206_gb300 import workloads as W
+        db = pa.DeviceBatch(W.gqa_decode(batch=3, max_len=500, seed=77))
+        run, status = db.forward, db.status
+    else:
+        H, Hk, d, q = call
+        c = Case(torch, 8, [q, 1], [300, 40], H, Hk, d, d, 16, "tree")
+        run, status = c.run, c.step.status
+    torch.cuda.synchronize()
+    failed = []
+
+    def first():
+        try:
+            run()
+        except Exception as e:
+            failed.append(e)
+    t = threading.Thread(target=first)
+    t.start()
+    t.join()
+    assert not failed and status() == (pa.PA_OK, 0), failed
+    got = (db.out if call == "forward" else c.out).clone()
+    assert torch.equal(run(), got)
