@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32) lengths_kernel(const int32_t* q_seqlens, i
 // Bytes bound these rows, and come close: 8192 tokens of 32 + 8 heads of 128 are turned in
 // 32.5 us (25.3 at the copy rate; issue slots 66 % full), and 2 x 32 heads of as many
 // written to 8 bits in 37 (29.6; conversions and maxima keep the ALU 64 % busy). The store
-// of 8 prompts of 1 to 2048 tokens, 48 heads, takes 47 us (53 with a cold cache) for 24 us of
+// of 8 prompts of 1 to 2048 tokens, 48 heads, takes 47 us (51 with a cold cache) for 24 us of
 // bytes: it makes the factors, looks the token up and quantises. Registers are held to what lets 32
 // warps an SM (40 in the write) have loads in flight; a warp that loaded the next token's rows
 // ahead, at half the warps, was slower (39 us for the 8192 tokens).
