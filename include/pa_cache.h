@@ -99,6 +99,36 @@ pa_status pa_qk_norm_rope(const pa_rotary* rot, int64_t tokens, const void* quer
                           void* stream);
 
 /*
+ * Positions of several axes, as tokens of images and video have them (time, height,
+ * width): pair i of the rotation turns by the position of one of them.
+ *
+ *   count     axes, 1 to PA_MAX_AXES
+ *   cyclic    0: the first sections[0] pairs turn by axis 0, the next sections[1] by
+ *             axis 1, and so on. Else pair i turns by axis a = i % count where a > 0 and
+ *             i < count * sections[a], and by axis 0 otherwise
+ *   sections  pairs of each axis, >= 0, together rotary_dim / 2; cyclic: each axis but
+ *             the first finds its places, count * (sections[a] - 1) + a < rotary_dim / 2
+ */
+#define PA_MAX_AXES 4
+typedef struct pa_axes {
+  int32_t count;
+  int32_t cyclic;
+  int32_t sections[PA_MAX_AXES];
+} pa_axes;
+
+/*
+ * pa_qk_norm_rope_axes -- pa_qk_norm_rope with positions int32 [axes->count][tokens].
+ * A token one of whose positions is -1 is left out as padding; one outside [-1,
+ * max_positions) sets the POSITION bit and leaves its token out. Tokens whose
+ * positions are the same on every axis get the bits that pa_qk_norm_rope gives.
+ */
+pa_status pa_qk_norm_rope_axes(const pa_rotary* rot, const pa_axes* axes, int64_t tokens,
+                               const void* query, int64_t query_stride, const void* key,
+                               int64_t key_stride, const void* q_weight, const void* k_weight,
+                               const float* cos_sin, const int32_t* positions, void* q_out,
+                               void* k_out, uint32_t* status, void* stream);
+
+/*
  * The 8-bit cache and a batch over it.
  *
  *   batch               0 < B <= 2048
@@ -158,6 +188,20 @@ pa_status pa_cache_store(const pa_cache_config* cfg, const pa_rotary* rot, int64
                          const int32_t* context_lens, const int32_t* q_seqlens, void* key_cache,
                          uint8_t* key_exps, void* value_cache, uint8_t* value_exps, void* q_out,
                          uint32_t* status, void* stream);
+
+/*
+ * pa_cache_store_axes -- pa_cache_store with positions int32 [axes->count][tokens], as in
+ * pa_qk_norm_rope_axes (not NULL; where a token is stored goes by the lengths alone).
+ */
+pa_status pa_cache_store_axes(const pa_cache_config* cfg, const pa_rotary* rot,
+                              const pa_axes* axes, int64_t tokens, const void* query,
+                              int64_t query_stride, const void* key, int64_t key_stride,
+                              const void* value, int64_t value_stride, const void* q_weight,
+                              const void* k_weight, const float* cos_sin,
+                              const int32_t* positions, const int32_t* block_tables,
+                              const int32_t* context_lens, const int32_t* q_seqlens,
+                              void* key_cache, uint8_t* key_exps, void* value_cache,
+                              uint8_t* value_exps, void* q_out, uint32_t* status, void* stream);
 
 /*
  * pa_cache_read -- read cached tokens back as fp16 rows.

@@ -40,11 +40,14 @@ PA_PF_PAIR_ROWS = 256
 
 # Every symbol include/*.h declares (pa.h, the attention ABI; pa_cache.h, the
 # norms, rotation and 8-bit cache; pa_tree.h, attention for drafted tokens;
+# pa_window.h, attention with a window; pa_blocks.h, the pool of a cache's blocks;
 # pa_probe.h, the HBM read probe; pa_testing.h, the test hook).
 EXPORTS = ("pa_plan", "pa_forward", "pa_forward_noalloc", "pa_plan_bounds", "pa_plan_device",
            "pa_forward_device_plan", "pa_status_clear", "pa_status_read", "pa_status_string",
            "pa_qk_norm_rope", "pa_cache_write", "pa_cache_store", "pa_cache_read",
+           "pa_qk_norm_rope_axes", "pa_cache_store_axes",
            "pa_tree_workspace", "pa_tree_forward",
+           "pa_window_workspace", "pa_window_forward", "pa_blocks_step",
            "pa_hbm_read_probe", "pa_testing_set_wait_limit")
 PA_PLAN_COUNTS = 4
 
@@ -54,9 +57,13 @@ PA_STATUS_BIT_WORKSPACE = 4
 PA_STATUS_BIT_PLAN = 8
 PA_STATUS_BIT_POSITION = 16
 PA_STATUS_BIT_TREE = 32
+PA_STATUS_BIT_POOL = 64
 
 # Most current tokens of a sequence that pa_tree_forward takes with parents.
 PA_TREE_MAX_TOKENS = 256
+
+# Most axes of a rotation's positions.
+PA_MAX_AXES = 4
 
 # Size of the device array pa_forward_noalloc uses as its workspace.
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -135,6 +142,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.pa_tree_workspace.argtypes = [cfgp, P]
     lib.pa_tree_forward.restype = ctypes.c_int
     lib.pa_tree_forward.argtypes = [cfgp, i64, P, P, P, P, P, P, P, P, P, P, sz, P, P]
+    lib.pa_qk_norm_rope_axes.restype = ctypes.c_int
+    lib.pa_qk_norm_rope_axes.argtypes = [P, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P]
+    lib.pa_cache_store_axes.restype = ctypes.c_int
+    lib.pa_cache_store_axes.argtypes = [P, P, P, i64, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P,
+                                        P, P, P, P, P]
+    lib.pa_window_workspace.restype = ctypes.c_int
+    lib.pa_window_workspace.argtypes = [cfgp, P, P]
+    lib.pa_window_forward.restype = ctypes.c_int
+    lib.pa_window_forward.argtypes = [cfgp, P, i64, P, P, P, P, P, P, P, P, P, sz, P, P]
+    lib.pa_blocks_step.restype = ctypes.c_int
+    lib.pa_blocks_step.argtypes = [P, P, P, P, P, P, P, P, i64, P, P, P, P]
     lib.pa_hbm_read_probe.restype = ctypes.c_int
     lib.pa_hbm_read_probe.argtypes = [P, sz, ctypes.c_int, P, P]
     lib.pa_testing_set_wait_limit.restype = ctypes.c_int
@@ -666,5 +684,6 @@ class GraphStep:
         return pa_status_read(self.workspace, self.stream)
 
 
-from .serving import (QuantCache, TreeStep, pa_cache_config, pa_qk_norm_rope,  # noqa: E402
-                      pa_rotary, pa_tree_workspace)
+from .serving import (BlockPool, QuantCache, TreeStep, WindowStep, pa_axes, pa_blocks_config,  # noqa: E402
+                      pa_cache_config, pa_qk_norm_rope, pa_rotary, pa_tree_workspace, pa_window,
+                      pa_window_workspace)

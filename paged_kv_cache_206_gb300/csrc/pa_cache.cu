@@ -38,7 +38,18 @@ struct RowParams {
   int batches;     // of rows in a warp, at most
   uint32_t q_slices, k_slices, slices;  // warps of a token: its queries', keys', all
   float eps, inv_hk;
+  // positions of several axes [axes][tokens]: a pair turns by axis 0 until axis_from[1], and so on;
+  // cyclic: pair i by axis i % axes as far as axis_upto says, else by axis 0
+  int axes, cyclic;
+  int axis_from[4], axis_upto[4];
 };
+
+// The axis whose position turns pair i.
+__device__ __forceinline__ int axis_of(const RowParams& P, int i) {
+  if (!P.cyclic) return (i >= P.axis_from[1]) + (i >= P.axis_from[2]) + (i >= P.axis_from[3]);
+  const int a = uint32_t(i) % uint32_t(P.axes);
+  return i < (a == 0 ? 0 : a == 1 ? P.axis_upto[1] : a == 2 ? P.axis_upto[2] : P.axis_upto[3]) ? a : 0;
+}
 
 __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
@@ -123,7 +134,11 @@ __global__ void __launch_bounds__(32) lengths_kernel(const int32_t* q_seqlens, i
 // bytes: it makes the factors, looks the token up and quantises. Registers are held to what lets 32
 // warps an SM (40 in the write) have loads in flight; a warp that loaded the next token's rows
 // ahead, at half the warps, was slower (39 us for the 8192 tokens).
-template <int MODE, int VPL, int U, bool IL>
+//
+// AXES: the pairs' positions lie on several axes. Four pairs next to one another take their
+// cosines in one load where they have one axis, as sections of at least eight pairs mostly do, else
+// one by one.
+template <int MODE, int VPL, int U, bool IL, bool AXES>
 __global__ void __launch_bounds__(256, VPL == 1 ? (MODE == kWrite ? 5 : 4) : 1)
 rows_kernel(const RowParams P) {
   const int lane = threadIdx.x & 31;
@@ -178,7 +193,7 @@ rows_kernel(const RowParams P) {
   int64_t slot = -1;
   int block = 0, place = 0, pos = 0;
   if constexpr (MODE == kRotate) {
-    pos = P.positions[t];
+    if (!AXES) pos = P.positions[t];
   } else {
     int i = 0;
     const int b = find_sequence(P, t, lane, i);
@@ -193,9 +208,20 @@ rows_kernel(const RowParams P) {
     place = pos % P.block_size;
     if (block >= 0 && block < P.num_blocks) slot = int64_t(block) * P.block_size + place;
     else report(P.status, PA_STATUS_BIT_BLOCK_INDEX);
-    if (MODE == kStore && P.positions) pos = P.positions[t];
+    if (MODE == kStore && !AXES && P.positions) pos = P.positions[t];
   }
-  if (MODE != kWrite) {
+  int axis_pos[4];  // (AXES)
+  if constexpr (AXES) {
+    bool bad = false, out = false;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      axis_pos[a] = a < P.axes ? P.positions[a * P.tokens + t] : 0;
+      bad |= axis_pos[a] < -1 || axis_pos[a] >= P.max_positions;
+      out |= axis_pos[a] < 0;
+    }
+    if (bad) report(P.status, PA_STATUS_BIT_POSITION);
+    if (bad || out) return;
+  } else if (MODE != kWrite) {
     if (pos < -1 || pos >= P.max_positions) report(P.status, PA_STATUS_BIT_POSITION);
     if (pos < 0 || pos >= P.max_positions) return;
   }
@@ -232,7 +258,30 @@ rows_kernel(const RowParams P) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (turn[v]) {
+        if constexpr (AXES) {
+          if (turn[v]) {
+            const int i = IL ? at[v][c] / 2 : at[v][0] + 4 * c;  // the first of four pairs
+            float* cw = reinterpret_cast<float*>(&cs);
+            float* sw = reinterpret_cast<float*>(&sn);
+            int of[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) of[j] = axis_of(P, i + j);
+            const auto row = [&](int a) {
+              return P.cos_sin + int64_t(a == 0 ? axis_pos[0] : a == 1 ? axis_pos[1] : a == 2 ? axis_pos[2] : axis_pos[3]) *
+                                     P.rot + i;
+            };
+            if (of[0] == of[1] && of[0] == of[2] && of[0] == of[3]) {
+              cs = *reinterpret_cast<const float4*>(row(of[0]));
+              sn = *reinterpret_cast<const float4*>(row(of[0]) + P.rot / 2);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                cw[j] = row(of[j])[j];
+                sw[j] = row(of[j])[j + P.rot / 2];
+              }
+            }
+          }
+        } else if (turn[v]) {
           const float* from = table + (IL ? at[v][c] / 2 : at[v][0] + 4 * c);
           cs = *reinterpret_cast<const float4*>(from);
           sn = *reinterpret_cast<const float4*>(from + P.rot / 2);
@@ -451,7 +500,7 @@ rows_kernel(const RowParams P) {
   }
 }
 
-template <int MODE, bool IL>
+template <int MODE, bool IL, bool AXES = false>
 pa_status launch_rows(RowParams P, cudaStream_t stream) {
   if (P.tokens == 0) return PA_OK;
   if (P.tokens > INT32_MAX) return PA_ERR_INVALID_ARG;  // (before it is multiplied)
@@ -470,12 +519,18 @@ pa_status launch_rows(RowParams P, cudaStream_t stream) {
   if (!many) slice(per_warp);
   if (P.tokens * P.slices > INT32_MAX) return PA_ERR_INVALID_ARG;
   const unsigned grid = unsigned(cdiv(P.tokens * P.slices, 8));
-  if (many) rows_kernel<MODE, 1, kRows, IL><<<grid, 256, 0, stream>>>(P);
-  else if (widest <= 32) rows_kernel<MODE, 1, 1, IL><<<grid, 256, 0, stream>>>(P);
-  else rows_kernel<MODE, 2, 1, IL><<<grid, 256, 0, stream>>>(P);
+  if (many) rows_kernel<MODE, 1, kRows, IL, AXES><<<grid, 256, 0, stream>>>(P);
+  else if (widest <= 32) rows_kernel<MODE, 1, 1, IL, AXES><<<grid, 256, 0, stream>>>(P);
+  else rows_kernel<MODE, 2, 1, IL, AXES><<<grid, 256, 0, stream>>>(P);
   if (MODE != kRotate && P.status && (P.q_seqlens || P.batch > P.tokens))
     lengths_kernel<<<1, 32, 0, stream>>>(P.q_seqlens, P.batch, P.max_rows, uint32_t(P.tokens), P.status);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int MODE>
+pa_status launch_turned(const RowParams& P, cudaStream_t s) {
+  if (P.axes) return P.interleaved ? launch_rows<MODE, true, true>(P, s) : launch_rows<MODE, false, true>(P, s);
+  return P.interleaved ? launch_rows<MODE, true>(P, s) : launch_rows<MODE, false>(P, s);
 }
 
 // ---- reading back
@@ -626,6 +681,29 @@ pa_status check_rotary(const pa_rotary* r, const void* q_weight, const void* k_w
   return PA_OK;
 }
 
+pa_status check_axes(const pa_axes* a, const pa_rotary* r, const int32_t* positions) {
+  if (!a || !positions || a->count < 1 || a->count > PA_MAX_AXES) return PA_ERR_INVALID_ARG;
+  const int64_t pairs = r->rotary_dim / 2;
+  int64_t sum = 0;
+  for (int i = 0; i < a->count; ++i) {
+    const int64_t n = a->sections[i];
+    if (n < 0 || (a->cyclic && i && n && a->count * (n - 1) + i >= pairs)) return PA_ERR_INVALID_ARG;
+    sum += n;
+  }
+  return sum == pairs ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
+void set_axes(RowParams& P, const pa_axes& a) {
+  P.axes = a.count;
+  P.cyclic = a.cyclic;
+  for (int i = 0, at = 0; i < PA_MAX_AXES; ++i) {
+    const int n = i < a.count ? a.sections[i] : 0;
+    P.axis_from[i] = i < a.count ? at : INT32_MAX;
+    P.axis_upto[i] = a.count * n;
+    at += n;
+  }
+}
+
 // A row tensor: head h of token t at [t * stride + h * hs].
 pa_status check_rows(const void* p, int64_t stride, int64_t width) {
   if (!p || !aligned16(p) || stride % 8 || stride < width) return PA_ERR_INVALID_ARG;
@@ -671,13 +749,17 @@ void set_cache(RowParams& P, const pa_cache_config& c, const int32_t* block_tabl
 
 }  // namespace pa
 
-extern "C" pa_status pa_qk_norm_rope(const pa_rotary* rot, int64_t tokens, const void* query,
-                                     int64_t query_stride, const void* key, int64_t key_stride,
-                                     const void* q_weight, const void* k_weight,
-                                     const float* cos_sin, const int32_t* positions, void* q_out,
-                                     void* k_out, uint32_t* status, void* stream) {
-  using namespace pa;
+namespace pa {
+
+namespace {
+
+// pa_qk_norm_rope, and pa_qk_norm_rope_axes with `axes`.
+pa_status norm_rope(const pa_rotary* rot, const pa_axes* axes, bool with_axes, int64_t tokens, const void* query,
+                    int64_t query_stride, const void* key, int64_t key_stride, const void* q_weight,
+                    const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
+                    uint32_t* status, void* stream) {
   pa_status st = check_rotary(rot, q_weight, k_weight, cos_sin);
+  if (st == PA_OK && with_axes) st = check_axes(axes, rot, positions);
   if (st != PA_OK) return st;
   const int64_t qw = int64_t(rot->num_heads) * rot->head_size;
   const int64_t kw = int64_t(rot->kv_heads) * rot->head_size;
@@ -697,8 +779,64 @@ extern "C" pa_status pa_qk_norm_rope(const pa_rotary* rot, int64_t tokens, const
   P.q_out = static_cast<__half*>(q_out);
   P.k_out = static_cast<__half*>(k_out);
   P.status = status;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return P.interleaved ? launch_rows<kRotate, true>(P, s) : launch_rows<kRotate, false>(P, s);
+  if (with_axes) set_axes(P, *axes);
+  return launch_turned<kRotate>(P, static_cast<cudaStream_t>(stream));
+}
+
+// pa_cache_store, and pa_cache_store_axes with `axes`.
+pa_status store(const pa_cache_config* cfg, const pa_rotary* rot, const pa_axes* axes, bool with_axes, int64_t tokens,
+                const void* query, int64_t query_stride, const void* key, int64_t key_stride, const void* value,
+                int64_t value_stride, const void* q_weight, const void* k_weight, const float* cos_sin,
+                const int32_t* positions, const int32_t* block_tables, const int32_t* context_lens,
+                const int32_t* q_seqlens, void* key_cache, uint8_t* key_exps, void* value_cache, uint8_t* value_exps,
+                void* q_out, uint32_t* status, void* stream) {
+  pa_status st = check_cache(cfg, key_cache, key_exps, value_cache, value_exps, block_tables, context_lens);
+  if (st != PA_OK) return st;
+  if ((st = check_rotary(rot, q_weight, k_weight, cos_sin)) != PA_OK) return st;
+  if (with_axes && (st = check_axes(axes, rot, positions)) != PA_OK) return st;
+  if (rot->kv_heads != cfg->kv_heads || rot->head_size != cfg->head_size_k) return PA_ERR_INVALID_ARG;
+  const int64_t qw = int64_t(rot->num_heads) * rot->head_size;
+  if (tokens < 0 || !q_out || !aligned16(q_out) || (q_out == query && query_stride != qw))
+    return PA_ERR_INVALID_ARG;
+  if ((st = check_rows(query, query_stride, qw)) != PA_OK) return st;
+  if ((st = check_rows(key, key_stride, int64_t(cfg->kv_heads) * cfg->head_size_k)) != PA_OK) return st;
+  if ((st = check_rows(value, value_stride, int64_t(cfg->kv_heads) * cfg->head_size_v)) != PA_OK) return st;
+  RowParams P{};
+  set_rotary(P, *rot, q_weight, k_weight, cos_sin, positions);
+  set_cache(P, *cfg, block_tables, context_lens, q_seqlens, key_cache, key_exps, value_cache, value_exps);
+  P.tokens = tokens;
+  P.query = static_cast<const __half*>(query);
+  P.key = static_cast<const __half*>(key);
+  P.value = static_cast<const __half*>(value);
+  P.query_stride = query_stride;
+  P.key_stride = key_stride;
+  P.value_stride = value_stride;
+  P.q_out = static_cast<__half*>(q_out);
+  P.status = status;
+  if (with_axes) set_axes(P, *axes);
+  return launch_turned<kStore>(P, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" pa_status pa_qk_norm_rope(const pa_rotary* rot, int64_t tokens, const void* query,
+                                     int64_t query_stride, const void* key, int64_t key_stride,
+                                     const void* q_weight, const void* k_weight,
+                                     const float* cos_sin, const int32_t* positions, void* q_out,
+                                     void* k_out, uint32_t* status, void* stream) {
+  return pa::norm_rope(rot, nullptr, false, tokens, query, query_stride, key, key_stride, q_weight, k_weight, cos_sin,
+                       positions, q_out, k_out, status, stream);
+}
+
+extern "C" pa_status pa_qk_norm_rope_axes(const pa_rotary* rot, const pa_axes* axes, int64_t tokens, const void* query,
+                                          int64_t query_stride, const void* key, int64_t key_stride,
+                                          const void* q_weight, const void* k_weight, const float* cos_sin,
+                                          const int32_t* positions, void* q_out, void* k_out, uint32_t* status,
+                                          void* stream) {
+  return pa::norm_rope(rot, axes, true, tokens, query, query_stride, key, key_stride, q_weight, k_weight, cos_sin,
+                       positions, q_out, k_out, status, stream);
 }
 
 extern "C" pa_status pa_cache_write(const pa_cache_config* cfg, int64_t tokens, const void* key,
@@ -733,31 +871,22 @@ extern "C" pa_status pa_cache_store(const pa_cache_config* cfg, const pa_rotary*
                                     const int32_t* q_seqlens, void* key_cache, uint8_t* key_exps,
                                     void* value_cache, uint8_t* value_exps, void* q_out,
                                     uint32_t* status, void* stream) {
-  using namespace pa;
-  pa_status st = check_cache(cfg, key_cache, key_exps, value_cache, value_exps, block_tables, context_lens);
-  if (st != PA_OK) return st;
-  if ((st = check_rotary(rot, q_weight, k_weight, cos_sin)) != PA_OK) return st;
-  if (rot->kv_heads != cfg->kv_heads || rot->head_size != cfg->head_size_k) return PA_ERR_INVALID_ARG;
-  const int64_t qw = int64_t(rot->num_heads) * rot->head_size;
-  if (tokens < 0 || !q_out || !aligned16(q_out) || (q_out == query && query_stride != qw))
-    return PA_ERR_INVALID_ARG;
-  if ((st = check_rows(query, query_stride, qw)) != PA_OK) return st;
-  if ((st = check_rows(key, key_stride, int64_t(cfg->kv_heads) * cfg->head_size_k)) != PA_OK) return st;
-  if ((st = check_rows(value, value_stride, int64_t(cfg->kv_heads) * cfg->head_size_v)) != PA_OK) return st;
-  RowParams P{};
-  set_rotary(P, *rot, q_weight, k_weight, cos_sin, positions);
-  set_cache(P, *cfg, block_tables, context_lens, q_seqlens, key_cache, key_exps, value_cache, value_exps);
-  P.tokens = tokens;
-  P.query = static_cast<const __half*>(query);
-  P.key = static_cast<const __half*>(key);
-  P.value = static_cast<const __half*>(value);
-  P.query_stride = query_stride;
-  P.key_stride = key_stride;
-  P.value_stride = value_stride;
-  P.q_out = static_cast<__half*>(q_out);
-  P.status = status;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return P.interleaved ? launch_rows<kStore, true>(P, s) : launch_rows<kStore, false>(P, s);
+  return pa::store(cfg, rot, nullptr, false, tokens, query, query_stride, key, key_stride, value, value_stride, q_weight,
+                   k_weight, cos_sin, positions, block_tables, context_lens, q_seqlens, key_cache, key_exps,
+                   value_cache, value_exps, q_out, status, stream);
+}
+
+extern "C" pa_status pa_cache_store_axes(const pa_cache_config* cfg, const pa_rotary* rot, const pa_axes* axes,
+                                         int64_t tokens, const void* query, int64_t query_stride, const void* key,
+                                         int64_t key_stride, const void* value, int64_t value_stride,
+                                         const void* q_weight, const void* k_weight, const float* cos_sin,
+                                         const int32_t* positions, const int32_t* block_tables,
+                                         const int32_t* context_lens, const int32_t* q_seqlens, void* key_cache,
+                                         uint8_t* key_exps, void* value_cache, uint8_t* value_exps, void* q_out,
+                                         uint32_t* status, void* stream) {
+  return pa::store(cfg, rot, axes, true, tokens, query, query_stride, key, key_stride, value, value_stride, q_weight,
+                   k_weight, cos_sin, positions, block_tables, context_lens, q_seqlens, key_cache, key_exps,
+                   value_cache, value_exps, q_out, status, stream);
 }
 
 extern "C" pa_status pa_cache_read(const pa_cache_config* cfg, const void* key_cache,

@@ -2,7 +2,7 @@
  * A Python module of one function: call(address, *arguments) -> int calls a C
  * function that takes pointers and 64-bit integers and returns an int. Arguments
  * are Python integers, or None for NULL. ctypes does the same in ten times the time
- * (3 to 5 us for the 14 to 23 arguments of the serving calls, as long as the
+ * (3 to 5 us for the 13 to 24 arguments of the serving calls, as long as the
  * launches themselves take).
  */
 #define PY_SSIZE_T_CLEAN
@@ -33,6 +33,10 @@ static PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   int known = 1;
   Py_BEGIN_ALLOW_THREADS;
   switch (n - 1) {
+    case 13:
+      r = ((int (*)(u, u, u, u, u, u, u, u, u, u, u, u, u))f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8],
+                                                              a[9], a[10], a[11], a[12]);
+      break;
     case 14:
       r = ((int (*)(u, u, u, u, u, u, u, u, u, u, u, u, u, u))f)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8],
                                                                  a[9], a[10], a[11], a[12], a[13]);
@@ -45,6 +49,11 @@ static PyObject* call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
       r = ((int (*)(u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u))f)(
           a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], a[14], a[15], a[16],
           a[17], a[18], a[19], a[20], a[21], a[22]);
+      break;
+    case 24:
+      r = ((int (*)(u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u, u))f)(
+          a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], a[14], a[15], a[16],
+          a[17], a[18], a[19], a[20], a[21], a[22], a[23]);
       break;
     default: known = 0;
   }

@@ -1,4 +1,4 @@
-// What the kernels of pa_tree_forward share: their parameters, the lookup of a
+// What the kernels of pa_tree_forward and pa_window_forward share: their parameters, the lookup of a
 // token's sequence, and the walk from a draft to its root.
 #pragma once
 
@@ -22,6 +22,7 @@ struct TreeParams {
   int64_t tokens;
   int batch, num_heads, kv_heads, group, hk, hv, block_size, num_blocks, max_blocks_per_seq;
   int max_q;
+  int window, sinks;  // (pa_window_forward)
   float scale_log2;  // scale * log2(e)
   uint32_t wait_limit;  // cycles a wait on another role's progress may take
 };

@@ -1,0 +1,52 @@
+// Attention with a sliding window and sinks over a paged cache (pa_window.h): the C entry
+// and the choice of the kernel.
+#include <cuda_runtime.h>
+
+#include "pa_internal.h"
+#include "pa_tree_any.cuh"
+#include "pa_tree_host.h"
+#include "pa_window.h"
+
+namespace pa {
+
+namespace {
+
+pa_status check_window(const pa_config* cfg, const pa_window* win) {
+  const pa_status st = check_tree(cfg);
+  if (st != PA_OK) return st;
+  return win && win->window > 0 && win->sinks >= 0 ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" pa_status pa_window_workspace(const pa_config* cfg, const pa_window* win, size_t* workspace_bytes) {
+  const pa_status st = pa::check_window(cfg, win);
+  if (st != PA_OK) return st;
+  if (!workspace_bytes) return PA_ERR_INVALID_ARG;
+  *workspace_bytes = PA_STATUS_BYTES;
+  return PA_OK;
+}
+
+extern "C" pa_status pa_window_forward(const pa_config* cfg, const pa_window* win, int64_t tokens, const void* query,
+                                       const void* key_cache, const void* value_cache, const uint8_t* key_exps,
+                                       const uint8_t* value_exps, const int32_t* block_tables,
+                                       const int32_t* context_lens, const int32_t* q_seqlens, void* workspace,
+                                       size_t workspace_bytes, void* out, void* stream_) {
+  using namespace pa;
+  size_t need = 0;
+  pa_status st = pa_window_workspace(cfg, win, &need);
+  if (st != PA_OK) return st;
+  TreeParams P{};
+  st = tree_arguments(*cfg, tokens, query, key_cache, value_cache, key_exps, value_exps, block_tables, context_lens,
+                      q_seqlens, workspace, workspace_bytes, need, out, P);
+  if (st != PA_OK || tokens == 0) return st;
+  P.window = win->window;
+  P.sinks = win->sinks;
+  const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const unsigned grid = unsigned(tokens * cfg->num_heads);
+  if (key_exps) tree_any_kernel<true, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
+  else tree_any_kernel<false, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
