@@ -36,11 +36,13 @@
 #pragma once
 
 #include "pa_decode_mma.cuh"
-#include "pa_tree_split.cuh"
+#include "pa_window_split.cuh"
 
 namespace pa {
 
-template <int HD, bool Q8, int NT>
+// WIN: pa_window_forward's kernel. Its tiles are those of pa_window_split.cuh, chains whose rows
+// leave keys out at the lower end too.
+template <int HD, bool Q8, int NT, bool WIN>
 struct TreeMma {
   static constexpr int kWarps = 4;
   static constexpr int kRowBytes = HD * (Q8 ? 1 : 2);
@@ -68,8 +70,9 @@ struct TreeMma {
   static constexpr uint32_t par_off = mask_off + kRows * kTreeWords * 4;
   static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
   static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
-  using Place = TreePlace<TreeWalk<kSub, kRows, kLead>>;
-  static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(TreeTile) + 7) & ~7u;
+  using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kSub, kRows, kLead>, TreeWalk<kSub, kRows, kLead>>, Tile>;
+  static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(Tile) + 7) & ~7u;
   static constexpr uint32_t exps_off = (place_off + sizeof(Place) + 15) & ~15u;  // [stage][K, V][32]
   static constexpr uint32_t bars_off = exps_off + (Q8 ? kMaxStages * 64 : 0);
   static constexpr uint32_t kRest = bars_off + kMaxStages * 8;
@@ -142,11 +145,12 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return hit != 0;
 }
 
-template <int HD, bool Q8, int NT>
-__global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
+template <int HD, bool Q8, int NT, bool WIN>
+__global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
     tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                     const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S, int box) {
-  using Cfg = TreeMma<HD, Q8, NT>;
+  using Cfg = TreeMma<HD, Q8, NT, WIN>;
+  using Tile = typename Cfg::Tile;
   constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows;
   constexpr int RB = Cfg::kRowBytes, C = Cfg::kChunks, E = Cfg::kElems;
   constexpr int RPB = RB < 128 ? RB : 128;  // bytes of a row that lie together
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + Cfg::mask_off);
   uint8_t* par_s = smem + Cfg::par_off;
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + Cfg::bad_off);
-  TreeTile* tile_s = reinterpret_cast<TreeTile*>(smem + Cfg::tile_off);
+  Tile* tile_s = reinterpret_cast<Tile*>(smem + Cfg::tile_off);
   uint8_t* exps_s = smem + Cfg::exps_off;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::bars_off);  // [stage] landed
   const int worker = blockIdx.x * Cfg::kWarps + warp;
@@ -183,11 +187,11 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   int unit = 0, unit_end = 0, win0 = 0, cut_L = 0, cut_b = 0, cut_kvh = 0;
   // Lane l holds the places of 16 keys each that the units to come need: MT a
   // unit, 32 / MT units a window, and the next window's.
-  constexpr int WIN = 32 / MT;
+  constexpr int AHEAD = 32 / MT;
   int block = 0, in_block = 0, next_block = 0, next_in = 0;
   auto next_tile = [&]() {
     if (!tree_next(P, place)) return false;
-    const TreeTile& t = place->tile;
+    const Tile& t = place->tile;
     if (lane == 0) {
       tile_s[made % Cfg::kTiles] = t;
       if (t.parts) tree_note(S, worker, t);
@@ -200,6 +204,16 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     unit_end = t.s1;
     return true;
   };
+  // The first key of a unit, and whether the box of 16 of its keys is none of the tile's (its table
+  // entry may be anything).
+  auto key_of = [&](int u) {
+    if constexpr (WIN) return place->tile.unit(u) * SUB;
+    else return u * SUB;
+  };
+  auto left_out = [&](int key) {
+    if constexpr (WIN) return window_hidden(P, place->tile.lo, key & -box, box);
+    else return false;
+  };
   // The next unit's copies: boxes of `box` keys, which lie in one block. Rows behind the
   // context come with the last box and are dealt with where the drafts are.
   const uint64_t pol = policy_evict_first();
@@ -207,15 +221,16 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   auto issue = [&]() {
     if (unit >= unit_end && !next_tile()) return;
     const bool fresh = unit == place->tile.s0;
-    if (fresh || unit >= win0 + WIN) {
-      win0 = fresh ? unit : win0 + WIN;
+    if (fresh || unit >= win0 + AHEAD) {
+      win0 = fresh ? unit : win0 + AHEAD;
 #pragma unroll 1
       for (int k = fresh ? 0 : 1; k < 2; ++k) {
         block = next_block;
         in_block = next_in;
-        const int at = win0 + k * WIN + lane / MT, key = at * SUB + (lane % MT) * 16, page = key / bs;
+        const int at = win0 + k * AHEAD + lane / MT, key = key_of(at) + (lane % MT) * 16, page = key / bs;
         next_in = key - page * bs;
-        next_block = at < unit_end && key < cut_L ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
+        next_block = at < unit_end && key < cut_L && !left_out(key)
+                         ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
       }
     }
     int blk[MT], in_blk[MT];
@@ -229,7 +244,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       uint32_t n = 0;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const bool there = blk[m] >= 0 && blk[m] < P.num_blocks, mine = m * 16 % box == 0 && unit * SUB + m * 16 < cut_L;
+        const int key = key_of(unit) + m * 16;
+        const bool there = blk[m] >= 0 && blk[m] < P.num_blocks, mine = m * 16 % box == 0 && key < cut_L && !left_out(key);
         if (!there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
         go[m] = there && mine;
         n += go[m] ? 1 : 0;
@@ -265,9 +281,16 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
   int n = 0, stage = 0, phase = 0;  // units done, the next one's stage
   for (int done = 0; done < made; ++done) {
     __syncwarp();
-    const TreeTile t = tile_s[done % Cfg::kTiles];
+    const Tile t = tile_s[done % Cfg::kTiles];
     const int L = t.L, prefix = L - t.q;
-    const bool drafts = t.s1 * SUB > prefix;  // the keys reach the current tokens
+    const bool drafts = WIN || t.s1 * SUB > prefix;  // the keys reach the current tokens
+    // (WIN) the last key before the tokens that not every row sees, and the rows' places
+    const int p0 = prefix + t.r0 / G;
+    int place_of[NT][2];
+    if constexpr (WIN) {
+#pragma unroll
+      for (int k = 0; k < NT * 2; ++k) place_of[k / 2][k % 2] = prefix + (t.r0 + k / 2 * 8 + 2 * c + k % 2) / G;
+    }
 
     // ---- the query rows as B fragments: dims of the chunks 2c, 2c + 1, ...
     uint2 qf[NT == 1 ? OT : 1];
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
     // ---- what the rows see of the drafts
     if (drafts) {
       if (lane < kTreeWords) bad_s[lane] = 0;
-      if (P.parents) {
+      if (!WIN && P.parents) {
         // parents as bytes (255: a root), then every row's walk to its root
         for (int i = lane; i < t.q; i += 32) {
           const int up = int64_t(t.q_start) + i < P.tokens ? P.parents[t.q_start + i] : -1;
@@ -340,8 +363,12 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
       uint8_t* vb = kb + Cfg::kV;
       const uint8_t* ex = exps_s + stage * 64;
       if (++stage == Cfg::kStages) stage = 0, phase ^= 1;
-      const int j0 = un * SUB;
-      const bool edge = j0 + SUB > prefix;
+      int j0 = un * SUB;
+      bool edge = j0 + SUB > prefix;  // keys that not every row sees
+      if constexpr (WIN) {
+        j0 = t.unit(un) * SUB;
+        edge = j0 + SUB > p0 + 1 || (j0 < t.lo1 && j0 + SUB > P.sinks);
+      }
 
       // ---- S^T = K . Q^T
       float s[MT][NT][4];
@@ -400,7 +427,9 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           unscale[mt][hf] = 1.f;
           if constexpr (Q8) {
             int ke = ex[kk], ve = max(int(ex[32 + kk]), kExpLeastByte);
-            if (edge && key >= L) ke = ve = kExpBias;  // exponents behind the context: anything
+            bool nothing = key >= L;  // exponents behind the context: anything
+            if constexpr (WIN) nothing |= window_hidden(P, t.lo, key, 1);
+            if (edge && nothing) ke = ve = kExpBias;
             f *= pow2(ke - kExpBias);
             add = float(ve - kExpBias);
             unscale[mt][hf] = pow2(kExpBias - ve);
@@ -413,7 +442,13 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
               x = fmaf(x, f, add);
             }
         }
-      if (edge) {
+      if (WIN && edge) {
+#pragma unroll
+        for (int k = 0; k < MT * NT * 4; ++k) {
+          const int key = j0 + k / 4 / NT * 16 + (k >> 1 & 1) * 8 + g;
+          if (!window_sees(P, place_of[k / 4 % NT][k & 1], key)) s[k / 4 / NT][k / 4 % NT][k % 4] = -INFINITY;
+        }
+      } else if (edge) {
         uint32_t seen = 0;
 #pragma unroll 1
         for (int k = 0; k < MT * NT * 4; ++k) {  // score k % 4 of s[k / 4 / NT][k / 4 % NT]
@@ -463,14 +498,20 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           }
       }
       if (edge) {
-        // V rows behind the context hold anything and become 0, and non-finite elements of
-        // the drafts' leave the product
+        // V rows behind the context (WIN: and before the first row's window) hold anything and become
+        // 0, and non-finite elements of the drafts' (WIN: those that not every row sees) leave the product
 #pragma unroll 1
         for (int at = lane; at < SUB * C; at += 32) {
           const int row = at / C, key = j0 + row;
-          if (key < prefix) continue;
+          bool nothing = key >= L;
+          if constexpr (WIN) {
+            nothing |= window_hidden(P, t.lo, key, 1);
+            if (key <= p0 && (key >= t.lo1 || key < P.sinks)) continue;
+          } else if (key < prefix) {
+            continue;
+          }
           uint4* p = reinterpret_cast<uint4*>(vb + tree_at<C, SUB>(at % C, row));
-          if (key >= L) {
+          if (nothing) {
             *p = make_uint4(0, 0, 0, 0);
             continue;
           }
@@ -481,7 +522,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           hit |= clear_nonfinite<Q8>(v.w);
           if (hit) {
             *p = v;
-            const int a = key - prefix;
+            const int a = WIN ? 0 : key - prefix;
             atomicOr(&bad_s[(a >> 5) % kTreeWords], 1u << (a & 31));
           }
         }
@@ -613,10 +654,13 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
           const int r = t.r0 + row, i = r / G;
           const int64_t tok = int64_t(t.q_start) + i;
           if (i >= t.q || tok >= P.tokens) continue;
-          tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, i, bad_s, P.parents ? mask_s + row * kTreeWords : nullptr,
-                         t.s0 * SUB, t.s1 * SUB,
-                         t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv : nullptr,
-                         S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD, 1, lane, 32, P.hv);
+          __half* whole = t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv : nullptr;
+          float* part = S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD;
+          if constexpr (WIN)
+            window_patch<Q8, SUB>(P, tile_s[done % Cfg::kTiles], prefix + i, whole, part, 1, lane, 32, P.hv);
+          else
+            tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, i, bad_s, P.parents ? mask_s + row * kTreeWords : nullptr,
+                           t.s0 * SUB, t.s1 * SUB, whole, part, 1, lane, 32, P.hv);
         }
         __syncwarp();
       }
@@ -629,5 +673,8 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT>::kCtas))
 cudaError_t tree_mma_64(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
 cudaError_t tree_mma_128(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
 cudaError_t tree_mma_256(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
+cudaError_t window_mma_64(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
+cudaError_t window_mma_128(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
+cudaError_t window_mma_256(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
 
 }  // namespace pa

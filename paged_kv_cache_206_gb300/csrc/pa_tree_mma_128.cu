@@ -5,7 +5,7 @@ namespace pa {
 
 cudaError_t tree_mma_128(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws,
                         cudaStream_t s) {
-  return tree_mma_pick<128>(P, q8, nt, sms, need, ws, s);
+  return tree_mma_pick<128, false>(P, q8, nt, sms, need, ws, s);
 }
 
 }  // namespace pa

@@ -201,14 +201,14 @@ struct TreeWalk {
 // functions of their own: they are rare, and inlined where they are called (with
 // their divisions) they pushed the kernels' loops out of the instruction cache.
 // All lanes hold and store the same values.
-template <class Walk>
+template <class Walk, class Tile = TreeTile>
 struct TreePlace {
   Walk walk;
-  TreeTile tile;
+  Tile tile;
 };
 
-template <class Walk>
-__device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S, TreePlace<Walk>* at, int worker,
+template <class Walk, class Tile>
+__device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S, TreePlace<Walk, Tile>* at, int worker,
                                         int lane) {
   Walk w;
   const bool some = w.begin(P, S, worker, lane);
@@ -217,10 +217,10 @@ __device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S,
   return some;
 }
 
-template <class Walk>
-__device__ __noinline__ bool tree_next(const TreeParams& P, TreePlace<Walk>* at) {
+template <class Walk, class Tile>
+__device__ __noinline__ bool tree_next(const TreeParams& P, TreePlace<Walk, Tile>* at) {
   Walk w = at->walk;
-  TreeTile d;
+  Tile d;
   const bool some = w.next(P, d);
   __syncwarp();
   if (some) at->tile = d;

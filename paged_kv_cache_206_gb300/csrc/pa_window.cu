@@ -5,6 +5,7 @@
 #include "pa_internal.h"
 #include "pa_tree_any.cuh"
 #include "pa_tree_host.h"
+#include "pa_tree_mma.cuh"
 #include "pa_window.h"
 
 namespace pa {
@@ -17,6 +18,23 @@ pa_status check_window(const pa_config* cfg, const pa_window* win) {
   return win && win->window > 0 && win->sinks >= 0 ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
+// The kernel for these head sizes and rows, if there is a faster one than tree_any_kernel.
+bool window_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws, cudaStream_t stream,
+                  cudaError_t* e) {
+  const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;
+  const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
+  const int nt = rows <= 8 ? 1 : 2;
+  if (hd <= 64)
+    *e = window_mma_64(P, q8, nt, c.num_sms, need, ws, stream);
+  else if (hd <= 128)
+    *e = window_mma_128(P, q8, nt, c.num_sms, need, ws, stream);
+  else if (hd <= 256)
+    *e = window_mma_256(P, q8, nt, c.num_sms, need, ws, stream);
+  else
+    return false;
+  return true;
+}
+
 }  // namespace
 
 }  // namespace pa
@@ -25,7 +43,14 @@ extern "C" pa_status pa_window_workspace(const pa_config* cfg, const pa_window* 
   const pa_status st = pa::check_window(cfg, win);
   if (st != PA_OK) return st;
   if (!workspace_bytes) return PA_ERR_INVALID_ARG;
+  // the larger of the two caches' needs, so that it does not depend on them
   *workspace_bytes = PA_STATUS_BYTES;
+  for (const bool q8 : {false, true}) {
+    size_t need = 0;
+    cudaError_t e;
+    if (pa::window_tiles(*cfg, pa::TreeParams{}, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
+      *workspace_bytes = need;
+  }
   return PA_OK;
 }
 
@@ -45,6 +70,9 @@ extern "C" pa_status pa_window_forward(const pa_config* cfg, const pa_window* wi
   P.window = win->window;
   P.sinks = win->sinks;
   const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  cudaError_t e = cudaSuccess;
+  if (window_tiles(*cfg, P, key_exps != nullptr, nullptr, workspace, stream, &e))
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   const unsigned grid = unsigned(tokens * cfg->num_heads);
   if (key_exps) tree_any_kernel<true, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
   else tree_any_kernel<false, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);

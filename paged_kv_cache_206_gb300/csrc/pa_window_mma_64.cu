@@ -1,0 +1,11 @@
+// The warp-level attention kernels with a window for heads of up to 64 dims (pa_tree_mma.cuh).
+#include "pa_tree_mma_launch.cuh"
+
+namespace pa {
+
+cudaError_t window_mma_64(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws,
+                        cudaStream_t s) {
+  return tree_mma_pick<64, true>(P, q8, nt, sms, need, ws, s);
+}
+
+}  // namespace pa
