@@ -48,10 +48,15 @@
 
 namespace pa {
 
-template <int HD, bool Q8, int QT>
+// WIN: pa_window_forward's kernel, for drafts, prompts and parts of prompts. Its tiles are those of
+// pa_window_split.cuh. As every row tile has keys that only some of its rows see, at both ends of their
+// windows, the fp16 cache's V tiles are looked through by a warp of their own (12), ahead of the
+// product's issuer.
+template <int HD, bool Q8, int QT, bool WIN>
 struct TreeTc {
   static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
-  static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : 384;
+  static constexpr bool kLook = WIN && !Q8;  // there is a warp that looks the V tiles through
+  static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : kLook ? 416 : 384;
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
   // What a row tile costs next to its key tiles, in these, measured at 32 trees over 64 to 8192
@@ -84,7 +89,7 @@ struct TreeTc {
   // 2^-9) times 2^-14 is still exact in fp16, and weights may stand 2^7 higher (2^(8 + 7) < 65504).
   static constexpr int kSpreadK = 14, kSpreadV = 7, kLift = Q8 ? kSpreadV : 0;
   static constexpr int kAhead = 4;                       // row tiles told to the roles
-  static constexpr int kRoles = Q8 ? 11 + 4 * kConv : 11;            // warps that are told
+  static constexpr int kRoles = Q8 ? 11 + 4 * kConv : kLook ? 12 : 11;  // warps that are told
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t k_off = q_off + QT * kTile;
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
@@ -96,10 +101,12 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
-  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead;
-  using Place = TreePlace<TreeWalk<kTok, kRows, kLead>>;
+  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead +
+                               (kLook ? kVSlots : 0);
+  using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
-  static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(TreeTile) + 15) & ~15u;
+  static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(Tile) + 15) & ~15u;
   static constexpr uint32_t tmem_off = (place_off + sizeof(Place) + 15) & ~15u;
   static constexpr uint32_t bytes = tmem_off + 16 + 1024;
   static_assert(bytes <= kTcMaxSmem, "shared memory");
@@ -181,16 +188,19 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t f) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// An fp16 V tile [HD / 64][128 rows][128 B] before its product (one warp): rows
-// from `hi` become 0, and non-finite elements of rows [lo, hi), drafts row + a0,
-// become 0 and are flagged. Rare, hence not inlined.
+// An fp16 V tile [HD / 64][128 rows][128 B] before its product (one warp): rows [lo, hi) become 0;
 template <int H2>
-__device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, uint32_t* bad, int lane) {
-  constexpr uint32_t HALF = 128 * 128;
-  for (int at = lane; at < (128 - hi) * 8 * H2; at += 32) {
-    const int r = hi + at / (8 * H2), ch = at % (8 * H2);
-    *reinterpret_cast<uint4*>(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_v_rows(uint8_t* vb, int lo, int hi, int lane) {
+  for (int at = lane; at < (hi - lo) * 8 * H2; at += 32) {
+    const int r = lo + at / (8 * H2), ch = at % (8 * H2);
+    *reinterpret_cast<uint4*>(vb + (ch >> 3) * (128 * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
+}
+
+// non-finite elements of rows [lo, hi) become 0, and `flag` is told their rows.
+template <int H2, class Flag>
+__device__ __forceinline__ void clear_v_rows(uint8_t* vb, int lo, int hi, int lane, Flag flag) {
+  constexpr uint32_t HALF = 128 * 128;
   constexpr int B = 8;  // chunks a lane has in registers at a time
   for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += 32 * B) {
     uint4 v[B];
@@ -207,12 +217,39 @@ __device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, u
       hit |= clear_nonfinite<false>(v[k].z);
       hit |= clear_nonfinite<false>(v[k].w);
       if (hit) {
-        const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2), a = a0 + r;
+        const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
         *reinterpret_cast<uint4*>(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16) = v[k];
-        atomicOr(&bad[(a >> 5) % kTreeWords], 1u << (a & 31));
+        flag(r);
       }
     }
   }
+}
+
+// Rows from `hi` become 0, and non-finite elements of rows [lo, hi), drafts row + a0,
+// become 0 and are flagged. Rare, hence not inlined.
+template <int H2>
+__device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, uint32_t* bad, int lane) {
+  zero_v_rows<H2>(vb, hi, 128, lane);
+  clear_v_rows<H2>(vb, lo, hi, lane, [&](int r) {
+    const int a = a0 + r;
+    atomicOr(&bad[(a >> 5) % kTreeWords], 1u << (a & 31));
+  });
+  fence_proxy_async();
+  __syncwarp();
+}
+
+// (WIN) Rows that no row of the tile attends become 0, behind its last token and before the first
+// row's window; of those that some attend the non-finite elements do, under a flag. key0: row 0's key.
+template <int H2>
+__device__ __noinline__ void clean_v_window(uint8_t* vb, const TreeParams& P, const WindowTile& t, int key0,
+                                            uint32_t* bad, int lane) {
+  const auto row = [&](int key) { return min(max(key - key0, 0), 128); };
+  const int p0 = t.first(P.group);
+  zero_v_rows<H2>(vb, row(t.L), 128, lane);
+  zero_v_rows<H2>(vb, row(P.sinks), row(t.lo), lane);
+  const auto flag = [&](int) { atomicOr(bad, 1u); };
+  clear_v_rows<H2>(vb, row(max(t.lo, P.sinks)), row(min(t.lo1, p0 + 1)), lane, flag);
+  clear_v_rows<H2>(vb, row(p0 + 1), row(t.L), lane, flag);
   fence_proxy_async();
   __syncwarp();
 }
@@ -237,8 +274,9 @@ __device__ __forceinline__ uint32_t tree_attends(const uint32_t* seen, int qi, i
 // s_j = S_j * scale * 2^k_j and k_j, v_j what is left of the exponents in `exps` (V's 128 bytes behind
 // K's). `left` columns lie in the context, the first is draft a0. *own: the largest s_j that
 // the row attends and the sum of 2^(s_j - it). Rare, hence not inlined and a loop of 16 columns.
-template <int SPREAD_K, int SPREAD_V>
-__device__ __noinline__ void tree_apart(uint32_t sbuf, const uint8_t* exps, int2 tile, float scale_log2, int left,
+// (WIN: the row's token stands at qi, the first column is the key a0.)
+template <int SPREAD_K, int SPREAD_V, bool WIN>
+__device__ __noinline__ void tree_apart(const TreeParams& P, uint32_t sbuf, const uint8_t* exps, int2 tile, int left,
                                         const uint32_t* seen, int qi, int a0, float2* own) {
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
@@ -248,7 +286,8 @@ __device__ __noinline__ void tree_apart(uint32_t sbuf, const uint8_t* exps, int2
     __syncwarp();
     tmem_ld<16>(sbuf + c, s);
     tmem_wait_ld();
-    const uint32_t bits = tree_attends(seen, qi, a0 + (c & 32)) >> (c & 16);
+    const int col = a0 + (c & 32);
+    const uint32_t bits = (WIN ? window_bits(P, qi, col) : tree_attends(seen, qi, col)) >> (c & 16);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       int k = (tile.x & 255) - kExpBias, v = (tile.y & 255) - kExpBias;
@@ -256,7 +295,7 @@ __device__ __noinline__ void tree_apart(uint32_t sbuf, const uint8_t* exps, int2
         k = min(k, max(int(exps[c + j]), kExpLeastByte) - kExpBias + SPREAD_K);
         v = min(v, max(int(exps[c + j + 128]), kExpLeastByte) - kExpBias + SPREAD_V);
       }
-      s[j] *= fmaxf(scale_log2 * pow2(k), FLT_MIN);
+      s[j] *= fmaxf(P.scale_log2 * pow2(k), FLT_MIN);
       x[j] = __float_as_uint(s[j] + float(v));
       if (!(bits >> j & 1)) s[j] = -INFINITY;
       most = fmaxf(most, s[j]);
@@ -275,11 +314,12 @@ __device__ __noinline__ void tree_apart(uint32_t sbuf, const uint8_t* exps, int2
   *own = make_float2(top, sum);
 }
 
-template <int HD, bool Q8, int QT>
-__global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
+template <int HD, bool Q8, int QT, bool WIN>
+__global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
-  using Cfg = TreeTc<HD, Q8, QT>;
+  using Cfg = TreeTc<HD, Q8, QT, WIN>;
+  using Tile = typename Cfg::Tile;
   constexpr int TOK = Cfg::kTok, H2 = Cfg::kHalves, KS = Cfg::kKSlots, VS = Cfg::kVSlots;
   constexpr uint32_t kTmemCols = 512;
   constexpr uint32_t kIdescQK = mma_idesc(128, TOK, 0, 0);
@@ -312,6 +352,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   uint64_t* q_empty = s_full + 12;            // the row tile's last S complete
   uint64_t* o_free = s_full + 13;             // both O read by the softmax warps
   uint64_t* all_done = s_full + 14;
+  uint64_t* vready = s_full + 15;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -327,6 +368,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     for (int i = 0; i < VS; ++i) {
       mbar_init(&vfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&vempty[i], 1);
+      if (Cfg::kLook) mbar_init(&vready[i], 1);
     }
     for (int i = 0; i < Cfg::kMeta; ++i) mbar_init(&meta_full[i], 2);
     for (int i = 0; i < 2 * Cfg::kExps; ++i) mbar_init(&exps_full[i], 1);
@@ -363,9 +405,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
 
   // The row tiles, as warp 3 finds them on the line, told to the other roles through
   // a ring (one reading of the lengths for the whole CTA); q < 0 ends them.
-  TreeTile* told = reinterpret_cast<TreeTile*>(smem + Cfg::tile_off);
+  Tile* told = reinterpret_cast<Tile*>(smem + Cfg::tile_off);
   int heard = 0;  // row tiles begun
-  auto next_tile = [&](TreeTile& t) {
+  auto next_tile = [&](Tile& t) {
     __syncwarp();
     if (heard > 0 && lane == 0) mbar_arrive(&tile_empty[(heard - 1) % Cfg::kAhead]);
     const int at = heard % Cfg::kAhead;
@@ -377,10 +419,20 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
   // Key tiles of a row tile: the keys past its last row's own position are no
   // row's, so a tile of early rows (or a worker's share of one) may have fewer
   // units than the line counts, or none.
-  auto key_tiles = [&](const TreeTile& w) {
+  auto key_tiles = [&](const Tile& w) {
+    if constexpr (WIN) return w.s1 - w.s0;  // (counted as they are)
     const int last = min(w.q - 1, (w.r0 + Cfg::kRows - 1) / G);
     const int units = (w.L - w.q + last + TOK) / TOK;
     return max(0, min(w.s1, units) - w.s0);
+  };
+  // The first key of a row tile's unit, and whether some of n keys are not seen by all of its rows.
+  auto key_of = [&](const Tile& w, int u) {
+    if constexpr (WIN) return w.unit(u) * TOK;
+    else return u * TOK;
+  };
+  auto edge_at = [&](const Tile& w, int key, int n) {
+    if constexpr (WIN) return key + n > w.first(G) + 1 || (key < w.lo1 && key + n > P.sinks);
+    else return key + n > w.L - w.q;
   };
   // The phase of key tile n's S and jobs on their barriers.
   auto phase_of = [](int n) { return QT == 2 ? n & 1 : n >> 1 & 1; };
@@ -406,14 +458,19 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     int n = 0, filled = 0;     // key tiles, and stages or tiles filled, so far
     int slot = 0, phase = 0;   // of the next stage or tile
     int round = 0;             // of the next key tile's barriers
-    TreeTile t;
+    Tile t;
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t);
       const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
-      int key = t.s0 * TOK + lane * box, blk = key / bs, off = key - blk * bs;
-      int id = tiles > 0 && lane < pieces && key < t.L ? table[blk] : -1;
+      const auto wanted = [&](int key) {
+        bool w = lane < pieces && key < t.L;
+        if constexpr (WIN) w = w && !window_hidden(P, t.lo, key, box);
+        return w;
+      };
+      int key = key_of(t, t.s0) + lane * box, blk = key / bs, off = key - blk * bs;
+      int id = tiles > 0 && wanted(key) ? table[blk] : -1;
       for (int i = 0; i < tiles; ++i, ++n) {
-        const bool want = lane < pieces && key < t.L, there = want && id >= 0 && id < P.num_blocks;
+        const bool want = wanted(key), there = want && id >= 0 && id < P.num_blocks;
         if (want && !there) set_status(P.status, PA_STATUS_BIT_BLOCK_INDEX);
         const unsigned valid = __ballot_sync(FULL, there);
         const int row = id * bs + off, id_now = id, off_now = off;
@@ -424,7 +481,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           off -= bs;
           ++blk;
         }
-        id = i + 1 < tiles && lane < pieces && key < t.L ? table[blk] : -1;
+        if constexpr (WIN) {
+          if (t.s0 + i + 1 == t.far && t.skip) {  // from the sinks to the window
+            key += t.skip * TOK;
+            blk = key / bs;
+            off = key - blk * bs;
+          }
+        }
+        id = i + 1 < tiles && wanted(key) ? table[blk] : -1;
         if constexpr (Q8) {
           const int slot1 = slot + 1 == nslots ? 0 : slot + 1, phase1 = slot1 == 0 ? phase ^ 1 : phase;
           const int em = n % Cfg::kExps;
@@ -502,7 +566,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     // 16-byte units (the address field, in the low bits, does not overflow).
     const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
     int tile = 0, n0 = 0, vslot = 0, vphase = 0;  // row tiles and key tiles so far; the next V tile
-    TreeTile t;
+    uint64_t* vcome = Cfg::kLook ? vready : vfull;
+    Tile t;
     while (ok && next_tile(t)) {
       const int tiles = uni(key_tiles(t));
       const int q_len = uni(t.q), prefix = uni(t.L) - q_len, s0 = uni(t.s0);
@@ -524,8 +589,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       for (int i = 0; i < tiles && ok; ++i) {
         const int n = n0 + i, phase = phase_of(n);
         const bool last = i + 1 == tiles;
-        if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) { ok = false; break; }
-        if constexpr (!Q8) {
+        if (!tree_wait(&vcome[vslot], vphase, P.wait_limit)) { ok = false; break; }
+        if constexpr (!Q8 && !WIN) {
           // Rows behind the context may hold anything and become 0; non-finite
           // elements of the drafts' rows leave the product
           const int key0 = (s0 + i) * TOK;
@@ -556,7 +621,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     int told_n = 0, tile = 0, n = 0, kslot = 0, kphase = 0;  // tiles told, begun; key tiles; the next K tile
     if (lane == 0) S.join[worker].parts = 0;                 // no divided tile yet
     typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
-    TreeTile t, following;
+    Tile t, following;
     tree_begin(P, S, place, worker, lane);
     auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
       const bool some = tree_next(P, place);
@@ -659,16 +724,16 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     // too (next_tile does not wait here), as one whose wait ran out would leave the others at one.
     if (!tree_wait(&tile_full[0], 0, P.wait_limit)) ok = false;
     bool alive = !tree_softmax_bar(!ok);
-    TreeTile t;
+    Tile t;
     while (alive && next_tile(t)) {
       const int tiles = key_tiles(t), nj = QT * tiles;
       const int prefix = t.L - t.q, r = t.r0 + tr, qi = r / G;
       const int64_t tok = int64_t(t.q_start) + qi;
       const bool row_ok = qi < t.q && tok < P.tokens;
       const bool any_row = __any_sync(FULL, row_ok);
-      const bool drafts = (t.s0 + tiles) * TOK > prefix;
-      uint32_t bits[kTreeWords] = {};  // the drafts that this row sees (indexed: in local memory)
-      if (drafts && P.parents) {
+      const bool drafts = WIN || (t.s0 + tiles) * TOK > prefix;
+      uint32_t bits[WIN ? 1 : kTreeWords] = {};  // the drafts that this row sees (indexed: in local memory)
+      if constexpr (!WIN) if (drafts && P.parents) {
         uint8_t* par = smem + Cfg::par_off + (tile & 1) * PA_TREE_MAX_TOKENS;
         for (int i = tid - 128; i < t.q; i += 256) {
           const int up = int64_t(t.q_start) + i < P.tokens ? P.parents[t.q_start + i] : -1;
@@ -688,7 +753,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       for (int m = 0; m < nj && ok; ++m) {
         const int i = QT == 2 ? m >> 1 : m, hf = QT == 2 ? m & 1 : g, n = n0 + i;
         const int y = QT == 2 ? hf : n & 1, x_of_s = QT == 2 ? g : n & 1, phase = phase_of(n);
-        const int key0 = (t.s0 + i) * TOK + hf * 64;
+        const int key0 = key_of(t, t.s0 + i) + hf * 64;
         float F = P.scale_log2, ev = 0.f, unscale = 1.f;
         int2 e = make_int2(0, 0);
         if constexpr (Q8) {
@@ -708,8 +773,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           if (Q8 && ((e.x | e.y) & 256)) {
             const int em = n % Cfg::kExps, ph = (n / Cfg::kExps) & 1;
             if (!tree_wait2(&exps_full[em], ph, &exps_full[Cfg::kExps + em], ph, P.wait_limit)) ok = false;
-            tree_apart<Cfg::kSpreadK, Cfg::kSpreadV>(sbuf, smem + Cfg::exps_off + em * 256 + hf * 64, e, P.scale_log2,
-                                                     t.L - key0, P.parents ? bits : nullptr, qi, key0 - prefix, &own);
+            tree_apart<Cfg::kSpreadK, Cfg::kSpreadV, WIN>(P, sbuf, smem + Cfg::exps_off + em * 256 + hf * 64, e,
+                                                          t.L - key0, P.parents ? bits : nullptr, WIN ? prefix + qi : qi,
+                                                          WIN ? key0 : key0 - prefix, &own);
             F = 1.f;
             ev = unscale = 0.f;
             __syncwarp();
@@ -717,12 +783,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
-          const bool edge = key0 + 64 > prefix;
+          const bool edge = edge_at(t, key0, 64);
           tmem_wait_ld();
           if (edge) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const uint32_t see = tree_attends(P.parents ? bits : nullptr, qi, key0 + 32 * w - prefix);
+              const uint32_t see = WIN ? window_bits(P, prefix + qi, key0 + 32 * w)
+                                       : tree_attends(P.parents ? bits : nullptr, qi, key0 + 32 * w - prefix);
 #pragma unroll
               for (int k = 0; k < 32; ++k) x[32 * w + k] = see >> k & 1 ? x[32 * w + k] : -INFINITY;
             }
@@ -854,10 +921,16 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       if (!whole && row_ok && (QT == 2 || g == 0))
         S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
       if (any_bad) {
-        if (row_ok && alive)
-          tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK,
-                         whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr,
-                         S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr, Cfg::kRows, col0, 1, col0 + cols);
+        if (row_ok && alive) {
+          __half* to = whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr;
+          float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;
+          if constexpr (WIN)
+            window_patch<Q8, TOK>(P, told[(heard - 1) % Cfg::kAhead], prefix + qi, to, part, Cfg::kRows, col0, 1,
+                                  col0 + cols);
+          else
+            tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK, to,
+                           part, Cfg::kRows, col0, 1, col0 + cols);
+        }
         tree_softmax_bar();
         if (tid - 128 < kTreeWords) bad_s[(tile % Cfg::kBad) * kTreeWords + tid - 128] = 0;
       }
@@ -865,6 +938,31 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
       ++tile;
     }
   } else if (warp >= 12) {
+    if constexpr (Cfg::kLook) {
+      // ================= V tiles looked through before their products =================
+      int tile = 0, vslot = 0, vphase = 0;
+      Tile t;
+      while (ok && next_tile(t)) {
+        const int tiles = key_tiles(t);
+        for (int i = 0; i < tiles; ++i) {
+          if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) {
+            ok = false;
+            break;
+          }
+          const int key0 = key_of(t, t.s0 + i);
+          if (edge_at(t, key0, TOK))
+            clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], key0,
+                               bad_s + (tile % Cfg::kBad) * kTreeWords, lane);
+          if (lane == 0) mbar_arrive(&vready[vslot]);
+          __syncwarp();
+          if (++vslot == VS) {
+            vslot = 0;
+            vphase ^= 1;
+          }
+        }
+        ++tile;
+      }
+    }
     if constexpr (Q8) {
     // ================= codes to fp16 operands =================
     const int part = (warp - 12) / Cfg::kConv, sub = (warp - 12) % Cfg::kConv, kv = part >> 1;
@@ -883,20 +981,26 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     // (rings of this warp's tile: slots and phases counted, as a remainder takes long)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
     int slot = 0, phase = 0, st = part & 1, round = 0, lphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
-    TreeTile t;
-    // The largest exponent of the tile in slot `es`, `keys` of whose rows are the context's; of each kind
-    // the first part's warp tells the softmax, and whether some lie far below it.
-    auto look = [&](int keys, int es, int ph, int m, int& top) {
+    Tile t;
+    // The largest exponent of the tile in slot `es`, from key `key0` on, of the rows that are the context's
+    // (WIN: attended by some row); of each kind the first part's warp tells the softmax, and whether
+    // some lie far below it.
+    auto nothing = [&](int key) {
+      bool none = key >= t.L;
+      if constexpr (WIN) none = none || window_hidden(P, t.lo, key, 1);
+      return none;
+    };
+    auto look = [&](int key0, int es, int ph, int m, int& top) {
       if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
-      const int left = keys - lane * 4;  // of this lane's four
       int low = 255;
       top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = int(e4 >> (8 * j) & 255);
-        top = max(top, left > j ? e : 0);
-        low = min(low, left > j ? e : 255);
+        const bool in = !nothing(key0 + lane * 4 + j);
+        top = max(top, in ? e : 0);
+        low = min(low, in ? e : 255);
       }
       top = max(__reduce_max_sync(FULL, top), kExpLeastByte);
       low = __reduce_min_sync(FULL, low);
@@ -909,12 +1013,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       int top = 0;
-      if (tiles > 0 && !look(t.L - t.s0 * TOK, em, ephase, mm, top)) {
+      if (tiles > 0 && !look(key_of(t, t.s0), em, ephase, mm, top)) {
         ok = false;
         break;
       }
       for (int i = 0; i < tiles; ++i) {
-        const int key0 = (t.s0 + i) * TOK;
+        const int key0 = key_of(t, t.s0 + i);
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
         if (!tree_wait(&landed[2 * round], lphase, P.wait_limit)) {
           ok = false;
@@ -922,22 +1026,23 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
         uint8_t* src = stage + st * Cfg::kStageBytes;
         uint8_t* dst = operand + slot * Cfg::kTile;
-        if (key0 + TOK > prefix) {
-          // the tile reaches the drafts: rows behind the context become 0, and
-          // non-finite elements of the drafts' V rows leave the product
+        if (edge_at(t, key0, TOK)) {
+          // the tile reaches the drafts (WIN: an end of the windows): rows behind the context become 0, and
+          // non-finite elements of the drafts' V rows (of those that not every row sees) leave the product
 #pragma unroll 1
           for (int k = 0; k < ROWS / RPI; ++k) {
             const int key = key0 + row0 + k * RPI, a = key - prefix;
             uint2* p = reinterpret_cast<uint2*>(src + k * 256);
             uint2 x = *p;
-            bool hit = key >= t.L;
+            bool hit = nothing(key), some = key >= prefix;
+            if constexpr (WIN) some = key > t.first(G) || (key < t.lo1 && key >= P.sinks);
             if (hit) {
               x = make_uint2(0, 0);
               if (ch == 0) exps[row0 + k * RPI] = uint8_t(top);
-            } else if (kv && key >= prefix) {
+            } else if (kv && some) {
               hit = clear_nonfinite<true>(x.x);
               hit |= clear_nonfinite<true>(x.y);
-              if (hit) atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
+              if (hit) atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords + (WIN ? 0 : a >> 5) % kTreeWords], 1u << (a & 31));
             }
             if (hit) *p = x;
           }
@@ -981,7 +1086,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
         }
         // the next tile's exponents now, or its softmax would wait for them (trees of 16: 93.8 us so, 103
         // at the tile's own turn, 98 before the wait for the place, 97 behind the hand-over)
-        if (i + 1 < tiles && !look(t.L - key0 - TOK, em, ephase, mm, top)) {
+        if (i + 1 < tiles && !look(key_of(t, t.s0 + i + 1), em, ephase, mm, top)) {
           ok = false;
           break;
         }
@@ -1018,5 +1123,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT>::kThreads, 1)
 // says how much workspace they take.
 cudaError_t tree_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
                     void* ws, cudaStream_t s);
+cudaError_t window_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
+                      void* ws, cudaStream_t s);
 
 }  // namespace pa

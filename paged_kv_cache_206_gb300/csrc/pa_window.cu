@@ -5,7 +5,7 @@
 #include "pa_internal.h"
 #include "pa_tree_any.cuh"
 #include "pa_tree_host.h"
-#include "pa_tree_mma.cuh"
+#include "pa_tree_tc.cuh"
 #include "pa_window.h"
 
 namespace pa {
@@ -24,7 +24,9 @@ bool window_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need
   const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;
   const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
   const int nt = rows <= 8 ? 1 : 2;
-  if (hd <= 64)
+  if (rows > 16 && c.head_size_k == c.head_size_v && (hd == 64 || hd == 128))
+    *e = window_tc(P, hd, q8, rows, c.num_sms, need, ws, stream);
+  else if (hd <= 64)
     *e = window_mma_64(P, q8, nt, c.num_sms, need, ws, stream);
   else if (hd <= 128)
     *e = window_mma_128(P, q8, nt, c.num_sms, need, ws, stream);

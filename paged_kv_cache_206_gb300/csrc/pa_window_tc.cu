@@ -1,0 +1,12 @@
+// Launch of the tcgen05 attention with a window kernels (pa_tree_tc.cuh).
+#include "pa_tree_tc_launch.cuh"
+
+namespace pa {
+
+cudaError_t window_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
+                    void* ws, cudaStream_t s) {
+  return head_size == 64 ? tree_tc_pick<64, true>(P, q8, rows, sms, need, ws, s)
+                         : tree_tc_pick<128, true>(P, q8, rows, sms, need, ws, s);
+}
+
+}  // namespace pa
