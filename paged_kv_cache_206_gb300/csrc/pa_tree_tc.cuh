@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     // in the block table moves on by additions, and the next tile's entry is read
     // before this one's slots are waited for.
     const int box = min(bs & -bs, 64), pieces = TOK / box, step_b = TOK / bs, step_o = TOK % bs;
-    const uint64_t pol = policy_evict_first();
+    // (WIN: the next row tiles read the window again)
+    const uint64_t pol = WIN && QT == 2 ? policy_evict_last() : policy_evict_first();
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
     const uint8_t* exps_of = is_k ? P.key_exps : P.value_exps;
@@ -749,6 +750,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           }
         }
       }
+      // (WIN) the places of the warp's first and last row
+      const int rw = t.r0 + (QT == 2 ? g * 128 : 0) + quarter * 32;
+      const int pw0 = prefix + rw / G, pw1 = prefix + min((rw + 31) / G, t.q - 1);
       float m_ref = -INFINITY, l = 0.f;
       for (int m = 0; m < nj && ok; ++m) {
         const int i = QT == 2 ? m >> 1 : m, hf = QT == 2 ? m & 1 : g, n = n0 + i;
@@ -766,7 +770,15 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
         if (!tree_wait(&s_full[x_of_s], phase, P.wait_limit)) { ok = false; break; }
         tc_fence_after();
-        if (any_row) {
+        if (WIN && any_row && (key0 > pw1 || (pw0 - key0 - 63 >= P.window && key0 >= P.sinks))) {
+          // keys that none of the warp's rows sees: weights of 0
+          const uint32_t none[16] = {};
+          const uint32_t sbuf = uni(tmem_s + x_of_s * 128 + hf * 64 + lane_base);
+          __syncwarp();
+          tmem_st16u(sbuf, none);
+          tmem_st16u(sbuf + 16, none);
+          tmem_wait_st();
+        } else if (any_row) {
           __syncwarp();
           const uint32_t sbuf = uni(tmem_s + x_of_s * 128 + hf * 64 + lane_base);
           float2 own;  // of keys with exponents of their own: the largest score, the sum
@@ -783,7 +795,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
-          const bool edge = edge_at(t, key0, 64);
+          const bool edge = WIN ? key0 + 63 > pw0 || (pw1 - key0 >= P.window && key0 + 64 > P.sinks) : edge_at(t, key0, 64);
           tmem_wait_ld();
           if (edge) {
 #pragma unroll
@@ -993,12 +1005,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     auto look = [&](int key0, int es, int ph, int m, int& top) {
       if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
+      const int left = t.L - key0 - lane * 4;  // of this lane's four
       int low = 255;
       top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = int(e4 >> (8 * j) & 255);
-        const bool in = !nothing(key0 + lane * 4 + j);
+        bool in = left > j;
+        if constexpr (WIN) in = in && !window_hidden(P, t.lo, key0 + lane * 4 + j, 1);
         top = max(top, in ? e : 0);
         low = min(low, in ? e : 255);
       }
