@@ -71,7 +71,7 @@ struct TreeMma {
   static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
   static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
   using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
-  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kSub, kRows, kLead>, TreeWalk<kSub, kRows, kLead>>, Tile>;
+  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kSub, kSub, kRows, kLead>, TreeWalk<kSub, kRows, kLead>>, Tile>;
   static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(Tile) + 7) & ~7u;
   static constexpr uint32_t exps_off = (place_off + sizeof(Place) + 15) & ~15u;  // [stage][K, V][32]
   static constexpr uint32_t bars_off = exps_off + (Q8 ? kMaxStages * 64 : 0);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
   // The first key of a unit, and whether the box of 16 of its keys is none of the tile's (its table
   // entry may be anything).
   auto key_of = [&](int u) {
-    if constexpr (WIN) return place->tile.unit(u) * SUB;
+    if constexpr (WIN) return place->tile.chunk(u) * SUB;
     else return u * SUB;
   };
   auto left_out = [&](int key) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
       int j0 = un * SUB;
       bool edge = j0 + SUB > prefix;  // keys that not every row sees
       if constexpr (WIN) {
-        j0 = t.unit(un) * SUB;
+        j0 = t.chunk(un) * SUB;
         edge = j0 + SUB > p0 + 1 || (j0 < t.lo1 && j0 + SUB > P.sinks);
       }
 
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
           __half* whole = t.slot < 0 ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv : nullptr;
           float* part = S.part_o + (int64_t(max(t.slot, 0)) * NR + row) * HD;
           if constexpr (WIN)
-            window_patch<Q8, SUB>(P, tile_s[done % Cfg::kTiles], prefix + i, whole, part, 1, lane, 32, P.hv);
+            window_patch<Q8, SUB, SUB>(P, tile_s[done % Cfg::kTiles], prefix + i, whole, part, 1, lane, 32, P.hv);
           else
             tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, i, bad_s, P.parents ? mask_s + row * kTreeWords : nullptr,
                            t.s0 * SUB, t.s1 * SUB, whole, part, 1, lane, 32, P.hv);

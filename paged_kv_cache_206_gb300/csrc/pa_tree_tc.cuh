@@ -101,10 +101,10 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
-  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead +
+  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead + (WIN ? 1 : 0) +
                                (kLook ? kVSlots : 0);
   using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
-  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
+  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
   static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(Tile) + 15) & ~15u;
   static constexpr uint32_t tmem_off = (place_off + sizeof(Place) + 15) & ~15u;
@@ -239,13 +239,14 @@ __device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, u
 }
 
 // (WIN) Rows that no row of the tile attends become 0, behind its last token and before the first
-// row's window; of those that some attend the non-finite elements do, under a flag. key0: row 0's key.
+// row's window; of those that some attend the non-finite elements do, under a flag. Of the 64 rows from
+// row0 on, the first one key0's.
 template <int H2>
-__device__ __noinline__ void clean_v_window(uint8_t* vb, const TreeParams& P, const WindowTile& t, int key0,
+__device__ __noinline__ void clean_v_window(uint8_t* vb, const TreeParams& P, const WindowTile& t, int row0, int key0,
                                             uint32_t* bad, int lane) {
-  const auto row = [&](int key) { return min(max(key - key0, 0), 128); };
+  const auto row = [&](int key) { return row0 + min(max(key - key0, 0), 64); };
   const int p0 = t.first(P.group);
-  zero_v_rows<H2>(vb, row(t.L), 128, lane);
+  zero_v_rows<H2>(vb, row(t.L), row0 + 64, lane);
   zero_v_rows<H2>(vb, row(P.sinks), row(t.lo), lane);
   const auto flag = [&](int) { atomicOr(bad, 1u); };
   clear_v_rows<H2>(vb, row(max(t.lo, P.sinks)), row(min(t.lo1, p0 + 1)), lane, flag);
@@ -317,6 +318,7 @@ __device__ __noinline__ void tree_apart(const TreeParams& P, uint32_t sbuf, cons
 template <int HD, bool Q8, int QT, bool WIN>
 __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                   const __grid_constant__ std::conditional_t<WIN, CUtensorMap, int> tmq,
                    const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
   using Cfg = TreeTc<HD, Q8, QT, WIN>;
   using Tile = typename Cfg::Tile;
@@ -352,7 +354,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   uint64_t* q_empty = s_full + 12;            // the row tile's last S complete
   uint64_t* o_free = s_full + 13;             // both O read by the softmax warps
   uint64_t* all_done = s_full + 14;
-  uint64_t* vready = s_full + 15;             // (kLook) [slot] V looked through
+  uint64_t* q_full = s_full + 15;             // (WIN) the queries, by TMA
+  uint64_t* vready = s_full + 16;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -387,6 +390,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
     mbar_init(all_done, 2);
+    if (WIN) mbar_init(q_full, 1);
     fence_barrier_init();
   }
   if (tid < Cfg::kBad * kTreeWords) bad_s[tid] = 0;
@@ -425,10 +429,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     const int units = (w.L - w.q + last + TOK) / TOK;
     return max(0, min(w.s1, units) - w.s0);
   };
-  // The first key of a row tile's unit, and whether some of n keys are not seen by all of its rows.
-  auto key_of = [&](const Tile& w, int u) {
-    if constexpr (WIN) return w.unit(u) * TOK;
-    else return u * TOK;
+  // The first key of a half of a row tile's unit, and whether some of n keys are not seen by all of its rows.
+  auto key_of = [&](const Tile& w, int u, int half) {
+    if constexpr (WIN) return w.chunk(2 * u + half) * 64;
+    else return u * TOK + half * 64;
   };
   auto edge_at = [&](const Tile& w, int key, int n) {
     if constexpr (WIN) return key + n > w.first(G) + 1 || (key < w.lo1 && key + n > P.sinks);
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         if constexpr (WIN) w = w && !window_hidden(P, t.lo, key, box);
         return w;
       };
-      int key = key_of(t, t.s0) + lane * box, blk = key / bs, off = key - blk * bs;
+      int key = key_of(t, t.s0, part) + (lane - part * half) * box, blk = key / bs, off = key - blk * bs;
       int id = tiles > 0 && wanted(key) ? table[blk] : -1;
       for (int i = 0; i < tiles; ++i, ++n) {
         const bool want = wanted(key), there = want && id >= 0 && id < P.num_blocks;
@@ -483,8 +487,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           ++blk;
         }
         if constexpr (WIN) {
-          if (t.s0 + i + 1 == t.far && t.skip) {  // from the sinks to the window
-            key += t.skip * TOK;
+          const int c = 2 * (t.s0 + i) + part;
+          if (t.skip && c < t.far && c + 2 >= t.far) {  // from the sinks to the window
+            key += t.skip * 64;
             blk = key / bs;
             off = key - blk * bs;
           }
@@ -623,6 +628,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     if (lane == 0) S.join[worker].parts = 0;                 // no divided tile yet
     typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
     Tile t, following;
+    int q_phase = 0;
     tree_begin(P, S, place, worker, lane);
     auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
       const bool some = tree_next(P, place);
@@ -654,8 +660,27 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy
       const int ch = lane % CH;
       const uint32_t base = smem_u32(q_s) + (ch >> 3) * Cfg::kHalf;
+      bool by_tma = false;
+      if constexpr (WIN) {
+        // Whole tokens whose heads make up 128 rows: one box of 64 dims of each half tile. Tokens behind
+        // the tile's last come along (their rows are not looked at), zeros behind the last of all.
+        by_tma = 128 % G == 0;
+        if (by_tma) {
+          if (lane == 0) {
+            const uint64_t keep = policy_evict_first();
+            mbar_arrive_expect_tx(q_full, QT * Cfg::kTile);
+#pragma unroll
+            for (int x = 0; x < QT; ++x)
+#pragma unroll
+              for (int h = 0; h < H2; ++h)
+                tma_load_3d(q_s + x * Cfg::kTile + h * Cfg::kHalf, &tmq, q_full, h * 64, t.kvh * G,
+                            t.q_start + t.r0 / G + x * (128 / G), keep);
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll 1
-      for (int r0 = 0; r0 < Cfg::kRows; r0 += 32) {
+      for (int r0 = by_tma ? Cfg::kRows : 0; r0 < Cfg::kRows; r0 += 32) {
         // lane l finds row r0 + l of the query tensor
         const int r = t.r0 + r0 + lane, i = r / G;
         const int64_t tok = int64_t(t.q_start) + i;
@@ -673,6 +698,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       cp_async_wait<0>();
       fence_proxy_async();
       __syncwarp();
+      if (WIN && by_tma) {
+        if (!tree_wait(q_full, q_phase, P.wait_limit)) ok = false;
+        if (!ok) tree_wait(q_full, q_phase);  // (landed before the CTA's memory is given back)
+        q_phase ^= 1;
+      }
       for (int i = 0; i < tiles && ok; ++i, ++n) {
         if (!tree_wait(&kfull[kslot], kphase, P.wait_limit)) { ok = false; break; }
         const bool last = i + 1 == tiles;
@@ -757,7 +787,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       for (int m = 0; m < nj && ok; ++m) {
         const int i = QT == 2 ? m >> 1 : m, hf = QT == 2 ? m & 1 : g, n = n0 + i;
         const int y = QT == 2 ? hf : n & 1, x_of_s = QT == 2 ? g : n & 1, phase = phase_of(n);
-        const int key0 = key_of(t, t.s0 + i) + hf * 64;
+        const int key0 = key_of(t, t.s0 + i, hf);
         float F = P.scale_log2, ev = 0.f, unscale = 1.f;
         int2 e = make_int2(0, 0);
         if constexpr (Q8) {
@@ -895,8 +925,62 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         for (int k = 0; k < kTreeWords; ++k) hit |= bad[k];
         any_bad = tree_softmax_bar(hit != 0);
       }
+      // A whole tile's rows in fp16, 32 columns at a time. Four lanes next to one another hold four rows,
+      // 64 bytes each, and exchange them by quarters, so that a store writes eight rows' 64 bytes
+      // rather than 16 of 32 rows (which took 3.2 us of 256 rows, 0.9 so).
+      const bool swap = WIN && whole;
+      __half* dst[4];
+      if (swap) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = t.r0 + (tr & ~3) + k, qq = rr / G;
+          const int64_t at = int64_t(t.q_start) + qq;
+          dst[k] = qq < t.q && at < P.tokens
+                       ? P.out + (at * P.num_heads + t.kvh * G + rr % G) * HD + col0 + (lane & 3) * 8 : nullptr;
+        }
+      }
 #pragma unroll 1
-      for (int cc = 0; cc < cols / 16; ++cc) {
+      for (int cc = 0; swap && cc < cols / 32; ++cc) {
+        uint32_t h[4][4];  // [eight columns][pairs of them]
+        __syncwarp();
+        const uint32_t from = uni(tmem_o + (QT == 2 ? g * 128 : 0) + col0 + cc * 32 + lane_base);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float o[16], x[16];
+          tmem_ld<16>(from + half * 16, o);
+          if (QT == 1) tmem_ld<16>(from + half * 16 + 128, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            o[k] = inv * (QT == 2 ? o[k] : (w[0] > 0.f ? o[k] * w[0] : 0.f) + (w[1] > 0.f ? x[k] * w[1] : 0.f));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[2 * half + k / 4][k % 4] = pack_half2(o[2 * k], o[2 * k + 1]);
+        }
+        if (cc + 1 == cols / 32) {  // both O are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
+#pragma unroll
+        for (int bit = 1; bit < 4; bit <<= 1) {
+          const bool upper = lane & bit;
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            if (a & bit) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t give = upper ? h[a][k] : h[a | bit][k];
+              const uint32_t got = __shfl_xor_sync(FULL, give, bit);
+              if (upper) h[a][k] = got; else h[a | bit][k] = got;
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (dst[k] && ok) *reinterpret_cast<uint4*>(dst[k] + cc * 32) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+      }
+#pragma unroll 1
+      for (int cc = 0; !swap && cc < cols / 16; ++cc) {
         const int d0 = col0 + cc * 16;
         float o[16], x[16];
         __syncwarp();  // rows that there are not have left the rest of the loop out
@@ -937,7 +1021,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           __half* to = whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr;
           float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;
           if constexpr (WIN)
-            window_patch<Q8, TOK>(P, told[(heard - 1) % Cfg::kAhead], prefix + qi, to, part, Cfg::kRows, col0, 1,
+            window_patch<Q8, TOK, 64>(P, told[(heard - 1) % Cfg::kAhead], prefix + qi, to, part, Cfg::kRows, col0, 1,
                                   col0 + cols);
           else
             tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK, to,
@@ -961,10 +1045,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
             ok = false;
             break;
           }
-          const int key0 = key_of(t, t.s0 + i);
-          if (edge_at(t, key0, TOK))
-            clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], key0,
-                               bad_s + (tile % Cfg::kBad) * kTreeWords, lane);
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            const int key0 = key_of(t, t.s0 + i, hf);
+            if (edge_at(t, key0, 64))
+              clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], hf * 64, key0,
+                                 bad_s + (tile % Cfg::kBad) * kTreeWords, lane);
+          }
           if (lane == 0) mbar_arrive(&vready[vslot]);
           __syncwarp();
           if (++vslot == VS) {
@@ -994,7 +1081,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     const int ns = kv ? VS : KS, nst = kv ? Cfg::kVStages : Cfg::kKStages;
     int slot = 0, phase = 0, st = part & 1, round = 0, lphase = 0, em = 0, ephase = 0, mm = 0, tile = 0;
     Tile t;
-    // The largest exponent of the tile in slot `es`, from key `key0` on, of the rows that are the context's
+    // The largest exponent of the tile in slot `es`, unit u of the row tile, of the rows that are the context's
     // (WIN: attended by some row); of each kind the first part's warp tells the softmax, and whether
     // some lie far below it.
     auto nothing = [&](int key) {
@@ -1002,17 +1089,17 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       if constexpr (WIN) none = none || window_hidden(P, t.lo, key, 1);
       return none;
     };
-    auto look = [&](int key0, int es, int ph, int m, int& top) {
+    auto look = [&](int u, int es, int ph, int m, int& top) {
       if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
-      const int left = t.L - key0 - lane * 4;  // of this lane's four
+      const int key0 = key_of(t, u, lane >> 4) + (lane & 15) * 4, left = t.L - key0;  // this lane's four
       int low = 255;
       top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = int(e4 >> (8 * j) & 255);
         bool in = left > j;
-        if constexpr (WIN) in = in && !window_hidden(P, t.lo, key0 + lane * 4 + j, 1);
+        if constexpr (WIN) in = in && !window_hidden(P, t.lo, key0 + j, 1);
         top = max(top, in ? e : 0);
         low = min(low, in ? e : 255);
       }
@@ -1027,12 +1114,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
       int top = 0;
-      if (tiles > 0 && !look(key_of(t, t.s0), em, ephase, mm, top)) {
+      if (tiles > 0 && !look(t.s0, em, ephase, mm, top)) {
         ok = false;
         break;
       }
       for (int i = 0; i < tiles; ++i) {
-        const int key0 = key_of(t, t.s0 + i);
+        const int key0 = key_of(t, t.s0 + i, part & 1) - (part & 1) * 64;  // of row 0, as this part counts
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
         if (!tree_wait(&landed[2 * round], lphase, P.wait_limit)) {
           ok = false;
@@ -1040,7 +1127,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
         uint8_t* src = stage + st * Cfg::kStageBytes;
         uint8_t* dst = operand + slot * Cfg::kTile;
-        if (edge_at(t, key0, TOK)) {
+        if (WIN ? edge_at(t, key0 + (part & 1) * 64, 64) : edge_at(t, key0, TOK)) {
           // the tile reaches the drafts (WIN: an end of the windows): rows behind the context become 0, and
           // non-finite elements of the drafts' V rows (of those that not every row sees) leave the product
 #pragma unroll 1
@@ -1100,7 +1187,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
         // the next tile's exponents now, or its softmax would wait for them (trees of 16: 93.8 us so, 103
         // at the tile's own turn, 98 before the wait for the place, 97 behind the hand-over)
-        if (i + 1 < tiles && !look(key_of(t, t.s0 + i + 1), em, ephase, mm, top)) {
+        if (i + 1 < tiles && !look(t.s0 + i + 1, em, ephase, mm, top)) {
           ok = false;
           break;
         }

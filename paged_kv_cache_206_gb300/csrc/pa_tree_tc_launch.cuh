@@ -30,6 +30,17 @@ inline bool tree_map(CUtensorMap* m, const void* base, const TreeParams& P, bool
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// The queries as (dims, heads, tokens), a box being 64 dims of a kv head's heads of as many tokens
+// as make 128 rows.
+inline bool window_query_map(CUtensorMap* m, const TreeParams& P) {
+  const cuuint64_t dims[3] = {cuuint64_t(P.hk), cuuint64_t(P.num_heads), cuuint64_t(P.tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(P.hk) * 2, cuuint64_t(P.num_heads) * P.hk * 2};
+  const cuuint32_t b[3] = {64, cuuint32_t(P.group), cuuint32_t(128 / P.group)}, es[3] = {1, 1, 1};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(P.query), dims, strides, b, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 template <int HD, bool Q8, int QT, bool WIN>
 cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cudaStream_t stream) {
   using Cfg = TreeTc<HD, Q8, QT, WIN>;
@@ -50,10 +61,13 @@ cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cu
   CUtensorMap tmk, tmv;
   if (!tree_map(&tmk, P.key_cache, P, Q8, box) || !tree_map(&tmv, P.value_cache, P, Q8, box))
     return cudaErrorInvalidValue;
+  std::conditional_t<WIN, CUtensorMap, int> tmq{};
+  if constexpr (WIN)
+    if (128 % P.group == 0 && !window_query_map(&tmq, P)) return cudaErrorInvalidValue;
   auto kern = tree_tc_kernel<HD, Q8, QT, WIN>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::bytes);
   if (e != cudaSuccess) return e;
-  kern<<<unsigned(sms), Cfg::kThreads, Cfg::bytes, stream>>>(tmk, tmv, P, S);
+  kern<<<unsigned(sms), Cfg::kThreads, Cfg::bytes, stream>>>(tmk, tmv, tmq, P, S);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sms), Cfg::kRows / 32);

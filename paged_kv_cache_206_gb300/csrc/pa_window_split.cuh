@@ -3,9 +3,9 @@
 //
 // A row tile is TT = NR / G whole tokens of one (sequence, kv head), or, for a group of more than
 // NR heads, NR of one token's (HP parts). Tile t's first token stands at position p0 = L - q +
-// t TT, its last at p1, and it walks the units of UNIT keys that any of its rows attends: those
-// of the sinks before the window, then those from the first row's window on up to p1. To the
-// kernels it is a tile of a sequence that ends with its last token; what the first row's window
+// t TT, its last at p1, and it walks the chunks of CHUNK keys that any of its rows attends, UNIT /
+// CHUNK to a unit: those of the sinks before the window, then those from the first row's window
+// on up to p1. To the kernels it is a tile of a sequence that ends with its last token; what the first row's window
 // has left behind is their only addition.
 //
 // On the line a tile takes a place for each key of [0, p1] but those between the sinks and its
@@ -26,9 +26,10 @@ namespace pa {
 // tile's last token (q tokens, L keys), and what its rows' windows leave out.
 struct WindowTile : TreeTile {
   int lo, lo1;    // the first keys of the first and of the last row's window
-  int far, skip;  // units of the sinks, then so many units are left out
+  int far, skip;  // chunks of the sinks, then so many chunks are left out
 
-  __device__ __forceinline__ int unit(int s) const { return s < far ? s : s + skip; }
+  // where the c-th chunk stands in the sequence
+  __device__ __forceinline__ int chunk(int c) const { return c < far ? c : c + skip; }
   // the position of the first row's token
   __device__ __forceinline__ int first(int group) const { return L - q + r0 / group; }
 };
@@ -51,10 +52,9 @@ __device__ __forceinline__ uint32_t window_bits(const TreeParams& P, int p, int 
 }
 
 // Adds to one row's result what was taken out of its product: the non-finite elements of the
-// values that it attends and another row of its tile does not. The row's token stands at p; first and
-// last: its tile's first and last token. The result is fp16 (`out`) or an fp32 partial one
+// values that it attends and another row of its tile does not. The row's token stands at p. The result is fp16 (`out`) or an fp32 partial one
 // (`part`, `stride` apart); dims d0, d0 + step, ... below d1. Rare, hence not inlined.
-template <bool Q8, int UNIT>
+template <bool Q8, int UNIT, int CHUNK>
 __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile& t, int p, __half* out, float* part,
                                           int stride, int d0, int step, int d1) {
   const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
@@ -62,7 +62,7 @@ __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile&
   for (int part_of = 0; part_of < 2; ++part_of) {
     const int from = part_of ? p0 + 1 : max(t.lo, P.sinks), upto = part_of ? t.L : min(t.lo1, p0 + 1);
     for (int key = from; key < upto; ++key) {
-      const int u = key / UNIT, s = u < t.far ? u : u - t.skip;
+      const int c = key / CHUNK, s = (c < t.far ? c : c - t.skip) / (UNIT / CHUNK);
       if (s < t.s0 || s >= t.s1 || !window_sees(P, p, key)) continue;
       const int block = table[key / P.block_size];
       if (block < 0 || block >= P.num_blocks) continue;
@@ -78,13 +78,12 @@ __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile&
   }
 }
 
-template <int UNIT, int NR, int LEAD>
+template <int UNIT, int CHUNK, int NR, int LEAD>
 struct WindowLine {
   // Sequence b's tokens, and the tiles that they make for a kv head. The tokens count as stated (at
   // most all that there are) whether the lengths keep the constraints or not.
   struct Seq {
     int q, L, tiles;  // token tiles; 0: none
-    int64_t head;     // places of a part of a kv head's heads
   };
   static __device__ __forceinline__ int tokens_of(const TreeParams& P) { return max(NR / P.group, 1); }
   static __device__ __forceinline__ int parts_of(const TreeParams& P) { return (P.group - 1) / NR + 1; }
@@ -101,7 +100,7 @@ struct WindowLine {
   }
 
   static __device__ __forceinline__ Seq load(const TreeParams& P, int b) {
-    if (b >= P.batch) return Seq{0, 0, 0, 0};
+    if (b >= P.batch) return Seq{0, 0, 0};
     Seq s;
     s.q = P.q_seqlens ? P.q_seqlens[b] : 1;
     s.L = P.context_lens[b];
@@ -110,11 +109,14 @@ struct WindowLine {
     s.q = tree_tokens(P, 0, max(s.q, 0));
     const bool some = ok && s.q > 0;
     s.tiles = some ? (s.q - 1) / tokens_of(P) + 1 : 0;
-    s.head = some ? upto(P, s, s.tiles) : 0;
     return s;
   }
+  // Places of a part of a kv head's heads, and of all of them.
+  static __device__ __forceinline__ int64_t of_head(const TreeParams& P, const Seq& s) {
+    return s.tiles ? upto(P, s, s.tiles) : 0;
+  }
   static __device__ __forceinline__ int64_t total(const TreeParams& P, const Seq& s) {
-    return s.head * P.kv_heads * parts_of(P);
+    return of_head(P, s) * P.kv_heads * parts_of(P);
   }
 
   // Where worker c's piece begins: total * c / n.
@@ -131,19 +133,22 @@ struct WindowLine {
   }
 };
 
-// One worker's way along the line (warp-collective, every lane the same).
-template <int UNIT, int NR, int LEAD>
+// One worker's way along the line (warp-collective, every lane the same). It finds its first tile by the
+// sums and goes on from tile to tile.
+template <int UNIT, int CHUNK, int NR, int LEAD>
 struct WindowWalk {
-  using Line = WindowLine<UNIT, NR, LEAD>;
-  int64_t u, u0, u1, before, total;
+  using Line = WindowLine<UNIT, CHUNK, NR, LEAD>;
+  int64_t u, u0, u1, total;
+  int64_t at;        // the place where the tile at hand begins,
+  int head, tile;    // part of a kv head's heads, token tile
   int q_start, b, nact, worker;
   typename Line::Seq seq;
 
   __device__ __forceinline__ bool begin(const TreeParams& P, const TreeSplit& S, int w, int lane) {
     constexpr unsigned FULL = 0xffffffffu;
     worker = w;
-    u = u0 = u1 = before = 0;
-    q_start = 0;
+    u = u0 = u1 = at = 0;
+    head = tile = q_start = 0;
     b = -1;
     // places and tokens of 32 sequences up to this lane's (the tokens stop at all that there are)
     int64_t places;
@@ -177,6 +182,7 @@ struct WindowWalk {
     u = u0 = Line::begin(total, worker, nact);
     u1 = Line::begin(total, worker + 1, nact);
     // the sequence that place u0 belongs to
+    int64_t before = 0;
     for (int b0 = 0; b0 < P.batch && u0 < u1; b0 += 32) {
       if (b0) {
         seq = Line::load(P, b0 + lane);
@@ -192,7 +198,16 @@ struct WindowWalk {
         seq.q = __shfl_sync(FULL, seq.q, l);
         seq.L = __shfl_sync(FULL, seq.L, l);
         seq.tiles = __shfl_sync(FULL, seq.tiles, l);
-        seq.head = __shfl_sync(FULL, seq.head, l);
+        // its tile: the last one that begins at or before u0
+        const int64_t of_head = Line::of_head(P, seq);
+        head = int(tree_div(u0 - before, of_head));
+        at = before + head * of_head;
+        int end = seq.tiles;
+        while (end - tile > 1) {
+          const int mid = (tile + end) >> 1;
+          if (Line::upto(P, seq, mid) <= u0 - at) tile = mid; else end = mid;
+        }
+        at += Line::upto(P, seq, tile);
         return true;
       }
       before += __shfl_sync(FULL, places, 31);
@@ -203,53 +218,56 @@ struct WindowWalk {
   }
 
   __device__ __forceinline__ bool next(const TreeParams& P, WindowTile& w) {
+    const int tt = Line::tokens_of(P), parts = Line::parts_of(P);
     while (u < u1) {
-      while (u >= before + Line::total(P, seq)) {
-        before += Line::total(P, seq);
-        q_start = tree_tokens(P, q_start, seq.q);
-        if (++b >= P.batch) {  // only if the lengths changed under the kernel
-          u = u1;
-          return false;
-        }
-        seq = Line::load(P, b);
-      }
-      const int head = int(tree_div(u - before, seq.head));  // part of a kv head's heads
-      const int64_t from = before + head * seq.head;
-      int t = 0, end = seq.tiles;  // the last tile that begins at or before place u
-      while (end - t > 1) {
-        const int mid = (t + end) >> 1;
-        if (Line::upto(P, seq, mid) <= u - from) t = mid; else end = mid;
-      }
-      const int64_t p_tile = from + Line::upto(P, seq, t);
-      const int width = int(from + Line::upto(P, seq, t + 1) - p_tile), keys = width - LEAD * UNIT;
-      const int p0 = int(u - p_tile), p1 = int(min(int64_t(width), p0 + (u1 - u)));
+      // the tile's tokens, places and units
+      const int pre = seq.L - seq.q, i0 = tile * tt, i1 = min(i0 + tt, seq.q) - 1;
+      const int64_t out = int64_t(pre) + i0 + 1 - P.window - P.sinks;
+      const int keys = pre + i1 + 1 - (out > 0 ? int(out) : 0), width = keys + LEAD * UNIT;
+      const int p0 = int(u - at), p1 = int(min(int64_t(width), p0 + (u1 - u)));
       const bool first = u == u0;
+      const int64_t end = at + width;
       u += p1 - p0;
-      // the tile's tokens and units
-      const int tt = Line::tokens_of(P), pre = seq.L - seq.q, i0 = t * tt, i1 = min(i0 + tt, seq.q) - 1;
       w.lo = max(pre + i0 - P.window + 1, 0);
       w.lo1 = max(pre + i1 - P.window + 1, 0);
-      const int near = w.lo / UNIT, end_unit = (pre + i1) / UNIT + 1;
-      w.far = P.sinks == 0 ? 0 : min((P.sinks - 1) / UNIT + 1, near);
+      const int near = w.lo / CHUNK, last = (pre + i1) / CHUNK;
+      w.far = P.sinks == 0 ? 0 : min((P.sinks - 1) / CHUNK + 1, near);
       w.skip = near - w.far;
-      const int units = end_unit - w.skip;
+      const int units = (last - w.skip) / (UNIT / CHUNK) + 1;
       const auto cut = [&](int x) {
         return x <= LEAD * UNIT ? 0 : x == width ? units : int(tree_div(int64_t(x - LEAD * UNIT) * units, keys));
       };
       w.s0 = cut(p0);
       w.s1 = cut(p1);
-      if (w.s0 == w.s1) continue;  // nothing but a lead, or less than a unit: the next worker's
-      if (tree_rows_missing(P, q_start, seq.q)) set_status(P.status, PA_STATUS_BIT_PLAN);
-      const int parts = Line::parts_of(P);
       w.b = b;
       w.q_start = q_start;
       w.q = i1 + 1;
       w.L = pre + i1 + 1;
       w.kvh = parts == 1 ? head : head / parts;
       w.r0 = i0 * P.group + (head - w.kvh * parts) * NR;
+      const bool missing = tree_rows_missing(P, q_start, seq.q);
+      if (u == end) {  // on to the next tile
+        at = end;
+        if (++tile == seq.tiles) {
+          tile = 0;
+          if (++head == P.kv_heads * parts && u < u1) {
+            head = 0;
+            do {
+              q_start = tree_tokens(P, q_start, seq.q);
+              if (++b >= P.batch) {  // only if the lengths changed under the kernel
+                u = u1;
+                break;
+              }
+              seq = Line::load(P, b);
+            } while (seq.tiles == 0);
+          }
+        }
+      }
+      if (w.s0 == w.s1) continue;  // nothing but a lead, or less than a unit: the next worker's
+      if (missing) set_status(P.status, PA_STATUS_BIT_PLAN);
       w.slot = w.s0 == 0 && w.s1 == units ? -1 : 2 * worker + (first ? 0 : 1);
       w.parts = 0;
-      if (w.s0 == 0 && w.s1 < units) w.parts = Line::last_before(total, p_tile + width, nact) - worker + 1;
+      if (w.s0 == 0 && w.s1 < units) w.parts = Line::last_before(total, end, nact) - worker + 1;
       return true;
     }
     return false;
