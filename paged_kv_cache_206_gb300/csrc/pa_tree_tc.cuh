@@ -50,13 +50,13 @@ namespace pa {
 
 // WIN: pa_window_forward's kernel, for drafts, prompts and parts of prompts. Its tiles are those of
 // pa_window_split.cuh. As every row tile has keys that only some of its rows see, at both ends of their
-// windows, the fp16 cache's V tiles are looked through by a warp of their own (12), ahead of the
+// windows, the fp16 cache's V tiles are looked through by four warps of their own (12-15), ahead of the
 // product's issuer.
 template <int HD, bool Q8, int QT, bool WIN>
 struct TreeTc {
   static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
   static constexpr bool kLook = WIN && !Q8;  // there is a warp that looks the V tiles through
-  static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : kLook ? 416 : 384;
+  static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : kLook ? 512 : 384;
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
   // What a row tile costs next to its key tiles, in these, measured at 32 trees over 64 to 8192
@@ -89,7 +89,7 @@ struct TreeTc {
   // 2^-9) times 2^-14 is still exact in fp16, and weights may stand 2^7 higher (2^(8 + 7) < 65504).
   static constexpr int kSpreadK = 14, kSpreadV = 7, kLift = Q8 ? kSpreadV : 0;
   static constexpr int kAhead = 4;                       // row tiles told to the roles
-  static constexpr int kRoles = Q8 ? 11 + 4 * kConv : kLook ? 12 : 11;  // warps that are told
+  static constexpr int kRoles = Q8 ? 11 + 4 * kConv : kLook ? 15 : 11;  // warps that are told
   static constexpr uint32_t q_off = 0;
   static constexpr uint32_t k_off = q_off + QT * kTile;
   static constexpr uint32_t v_off = k_off + kKSlots * kTile;
@@ -188,25 +188,26 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t f) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// An fp16 V tile [HD / 64][128 rows][128 B] before its product (one warp): rows [lo, hi) become 0;
-template <int H2>
+// An fp16 V tile [HD / 64][128 rows][128 B] before its product (N threads, this one the `lane`-th): rows
+// [lo, hi) become 0;
+template <int H2, int N = 32>
 __device__ __forceinline__ void zero_v_rows(uint8_t* vb, int lo, int hi, int lane) {
-  for (int at = lane; at < (hi - lo) * 8 * H2; at += 32) {
+  for (int at = lane; at < (hi - lo) * 8 * H2; at += N) {
     const int r = lo + at / (8 * H2), ch = at % (8 * H2);
     *reinterpret_cast<uint4*>(vb + (ch >> 3) * (128 * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
 }
 
 // non-finite elements of rows [lo, hi) become 0, and `flag` is told their rows.
-template <int H2, class Flag>
+template <int H2, int N = 32, class Flag>
 __device__ __forceinline__ void clear_v_rows(uint8_t* vb, int lo, int hi, int lane, Flag flag) {
   constexpr uint32_t HALF = 128 * 128;
   constexpr int B = 8;  // chunks a lane has in registers at a time
-  for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += 32 * B) {
+  for (int at0 = lane; at0 < (hi - lo) * 8 * H2; at0 += N * B) {
     uint4 v[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
+      const int at = at0 + N * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
       v[k] = make_uint4(0, 0, 0, 0);
       if (r < hi) v[k] = lds128(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16);
     }
@@ -217,7 +218,7 @@ __device__ __forceinline__ void clear_v_rows(uint8_t* vb, int lo, int hi, int la
       hit |= clear_nonfinite<false>(v[k].z);
       hit |= clear_nonfinite<false>(v[k].w);
       if (hit) {
-        const int at = at0 + 32 * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
+        const int at = at0 + N * k, r = lo + at / (8 * H2), ch = at % (8 * H2);
         *reinterpret_cast<uint4*>(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16) = v[k];
         flag(r);
       }
@@ -240,17 +241,17 @@ __device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, u
 
 // (WIN) Rows that no row of the tile attends become 0, behind its last token and before the first
 // row's window; of those that some attend the non-finite elements do, under a flag. Of the 64 rows from
-// row0 on, the first one key0's.
+// row0 on, the first one key0's (four warps; `lane` of their 128).
 template <int H2>
 __device__ __noinline__ void clean_v_window(uint8_t* vb, const TreeParams& P, const WindowTile& t, int row0, int key0,
                                             uint32_t* bad, int lane) {
   const auto row = [&](int key) { return row0 + min(max(key - key0, 0), 64); };
   const int p0 = t.first(P.group);
-  zero_v_rows<H2>(vb, row(t.L), row0 + 64, lane);
-  zero_v_rows<H2>(vb, row(P.sinks), row(t.lo), lane);
+  zero_v_rows<H2, 128>(vb, row(t.L), row0 + 64, lane);
+  zero_v_rows<H2, 128>(vb, row(P.sinks), row(t.lo), lane);
   const auto flag = [&](int) { atomicOr(bad, 1u); };
-  clear_v_rows<H2>(vb, row(max(t.lo, P.sinks)), row(min(t.lo1, p0 + 1)), lane, flag);
-  clear_v_rows<H2>(vb, row(p0 + 1), row(t.L), lane, flag);
+  clear_v_rows<H2, 128>(vb, row(max(t.lo, P.sinks)), row(min(t.lo1, p0 + 1)), lane, flag);
+  clear_v_rows<H2, 128>(vb, row(p0 + 1), row(t.L), lane, flag);
   fence_proxy_async();
   __syncwarp();
 }
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     for (int i = 0; i < VS; ++i) {
       mbar_init(&vfull[i], Q8 ? 2 * Cfg::kConv : 1);
       mbar_init(&vempty[i], 1);
-      if (Cfg::kLook) mbar_init(&vready[i], 1);
+      if (Cfg::kLook) mbar_init(&vready[i], 4);
     }
     for (int i = 0; i < Cfg::kMeta; ++i) mbar_init(&meta_full[i], 2);
     for (int i = 0; i < 2 * Cfg::kExps; ++i) mbar_init(&exps_full[i], 1);
@@ -1050,7 +1051,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
             const int key0 = key_of(t, t.s0 + i, hf);
             if (edge_at(t, key0, 64))
               clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], hf * 64, key0,
-                                 bad_s + (tile % Cfg::kBad) * kTreeWords, lane);
+                                 bad_s + (tile % Cfg::kBad) * kTreeWords, tid - 384);
           }
           if (lane == 0) mbar_arrive(&vready[vslot]);
           __syncwarp();
