@@ -102,7 +102,7 @@ struct TreeTc {
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
   static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead + (WIN ? 1 : 0) +
-                               (kLook ? kVSlots : 0);
+                               (kLook ? kVSlots + 2 : 0);
   using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
   using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   uint64_t* o_free = s_full + 13;             // both O read by the softmax warps
   uint64_t* all_done = s_full + 14;
   uint64_t* q_full = s_full + 15;             // (WIN) the queries, by TMA
-  uint64_t* vready = s_full + 16;             // (kLook) [slot] V looked through
+  uint64_t* stat_full = s_full + 16;          // (kLook) [row tile's parity] maxima and sums told
+  uint64_t* vready = s_full + 18;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -389,9 +390,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       mbar_init(&o_full[g], 1);
     }
     mbar_init(q_empty, 1);
-    mbar_init(o_free, 8);
-    mbar_init(all_done, 2);
+    mbar_init(o_free, Cfg::kLook ? 4 : 8);
+    mbar_init(all_done, WIN ? 1 : 2);
     if (WIN) mbar_init(q_full, 1);
+    if (Cfg::kLook) {
+      mbar_init(&stat_full[0], 8);
+      mbar_init(&stat_full[1], 8);
+    }
     fence_barrier_init();
   }
   if (tid < Cfg::kBad * kTreeWords) bad_s[tid] = 0;
@@ -438,6 +443,41 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   auto edge_at = [&](const Tile& w, int key, int n) {
     if constexpr (WIN) return key + n > w.first(G) + 1 || (key < w.lo1 && key + n > P.sinks);
     else return key + n > w.L - w.q;
+  };
+  // Where four rows of a row tile, from row tr & ~3 on, go to in the output; null for rows that are not.
+  auto rows_out = [&](const Tile& w, int tr, __half* (&dst)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = w.r0 + (tr & ~3) + k, i = r / G;
+      const int64_t tok = int64_t(w.q_start) + i;
+      dst[k] = i < w.q && tok < P.tokens
+                   ? P.out + (tok * P.num_heads + w.kvh * G + r % G) * HD + (lane & 3) * 8 : nullptr;
+    }
+  };
+  // 32 columns of a row a thread in fp16. Four lanes next to one another hold four rows, 64 bytes each, and
+  // exchange them by quarters, so that a store writes eight rows' 64 bytes rather than 16 of 32
+  // rows (which took 3.2 us of a tile of 256 rows, 2 so).
+  auto store32 = [&](const float* o, float inv, __half* const (&dst)[4], int col) {
+    uint32_t h[4][4];  // [eight columns][pairs of them]
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k / 4][k % 4] = pack_half2(o[2 * k] * inv, o[2 * k + 1] * inv);
+#pragma unroll
+    for (int bit = 1; bit < 4; bit <<= 1) {
+      const bool upper = lane & bit;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        if (a & bit) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t give = upper ? h[a][k] : h[a | bit][k];
+          const uint32_t got = __shfl_xor_sync(FULL, give, bit);
+          if (upper) h[a][k] = got; else h[a | bit][k] = got;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + col) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
   };
   // The phase of key tile n's S and jobs on their barriers.
   auto phase_of = [](int n) { return QT == 2 ? n & 1 : n >> 1 & 1; };
@@ -566,6 +606,91 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         tree_wait(&exps_full[(is_k ? 0 : Cfg::kExps) + i % Cfg::kExps], (i / Cfg::kExps) & 1);
     }
   } else if (warp == 1) {
+    if constexpr (WIN) {
+    // ================= S = Q K^T and O_g += P_g V =================
+    // Both products in one order, each S right behind the product that read the P in its columns: products of one
+    // thread are done in their order, so no wait stands between them. (With S issued by warp 3 behind a wait for that product
+    // the chains' period was 1.85 us a key tile, QT = 2.) The whole warp waits and counts, one lane issues.
+    const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
+    const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
+    uint64_t* vcome = Cfg::kLook ? vready : vfull;
+    int tile = 0, n0 = 0;  // row tiles and key tiles so far
+    int kslot = 0, kphase = 0, vslot = 0, vphase = 0;
+    Tile t;
+    while (ok && next_tile(t)) {
+      const int tiles = uni(key_tiles(t));
+      // S of key tile i, of query tile g (QT = 2)
+      auto scores = [&](int i, int g) {
+        if (g == 0 && !tree_wait(&kfull[kslot], kphase, P.wait_limit)) {
+          ok = false;
+          return;
+        }
+        const int x = QT == 2 ? g : (n0 + i) & 1;
+        const bool last = i + 1 == tiles && g == QT - 1;
+        const uint64_t bk = dk + uint32_t(kslot * (Cfg::kTile >> 4));
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < H2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma(tmem_s + x * 128, dq + g * (Cfg::kTile >> 4) + ((h * Cfg::kHalf + k * 32) >> 4),
+                     bk + ((h * Cfg::kHalf + k * 32) >> 4), kIdescQK, (h | k) != 0);
+          tc_commit(&s_full[x]);
+          if (g == QT - 1) tc_commit(&kempty[kslot]);
+          if (last) tc_commit(q_empty);  // the queries may be replaced
+        }
+        __syncwarp();
+        if (g == QT - 1 && ++kslot == KS) {
+          kslot = 0;
+          kphase ^= 1;
+        }
+      };
+      if (!tree_wait(q_full, tile & 1, P.wait_limit)) {
+        ok = false;
+        break;
+      }
+      scores(0, 0);
+      if (ok && QT == 2) scores(0, 1);
+      if (ok && QT == 1 && tiles > 1) scores(1, 0);
+      // the last row tile's O has been read before the first product overwrites it
+      if (ok && tile > 0 && !tree_wait(o_free, (tile - 1) & 1, P.wait_limit)) ok = false;
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int n = n0 + i, phase = phase_of(n);
+        const bool last = i + 1 == tiles;
+        if (!tree_wait(&vcome[vslot], vphase, P.wait_limit)) { ok = false; break; }
+#pragma unroll
+        for (int j = 0; j < 2 * QT; ++j) {
+          const int g = j & 1, hf = QT == 2 ? j >> 1 : g, y = QT == 2 ? hf : n & 1;
+          if (!tree_wait(&p_full[2 * g + y], phase, P.wait_limit)) { ok = false; break; }
+          const uint64_t bv = dv + uint32_t(vslot * (Cfg::kTile >> 4) + hf * (8192 >> 4));
+          const uint32_t p_col = tmem_s + (QT == 2 ? g : n & 1) * 128 + hf * 64;
+          const bool more = i != 0 || (QT == 2 && hf);
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_tmem_a(tmem_o + g * 128, p_col + k * 8, bv + (k * 2048 >> 4), kIdescPV, k || more);
+            tc_commit(&pv_done[2 * g + y]);
+            if (j == 2 * QT - 1) tc_commit(&vempty[vslot]);
+            if (last && (QT == 1 || hf)) tc_commit(&o_full[g]);
+          }
+          __syncwarp();
+          if (QT == 2 && hf == 1 && !last) scores(i + 1, g);
+          if (!ok) break;
+        }
+        if (QT == 1 && ok && i + 2 < tiles) scores(i + 2, 0);
+        if (++vslot == VS) {
+          vslot = 0;
+          vphase ^= 1;
+        }
+      }
+      n0 += tiles;
+      ++tile;
+    }
+    if (elect_one()) tc_commit(all_done);
+    __syncwarp();
+    } else {
     // ================= O_g += P_g V =================
     // Per key tile the two chains' products in turn (QT = 2: of its halves in turn).
     // The whole warp waits and counts, one lane issues: what the instructions take
@@ -573,7 +698,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     // 16-byte units (the address field, in the low bits, does not overflow).
     const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
     int tile = 0, n0 = 0, vslot = 0, vphase = 0;  // row tiles and key tiles so far; the next V tile
-    uint64_t* vcome = Cfg::kLook ? vready : vfull;
     Tile t;
     while (ok && next_tile(t)) {
       const int tiles = uni(key_tiles(t));
@@ -596,8 +720,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       for (int i = 0; i < tiles && ok; ++i) {
         const int n = n0 + i, phase = phase_of(n);
         const bool last = i + 1 == tiles;
-        if (!tree_wait(&vcome[vslot], vphase, P.wait_limit)) { ok = false; break; }
-        if constexpr (!Q8 && !WIN) {
+        if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) { ok = false; break; }
+        if constexpr (!Q8) {
           // Rows behind the context may hold anything and become 0; non-finite
           // elements of the drafts' rows leave the product
           const int key0 = (s0 + i) * TOK;
@@ -622,14 +746,94 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     }
     if (elect_one()) tc_commit(all_done);
     __syncwarp();
+    }
   } else if (warp == 3) {
+    if constexpr (WIN) {
+    // ================= row tiles and their queries =================
+    int told_n = 0, tile = 0;  // row tiles told, begun
+    bool by_tma = false;
+    if (lane == 0) S.join[worker].parts = 0;  // no divided tile yet
+    typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
+    Tile t, following;
+    tree_begin(P, S, place, worker, lane);
+    auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
+      const bool some = tree_next(P, place);
+      following = place->tile;
+      if (!some) following.q = -1;
+      const int at = told_n % Cfg::kAhead;
+      if (!tree_wait(&tile_empty[at], ((told_n / Cfg::kAhead) & 1) ^ 1, P.wait_limit)) {
+        ok = false;
+        return;
+      }
+      if (lane == 0) {
+        told[at] = following;
+        if (following.q >= 0 && following.parts) tree_note(S, worker, following);
+        mbar_arrive(&tile_full[at]);
+      }
+      __syncwarp();
+      ++told_n;
+      if (place->walk.u >= place->walk.u1) launch_dependents();  // the worker's last tile is known
+    };
+    tell();
+    while (ok && following.q >= 0) {
+      t = following;
+      // the queries, once the last row tile's S are complete
+      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit)) {
+        ok = false;
+        break;
+      }
+      // Whole tokens whose heads make up 128 rows: one box of 64 dims of each half tile. Tokens behind
+      // the tile's last come along (their rows are not looked at), zeros behind the last of all.
+      by_tma = 128 % G == 0;
+      if (by_tma) {
+        if (lane == 0) {
+          const uint64_t keep = policy_evict_first();
+          mbar_arrive_expect_tx(q_full, QT * Cfg::kTile);
+#pragma unroll
+          for (int x = 0; x < QT; ++x)
+#pragma unroll
+            for (int h = 0; h < H2; ++h)
+              tma_load_3d(q_s + x * Cfg::kTile + h * Cfg::kHalf, &tmq, q_full, h * 64, t.kvh * G,
+                          t.q_start + t.r0 / G + x * (128 / G), keep);
+        }
+        __syncwarp();
+      } else {
+        constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy
+        const int ch = lane % CH;
+        const uint32_t base = smem_u32(q_s) + (ch >> 3) * Cfg::kHalf;
+#pragma unroll 1
+        for (int r0 = 0; r0 < Cfg::kRows; r0 += 32) {
+          // lane l finds row r0 + l of the query tensor
+          const int r = t.r0 + r0 + lane, i = r / G;
+          const int64_t tok = int64_t(t.q_start) + i;
+          const int from = i < t.q && tok < P.tokens ? int(tok * P.num_heads + t.kvh * G + r % G) : -1;
+#pragma unroll
+          for (int k = 0; k < 32 / RPI; ++k) {
+            const int row = r0 + k * RPI + lane / CH;
+            const int src = __shfl_sync(FULL, from, k * RPI + lane / CH);
+            cp_async16(base + (row >> 7) * Cfg::kTile + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                       P.query + int64_t(max(src, 0)) * HD + ch * 8, src >= 0);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        __syncwarp();
+      }
+      tell();  // the next row tile, while these queries come
+      ++tile;
+    }
+    // (landed before the CTA's memory is given back)
+    if (by_tma) tree_wait(q_full, (tile - 1) & 1);
+    } else {
     // ================= row tiles, their queries, S = Q K^T =================
     const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
     int told_n = 0, tile = 0, n = 0, kslot = 0, kphase = 0;  // tiles told, begun; key tiles; the next K tile
     if (lane == 0) S.join[worker].parts = 0;                 // no divided tile yet
     typename Cfg::Place* place = reinterpret_cast<typename Cfg::Place*>(smem + Cfg::place_off);
     Tile t, following;
-    int q_phase = 0;
     tree_begin(P, S, place, worker, lane);
     auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
       const bool some = tree_next(P, place);
@@ -661,27 +865,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy
       const int ch = lane % CH;
       const uint32_t base = smem_u32(q_s) + (ch >> 3) * Cfg::kHalf;
-      bool by_tma = false;
-      if constexpr (WIN) {
-        // Whole tokens whose heads make up 128 rows: one box of 64 dims of each half tile. Tokens behind
-        // the tile's last come along (their rows are not looked at), zeros behind the last of all.
-        by_tma = 128 % G == 0;
-        if (by_tma) {
-          if (lane == 0) {
-            const uint64_t keep = policy_evict_first();
-            mbar_arrive_expect_tx(q_full, QT * Cfg::kTile);
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-#pragma unroll
-              for (int h = 0; h < H2; ++h)
-                tma_load_3d(q_s + x * Cfg::kTile + h * Cfg::kHalf, &tmq, q_full, h * 64, t.kvh * G,
-                            t.q_start + t.r0 / G + x * (128 / G), keep);
-          }
-          __syncwarp();
-        }
-      }
 #pragma unroll 1
-      for (int r0 = by_tma ? Cfg::kRows : 0; r0 < Cfg::kRows; r0 += 32) {
+      for (int r0 = 0; r0 < Cfg::kRows; r0 += 32) {
         // lane l finds row r0 + l of the query tensor
         const int r = t.r0 + r0 + lane, i = r / G;
         const int64_t tok = int64_t(t.q_start) + i;
@@ -699,11 +884,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       cp_async_wait<0>();
       fence_proxy_async();
       __syncwarp();
-      if (WIN && by_tma) {
-        if (!tree_wait(q_full, q_phase, P.wait_limit)) ok = false;
-        if (!ok) tree_wait(q_full, q_phase);  // (landed before the CTA's memory is given back)
-        q_phase ^= 1;
-      }
       for (int i = 0; i < tiles && ok; ++i, ++n) {
         if (!tree_wait(&kfull[kslot], kphase, P.wait_limit)) { ok = false; break; }
         const bool last = i + 1 == tiles;
@@ -745,6 +925,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     }
     if (elect_one()) tc_commit(all_done);
     __syncwarp();
+    }
   } else if (warp >= 4 && warp < 12) {
     // ================= softmax: group g (warps 4-7, 8-11) is chain g =================
     const int g = (warp - 4) >> 2, quarter = warp & 3, m_lane = quarter * 32 + lane;
@@ -893,12 +1074,19 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 
       // ---- the end of the row tile
       float w[2] = {1.f, 0.f}, M = m_ref, sum = l;  // weights of O_0 and O_1 (QT = 2: of its own)
-      if constexpr (QT == 1) {
+      if constexpr (QT == 1 || Cfg::kLook) {
         float2* st = stat + (tile & 1) * 256;
         st[g * 128 + m_lane] = make_float2(m_ref, l);
       }
       if (!tree_wait(&tile_full[heard % Cfg::kAhead], (heard / Cfg::kAhead) & 1, P.wait_limit)) ok = false;
       alive = !tree_softmax_bar(!ok);
+      if constexpr (Cfg::kLook) {  // the looking warps write the rows out
+        if (lane == 0) mbar_arrive(&stat_full[tile & 1]);
+        __syncwarp();
+        n0 += tiles;
+        ++tile;
+        continue;
+      }
       if constexpr (QT == 1) {
         const float2* st = stat + (tile & 1) * 256;
         const float2 a = st[m_lane], b = st[128 + m_lane];
@@ -926,59 +1114,32 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         for (int k = 0; k < kTreeWords; ++k) hit |= bad[k];
         any_bad = tree_softmax_bar(hit != 0);
       }
-      // A whole tile's rows in fp16, 32 columns at a time. Four lanes next to one another hold four rows,
-      // 64 bytes each, and exchange them by quarters, so that a store writes eight rows' 64 bytes
-      // rather than 16 of 32 rows (which took 3.2 us of 256 rows, 0.9 so).
       const bool swap = WIN && whole;
-      __half* dst[4];
-      if (swap) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = t.r0 + (tr & ~3) + k, qq = rr / G;
-          const int64_t at = int64_t(t.q_start) + qq;
-          dst[k] = qq < t.q && at < P.tokens
-                       ? P.out + (at * P.num_heads + t.kvh * G + rr % G) * HD + col0 + (lane & 3) * 8 : nullptr;
-        }
-      }
+      __half* dst4[4];
+      if (swap) rows_out(t, tr, dst4);
 #pragma unroll 1
       for (int cc = 0; swap && cc < cols / 32; ++cc) {
-        uint32_t h[4][4];  // [eight columns][pairs of them]
+        float o[32];
         __syncwarp();
         const uint32_t from = uni(tmem_o + (QT == 2 ? g * 128 : 0) + col0 + cc * 32 + lane_base);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float o[16], x[16];
-          tmem_ld<16>(from + half * 16, o);
-          if (QT == 1) tmem_ld<16>(from + half * 16 + 128, x);
+        for (int half = 0; half < 32; half += 16) {
+          float x[16];
+          tmem_ld<16>(from + half, o + half);
+          if (QT == 1) tmem_ld<16>(from + half + 128, x);
           tmem_wait_ld();
+          if constexpr (QT == 1) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            o[k] = inv * (QT == 2 ? o[k] : (w[0] > 0.f ? o[k] * w[0] : 0.f) + (w[1] > 0.f ? x[k] * w[1] : 0.f));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[2 * half + k / 4][k % 4] = pack_half2(o[2 * k], o[2 * k + 1]);
+            for (int k = 0; k < 16; ++k)
+              o[half + k] = (w[0] > 0.f ? o[half + k] * w[0] : 0.f) + (w[1] > 0.f ? x[k] * w[1] : 0.f);
+          }
         }
         if (cc + 1 == cols / 32) {  // both O are read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free);
         }
-#pragma unroll
-        for (int bit = 1; bit < 4; bit <<= 1) {
-          const bool upper = lane & bit;
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            if (a & bit) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t give = upper ? h[a][k] : h[a | bit][k];
-              const uint32_t got = __shfl_xor_sync(FULL, give, bit);
-              if (upper) h[a][k] = got; else h[a | bit][k] = got;
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (dst[k] && ok) *reinterpret_cast<uint4*>(dst[k] + cc * 32) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+        if (ok) store32(o, inv, dst4, col0 + cc * 32);
       }
 #pragma unroll 1
       for (int cc = 0; !swap && cc < cols / 16; ++cc) {
@@ -1018,6 +1179,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       if (!whole && row_ok && (QT == 2 || g == 0))
         S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
       if (any_bad) {
+        __syncwarp();  // (WIN: a row's results are stored by four lanes)
         if (row_ok && alive) {
           __half* to = whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr;
           float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;
@@ -1036,31 +1198,105 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     }
   } else if (warp >= 12) {
     if constexpr (Cfg::kLook) {
-      // ================= V tiles looked through before their products =================
-      int tile = 0, vslot = 0, vphase = 0;
-      Tile t;
-      while (ok && next_tile(t)) {
-        const int tiles = key_tiles(t);
-        for (int i = 0; i < tiles; ++i) {
-          if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) {
-            ok = false;
-            break;
-          }
+      // ================= V tiles looked through before their products; rows written out =================
+      // The first V tile of the next row tile is looked through before a row tile's rows are written: its
+      // product waits for both.
+      const int quarter = warp & 3, m_lane = quarter * 32 + lane;
+      const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+      const float2* stat = reinterpret_cast<const float2*>(smem + Cfg::stat_off);
+      int tile = 0, vslot = 0, vphase = 0, oc = 0;
+      auto look = [&](const Tile& t, int i) {
+        if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) {
+          ok = false;
+          return;
+        }
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            const int key0 = key_of(t, t.s0 + i, hf);
-            if (edge_at(t, key0, 64))
-              clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], hf * 64, key0,
-                                 bad_s + (tile % Cfg::kBad) * kTreeWords, tid - 384);
+        for (int hf = 0; hf < 2; ++hf) {
+          const int key0 = key_of(t, t.s0 + i, hf);
+          if (edge_at(t, key0, 64))
+            clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], hf * 64, key0,
+                               bad_s + (tile % Cfg::kBad) * kTreeWords, tid - 384);
+        }
+        if (lane == 0) mbar_arrive(&vready[vslot]);
+        __syncwarp();
+        if (++vslot == VS) {
+          vslot = 0;
+          vphase ^= 1;
+        }
+      };
+      auto write_out = [&](const Tile& t, int k) {
+        const float2* st = stat + (k & 1) * 256;
+        if (!tree_wait(&stat_full[k & 1], (k >> 1) & 1, P.wait_limit) ||
+            !tree_wait2(&o_full[0], oc & 1, &o_full[1], oc & 1, P.wait_limit)) {
+          ok = false;
+          return;
+        }
+        ++oc;
+        tc_fence_after();
+        const bool whole = t.slot < 0;
+        const uint32_t bad = bad_s[(k % Cfg::kBad) * kTreeWords];
+#pragma unroll 1
+        for (int x = 0; x < QT; ++x) {
+          const int tr = x * 128 + m_lane, r = t.r0 + tr, qi = r / G;
+          const int64_t tok = int64_t(t.q_start) + qi;
+          const bool row_ok = qi < t.q && tok < P.tokens;
+          const float2 a = st[tr], b = QT == 1 ? st[128 + tr] : make_float2(-INFINITY, 0.f);
+          const float M = fmaxf(a.x, b.x), ref = M == -INFINITY ? 0.f : M;
+          const float w0 = QT == 1 ? ex2(a.x - ref) : 1.f, w1 = ex2(b.x - ref);  // (0: a chain none of whose keys it saw)
+          const float sum = a.y * w0 + b.y * w1, inv = whole ? 1.f / sum : 1.f;
+          __half* dst[4];
+          if (whole) rows_out(t, tr, dst);
+          float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;  // by columns
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            float o[64];
+            __syncwarp();
+            const uint32_t from = uni(tmem_o + x * 128 + cc * 32 + lane_base);
+            tmem_ld32(from, o);
+            if (QT == 1) tmem_ld32(from + 128, o + 32);
+            tmem_wait_ld();
+            if (x == QT - 1 && cc + 1 == HD / 32) {  // both O are read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(o_free);
+            }
+            if constexpr (QT == 1) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = (w0 > 0.f ? o[j] * w0 : 0.f) + (w1 > 0.f ? o[j + 32] * w1 : 0.f);
+            }
+            if (whole) {
+              store32(o, inv, dst, cc * 32);
+            } else if (row_ok) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) part[int64_t(cc * 32 + j) * Cfg::kRows] = o[j];
+            }
           }
-          if (lane == 0) mbar_arrive(&vready[vslot]);
-          __syncwarp();
-          if (++vslot == VS) {
-            vslot = 0;
-            vphase ^= 1;
+          if (!whole && row_ok) S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
+          if (bad) {
+            __syncwarp();
+            if (row_ok)
+              window_patch<Q8, TOK, 64>(P, t, t.L - t.q + qi,
+                                        whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr, part,
+                                        Cfg::kRows, 0, 1, HD);
+            __syncwarp();
           }
         }
+      };
+      Tile t;
+      bool have = next_tile(t);
+      if (have) look(t, 0);
+      while (ok && have) {
+        // the flags of four row tiles ago, which every warp has written out
+        if (warp == 12 && lane == 0) bad_s[((tile + 4) % Cfg::kBad) * kTreeWords] = 0;
+        const int tiles = key_tiles(t);
+        for (int i = 1; i < tiles && ok; ++i) look(t, i);
+        if (!ok) break;
+        const Tile done = t;
         ++tile;
+        have = next_tile(t);
+        if (have) look(t, 0);
+        if (ok) write_out(done, tile - 1);
       }
     }
     if constexpr (Q8) {
