@@ -23,6 +23,7 @@ struct TreeParams {
   int batch, num_heads, kv_heads, group, hk, hv, block_size, num_blocks, max_blocks_per_seq;
   int max_q;
   int window, sinks;  // (pa_window_forward)
+  uint32_t group_inverse;  // ceil(2^32 / group) where the group is below 2^15 and above 1, else 0
   float scale_log2;  // scale * log2(e)
   uint32_t wait_limit;  // cycles a wait on another role's progress may take
 };

@@ -53,6 +53,7 @@ inline pa_status tree_arguments(const pa_config& c, int64_t tokens, const void* 
   P.num_heads = c.num_heads;
   P.kv_heads = c.kv_heads;
   P.group = c.num_heads / c.kv_heads;
+  P.group_inverse = P.group > 1 && P.group < (1 << 15) ? uint32_t((uint64_t(1) << 32) / P.group + 1) : 0;
   P.hk = c.head_size_k;
   P.hv = c.head_size_v;
   P.block_size = c.block_size;

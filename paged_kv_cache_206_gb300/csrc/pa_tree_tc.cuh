@@ -55,7 +55,8 @@ namespace pa {
 template <int HD, bool Q8, int QT, bool WIN>
 struct TreeTc {
   static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
-  static constexpr bool kLook = WIN && !Q8;  // there is a warp that looks the V tiles through
+  static constexpr bool kLook = WIN && !Q8;  // there are warps that look the V tiles through,
+  static constexpr bool kShare = kLook && HD == 128 && QT == 2;  // and write the second half of the rows out
   static constexpr int kThreads = Q8 ? 384 + 4 * 32 * kConv : kLook ? 512 : 384;
   static constexpr int kTok = 128;
   static constexpr int kRows = 128 * QT;
@@ -101,7 +102,7 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
-  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead + (WIN ? 1 : 0) +
+  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead + (WIN ? 2 : 0) +
                                (kLook ? kVSlots + 2 : 0);
   using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
   using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
@@ -211,6 +212,16 @@ __device__ __forceinline__ void clear_v_rows(uint8_t* vb, int lo, int hi, int la
       v[k] = make_uint4(0, 0, 0, 0);
       if (r < hi) v[k] = lds128(vb + (ch >> 3) * HALF + r * 128 + (ch & 7) * 16);
     }
+    // zero times anything finite is zero: one product a word tells whether there is something to look for
+    __half2 sum = __float2half2_rn(0.f);
+    const __half2 zero = sum;
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const __half2* h = reinterpret_cast<const __half2*>(&v[k]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = __hfma2(h[j], zero, sum);
+    }
+    if (__hbeq2(sum, zero)) continue;
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       bool hit = clear_nonfinite<false>(v[k].x);
@@ -239,19 +250,21 @@ __device__ __noinline__ void clean_v_tile(uint8_t* vb, int lo, int hi, int a0, u
   __syncwarp();
 }
 
-// (WIN) Rows that no row of the tile attends become 0, behind its last token and before the first
-// row's window; of those that some attend the non-finite elements do, under a flag. Of the 64 rows from
-// row0 on, the first one key0's (four warps; `lane` of their 128).
+// (WIN) Of the 64 rows from row0 on, the first one key0's, of which some are not seen by every row of the
+// tile: those that no row attends become 0, behind its last token and before the first row's window; of
+// those that some attend the non-finite elements do, under a flag (four warps; `lane` of their 128).
+// p0: the place of the tile's first token.
 template <int H2>
-__device__ __noinline__ void clean_v_window(uint8_t* vb, const TreeParams& P, const WindowTile& t, int row0, int key0,
-                                            uint32_t* bad, int lane) {
+__device__ __forceinline__ void clean_v_window(uint8_t* vb, const WindowTile& t, int p0, int sinks, int row0, int key0,
+                                               uint32_t* bad, int lane) {
   const auto row = [&](int key) { return row0 + min(max(key - key0, 0), 64); };
-  const int p0 = t.first(P.group);
-  zero_v_rows<H2, 128>(vb, row(t.L), row0 + 64, lane);
-  zero_v_rows<H2, 128>(vb, row(P.sinks), row(t.lo), lane);
   const auto flag = [&](int) { atomicOr(bad, 1u); };
-  clear_v_rows<H2, 128>(vb, row(max(t.lo, P.sinks)), row(min(t.lo1, p0 + 1)), lane, flag);
-  clear_v_rows<H2, 128>(vb, row(p0 + 1), row(t.L), lane, flag);
+  // two ranges of each kind, by one loop's code each
+#pragma unroll 1
+  for (int upper = 0; upper < 2; ++upper) {
+    zero_v_rows<H2, 128>(vb, row(upper ? t.L : sinks), upper ? row0 + 64 : row(t.lo), lane);
+    clear_v_rows<H2, 128>(vb, row(upper ? p0 + 1 : max(t.lo, sinks)), row(upper ? t.L : min(t.lo1, p0 + 1)), lane, flag);
+  }
   fence_proxy_async();
   __syncwarp();
 }
@@ -356,8 +369,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   uint64_t* o_free = s_full + 13;             // both O read by the softmax warps
   uint64_t* all_done = s_full + 14;
   uint64_t* q_full = s_full + 15;             // (WIN) the queries, by TMA
-  uint64_t* stat_full = s_full + 16;          // (kLook) [row tile's parity] maxima and sums told
-  uint64_t* vready = s_full + 18;             // (kLook) [slot] V looked through
+  uint64_t* o_free1 = s_full + 16;            // (WIN, QT = 2) O_1 read, o_free O_0 alone
+  uint64_t* stat_full = s_full + 17;          // (kLook) [row tile's parity] maxima and sums told
+  uint64_t* vready = s_full + 19;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
   const int worker = blockIdx.x;
 
@@ -390,7 +404,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       mbar_init(&o_full[g], 1);
     }
     mbar_init(q_empty, 1);
-    mbar_init(o_free, Cfg::kLook ? 4 : 8);
+    mbar_init(o_free, (WIN && QT == 2 ? 4 : 8) + (Cfg::kShare ? 4 : 0));
+    if (WIN) mbar_init(o_free1, 4 + (Cfg::kShare ? 4 : 0));
     mbar_init(all_done, WIN ? 1 : 2);
     if (WIN) mbar_init(q_full, 1);
     if (Cfg::kLook) {
@@ -440,27 +455,30 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     if constexpr (WIN) return w.chunk(2 * u + half) * 64;
     else return u * TOK + half * 64;
   };
-  auto edge_at = [&](const Tile& w, int key, int n) {
-    if constexpr (WIN) return key + n > w.first(G) + 1 || (key < w.lo1 && key + n > P.sinks);
-    else return key + n > w.L - w.q;
+  // (first: the place of its first token, WIN; of the first token of all)
+  auto edge_at = [&](const Tile& w, int first, int key, int n) {
+    if constexpr (WIN) return key + n > first + 1 || (key < w.lo1 && key + n > P.sinks);
+    else return key + n > first;
   };
-  // Where four rows of a row tile, from row tr & ~3 on, go to in the output; null for rows that are not.
-  auto rows_out = [&](const Tile& w, int tr, __half* (&dst)[4]) {
+  // The token of a row of a row tile, and its head of the group.
+  auto token_of = [&](const Tile& w, int row) {
+    if constexpr (WIN) return w.token(P, row);
+    else return (w.r0 + row) / G;
+  };
+  auto head_of = [&](const Tile& w, int row, int token) { return w.r0 + row - token * G; };
+  // Where the rows of four lanes next to one another go to in the output, this lane's to `mine`; null for
+  // rows that are not.
+  auto rows_out = [&](__half* mine, __half* (&dst)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = w.r0 + (tr & ~3) + k, i = r / G;
-      const int64_t tok = int64_t(w.q_start) + i;
-      dst[k] = i < w.q && tok < P.tokens
-                   ? P.out + (tok * P.num_heads + w.kvh * G + r % G) * HD + (lane & 3) * 8 : nullptr;
+      const uint64_t a = __shfl_sync(FULL, reinterpret_cast<uint64_t>(mine), (lane & ~3) + k);
+      dst[k] = a ? reinterpret_cast<__half*>(a) + (lane & 3) * 8 : nullptr;
     }
   };
   // 32 columns of a row a thread in fp16. Four lanes next to one another hold four rows, 64 bytes each, and
   // exchange them by quarters, so that a store writes eight rows' 64 bytes rather than 16 of 32
   // rows (which took 3.2 us of a tile of 256 rows, 2 so).
-  auto store32 = [&](const float* o, float inv, __half* const (&dst)[4], int col) {
-    uint32_t h[4][4];  // [eight columns][pairs of them]
-#pragma unroll
-    for (int k = 0; k < 16; ++k) h[k / 4][k % 4] = pack_half2(o[2 * k] * inv, o[2 * k + 1] * inv);
+  auto store32 = [&](uint32_t (&h)[4][4], __half* const (&dst)[4], int col) {  // [eight columns][pairs of them]
 #pragma unroll
     for (int bit = 1; bit < 4; bit <<= 1) {
       const bool upper = lane & bit;
@@ -478,6 +496,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + col) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+  };
+  auto pack32 = [&](const float* o, float inv, uint32_t (&h)[4][4]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k / 4][k % 4] = pack_half2(o[2 * k] * inv, o[2 * k + 1] * inv);
   };
   // The phase of key tile n's S and jobs on their barriers.
   auto phase_of = [](int n) { return QT == 2 ? n & 1 : n >> 1 & 1; };
@@ -653,8 +675,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       scores(0, 0);
       if (ok && QT == 2) scores(0, 1);
       if (ok && QT == 1 && tiles > 1) scores(1, 0);
-      // the last row tile's O has been read before the first product overwrites it
-      if (ok && tile > 0 && !tree_wait(o_free, (tile - 1) & 1, P.wait_limit)) ok = false;
       for (int i = 0; i < tiles && ok; ++i) {
         const int n = n0 + i, phase = phase_of(n);
         const bool last = i + 1 == tiles;
@@ -662,6 +682,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 2 * QT; ++j) {
           const int g = j & 1, hf = QT == 2 ? j >> 1 : g, y = QT == 2 ? hf : n & 1;
+          // the last row tile's O has been read before the first product overwrites it
+          if (i == 0 && tile > 0 && (QT == 2 ? hf == 0 : g == 0) &&
+              !tree_wait(QT == 2 && g ? o_free1 : o_free, (tile - 1) & 1, P.wait_limit)) {
+            ok = false;
+            break;
+          }
           if (!tree_wait(&p_full[2 * g + y], phase, P.wait_limit)) { ok = false; break; }
           const uint64_t bv = dv + uint32_t(vslot * (Cfg::kTile >> 4) + hf * (8192 >> 4));
           const uint32_t p_col = tmem_s + (QT == 2 ? g : n & 1) * 128 + hf * 64;
@@ -940,7 +966,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     Tile t;
     while (alive && next_tile(t)) {
       const int tiles = key_tiles(t), nj = QT * tiles;
-      const int prefix = t.L - t.q, r = t.r0 + tr, qi = r / G;
+      const int prefix = t.L - t.q, qi = token_of(t, tr), head = head_of(t, tr, qi);
       const int64_t tok = int64_t(t.q_start) + qi;
       const bool row_ok = qi < t.q && tok < P.tokens;
       const bool any_row = __any_sync(FULL, row_ok);
@@ -963,8 +989,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
       }
       // (WIN) the places of the warp's first and last row
-      const int rw = t.r0 + (QT == 2 ? g * 128 : 0) + quarter * 32;
-      const int pw0 = prefix + rw / G, pw1 = prefix + min((rw + 31) / G, t.q - 1);
+      const int rw = (QT == 2 ? g * 128 : 0) + quarter * 32;
+      const int pw0 = WIN ? prefix + token_of(t, rw) : 0, pw1 = WIN ? prefix + min(token_of(t, rw + 31), t.q - 1) : 0;
       float m_ref = -INFINITY, l = 0.f;
       for (int m = 0; m < nj && ok; ++m) {
         const int i = QT == 2 ? m >> 1 : m, hf = QT == 2 ? m & 1 : g, n = n0 + i;
@@ -1007,7 +1033,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
-          const bool edge = WIN ? key0 + 63 > pw0 || (pw1 - key0 >= P.window && key0 + 64 > P.sinks) : edge_at(t, key0, 64);
+          const bool edge = WIN ? key0 + 63 > pw0 || (pw1 - key0 >= P.window && key0 + 64 > P.sinks) : edge_at(t, prefix, key0, 64);
           tmem_wait_ld();
           if (edge) {
 #pragma unroll
@@ -1074,19 +1100,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 
       // ---- the end of the row tile
       float w[2] = {1.f, 0.f}, M = m_ref, sum = l;  // weights of O_0 and O_1 (QT = 2: of its own)
-      if constexpr (QT == 1 || Cfg::kLook) {
+      if constexpr (QT == 1 || Cfg::kShare) {
         float2* st = stat + (tile & 1) * 256;
         st[g * 128 + m_lane] = make_float2(m_ref, l);
       }
       if (!tree_wait(&tile_full[heard % Cfg::kAhead], (heard / Cfg::kAhead) & 1, P.wait_limit)) ok = false;
       alive = !tree_softmax_bar(!ok);
-      if constexpr (Cfg::kLook) {  // the looking warps write the rows out
-        if (lane == 0) mbar_arrive(&stat_full[tile & 1]);
-        __syncwarp();
-        n0 += tiles;
-        ++tile;
-        continue;
-      }
+      if (Cfg::kShare && lane == 0) mbar_arrive(&stat_full[tile & 1]);
+      __syncwarp();
       if constexpr (QT == 1) {
         const float2* st = stat + (tile & 1) * 256;
         const float2 a = st[m_lane], b = st[128 + m_lane];
@@ -1106,9 +1127,13 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       const bool whole = t.slot < 0;
       const float inv = whole ? 1.f / sum : 1.f;
       const uint32_t* bad = bad_s + (tile % Cfg::kBad) * kTreeWords;
-      const int col0 = QT == 1 ? g * (HD / 2) : 0, cols = QT == 1 ? HD / 2 : HD;
+      // (kShare: of the first half of the columns)
+      constexpr int kCols = (QT == 1 ? HD / 2 : HD) / (Cfg::kShare ? 2 : 1);
+      const int col0 = QT == 1 ? g * kCols : 0, cols = kCols;
       bool any_bad = false;
-      if (drafts) {
+      if constexpr (Cfg::kLook) {
+        any_bad = bad[0] != 0;
+      } else if (drafts) {
         uint32_t hit = 0;
 #pragma unroll
         for (int k = 0; k < kTreeWords; ++k) hit |= bad[k];
@@ -1116,7 +1141,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       }
       const bool swap = WIN && whole;
       __half* dst4[4];
-      if (swap) rows_out(t, tr, dst4);
+      if (swap) rows_out(row_ok ? P.out + (tok * P.num_heads + t.kvh * G + head) * HD : nullptr, dst4);
 #pragma unroll 1
       for (int cc = 0; swap && cc < cols / 32; ++cc) {
         float o[32];
@@ -1134,12 +1159,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
               o[half + k] = (w[0] > 0.f ? o[half + k] * w[0] : 0.f) + (w[1] > 0.f ? x[k] * w[1] : 0.f);
           }
         }
-        if (cc + 1 == cols / 32) {  // both O are read
+        if (cc + 1 == cols / 32) {  // both O (QT = 2: the chain's own) are read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
+          if (lane == 0) mbar_arrive(QT == 2 && g ? o_free1 : o_free);
         }
-        if (ok) store32(o, inv, dst4, col0 + cc * 32);
+        uint32_t h[4][4];
+        pack32(o, inv, h);
+        if (ok) store32(h, dst4, col0 + cc * 32);
       }
 #pragma unroll 1
       for (int cc = 0; !swap && cc < cols / 16; ++cc) {
@@ -1153,7 +1180,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         if (cc + 1 == cols / 16) {  // both O are read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
+          if (lane == 0) mbar_arrive(WIN && QT == 2 && g ? o_free1 : o_free);
         }
         if (!row_ok || !ok) continue;
 #pragma unroll
@@ -1163,7 +1190,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           o[k] = tiles > 0 ? v : 0.f;
         }
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD + d0);
+          uint4* dst = reinterpret_cast<uint4*>(P.out + (tok * P.num_heads + t.kvh * G + head) * HD + d0);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             dst[k] = make_uint4(pack_half2(o[8 * k] * inv, o[8 * k + 1] * inv),
@@ -1181,7 +1208,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       if (any_bad) {
         __syncwarp();  // (WIN: a row's results are stored by four lanes)
         if (row_ok && alive) {
-          __half* to = whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr;
+          __half* to = whole ? P.out + (tok * P.num_heads + t.kvh * G + head) * HD : nullptr;
           float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;
           if constexpr (WIN)
             window_patch<Q8, TOK, 64>(P, told[(heard - 1) % Cfg::kAhead], prefix + qi, to, part, Cfg::kRows, col0, 1,
@@ -1190,8 +1217,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
             tree_patch<Q8>(P, t.b, t.q, prefix, t.kvh, qi, bad, P.parents ? bits : nullptr, t.s0 * TOK, t.s1 * TOK, to,
                            part, Cfg::kRows, col0, 1, col0 + cols);
         }
-        tree_softmax_bar();
-        if (tid - 128 < kTreeWords) bad_s[(tile % Cfg::kBad) * kTreeWords + tid - 128] = 0;
+        if constexpr (!Cfg::kLook) {  // (the looking warps clear their flags themselves)
+          tree_softmax_bar();
+          if (tid - 128 < kTreeWords) bad_s[(tile % Cfg::kBad) * kTreeWords + tid - 128] = 0;
+        }
       }
       n0 += tiles;
       ++tile;
@@ -1205,7 +1234,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       const uint32_t lane_base = uint32_t(quarter * 32) << 16;
       const float2* stat = reinterpret_cast<const float2*>(smem + Cfg::stat_off);
       int tile = 0, vslot = 0, vphase = 0, oc = 0;
-      auto look = [&](const Tile& t, int i) {
+      auto look = [&](const Tile& t, int p0, int i) {
         if (!tree_wait(&vfull[vslot], vphase, P.wait_limit)) {
           ok = false;
           return;
@@ -1213,8 +1242,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           const int key0 = key_of(t, t.s0 + i, hf);
-          if (edge_at(t, key0, 64))
-            clean_v_window<H2>(vring + vslot * Cfg::kTile, P, told[(heard - 1) % Cfg::kAhead], hf * 64, key0,
+          if (edge_at(t, p0, key0, 64))
+            clean_v_window<H2>(vring + vslot * Cfg::kTile, t, p0, P.sinks, hf * 64, key0,
                                bad_s + (tile % Cfg::kBad) * kTreeWords, tid - 384);
         }
         if (lane == 0) mbar_arrive(&vready[vslot]);
@@ -1226,77 +1255,71 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       };
       auto write_out = [&](const Tile& t, int k) {
         const float2* st = stat + (k & 1) * 256;
-        if (!tree_wait(&stat_full[k & 1], (k >> 1) & 1, P.wait_limit) ||
-            !tree_wait2(&o_full[0], oc & 1, &o_full[1], oc & 1, P.wait_limit)) {
+        const bool whole = t.slot < 0;
+        if (!tree_wait(&stat_full[k & 1], (k >> 1) & 1, P.wait_limit)) {
           ok = false;
           return;
         }
-        ++oc;
-        tc_fence_after();
-        const bool whole = t.slot < 0;
-        const uint32_t bad = bad_s[(k % Cfg::kBad) * kTreeWords];
 #pragma unroll 1
-        for (int x = 0; x < QT; ++x) {
-          const int tr = x * 128 + m_lane, r = t.r0 + tr, qi = r / G;
+        for (int x = 0; x < 2; ++x) {
+          const int tr = x * 128 + m_lane, qi = token_of(t, tr);
           const int64_t tok = int64_t(t.q_start) + qi;
           const bool row_ok = qi < t.q && tok < P.tokens;
-          const float2 a = st[tr], b = QT == 1 ? st[128 + tr] : make_float2(-INFINITY, 0.f);
-          const float M = fmaxf(a.x, b.x), ref = M == -INFINITY ? 0.f : M;
-          const float w0 = QT == 1 ? ex2(a.x - ref) : 1.f, w1 = ex2(b.x - ref);  // (0: a chain none of whose keys it saw)
-          const float sum = a.y * w0 + b.y * w1, inv = whole ? 1.f / sum : 1.f;
+          const float inv = whole ? 1.f / st[tr].y : 1.f;
+          __half* mine = row_ok ? P.out + (tok * P.num_heads + t.kvh * G + head_of(t, tr, qi)) * HD : nullptr;
           __half* dst[4];
-          if (whole) rows_out(t, tr, dst);
+          rows_out(mine, dst);
           float* part = S.part_o + int64_t(max(t.slot, 0)) * HD * Cfg::kRows + tr;  // by columns
-#pragma unroll 1
-          for (int cc = 0; cc < HD / 32; ++cc) {
-            float o[64];
-            __syncwarp();
-            const uint32_t from = uni(tmem_o + x * 128 + cc * 32 + lane_base);
-            tmem_ld32(from, o);
-            if (QT == 1) tmem_ld32(from + 128, o + 32);
-            tmem_wait_ld();
-            if (x == QT - 1 && cc + 1 == HD / 32) {  // both O are read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(o_free);
-            }
-            if constexpr (QT == 1) {
+          if (!tree_wait(&o_full[x], oc & 1, P.wait_limit)) {
+            ok = false;
+            return;
+          }
+          tc_fence_after();
+          float o[2][32];
+          __syncwarp();
+          const uint32_t from = uni(tmem_o + x * 128 + HD / 2 + lane_base);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                o[j] = (w0 > 0.f ? o[j] * w0 : 0.f) + (w1 > 0.f ? o[j + 32] * w1 : 0.f);
-            }
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(from + cc * 32, o[cc]);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x ? o_free1 : o_free);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
             if (whole) {
-              store32(o, inv, dst, cc * 32);
+              uint32_t h[4][4];
+              pack32(o[cc], inv, h);
+              store32(h, dst, HD / 2 + cc * 32);
             } else if (row_ok) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) part[int64_t(cc * 32 + j) * Cfg::kRows] = o[j];
+              for (int j = 0; j < 32; ++j) part[int64_t(HD / 2 + cc * 32 + j) * Cfg::kRows] = o[cc][j];
             }
           }
-          if (!whole && row_ok) S.part_ml[int64_t(t.slot) * Cfg::kRows + tr] = make_float2(M, sum);
-          if (bad) {
+          if (bad_s[(k % Cfg::kBad) * kTreeWords]) {
             __syncwarp();
             if (row_ok)
-              window_patch<Q8, TOK, 64>(P, t, t.L - t.q + qi,
-                                        whole ? P.out + (tok * P.num_heads + t.kvh * G + r % G) * HD : nullptr, part,
-                                        Cfg::kRows, 0, 1, HD);
+              window_patch<Q8, TOK, 64>(P, t, t.L - t.q + qi, whole ? mine : nullptr, part, Cfg::kRows, HD / 2, 1, HD);
             __syncwarp();
           }
         }
+        ++oc;
       };
       Tile t;
       bool have = next_tile(t);
-      if (have) look(t, 0);
+      int p0 = t.first();
+      if (have) look(t, p0, 0);
       while (ok && have) {
         // the flags of four row tiles ago, which every warp has written out
         if (warp == 12 && lane == 0) bad_s[((tile + 4) % Cfg::kBad) * kTreeWords] = 0;
         const int tiles = key_tiles(t);
-        for (int i = 1; i < tiles && ok; ++i) look(t, i);
+        for (int i = 1; i < tiles && ok; ++i) look(t, p0, i);
         if (!ok) break;
         const Tile done = t;
         ++tile;
         have = next_tile(t);
-        if (have) look(t, 0);
-        if (ok) write_out(done, tile - 1);
+        p0 = t.first();
+        if (have) look(t, p0, 0);
+        if (Cfg::kShare && ok) write_out(done, tile - 1);
       }
     }
     if constexpr (Q8) {
@@ -1350,6 +1373,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     };
     while (ok && next_tile(t)) {
       const int tiles = key_tiles(t), prefix = t.L - t.q;
+      int p0 = prefix;
+      if constexpr (WIN) p0 = t.first();
       int top = 0;
       if (tiles > 0 && !look(t.s0, em, ephase, mm, top)) {
         ok = false;
@@ -1364,7 +1389,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
         uint8_t* src = stage + st * Cfg::kStageBytes;
         uint8_t* dst = operand + slot * Cfg::kTile;
-        if (WIN ? edge_at(t, key0 + (part & 1) * 64, 64) : edge_at(t, key0, TOK)) {
+        if (WIN ? edge_at(t, p0, key0 + (part & 1) * 64, 64) : edge_at(t, p0, key0, TOK)) {
           // the tile reaches the drafts (WIN: an end of the windows): rows behind the context become 0, and
           // non-finite elements of the drafts' V rows (of those that not every row sees) leave the product
 #pragma unroll 1
@@ -1373,7 +1398,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
             uint2* p = reinterpret_cast<uint2*>(src + k * 256);
             uint2 x = *p;
             bool hit = nothing(key), some = key >= prefix;
-            if constexpr (WIN) some = key > t.first(G) || (key < t.lo1 && key >= P.sinks);
+            if constexpr (WIN) some = key > p0 || (key < t.lo1 && key >= P.sinks);
             if (hit) {
               x = make_uint2(0, 0);
               if (ch == 0) exps[row0 + k * RPI] = uint8_t(top);

@@ -27,11 +27,18 @@ namespace pa {
 struct WindowTile : TreeTile {
   int lo, lo1;    // the first keys of the first and of the last row's window
   int far, skip;  // chunks of the sinks, then so many chunks are left out
+  int token0;     // the first row's token
 
   // where the c-th chunk stands in the sequence
   __device__ __forceinline__ int chunk(int c) const { return c < far ? c : c + skip; }
   // the position of the first row's token
-  __device__ __forceinline__ int first(int group) const { return L - q + r0 / group; }
+  __device__ __forceinline__ int first() const { return L - q + token0; }
+  // The token of the n-th row: the first one's and (its place in the group + n) / group, as a product with
+  // 2^32 / group, which is exact while that and the group stay below 2^16.
+  __device__ __forceinline__ int token(const TreeParams& P, int n) const {
+    const int at = r0 - token0 * P.group + n;
+    return token0 + (P.group_inverse ? int(__umulhi(uint32_t(at), P.group_inverse)) : at / P.group);
+  }
 };
 
 // Whether none of the keys [key, key + n) is attended by a tile's rows, the first one's window beginning at lo.
@@ -58,7 +65,7 @@ template <bool Q8, int UNIT, int CHUNK>
 __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile& t, int p, __half* out, float* part,
                                           int stride, int d0, int step, int d1) {
   const int32_t* table = P.block_tables + int64_t(t.b) * P.max_blocks_per_seq;
-  const int p0 = t.first(P.group);
+  const int p0 = t.first();
   for (int part_of = 0; part_of < 2; ++part_of) {
     const int from = part_of ? p0 + 1 : max(t.lo, P.sinks), upto = part_of ? t.L : min(t.lo1, p0 + 1);
     for (int key = from; key < upto; ++key) {
@@ -245,6 +252,7 @@ struct WindowWalk {
       w.L = pre + i1 + 1;
       w.kvh = parts == 1 ? head : head / parts;
       w.r0 = i0 * P.group + (head - w.kvh * parts) * NR;
+      w.token0 = i0;
       const bool missing = tree_rows_missing(P, q_start, seq.q);
       if (u == end) {  // on to the next tile
         at = end;
