@@ -62,8 +62,10 @@ struct TreeTc {
   static constexpr int kRows = 128 * QT;
   // What a row tile costs next to its key tiles, in these, measured at 32 trees over 64 to 8192
   // keys, heads of 128: trees of 5 to 16 in 8 bits 108 us at 3, 97 at 5, 95 at 6, 96 at 8, 99 at 12; of
-  // 64 in fp16 144 at 3, 135 at 4, 132 at 5, 136 at 8 (and 16 of those 75, 76, 77 and 81).
-  static constexpr int kLead = Q8 ? 6 : 4;
+  // 64 in fp16 144 at 3, 135 at 4, 132 at 5, 136 at 8 (and 16 of those 75, 76, 77 and 81). With a window, whose tiles
+  // end with less: prompts in fp16 317 at 2, 315 at 3, 320 at 4; parts in 8 bits 210, 198, - and 195 at 5, 197 at 6;
+  // drafts in 8 bits 57 at 2 and 3, 60 at 5.
+  static constexpr int kLead = WIN ? (Q8 && QT == 2 ? 5 : 3) : Q8 ? 6 : 4;
   static constexpr int kHalves = HD / 64;
   static constexpr uint32_t kHalf = 128 * 128;           // 64 dims of 128 fp16 rows
   static constexpr uint32_t kTile = kHalf * kHalves;     // a K or V tile, a query tile
@@ -188,6 +190,9 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t f) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// Nonzero if one of four e4m3 codes is a NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 // An fp16 V tile [HD / 64][128 rows][128 B] before its product (N threads, this one the `lane`-th): rows
 // [lo, hi) become 0;
@@ -1389,25 +1394,50 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         }
         uint8_t* src = stage + st * Cfg::kStageBytes;
         uint8_t* dst = operand + slot * Cfg::kTile;
-        if (WIN ? edge_at(t, p0, key0 + (part & 1) * 64, 64) : edge_at(t, p0, key0, TOK)) {
-          // the tile reaches the drafts (WIN: an end of the windows): rows behind the context become 0, and
-          // non-finite elements of the drafts' V rows (of those that not every row sees) leave the product
+        if (!WIN && edge_at(t, p0, key0, TOK)) {
+          // the tile reaches the drafts: rows behind the context become 0, and
+          // non-finite elements of the drafts' V rows leave the product
 #pragma unroll 1
           for (int k = 0; k < ROWS / RPI; ++k) {
             const int key = key0 + row0 + k * RPI, a = key - prefix;
             uint2* p = reinterpret_cast<uint2*>(src + k * 256);
             uint2 x = *p;
-            bool hit = nothing(key), some = key >= prefix;
-            if constexpr (WIN) some = key > p0 || (key < t.lo1 && key >= P.sinks);
+            bool hit = key >= t.L;
             if (hit) {
               x = make_uint2(0, 0);
               if (ch == 0) exps[row0 + k * RPI] = uint8_t(top);
-            } else if (kv && some) {
+            } else if (kv && key >= prefix) {
               hit = clear_nonfinite<true>(x.x);
               hit |= clear_nonfinite<true>(x.y);
-              if (hit) atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords + (WIN ? 0 : a >> 5) % kTreeWords], 1u << (a & 31));
+              if (hit) atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords + (a >> 5) % kTreeWords], 1u << (a & 31));
             }
             if (hit) *p = x;
+          }
+          __syncwarp();
+        }
+        if constexpr (WIN) if (edge_at(t, p0, key0 + (part & 1) * 64, 64)) {
+          // An end of the windows: rows that no row of the tile attends become 0, whatever their exponents, and
+          // non-finite elements of the V rows that not every row sees leave the product. By ranges of
+          // rows (a look at every row took 2.5 us).
+          uint8_t* rows = src - lane * 8;
+          const auto row = [&](int key) { return min(max(key - (key0 + (part & 1) * 64), 0), 64) * HD; };
+#pragma unroll 1
+          for (int upper = 0; upper < 2; ++upper) {
+            const int end = upper ? 64 * HD : row(t.lo);
+            for (int at = row(upper ? t.L : P.sinks) + lane * 16; at < end; at += 512)
+              *reinterpret_cast<uint4*>(rows + at) = make_uint4(0, 0, 0, 0);
+            const int last = kv ? row(upper ? t.L : min(t.lo1, p0 + 1)) : 0;
+#pragma unroll 1
+            for (int at = row(upper ? p0 + 1 : max(t.lo, P.sinks)) + lane * 16; at < last; at += 512) {
+              uint4 v = lds128(rows + at);
+              if (!(nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w))) continue;
+              clear_nonfinite<true>(v.x);
+              clear_nonfinite<true>(v.y);
+              clear_nonfinite<true>(v.z);
+              clear_nonfinite<true>(v.w);
+              *reinterpret_cast<uint4*>(rows + at) = v;
+              atomicOr(&bad_s[(tile % Cfg::kBad) * kTreeWords], 1u);
+            }
           }
           __syncwarp();
         }
