@@ -38,18 +38,9 @@ struct RowParams {
   int batches;     // of rows in a warp, at most
   uint32_t q_slices, k_slices, slices;  // warps of a token: its queries', keys', all
   float eps, inv_hk;
-  // positions of several axes [axes][tokens]: a pair turns by axis 0 until axis_from[1], and so on;
-  // cyclic: pair i by axis i % axes as far as axis_upto says, else by axis 0
-  int axes, cyclic;
-  int axis_from[4], axis_upto[4];
+  int axes;                                 // of the positions [axes][tokens]; 0: one, [tokens]
+  uint32_t axis_of[PA_MAX_HEAD_SIZE / 32];  // the axis of each pair, two bits a pair
 };
-
-// The axis whose position turns pair i.
-__device__ __forceinline__ int axis_of(const RowParams& P, int i) {
-  if (!P.cyclic) return (i >= P.axis_from[1]) + (i >= P.axis_from[2]) + (i >= P.axis_from[3]);
-  const int a = uint32_t(i) % uint32_t(P.axes);
-  return i < (a == 0 ? 0 : a == 1 ? P.axis_upto[1] : a == 2 ? P.axis_upto[2] : P.axis_upto[3]) ? a : 0;
-}
 
 __device__ __forceinline__ void report(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
@@ -263,21 +254,20 @@ rows_kernel(const RowParams P) {
             const int i = IL ? at[v][c] / 2 : at[v][0] + 4 * c;  // the first of four pairs
             float* cw = reinterpret_cast<float*>(&cs);
             float* sw = reinterpret_cast<float*>(&sn);
-            int of[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) of[j] = axis_of(P, i + j);
-            const auto row = [&](int a) {
-              return P.cos_sin + int64_t(a == 0 ? axis_pos[0] : a == 1 ? axis_pos[1] : a == 2 ? axis_pos[2] : axis_pos[3]) *
-                                     P.rot + i;
+            const uint32_t of = P.axis_of[i / 16] >> (i % 16 * 2) & 255;  // two bits each
+            const float *cosines = P.cos_sin + i, *sines = cosines + P.rot / 2;
+            const auto row = [&](uint32_t a) {  // where the position of axis a has its row
+              return int64_t(a & 2 ? (a & 1 ? axis_pos[3] : axis_pos[2]) : (a & 1 ? axis_pos[1] : axis_pos[0])) * P.rot;
             };
-            if (of[0] == of[1] && of[0] == of[2] && of[0] == of[3]) {
-              cs = *reinterpret_cast<const float4*>(row(of[0]));
-              sn = *reinterpret_cast<const float4*>(row(of[0]) + P.rot / 2);
+            if (of == (of & 3) * 0x55) {
+              cs = *reinterpret_cast<const float4*>(cosines + row(of));
+              sn = *reinterpret_cast<const float4*>(sines + row(of));
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                cw[j] = row(of[j])[j];
-                sw[j] = row(of[j])[j + P.rot / 2];
+                const int64_t at = row(of >> 2 * j) + j;
+                cw[j] = cosines[at];
+                sw[j] = sines[at];
               }
             }
           }
@@ -695,12 +685,16 @@ pa_status check_axes(const pa_axes* a, const pa_rotary* r, const int32_t* positi
 
 void set_axes(RowParams& P, const pa_axes& a) {
   P.axes = a.count;
-  P.cyclic = a.cyclic;
-  for (int i = 0, at = 0; i < PA_MAX_AXES; ++i) {
-    const int n = i < a.count ? a.sections[i] : 0;
-    P.axis_from[i] = i < a.count ? at : INT32_MAX;
-    P.axis_upto[i] = a.count * n;
-    at += n;
+  int axis = 0, left = a.sections[0];  // of the sections behind one another
+  for (int i = 0; i < P.rot / 2; ++i) {
+    if (a.cyclic) {
+      axis = i % a.count;
+      if (i >= a.count * int64_t(a.sections[axis])) axis = 0;
+    } else {
+      while (left == 0) left = a.sections[++axis];
+      --left;
+    }
+    P.axis_of[i / 16] |= uint32_t(axis) << (i % 16 * 2);
   }
 }
 
