@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(const BlocksParams P) {
     if (k >= per || b >= n) continue;
     tok[b] = at;
     // more tokens than there are, of this row or behind it
-    if (blockIdx.x == 0 && max(P.q_seqlens ? P.q_seqlens[b] : 1, 0) > P.tokens - at) report(P.status, PA_STATUS_BIT_PLAN);
+    if (blockIdx.x == 0 && max(P.q_seqlens ? P.q_seqlens[b] : 1, 0) > P.tokens - at)
+      report(P.status, PA_STATUS_BIT_PLAN);
     at = add_tokens(P, at, tokens[k]);
     if (b == n - 1) tok[n] = at;
   }
@@ -325,15 +326,9 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(const BlocksParams P) {
   }
 }
 
-}  // namespace
-
-}  // namespace pa
-
-extern "C" pa_status pa_blocks_step(const pa_blocks_config* cfg, const int32_t* context_lens,
-                                    const int32_t* q_seqlens, int32_t* block_tables, int32_t* held,
-                                    int32_t* gone, int32_t* free_blocks, int32_t* count, int64_t tokens,
-                                    int64_t* slots, int32_t* positions, uint32_t* status, void* stream) {
-  using namespace pa;
+pa_status blocks_step(const pa_blocks_config* cfg, const int32_t* context_lens, const int32_t* q_seqlens,
+                      int32_t* block_tables, int32_t* held, int32_t* gone, int32_t* free_blocks, int32_t* count,
+                      int64_t tokens, int64_t* slots, int32_t* positions, uint32_t* status, void* stream) {
   if (!cfg || !context_lens || !block_tables || !held || !gone || !free_blocks || !count) return PA_ERR_INVALID_ARG;
   const pa_blocks_config& c = *cfg;
   if (c.batch <= 0 || c.batch > PA_MAX_BATCH || c.block_size <= 0 || c.block_size % 16 || c.num_blocks <= 0 ||
@@ -346,6 +341,14 @@ extern "C" pa_status pa_blocks_step(const pa_blocks_config* cfg, const int32_t* 
       free_blocks == gone || block_tables == held || block_tables == gone || block_tables == free_blocks ||
       block_tables == count)
     return PA_ERR_INVALID_ARG;
+  const auto aligned = [](const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; };
+  for (const void* p : {static_cast<const void*>(context_lens), static_cast<const void*>(q_seqlens),
+                        static_cast<const void*>(block_tables), static_cast<const void*>(held),
+                        static_cast<const void*>(gone), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(count), static_cast<const void*>(positions),
+                        static_cast<const void*>(status)})
+    if (!aligned(p, 4)) return PA_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return PA_ERR_INVALID_ARG;
   BlocksParams P{};
   P.context_lens = context_lens;
   P.q_seqlens = q_seqlens;
@@ -389,4 +392,20 @@ extern "C" pa_status pa_blocks_step(const pa_blocks_config* cfg, const int32_t* 
   launch.gridDim = dim3(unsigned(std::min<int64_t>(cdiv(P.tokens, kThreads * kTokens), 304)));
   launch.dynamicSmemBytes = (3 * c.batch + 1) * int(sizeof(int));
   return cudaLaunchKernelEx(&launch, slots_kernel, P) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" pa_status pa_blocks_step(const pa_blocks_config* cfg, const int32_t* context_lens,
+                                    const int32_t* q_seqlens, int32_t* block_tables, int32_t* held,
+                                    int32_t* gone, int32_t* free_blocks, int32_t* count, int64_t tokens,
+                                    int64_t* slots, int32_t* positions, uint32_t* status, void* stream) {
+  try {
+    return pa::blocks_step(cfg, context_lens, q_seqlens, block_tables, held, gone, free_blocks, count, tokens, slots,
+                           positions, status, stream);
+  } catch (...) {  // of the host's memory or locks
+    return PA_ERR_CUDA;
+  }
 }

@@ -104,10 +104,11 @@ struct TreeTc {
   static constexpr uint32_t par_off = stat_off + 2 * 2 * 128 * 8;          // [2][256]
   static constexpr uint32_t bad_off = par_off + 2 * PA_TREE_MAX_TOKENS;    // [kBad][words]
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
-  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead + (WIN ? 2 : 0) +
-                               (kLook ? kVSlots + 2 : 0);
+  static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead +
+                               (WIN ? 2 : 0) + (kLook ? kVSlots + 2 : 0);
   using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
-  using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>, Tile>;
+  using Walk = std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>;
+  using Place = TreePlace<Walk, Tile>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
   static constexpr uint32_t place_off = (tile_off + kAhead * sizeof(Tile) + 15) & ~15u;
   static constexpr uint32_t tmem_off = (place_off + sizeof(Place) + 15) & ~15u;
@@ -268,7 +269,8 @@ __device__ __forceinline__ void clean_v_window(uint8_t* vb, const WindowTile& t,
 #pragma unroll 1
   for (int upper = 0; upper < 2; ++upper) {
     zero_v_rows<H2, 128>(vb, row(upper ? t.L : sinks), upper ? row0 + 64 : row(t.lo), lane);
-    clear_v_rows<H2, 128>(vb, row(upper ? p0 + 1 : max(t.lo, sinks)), row(upper ? t.L : min(t.lo1, p0 + 1)), lane, flag);
+    clear_v_rows<H2, 128>(vb, row(upper ? p0 + 1 : max(t.lo, sinks)), row(upper ? t.L : min(t.lo1, p0 + 1)), lane,
+                          flag);
   }
   fence_proxy_async();
   __syncwarp();
@@ -635,9 +637,10 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   } else if (warp == 1) {
     if constexpr (WIN) {
     // ================= S = Q K^T and O_g += P_g V =================
-    // Both products in one order, each S right behind the product that read the P in its columns: products of one
-    // thread are done in their order, so no wait stands between them. (With S issued by warp 3 behind a wait for that product
-    // the chains' period was 1.85 us a key tile, QT = 2.) The whole warp waits and counts, one lane issues.
+    // Both products in one order, each S right behind the product that read the P in its columns: the
+    // products of one thread are done in their order, so no wait stands between them. (256 rows x 128 keys
+    // in 1.70 us; 1.85 with S issued by warp 3, behind a wait.) The whole warp waits and counts, one
+    // lane issues.
     const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024), dk = smem_desc(smem_u32(kring), 16, 1024);
     const uint64_t dv = smem_desc(smem_u32(vring), Cfg::kHalf, 1024);
     uint64_t* vcome = Cfg::kLook ? vready : vfull;
@@ -1029,8 +1032,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
             const int em = n % Cfg::kExps, ph = (n / Cfg::kExps) & 1;
             if (!tree_wait2(&exps_full[em], ph, &exps_full[Cfg::kExps + em], ph, P.wait_limit)) ok = false;
             tree_apart<Cfg::kSpreadK, Cfg::kSpreadV, WIN>(P, sbuf, smem + Cfg::exps_off + em * 256 + hf * 64, e,
-                                                          t.L - key0, P.parents ? bits : nullptr, WIN ? prefix + qi : qi,
-                                                          WIN ? key0 : key0 - prefix, &own);
+                                                          t.L - key0, P.parents ? bits : nullptr,
+                                                          WIN ? prefix + qi : qi, WIN ? key0 : key0 - prefix, &own);
             F = 1.f;
             ev = unscale = 0.f;
             __syncwarp();
@@ -1038,7 +1041,9 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           float x[64];
           tmem_ld32(sbuf, x);
           tmem_ld32(sbuf + 32, x + 32);
-          const bool edge = WIN ? key0 + 63 > pw0 || (pw1 - key0 >= P.window && key0 + 64 > P.sinks) : edge_at(t, prefix, key0, 64);
+          // (WIN: whether the warp's own rows see unlike keys)
+          const bool edge = WIN ? key0 + 63 > pw0 || (pw1 - key0 >= P.window && key0 + 64 > P.sinks)
+                                : edge_at(t, prefix, key0, 64);
           tmem_wait_ld();
           if (edge) {
 #pragma unroll

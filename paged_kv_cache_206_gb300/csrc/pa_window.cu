@@ -56,12 +56,15 @@ extern "C" pa_status pa_window_workspace(const pa_config* cfg, const pa_window* 
   return PA_OK;
 }
 
-extern "C" pa_status pa_window_forward(const pa_config* cfg, const pa_window* win, int64_t tokens, const void* query,
-                                       const void* key_cache, const void* value_cache, const uint8_t* key_exps,
-                                       const uint8_t* value_exps, const int32_t* block_tables,
-                                       const int32_t* context_lens, const int32_t* q_seqlens, void* workspace,
-                                       size_t workspace_bytes, void* out, void* stream_) {
-  using namespace pa;
+namespace pa {
+
+namespace {
+
+pa_status window_forward(const pa_config* cfg, const pa_window* win, int64_t tokens, const void* query,
+                         const void* key_cache, const void* value_cache, const uint8_t* key_exps,
+                         const uint8_t* value_exps, const int32_t* block_tables,
+                         const int32_t* context_lens, const int32_t* q_seqlens, void* workspace,
+                         size_t workspace_bytes, void* out, void* stream_) {
   size_t need = 0;
   pa_status st = pa_window_workspace(cfg, win, &need);
   if (st != PA_OK) return st;
@@ -79,4 +82,21 @@ extern "C" pa_status pa_window_forward(const pa_config* cfg, const pa_window* wi
   if (key_exps) tree_any_kernel<true, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
   else tree_any_kernel<false, true><<<grid, kAnyWarps * 32, 0, stream>>>(P);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" pa_status pa_window_forward(const pa_config* cfg, const pa_window* win, int64_t tokens, const void* query,
+                                       const void* key_cache, const void* value_cache, const uint8_t* key_exps,
+                                       const uint8_t* value_exps, const int32_t* block_tables,
+                                       const int32_t* context_lens, const int32_t* q_seqlens, void* workspace,
+                                       size_t workspace_bytes, void* out, void* stream_) {
+  try {
+    return pa::window_forward(cfg, win, tokens, query, key_cache, value_cache, key_exps, value_exps, block_tables,
+                              context_lens, q_seqlens, workspace, workspace_bytes, out, stream_);
+  } catch (...) {  // of the host's memory or locks
+    return PA_ERR_CUDA;
+  }
 }

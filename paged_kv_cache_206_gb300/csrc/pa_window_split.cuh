@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t window_bits(const TreeParams& P, int p, int 
 }
 
 // Adds to one row's result what was taken out of its product: the non-finite elements of the
-// values that it attends and another row of its tile does not. The row's token stands at p. The result is fp16 (`out`) or an fp32 partial one
+// values that it attends and another row of its tile does not. The row's token stands at p. The
+// result is fp16 (`out`) or an fp32 partial one
 // (`part`, `stride` apart); dims d0, d0 + step, ... below d1. Rare, hence not inlined.
 template <bool Q8, int UNIT, int CHUNK>
 __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile& t, int p, __half* out, float* part,

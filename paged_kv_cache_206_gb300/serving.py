@@ -184,9 +184,13 @@ def _status_arg(where, status, device):
 
 def _axes_of(where, sections, cyclic, positions):
     """The configuration of positions [axes, tokens] whose pairs are divided into ``sections``."""
-    n = len(sections)
-    if not 1 <= n <= PA_MAX_AXES or positions is None:
-        _refuse(where, f"sections must name 1 to {PA_MAX_AXES} axes of positions that are given")
+    if positions is None:
+        _refuse(where, "positions of several axes must be given")
+    got = _axes.get((cyclic, *sections))
+    if got is not None:
+        return got
+    if not 1 <= len(sections) <= PA_MAX_AXES:
+        _refuse(where, f"sections must be those of 1 to {PA_MAX_AXES} axes, got {tuple(sections)}")
     if any(not 0 <= int(s) < 2**31 for s in sections):
         _refuse(where, f"sections must be numbers of pairs, got {tuple(sections)}")
     return _axes[(1 if cyclic else 0, *map(int, sections))]

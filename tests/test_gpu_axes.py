@@ -145,7 +145,8 @@ def test_store(torch, case):
         blk, off = batch.slots(b, L - n, L)
         e = exps[blk, :, off].astype(np.int64) - 127
         y, err = want[t0:t0 + n], error[t0:t0 + n]
-        assert ((e >= ref.row_exponent(np.maximum(np.abs(y) - err, 0))) & (e <= ref.row_exponent(np.abs(y) + err))).all()
+        least, most = ref.row_exponent(np.maximum(np.abs(y) - err, 0)), ref.row_exponent(np.abs(y) + err)
+        assert ((e >= least) & (e <= most)).all()
         held = ref.decode(codes[blk, off]) * 2.0 ** e[..., None]
         half_step = np.maximum(2.0**-4 * (np.abs(y) + err), 2.0**-10 * 2.0 ** e[..., None])
         assert (np.abs(held - y) <= half_step + err).all()

@@ -123,7 +123,8 @@ def test_blocks_refusals(lib):
     assert call() == INVALID
     for kw in (dict(cl=None), dict(bt=None), dict(held=None), dict(gone=None), dict(free=None), dict(count=None),
                dict(held=P[4]), dict(count=P[3]), dict(free=P[3]), dict(bt=P[5]), dict(tokens=2**30),
-               dict(tokens=2**62)):
+               dict(tokens=2**62), dict(slots=ctypes.c_void_p((9 << 20) + 4)), dict(pos=ctypes.c_void_p((9 << 20) + 2)),
+               dict(cl=ctypes.c_void_p((2 << 20) + 1)), dict(count=ctypes.c_void_p((8 << 20) + 3))):
         assert call(**{"tokens": 0, **kw}) == INVALID, kw
     for c in (dict(batch=0), dict(batch=2049), dict(block_size=0), dict(block_size=24), dict(num_blocks=0),
               dict(max_blocks_per_seq=0), dict(window=-1), dict(sinks=-1), dict(num_blocks=1 << 27),
@@ -253,7 +254,7 @@ def test_calls_of_13_and_24_arguments(monkeypatch, lib, module):
     assert store(O) == pa.PA_OK
     assert store(O + 8) == INVALID and store(None) == INVALID and store(O, -1) == INVALID
     b = pa.pa_blocks_config(**BLOCKS)
-    assert serving._call(serving._blocks, ctypes.addressof(b), F, F, F + 256, F + 512, F + 768, F + 1024, F + 1280, -1, F,
-                         F, None, 0) == INVALID
+    pool = F + 256, F + 512, F + 768, F + 1024, F + 1280
+    assert serving._call(serving._blocks, ctypes.addressof(b), F, F, *pool, -1, F, F, None, 0) == INVALID
     monkeypatch.undo()
     serving._start()
