@@ -1363,13 +1363,19 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
       const int key0 = key_of(t, u, lane >> 4) + (lane & 15) * 4, left = t.L - key0;  // this lane's four
+      // (WIN: the keys between the sinks and the first row's window are nobody's)
+      int behind = 0;
+      uint32_t gap = 0;
+      if constexpr (WIN) {
+        behind = key0 - P.sinks;
+        gap = uint32_t(max(t.lo - P.sinks, 0));
+      }
       int low = 255;
       top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = int(e4 >> (8 * j) & 255);
-        bool in = left > j;
-        if constexpr (WIN) in = in && !window_hidden(P, t.lo, key0 + j, 1);
+        const bool in = left > j && uint32_t(behind + j) >= gap;
         top = max(top, in ? e : 0);
         low = min(low, in ? e : 255);
       }
