@@ -1,6 +1,6 @@
-// Tree attention on the tcgen05 tensor cores, for tiles of 128 or 256 rows (a
-// group of heads times many drafts) and heads of 64 or 128 dims, over the fp16 or
-// the 8-bit cache.
+// Tree attention, and attention with a window, on the tcgen05 tensor cores, for tiles of 128 or 256
+// rows (a group of heads times many drafts, or a prompt's tokens) and heads of 64 or 128 dims, over
+// the fp16 or the 8-bit cache.
 //
 // One persistent CTA per SM, a worker of the line (pa_tree_split.cuh) with units of
 // 128 keys. Two chains of softmax and O += P V run against each other in jobs of 64
@@ -48,10 +48,24 @@
 
 namespace pa {
 
-// WIN: pa_window_forward's kernel, for drafts, prompts and parts of prompts. Its tiles are those of
-// pa_window_split.cuh. As every row tile has keys that only some of its rows see, at both ends of their
-// windows, the fp16 cache's V tiles are looked through by four warps of their own (12-15), ahead of the
-// product's issuer.
+// WIN: pa_window_forward's kernel, for drafts, prompts and parts of prompts. Its row tiles are those of
+// pa_window_split.cuh, of some ten key tiles each where the window is of a thousand keys, so that what a row tile costs
+// at its ends counts as much as the key tiles do (10 us beside 1.85 each in the division of the work above, 4
+// beside 1.70 now: 256 rows of fp16):
+//   warp 1       issues both products, each S behind the product that frees its columns
+//   warp 3       finds the row tiles (one from the other: with a search in each it took 4 us a tile), and
+//                fetches their queries by TMA (2.6 to 5 us by cp.async)
+//   warps 4-11   leave out the keys that none of their rows sees, mask those that not all of them see, and
+//                write the rows out, eight rows' 64 bytes a store
+//   warps 12-15  fp16 cache: make the V rows that no row of the tile sees 0 and look for non-finite
+//                elements in those that not every row sees, at both ends of the windows, before the product
+//                (the 8-bit cache's widening warps do that on the way); of heads of 128 dims and 256 rows they also write
+//                half of each row out
+// Sinks and window share a key tile by halves of 64 keys.
+// What it reaches: 18,700 tokens of prompts, window 1024, 32 heads on 8, in 318 us (0.97 PFLOP/s of the pairs that
+// are attended, 49 % of the tensor pipe's time; chains of S, softmax and P V of two query tiles that wait for each
+// other); 8 x 512 tokens over 8 bits, window 2048, 32 heads, in 162 us (0.76; the widening warps share the schedulers
+// with the softmax, issue slots 42 % full).
 template <int HD, bool Q8, int QT, bool WIN>
 struct TreeTc {
   static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
