@@ -41,7 +41,10 @@
 namespace pa {
 
 // WIN: pa_window_forward's kernel. Its tiles are those of pa_window_split.cuh, chains whose rows
-// leave keys out at the lower end too.
+// leave keys out at the lower end too. 64 decode steps with a window of 2048 keys and 4 sinks, 8 kv heads
+// of 128 dims in fp16, take 79 us for 416 MB, 5.3 TB/s with the start (3) and the join (3); a window of 4096 over 8
+// bits takes 80 to 91 for 421 MB (690 instructions for 32 keys, two warps a scheduler; three made
+// no difference). One step with 1024 keys takes 14.8, of which the join is a third.
 template <int HD, bool Q8, int NT, bool WIN>
 struct TreeMma {
   static constexpr int kWarps = 4;

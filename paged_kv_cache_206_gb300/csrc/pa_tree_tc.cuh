@@ -59,8 +59,8 @@ namespace pa {
 //                write the rows out, eight rows' 64 bytes a store
 //   warps 12-15  fp16 cache: make the V rows that no row of the tile sees 0 and look for non-finite
 //                elements in those that not every row sees, at both ends of the windows, before the product
-//                (the 8-bit cache's widening warps do that on the way); of heads of 128 dims and 256 rows they also write
-//                half of each row out
+//                (the 8-bit cache's widening warps do that on the way); of heads of 128 dims and 256 rows they
+//                also write half of each row out
 // Sinks and window share a key tile by halves of 64 keys.
 // What it reaches: 18,700 tokens of prompts, window 1024, 32 heads on 8, in 318 us (0.97 PFLOP/s of the pairs that
 // are attended, 49 % of the tensor pipe's time; chains of S, softmax and P V of two query tiles that wait for each

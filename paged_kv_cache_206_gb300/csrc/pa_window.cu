@@ -18,13 +18,18 @@ pa_status check_window(const pa_config* cfg, const pa_window* win) {
   return win && win->window > 0 && win->sinks >= 0 ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
-// The kernel for these head sizes and rows, if there is a faster one than tree_any_kernel.
+// The kernel for these head sizes and rows, if there is a faster one than tree_any_kernel: of 64 and 128 dims the
+// tcgen05 tensor cores from 17 rows of a kv head on over the fp16 cache and from 33 on over the 8-bit
+// one, else the warp-level tensor instructions with the least of 64, 128 and 256 dims that hold a head,
+// in tiles of 8 rows or several of 16. 32 sequences, 8 kv heads of 128 dims, window 1024: 20 rows take 41 us here and
+// 57 there in fp16, 53 and 43 in 8 bits; 32 rows 42 and 60, 53 and 46; 64 rows 44 and 107, 54 and 76.
+// Window 4096: 20 rows 99 and 178 us, 105 and 108; 32 rows 100 and 184, 106 and 111.
 bool window_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws, cudaStream_t stream,
                   cudaError_t* e) {
   const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;
   const int64_t rows = int64_t(c.num_heads / c.kv_heads) * max_q(c);
   const int nt = rows <= 8 ? 1 : 2;
-  if (rows > 16 && c.head_size_k == c.head_size_v && (hd == 64 || hd == 128))
+  if (rows > (q8 ? 32 : 16) && c.head_size_k == c.head_size_v && (hd == 64 || hd == 128))
     *e = window_tc(P, hd, q8, rows, c.num_sms, need, ws, stream);
   else if (hd <= 64)
     *e = window_mma_64(P, q8, nt, c.num_sms, need, ws, stream);
