@@ -316,18 +316,35 @@ __global__ void __launch_bounds__(256) tree_combine_cols_kernel(const TreeParams
   float M = -INFINITY, sum = 0.f, acc[COLS];
 #pragma unroll
   for (int d = 0; d < COLS; ++d) acc[d] = 0.f;
-  for (int k = 0; k < parts; ++k) M = fmaxf(M, S.part_ml[slot_of(k) * NR + n].x);
+  // several parts' loads in flight at a time: a tile of one long sequence has some twenty
+  constexpr int BATCH = 2;
+  for (int k0 = 0; k0 < parts; k0 += 4) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = k0 + k < parts ? S.part_ml[slot_of(k0 + k) * NR + n].x : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) M = fmaxf(M, m[k]);
+  }
   if (M == -INFINITY) M = 0.f;  // no score above -inf: the sum below is 0
-  for (int k = 0; k < parts; ++k) {
-    const int64_t slot = slot_of(k);
-    const float2 ml = S.part_ml[slot * NR + n];
-    float x[COLS];
+  for (int k0 = 0; k0 < parts; k0 += BATCH) {
+    float2 ml[BATCH];
+    float x[BATCH][COLS];
 #pragma unroll
-    for (int d = 0; d < COLS; ++d) x[d] = S.part_o[(slot * HD + d0 + d) * NR + n];
-    const float w = ex2(ml.x - M);
-    sum = fmaf(ml.y, w, sum);
+    for (int k = 0; k < BATCH; ++k) {
+      if (k0 + k >= parts) break;
+      const int64_t slot = slot_of(k0 + k);
+      ml[k] = S.part_ml[slot * NR + n];
 #pragma unroll
-    for (int d = 0; d < COLS; ++d) acc[d] = fmaf(w, x[d], acc[d]);
+      for (int d = 0; d < COLS; ++d) x[k][d] = S.part_o[(slot * HD + d0 + d) * NR + n];
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (k0 + k >= parts) break;
+      const float w = ex2(ml[k].x - M);
+      sum = fmaf(ml[k].y, w, sum);
+#pragma unroll
+      for (int d = 0; d < COLS; ++d) acc[d] = fmaf(w, x[k][d], acc[d]);
+    }
   }
   const float inv = 1.f / sum;
   uint4* dst = reinterpret_cast<uint4*>(
