@@ -42,9 +42,11 @@ namespace pa {
 
 // WIN: pa_window_forward's kernel. Its tiles are those of pa_window_split.cuh, chains whose rows
 // leave keys out at the lower end too. 64 decode steps with a window of 2048 keys and 4 sinks, 8 kv heads
-// of 128 dims in fp16, take 79 us for 416 MB, 5.3 TB/s with the start (3) and the join (3); a window of 4096 over 8
-// bits takes 80 to 91 for 421 MB (690 instructions for 32 keys, two warps a scheduler; three made
-// no difference). One step with 1024 keys takes 14.8, of which the join is a third.
+// of 128 dims in fp16, take 78 us for 416 MB, of which 6 pass before the first copies (the lengths from
+// memory 1, the place on the line 3, a look into the block table 1) and 3 at the join, and the slowest SM ends 10
+// behind the median one; without any arithmetic the copies take 75. A window of 4096 over 8 bits takes 80 to 90 for
+// 421 MB (copies alone 83 where it takes 91). One step with 1024 keys takes 14.3: the same 5, four
+// units 3, partial rows and their join 5.
 template <int HD, bool Q8, int NT, bool WIN>
 struct TreeMma {
   static constexpr int kWarps = 4;
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
   constexpr int AHEAD = 32 / MT;
   int block = 0, in_block = 0, next_block = 0, next_in = 0;
   auto next_tile = [&]() {
-    if (!tree_next(P, place)) return false;
+    if (!tree_next(P, S, place)) return false;
     const Tile& t = place->tile;
     if (lane == 0) {
       tile_s[made % Cfg::kTiles] = t;
@@ -226,14 +228,21 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
     const bool fresh = unit == place->tile.s0;
     if (fresh || unit >= win0 + AHEAD) {
       win0 = fresh ? unit : win0 + AHEAD;
+      // (both lookups of a fresh tile on their way at once)
+      block = next_block;
+      in_block = next_in;
 #pragma unroll 1
       for (int k = fresh ? 0 : 1; k < 2; ++k) {
-        block = next_block;
-        in_block = next_in;
         const int at = win0 + k * AHEAD + lane / MT, key = key_of(at) + (lane % MT) * 16, page = key / bs;
-        next_in = key - page * bs;
-        next_block = at < unit_end && key < cut_L && !left_out(key)
-                         ? P.block_tables[int64_t(cut_b) * P.max_blocks_per_seq + page] : 0;
+        const bool there = at < unit_end && key < cut_L && !left_out(key);
+        const int32_t* entry = P.block_tables + int64_t(cut_b) * P.max_blocks_per_seq + page;
+        if (k == 0) {
+          in_block = key - page * bs;
+          block = there ? *entry : 0;
+        } else {
+          next_in = key - page * bs;
+          next_block = there ? *entry : 0;
+        }
       }
     }
     int blk[MT], in_blk[MT];

@@ -1,6 +1,8 @@
 // Host side of pa_tree_mma.cuh, included by one source file per head size.
 #pragma once
 
+#include <algorithm>
+
 #include "pa_internal.h"
 #include "pa_launch.h"
 #include "pa_tree_mma.cuh"
@@ -34,6 +36,8 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   S.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o_off);
   S.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + ml_off);
   S.join = reinterpret_cast<TreeJoin*>(static_cast<char*>(ws) + join_off);
+  S.tile_tokens = std::max(Cfg::kRows / P.group, 1);
+  S.tile_parts = (P.group - 1) / Cfg::kRows + 1;
   S.workers = workers;
   // a partial result (kRows rows of fp32) should stay below the keys it stands for
   S.min_units = (Cfg::kLead + (NT + Cfg::kMT - 1) / Cfg::kMT) * (WIN ? Cfg::kSub : 1);

@@ -31,6 +31,7 @@ struct TreeSplit {
   struct TreeJoin* join;  // [workers]
   int workers;
   int min_units;    // fewest places of the line worth a worker
+  int tile_tokens, tile_parts;  // (pa_window_split.cuh) whole tokens of a row tile, parts of a token's heads
 };
 
 // a / b for a >= 0, b > 0: the 64-bit division takes several times the 32-bit one's time.
@@ -161,7 +162,7 @@ struct TreeWalk {
     return false;
   }
 
-  __device__ __forceinline__ bool next(const TreeParams& P, TreeTile& t) {
+  __device__ __forceinline__ bool next(const TreeParams& P, const TreeSplit&, TreeTile& t) {
     while (u < u1) {
       while (u >= before + seq.total(P)) {
         before += seq.total(P);
@@ -218,10 +219,10 @@ __device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S,
 }
 
 template <class Walk, class Tile>
-__device__ __noinline__ bool tree_next(const TreeParams& P, TreePlace<Walk, Tile>* at) {
+__device__ __noinline__ bool tree_next(const TreeParams& P, const TreeSplit& S, TreePlace<Walk, Tile>* at) {
   Walk w = at->walk;
   Tile d;
-  const bool some = w.next(P, d);
+  const bool some = w.next(P, S, d);
   __syncwarp();
   if (some) at->tile = d;
   at->walk = w;

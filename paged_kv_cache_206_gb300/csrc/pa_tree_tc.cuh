@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     Tile t, following;
     tree_begin(P, S, place, worker, lane);
     auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
-      const bool some = tree_next(P, place);
+      const bool some = tree_next(P, S, place);
       following = place->tile;
       if (!some) following.q = -1;
       const int at = told_n % Cfg::kAhead;
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     Tile t, following;
     tree_begin(P, S, place, worker, lane);
     auto tell = [&]() {  // finds the next row tile and tells it; q < 0: there is none
-      const bool some = tree_next(P, place);
+      const bool some = tree_next(P, S, place);
       following = place->tile;
       if (!some) following.q = -1;
       const int at = told_n % Cfg::kAhead;

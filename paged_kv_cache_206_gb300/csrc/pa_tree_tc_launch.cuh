@@ -55,6 +55,8 @@ cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cu
   S.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + o_off);
   S.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + ml_off);
   S.join = reinterpret_cast<TreeJoin*>(static_cast<char*>(ws) + join_off);
+  S.tile_tokens = std::max(Cfg::kRows / P.group, 1);
+  S.tile_parts = (P.group - 1) / Cfg::kRows + 1;
   S.workers = sms;
   S.min_units = (Cfg::kLead + 1) * (WIN ? Cfg::kTok : 1);
   const int box = std::min(P.block_size & -P.block_size, 64);

@@ -86,19 +86,28 @@ __device__ __noinline__ void window_patch(const TreeParams& P, const WindowTile&
   }
 }
 
-template <int UNIT, int CHUNK, int NR, int LEAD>
+template <int UNIT, int NR, int LEAD>
 struct WindowLine {
+  int tt, parts;  // whole tokens of a tile, parts of a token's heads
+
+  __device__ __forceinline__ explicit WindowLine(const TreeSplit& S) : tt(S.tile_tokens), parts(S.tile_parts) {}
+
   // Sequence b's tokens, and the tiles that they make for a kv head. The tokens count as stated (at
   // most all that there are) whether the lengths keep the constraints or not.
   struct Seq {
     int q, L, tiles;  // token tiles; 0: none
   };
-  static __device__ __forceinline__ int tokens_of(const TreeParams& P) { return max(NR / P.group, 1); }
-  static __device__ __forceinline__ int parts_of(const TreeParams& P) { return (P.group - 1) / NR + 1; }
+
+  // The keys between the sinks and the window of a token at position p.
+  static __device__ __forceinline__ int64_t left_out(const TreeParams& P, int64_t p) {
+    const int64_t n = p + 1 - P.window - P.sinks;
+    return n > 0 ? n : 0;
+  }
 
   // The places of the first t of a sequence's tiles.
-  static __device__ __forceinline__ int64_t upto(const TreeParams& P, const Seq& s, int t) {
-    const int tt = tokens_of(P);
+  __device__ __forceinline__ int64_t upto(const TreeParams& P, const Seq& s, int t) const {
+    if (t == 0) return 0;
+    if (s.tiles == 1) return s.L - left_out(P, s.L - s.q) + LEAD * UNIT;
     const int64_t n = t, pre = s.L - s.q, c = pre + 1 - P.window - P.sinks;
     int64_t sum = n * (pre + LEAD * UNIT) + tt * (n * (n + 1) / 2);
     if (t == s.tiles) sum -= n * tt - s.q;
@@ -107,7 +116,7 @@ struct WindowLine {
     return sum;
   }
 
-  static __device__ __forceinline__ Seq load(const TreeParams& P, int b) {
+  __device__ __forceinline__ Seq load(const TreeParams& P, int b) const {
     if (b >= P.batch) return Seq{0, 0, 0};
     Seq s;
     s.q = P.q_seqlens ? P.q_seqlens[b] : 1;
@@ -115,23 +124,14 @@ struct WindowLine {
     const bool ok = tree_lengths_ok(P, s.q, s.L);
     if (!ok) set_status(P.status, PA_STATUS_BIT_PLAN);
     s.q = tree_tokens(P, 0, max(s.q, 0));
-    const bool some = ok && s.q > 0;
-    s.tiles = some ? (s.q - 1) / tokens_of(P) + 1 : 0;
+    s.tiles = !ok || s.q == 0 ? 0 : s.q <= tt ? 1 : (s.q - 1) / tt + 1;
     return s;
   }
-  // Places of a part of a kv head's heads, and of all of them.
-  static __device__ __forceinline__ int64_t of_head(const TreeParams& P, const Seq& s) {
-    return s.tiles ? upto(P, s, s.tiles) : 0;
-  }
-  static __device__ __forceinline__ int64_t total(const TreeParams& P, const Seq& s) {
-    return of_head(P, s) * P.kv_heads * parts_of(P);
+  // Places of all parts of all kv heads.
+  __device__ __forceinline__ int64_t total(const TreeParams& P, const Seq& s) const {
+    return upto(P, s, s.tiles) * (P.kv_heads * parts);
   }
 
-  // Where worker c's piece begins: total * c / n.
-  static __device__ __forceinline__ int64_t begin(int64_t total, int c, int n) {
-    const int64_t q = tree_div(total, n);
-    return q * c + tree_div((total - q * n) * c, n);
-  }
   // The last worker whose piece begins before place u: total * k / n < u. (The product leaves 64 bits
   // for thousands of sequences of 2^30 keys only.)
   static __device__ __forceinline__ int last_before(int64_t total, int64_t u, int n) {
@@ -145,7 +145,7 @@ struct WindowLine {
 // sums and goes on from tile to tile.
 template <int UNIT, int CHUNK, int NR, int LEAD>
 struct WindowWalk {
-  using Line = WindowLine<UNIT, CHUNK, NR, LEAD>;
+  using Line = WindowLine<UNIT, NR, LEAD>;
   int64_t u, u0, u1, total;
   int64_t at;        // the place where the tile at hand begins,
   int head, tile;    // part of a kv head's heads, token tile
@@ -158,11 +158,12 @@ struct WindowWalk {
     u = u0 = u1 = at = 0;
     head = tile = q_start = 0;
     b = -1;
+    const Line line(S);
     // places and tokens of 32 sequences up to this lane's (the tokens stop at all that there are)
     int64_t places;
     int tokens;
     const auto scan = [&] {
-      places = Line::total(P, seq);
+      places = line.total(P, seq);
       tokens = seq.q;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -174,48 +175,49 @@ struct WindowWalk {
         }
       }
     };
-    seq = Line::load(P, lane);
+    seq = line.load(P, lane);
     scan();
     total = __shfl_sync(FULL, places, 31);
     if (P.batch > 32) {
       int64_t rest = 0;
-      for (int k = lane + 32; k < P.batch; k += 32) rest += Line::total(P, Line::load(P, k));
+      for (int k = lane + 32; k < P.batch; k += 32) rest += line.total(P, line.load(P, k));
 #pragma unroll
       for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(FULL, rest, o);
       total += rest;
     }
-    const int64_t n = tree_div(total, S.min_units);
-    nact = int(n < 1 ? 1 : n < S.workers ? n : S.workers);
+    nact = total >= int64_t(S.workers) * S.min_units ? S.workers : max(int(tree_div(total, S.min_units)), 1);
     if (worker >= nact) return false;
-    u = u0 = Line::begin(total, worker, nact);
-    u1 = Line::begin(total, worker + 1, nact);
+    // piece c begins at total * c / nact
+    const int64_t each = tree_div(total, nact), rest = total - each * nact;
+    u = u0 = each * worker + tree_div(rest * worker, nact);
+    u1 = each * (worker + 1) + tree_div(rest * (worker + 1), nact);
     // the sequence that place u0 belongs to
     int64_t before = 0;
     for (int b0 = 0; b0 < P.batch && u0 < u1; b0 += 32) {
       if (b0) {
-        seq = Line::load(P, b0 + lane);
+        seq = line.load(P, b0 + lane);
         scan();
       }
       const unsigned who = __ballot_sync(FULL, u0 - before < places);
       if (who) {
         const int l = __ffs(who) - 1;
         b = b0 + l;
-        before += __shfl_sync(FULL, places - Line::total(P, seq), l);
+        before += __shfl_sync(FULL, places - line.total(P, seq), l);
         const int ahead = __shfl_sync(FULL, tokens, l > 0 ? l - 1 : 0);
         if (l > 0) q_start = tree_tokens(P, q_start, ahead);
         seq.q = __shfl_sync(FULL, seq.q, l);
         seq.L = __shfl_sync(FULL, seq.L, l);
         seq.tiles = __shfl_sync(FULL, seq.tiles, l);
         // its tile: the last one that begins at or before u0
-        const int64_t of_head = Line::of_head(P, seq);
+        const int64_t of_head = line.upto(P, seq, seq.tiles);
         head = int(tree_div(u0 - before, of_head));
         at = before + head * of_head;
         int end = seq.tiles;
         while (end - tile > 1) {
           const int mid = (tile + end) >> 1;
-          if (Line::upto(P, seq, mid) <= u0 - at) tile = mid; else end = mid;
+          if (line.upto(P, seq, mid) <= u0 - at) tile = mid; else end = mid;
         }
-        at += Line::upto(P, seq, tile);
+        at += line.upto(P, seq, tile);
         return true;
       }
       before += __shfl_sync(FULL, places, 31);
@@ -225,13 +227,13 @@ struct WindowWalk {
     return false;
   }
 
-  __device__ __forceinline__ bool next(const TreeParams& P, WindowTile& w) {
-    const int tt = Line::tokens_of(P), parts = Line::parts_of(P);
+  __device__ __forceinline__ bool next(const TreeParams& P, const TreeSplit& S, WindowTile& w) {
+    const Line line(S);
+    const int tt = line.tt, parts = line.parts;
     while (u < u1) {
       // the tile's tokens, places and units
       const int pre = seq.L - seq.q, i0 = tile * tt, i1 = min(i0 + tt, seq.q) - 1;
-      const int64_t out = int64_t(pre) + i0 + 1 - P.window - P.sinks;
-      const int keys = pre + i1 + 1 - (out > 0 ? int(out) : 0), width = keys + LEAD * UNIT;
+      const int keys = pre + i1 + 1 - int(Line::left_out(P, int64_t(pre) + i0)), width = keys + LEAD * UNIT;
       const int p0 = int(u - at), p1 = int(min(int64_t(width), p0 + (u1 - u)));
       const bool first = u == u0;
       const int64_t end = at + width;
@@ -267,7 +269,7 @@ struct WindowWalk {
                 u = u1;
                 break;
               }
-              seq = Line::load(P, b);
+              seq = line.load(P, b);
             } while (seq.tiles == 0);
           }
         }
