@@ -61,7 +61,8 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  *                different caches
  * key_exps, value_exps    NULL for the fp16 cache, else as in pa_cache.h
  * block_tables   device int32 [batch, max_blocks_per_seq]
- * context_lens   device int32 [batch], L_b counting the current tokens
+ * context_lens   device int32 [batch], L_b counting the current tokens, at most
+ *                max_blocks_per_seq * block_size and 2^31 - 4096
  * q_seqlens      device int32 [batch], 0 <= q_b <= max_seqlen_q (0: a padding
  *                sequence), or NULL when every q_b = 1
  * parents        device int32 [tokens]: -1 for a root (a child of the last

@@ -56,7 +56,8 @@ pa_status pa_window_workspace(const pa_config* cfg, const pa_window* win, size_t
  *                different caches
  * key_exps, value_exps    NULL for the fp16 cache, else as in pa_cache.h
  * block_tables   device int32 [batch, max_blocks_per_seq]
- * context_lens   device int32 [batch], L_b counting the current tokens
+ * context_lens   device int32 [batch], L_b counting the current tokens, at most
+ *                max_blocks_per_seq * block_size and 2^31 - 4096
  * q_seqlens      device int32 [batch], 0 <= q_b <= max_seqlen_q (0: a padding
  *                sequence), or NULL when every q_b = 1
  * workspace      device, >= pa_window_workspace's bytes, 256-byte aligned; its

@@ -21,7 +21,7 @@ struct TreeParams {
   uint32_t* status;
   int64_t tokens;
   int batch, num_heads, kv_heads, group, hk, hv, block_size, num_blocks, max_blocks_per_seq;
-  int max_q;
+  int max_q, max_keys;
   int window, sinks;  // (pa_window_forward)
   uint32_t group_inverse;  // ceil(2^32 / group) where the group is below 2^15 and above 1, else 0
   float scale_log2;  // scale * log2(e)
@@ -30,8 +30,7 @@ struct TreeParams {
 
 // Whether a sequence's lengths keep the constraints.
 __device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int L) {
-  return q >= 0 && q <= P.max_q && q <= P.tokens && L >= q &&
-         int64_t(L) <= int64_t(P.max_blocks_per_seq) * P.block_size;
+  return q >= 0 && q <= P.max_q && q <= P.tokens && L >= q && L <= P.max_keys;
 }
 
 // Whether the tokens end before sequence rows begun at q_start do (the rows past them are left out).

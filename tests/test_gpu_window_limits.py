@@ -115,3 +115,61 @@ def test_rows_beyond_the_sequences_are_left_in_captured_batches(torch):
         torch.cuda.synchronize()
         assert bool((c.out[2 * q:] == 7).all()) and not bool((c.out[:2 * q] == 7).all(-1).any())
         assert c.step.status() == (pa.PA_OK, 0)
+
+
+LONGEST = 2**31 - 4096
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("q,H,Hk,d", [(1, 8, 2, 128), (5, 8, 2, 64), (60, 4, 2, 128), (200, 4, 1, 64), (2, 4, 2, 320)])
+def test_the_longest_context(torch, bits, q, H, Hk, d):
+    """The keys of a short sequence at the two ends of the longest one, whose table has blocks nowhere
+    else; one key more is refused."""
+    bs, short = 128, 640
+    c = Case(torch, bits, [q], [short], H, Hk, d, d, bs, 200, 20)
+    tables = torch.full((1, 2**31 // bs), -1, dtype=torch.int32, device="cuda")
+    tables[0, 0] = c.args[1][0, 0]
+    tables[0, (LONGEST - short) // bs + 1:LONGEST // bs] = c.args[1][0, 1:short // bs]
+    (k, ke), (v, ve) = c.dev
+    c.step = pa.WindowStep(k, v, ke, ve, batch=1, num_heads=H, max_seqlen_q=q, max_blocks_per_seq=tables.shape[1],
+                           window=200, sinks=20)
+    c.args[1:3] = tables, torch.tensor([LONGEST + 1], dtype=torch.int32, device="cuda")
+    c.run()
+    assert c.step.status() == (pa.PA_ERR_INVALID_ARG, pa.PA_STATUS_BIT_PLAN)
+    assert bool((c.out == 7).all())
+    tree = pa.TreeStep(k, v, ke, ve, batch=1, num_heads=H, max_seqlen_q=q, max_blocks_per_seq=tables.shape[1])
+    tree.run(*c.args, None, c.out)
+    assert tree.status() == (pa.PA_ERR_INVALID_ARG, pa.PA_STATUS_BIT_PLAN)
+    assert bool((c.out == 7).all())
+    pa.pa_status_clear(c.step.workspace)
+    c.args[2].fill_(LONGEST)
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    c.check()
+
+
+@pytest.mark.parametrize("q", [1, 40, 200])
+def test_all_keys_of_the_longest_context(torch, q):
+    """Keys of zero, so that every weight is the same, values of 1 in three quarters of the blocks and
+    -1 in the others. A worker's sums are of whole numbers below 2^24 (a power of two's multiples), so
+    only the join of at most 1216 parts (half a step each in the sums of weights and of values) and the
+    result's rounding are off: 2 * 1216 * 2^-24 + 2^-12 < 4e-4 of 1/2 to 1."""
+    bs, nb, d = 128, 512, 64
+    cols, ones = 2**31 // bs, LONGEST // bs * 3 // 4
+    g = torch.Generator(device="cuda").manual_seed(q)
+    key = torch.zeros((nb, bs, 1, d), device="cuda").to(torch.float8_e4m3fn)
+    value = torch.ones((nb, bs, 1, d), device="cuda")
+    value[nb // 2:] = -1
+    exps = [torch.full((nb, 1, bs), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    tables = torch.randint(0, nb // 2, (1, cols), generator=g, device="cuda", dtype=torch.int32)
+    tables[0, ones:] += nb // 2
+    step = pa.WindowStep(key, value.to(torch.float8_e4m3fn), *exps, batch=1, num_heads=1, max_seqlen_q=q,
+                         max_blocks_per_seq=cols, window=2**31 - 1)
+    out = torch.full((q, 1, d), 7.0, dtype=torch.float16, device="cuda")
+    step.run(torch.ones((q, 1, d), dtype=torch.float16, device="cuda"), tables,
+             torch.tensor([LONGEST], dtype=torch.int32, device="cuda"),
+             torch.tensor([q], dtype=torch.int32, device="cuda"), out)
+    assert step.status() == (pa.PA_OK, 0)
+    seen = LONGEST - q + 1 + np.arange(q)
+    want = (2.0 * ones * bs - seen) / seen
+    assert np.abs(out.cpu().numpy()[:, 0].astype(np.float64) - want[:, None]).max() < 4e-4
