@@ -150,6 +150,18 @@ __device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b
   return false;
 }
 
+// What is left of a wait that ran out although what it waits for may well go on, told by `count`: until that
+// stands still for as long as the limit.
+inline __device__ __noinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, uint32_t limit,
+                                                   const volatile uint32_t* count) {
+  uint32_t before;
+  do {
+    before = __shfl_sync(0xffffffffu, *count, 0);
+    if (tree_wait(bar, parity, limit)) return true;
+  } while (__shfl_sync(0xffffffffu, *count, 0) != before);
+  return false;
+}
+
 // A value that is the same in every lane, said so in a way that the compiler
 // believes: tcgen05 instructions take their addresses and descriptors from
 // uniform registers, and for a value that it must take for divergent it emits a loop
@@ -394,11 +406,15 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   uint64_t* stat_full = s_full + 17;          // (kLook) [row tile's parity] maxima and sums told
   uint64_t* vready = s_full + 19;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
+  // (WIN) Key tiles whose S are issued. Every wait is for a step a few key tiles away but one, that of the
+  // queries for the row tile before: a second and a half at 800,000 key tiles.
+  volatile uint32_t* issued = tmem_slot + 1;
   const int worker = blockIdx.x;
 
   if (tid == 0) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
+    *issued = 0;
     for (int i = 0; i < Cfg::kLanded; ++i) mbar_init(&sfull[i], 1);
     for (int i = 0; i < Cfg::kStages; ++i) mbar_init(&sempty[i], Cfg::kConv);
     for (int i = 0; i < KS; ++i) {
@@ -683,6 +699,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           tc_commit(&s_full[x]);
           if (g == QT - 1) tc_commit(&kempty[kslot]);
           if (last) tc_commit(q_empty);  // the queries may be replaced
+          if (g == QT - 1) *issued = uint32_t(n0 + i + 1);
         }
         __syncwarp();
         if (g == QT - 1 && ++kslot == KS) {
@@ -826,7 +843,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     while (ok && following.q >= 0) {
       t = following;
       // the queries, once the last row tile's S are complete
-      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit)) {
+      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit) &&
+          !tree_wait_long(q_empty, (tile - 1) & 1, P.wait_limit, issued)) {
         ok = false;
         break;
       }
