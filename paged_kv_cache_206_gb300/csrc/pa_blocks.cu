@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams P) 
     else report(P.status, PA_STATUS_BIT_POOL);
   }
   launch_dependents();
+  __syncwarp();  // (the barrier wants the warp converged, and the loop's last round may be some lanes' alone)
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 
   // ---- handed out, block k of all that are needed
