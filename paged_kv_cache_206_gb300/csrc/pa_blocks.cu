@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams P) 
   const int top = int(min(int64_t(free0) + n_back, int64_t(P.num_blocks)));
 
   // ---- given back
-  for (int j = me; j < n_back; j += all) {
+  for (uint32_t i = me; i < uint32_t(n_back); i += all) {  // (up to 2^31 - 1, and a step of all threads past it)
+    const int j = int(i);
     const int b = row_of(back, n, j), k = j - back[b];
     const int64_t entry = int64_t(b) * P.cols + (k < sinks[b] ? k : from[b] + k - sinks[b]);
     int block = P.tables[entry];

@@ -42,3 +42,17 @@ def test_blocks_given_back_that_fill_no_round(torch, back):
     assert pool.count.item() == blocks and bool((pool.block_tables == -1).all())
     free = pool.free.tolist()
     assert free.count(-1) == lost and len(set(free) - {-1}) == blocks - lost
+
+
+def test_as_many_entries_given_back_as_a_table_may_have(torch):
+    """Rows that say that they hold every entry of a table of 2^31 - 2048, none of which names a block."""
+    rows, cols, blocks = 2048, 2**20 - 1, 16
+    tables = torch.full((rows, cols), -5, dtype=torch.int32, device="cuda")
+    held = torch.full((rows,), cols, dtype=torch.int32, device="cuda")
+    gone = torch.zeros_like(held)
+    free = torch.full((blocks,), 7, dtype=torch.int32, device="cuda")
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pool = pa.BlockPool(tables, held, gone, free, count, block_size=16)
+    pool.step(torch.zeros_like(held))
+    assert all(bool((part == -1).all()) for part in tables.split(64))
+    assert bool((held == 0).all()) and count.item() == blocks and free.tolist() == [-1] * blocks
