@@ -159,7 +159,8 @@ typedef struct pa_cache_config {
  *
  * tokens        rows of key and value; rows past sum q_b are not read
  * key, value    fp16, as in pa_qk_norm_rope (strides in elements)
- * q_seqlens     device int32 [batch], or NULL when every q_b = 1
+ * q_seqlens     device int32 [batch], or NULL when every row is one token of its
+ *               sequence (a row of context_lens[b] = 0 is then padding)
  * No two current tokens may name the same cache slot (a block that two
  * sequences share must be copied before one of them writes into it); a slot
  * that is named twice ends up holding bytes of either row.

@@ -64,7 +64,8 @@ pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_bytes);
  * context_lens   device int32 [batch], L_b counting the current tokens, at most
  *                max_blocks_per_seq * block_size and 2^31 - 4096
  * q_seqlens      device int32 [batch], 0 <= q_b <= max_seqlen_q (0: a padding
- *                sequence), or NULL when every q_b = 1
+ *                sequence), or NULL when every row is one token of its sequence (a row
+ *                of L_b = 0 is then padding)
  * parents        device int32 [tokens]: -1 for a root (a child of the last
  *                token before the drafts), else the index within the
  *                sequence's current tokens of an earlier one; or NULL

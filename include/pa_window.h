@@ -59,7 +59,8 @@ pa_status pa_window_workspace(const pa_config* cfg, const pa_window* win, size_t
  * context_lens   device int32 [batch], L_b counting the current tokens, at most
  *                max_blocks_per_seq * block_size and 2^31 - 4096
  * q_seqlens      device int32 [batch], 0 <= q_b <= max_seqlen_q (0: a padding
- *                sequence), or NULL when every q_b = 1
+ *                sequence), or NULL when every row is one token of its sequence (a row
+ *                of L_b = 0 is then padding)
  * workspace      device, >= pa_window_workspace's bytes, 256-byte aligned; its
  *                status word zero before the first call, as in pa.h. Calls
  *                whose work overlaps on the GPU need a workspace each.

@@ -33,6 +33,9 @@ __device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int 
   return q >= 0 && q <= P.max_q && q <= P.tokens && L >= q && L <= P.max_keys;
 }
 
+// Whether a row is padding although it counts as one: without q_seqlens, that of a sequence without keys.
+__device__ __forceinline__ bool tree_padding(const TreeParams& P, int L) { return !P.q_seqlens && L == 0; }
+
 // Whether the tokens end before sequence rows begun at q_start do (the rows past them are left out).
 __device__ __forceinline__ bool tree_rows_missing(const TreeParams& P, int q_start, int q) {
   return P.tokens - q_start < q;

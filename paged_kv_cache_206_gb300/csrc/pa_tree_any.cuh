@@ -51,7 +51,8 @@ inline __device__ __noinline__ void tree_check_lengths(const TreeParams& P, int 
   int64_t sum = 0;
   for (int b = lane; b < P.batch; b += 32) {
     const int q = P.q_seqlens ? P.q_seqlens[b] : 1;
-    if (!tree_lengths_ok(P, q, P.context_lens[b])) set_status(P.status, PA_STATUS_BIT_PLAN);
+    const int L = P.context_lens[b];
+    if (!tree_lengths_ok(P, q, L) && !tree_padding(P, L)) set_status(P.status, PA_STATUS_BIT_PLAN);
     sum += max(q, 0);
   }
 #pragma unroll
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32, 5) tree_any_kernel(const TreeP
   if (b < 0) return;
   const int q = P.q_seqlens ? P.q_seqlens[b] : 1, L = P.context_lens[b];
   if (!tree_lengths_ok(P, q, L)) {
-    set_status(P.status, PA_STATUS_BIT_PLAN);
+    if (!tree_padding(P, L)) set_status(P.status, PA_STATUS_BIT_PLAN);
     return;
   }
   const int prefix = L - q;

@@ -122,7 +122,7 @@ struct WindowLine {
     s.q = P.q_seqlens ? P.q_seqlens[b] : 1;
     s.L = P.context_lens[b];
     const bool ok = tree_lengths_ok(P, s.q, s.L);
-    if (!ok) set_status(P.status, PA_STATUS_BIT_PLAN);
+    if (!ok && !tree_padding(P, s.L)) set_status(P.status, PA_STATUS_BIT_PLAN);
     s.q = tree_tokens(P, 0, max(s.q, 0));
     s.tiles = !ok || s.q == 0 ? 0 : s.q <= tt ? 1 : (s.q - 1) / tt + 1;
     return s;
