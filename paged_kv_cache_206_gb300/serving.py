@@ -569,6 +569,9 @@ class BlockPool:
         if not all(0 <= n < 2**31 for n in (block_size, window, sinks)):
             _refuse(where, f"block_size, window and sinks must not be negative, got {block_size}, {window}, "
                            f"{sinks}")
+        if max(batch, cols, free.shape[0]) >= 2**31:  # (before they are cut to 32 bits)
+            _refuse(where, f"a pool has fewer than 2^31 rows, entries a row and blocks, got {batch}, {cols}, "
+                           f"{free.shape[0]}")
         self.block_tables, self.held, self.gone, self.free, self.count = block_tables, held, gone, free, count
         self.cfg = pa_blocks_config(batch, block_size, free.shape[0], cols, window, sinks)
         self.device, self._at, self._rows = dev, block_tables.get_device(), (batch,)
