@@ -1348,7 +1348,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
       };
       Tile t;
       bool have = next_tile(t);
-      int p0 = t.first();
+      int p0 = have ? t.first() : 0;  // (no tile told, t is nothing)
       if (have) look(t, p0, 0);
       while (ok && have) {
         // the flags of four row tiles ago, which every warp has written out
@@ -1359,7 +1359,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
         const Tile done = t;
         ++tile;
         have = next_tile(t);
-        p0 = t.first();
+        p0 = have ? t.first() : 0;
         if (have) look(t, p0, 0);
         if (Cfg::kShare && ok) write_out(done, tile - 1);
       }
