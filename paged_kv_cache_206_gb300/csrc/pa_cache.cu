@@ -190,9 +190,8 @@ rows_kernel(const RowParams P) {
     const int b = find_sequence(P, t, lane, i);
     if (b < 0) return;
     const int q = P.q_seqlens ? P.q_seqlens[b] : 1, L = P.context_lens[b];
-    if (L == 0 && !P.q_seqlens) return;  // padding
     if (q > P.max_rows || L < q || int64_t(L) > int64_t(P.max_blocks_per_seq) * P.block_size) {
-      report(P.status, PA_STATUS_BIT_PLAN);
+      if (L != 0 || P.q_seqlens) report(P.status, PA_STATUS_BIT_PLAN);  // (else padding)
       return;
     }
     pos = L - q + i;
