@@ -18,7 +18,9 @@
  *
  * Scores, softmax sums and outputs are accumulated in fp32, the 8-bit cache's codes and
  * exponents enter them exactly; the weights are rounded to fp16 for their product
- * with V. The same batch gives the same bits every time; a
+ * with V. However long a context, no fp32 sum is of more than 65536 keys before it is
+ * rounded to nearest into the next (the tensor cores' additions cut off, less than 2^-12 of
+ * sum p |v| in as many). The same batch gives the same bits every time; a
  * sequence in another batch may differ in its last bits, as the work is divided
  * otherwise.
  */

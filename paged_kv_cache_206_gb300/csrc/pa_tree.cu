@@ -48,10 +48,12 @@ extern "C" pa_status pa_tree_workspace(const pa_config* cfg, size_t* workspace_b
   if (!workspace_bytes) return PA_ERR_INVALID_ARG;
   // the larger of the two caches' needs, so that it does not depend on them
   *workspace_bytes = PA_STATUS_BYTES;
+  pa::TreeParams P{};
+  pa::tree_lengths(*cfg, P);
   for (const bool q8 : {false, true}) {
     size_t need = 0;
     cudaError_t e;
-    if (pa::tree_tiles(*cfg, pa::TreeParams{}, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
+    if (pa::tree_tiles(*cfg, P, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
       *workspace_bytes = need;
   }
   return PA_OK;

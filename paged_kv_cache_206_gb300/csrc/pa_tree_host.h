@@ -25,6 +25,11 @@ inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintpt
 // past a context's end.
 constexpr int64_t kMostKeys = (int64_t(1) << 31) - 4096;
 
+// What of P says how long a tile may be: all that a workspace's size asks of it.
+inline void tree_lengths(const pa_config& c, TreeParams& P) {
+  P.max_keys = int(std::min<int64_t>(int64_t(c.max_blocks_per_seq) * c.block_size, kMostKeys));
+}
+
 // The checks behind check_tree, and P of the arguments (of no tokens: nothing).
 inline pa_status tree_arguments(const pa_config& c, int64_t tokens, const void* query, const void* key_cache,
                                 const void* value_cache, const uint8_t* key_exps, const uint8_t* value_exps,
@@ -64,7 +69,7 @@ inline pa_status tree_arguments(const pa_config& c, int64_t tokens, const void* 
   P.num_blocks = c.num_blocks;
   P.max_blocks_per_seq = c.max_blocks_per_seq;
   P.max_q = int(max_q(c));
-  P.max_keys = int(std::min<int64_t>(int64_t(c.max_blocks_per_seq) * c.block_size, kMostKeys));
+  tree_lengths(c, P);
   P.scale_log2 = (c.scale > 0.f ? c.scale : 1.0f / std::sqrt(float(c.head_size_k))) * kLog2e;
   P.wait_limit = uint32_t(std::min<long long>(wait_limit(), kTreeWaitLimit));
   return PA_OK;

@@ -47,7 +47,7 @@ namespace pa {
 // behind the median one; without any arithmetic the copies take 75. A window of 4096 over 8 bits takes 80 to 90 for
 // 421 MB (copies alone 83 where it takes 91). One step with 1024 keys takes 14.3: the same 5, four
 // units 3, partial rows and their join 5.
-template <int HD, bool Q8, int NT, bool WIN>
+template <int HD, bool Q8, int NT, bool WIN, bool SEG>
 struct TreeMma {
   static constexpr int kWarps = 4;
   static constexpr int kRowBytes = HD * (Q8 ? 1 : 2);
@@ -75,7 +75,8 @@ struct TreeMma {
   static constexpr uint32_t par_off = mask_off + kRows * kTreeWords * 4;
   static constexpr uint32_t bad_off = par_off + PA_TREE_MAX_TOKENS;
   static constexpr uint32_t tile_off = bad_off + kTreeWords * 4;
-  using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Whole = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Tile = std::conditional_t<SEG, TreeSegment<Whole>, Whole>;
   using Place = TreePlace<std::conditional_t<WIN, WindowWalk<kSub, kSub, kRows, kLead>, TreeWalk<kSub, kRows, kLead>>, Tile>;
   static constexpr uint32_t place_off = (tile_off + kTiles * sizeof(Tile) + 7) & ~7u;
   static constexpr uint32_t exps_off = (place_off + sizeof(Place) + 15) & ~15u;  // [stage][K, V][32]
@@ -150,11 +151,11 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return hit != 0;
 }
 
-template <int HD, bool Q8, int NT, bool WIN>
-__global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
+template <int HD, bool Q8, int NT, bool WIN, bool SEG>
+__global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN, SEG>::kCtas))
     tree_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                     const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S, int box) {
-  using Cfg = TreeMma<HD, Q8, NT, WIN>;
+  using Cfg = TreeMma<HD, Q8, NT, WIN, SEG>;
   using Tile = typename Cfg::Tile;
   constexpr int SUB = Cfg::kSub, MT = Cfg::kMT, NR = Cfg::kRows;
   constexpr int RB = Cfg::kRowBytes, C = Cfg::kChunks, E = Cfg::kElems;
@@ -677,16 +678,33 @@ __global__ void __launch_bounds__(128, (TreeMma<HD, Q8, NT, WIN>::kCtas))
         __syncwarp();
       }
     }
+    int seg = 0;
+    if constexpr (SEG) seg = t.seg;
+    if (SEG && seg) {
+#pragma unroll 1
+      for (int row = 0; row < NR; ++row) {
+        const int r = t.r0 + row, i = r / G;
+        const int64_t tok = int64_t(t.q_start) + i;
+        if (i >= t.q || tok >= P.tokens) continue;
+        tree_fold<HD, NR, 32>(S, worker, seg, 0, row, S.part_ml[int64_t(t.slot) * NR + row], row * HD, 1,
+                              P.out + (tok * P.num_heads + t.kvh * G + r % G) * P.hv, lane, P.hv);
+      }
+      __syncwarp();
+    }
   }
 }
 
 // Launches the kernel of a tile shape and its combine pass; with `need`, only
-// says how much workspace they take.
-cudaError_t tree_mma_64(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
-cudaError_t tree_mma_128(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
-cudaError_t tree_mma_256(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
-cudaError_t window_mma_64(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
-cudaError_t window_mma_128(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
-cudaError_t window_mma_256(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
+// says how much workspace they take. (long: called by the others, for tiles in segments)
+#define PA_MMA_SIZE(n)                                                                                               \
+  cudaError_t tree_mma_##n(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);   \
+  cudaError_t window_mma_##n(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws, cudaStream_t s);
+PA_MMA_SIZE(64)
+PA_MMA_SIZE(128)
+PA_MMA_SIZE(256)
+PA_MMA_SIZE(long_64)
+PA_MMA_SIZE(long_128)
+PA_MMA_SIZE(long_256)
+#undef PA_MMA_SIZE
 
 }  // namespace pa

@@ -5,7 +5,8 @@ namespace pa {
 
 cudaError_t tree_mma_256(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws,
                         cudaStream_t s) {
-  return tree_mma_pick<256, false>(P, q8, nt, sms, need, ws, s);
+  if (tree_segments(P, 8 * nt)) return tree_mma_long_256(P, q8, nt, sms, need, ws, s);
+  return tree_mma_pick<256, false, false>(P, q8, nt, sms, need, ws, s);
 }
 
 }  // namespace pa

@@ -21,15 +21,16 @@ inline bool tree_rows_map(CUtensorMap* m, const void* base, const TreeParams& P,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <int HD, bool Q8, int NT, bool WIN>
+template <int HD, bool Q8, int NT, bool WIN, bool SEG>
 cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, cudaStream_t stream) {
-  using Cfg = TreeMma<HD, Q8, NT, WIN>;
+  using Cfg = TreeMma<HD, Q8, NT, WIN, SEG>;
   const int grid = sms * Cfg::kCtas, workers = grid * Cfg::kWarps;
-  const size_t rows = size_t(2) * workers * Cfg::kRows;
+  const size_t rows = size_t(SEG ? 3 : 2) * workers * Cfg::kRows;
   const size_t o_off = PA_STATUS_BYTES, ml_off = align256(o_off + rows * HD * 4);
   const size_t join_off = align256(ml_off + rows * sizeof(float2));
+  const size_t fold_off = align256(join_off + workers * sizeof(TreeJoin));
   if (need) {
-    *need = align256(join_off + workers * sizeof(TreeJoin));
+    *need = align256(fold_off + (SEG ? size_t(workers) * Cfg::kRows * sizeof(float2) : 0));
     return cudaSuccess;
   }
   TreeSplit S;
@@ -38,10 +39,12 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   S.join = reinterpret_cast<TreeJoin*>(static_cast<char*>(ws) + join_off);
   S.tile_tokens = std::max(Cfg::kRows / P.group, 1);
   S.tile_parts = (P.group - 1) / Cfg::kRows + 1;
+  S.fold_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + fold_off);
   S.workers = workers;
+  S.segment = SEG ? kSegmentKeys / Cfg::kSub : 0;
   // a partial result (kRows rows of fp32) should stay below the keys it stands for
   S.min_units = (Cfg::kLead + (NT + Cfg::kMT - 1) / Cfg::kMT) * (WIN ? Cfg::kSub : 1);
-  auto kern = tree_mma_kernel<HD, Q8, NT, WIN>;
+  auto kern = tree_mma_kernel<HD, Q8, NT, WIN, SEG>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::bytes);
   if (e != cudaSuccess) return e;
   const int low = P.block_size & -P.block_size, box = low < Cfg::kSub ? low : Cfg::kSub;
@@ -64,14 +67,14 @@ cudaError_t tree_mma_run(const TreeParams& P, int sms, size_t* need, void* ws, c
   return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, Cfg::kRows>, P, S);
 }
 
-template <int HD, bool WIN>
+template <int HD, bool WIN, bool SEG>
 cudaError_t tree_mma_pick(const TreeParams& P, bool q8, int nt, int sms, size_t* need, void* ws,
                           cudaStream_t s) {
   if (nt >= 2)
-    return q8 ? tree_mma_run<HD, true, 2, WIN>(P, sms, need, ws, s)
-              : tree_mma_run<HD, false, 2, WIN>(P, sms, need, ws, s);
-  return q8 ? tree_mma_run<HD, true, 1, WIN>(P, sms, need, ws, s)
-            : tree_mma_run<HD, false, 1, WIN>(P, sms, need, ws, s);
+    return q8 ? tree_mma_run<HD, true, 2, WIN, SEG>(P, sms, need, ws, s)
+              : tree_mma_run<HD, false, 2, WIN, SEG>(P, sms, need, ws, s);
+  return q8 ? tree_mma_run<HD, true, 1, WIN, SEG>(P, sms, need, ws, s)
+            : tree_mma_run<HD, false, 1, WIN, SEG>(P, sms, need, ws, s);
 }
 
 }  // namespace pa

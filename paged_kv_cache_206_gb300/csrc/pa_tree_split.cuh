@@ -13,6 +13,14 @@
 // a divided tile's first keys also leaves a note of it, by which the combine kernel
 // joins the parts in key order. The lengths are read on the device only, so a launch
 // fits any.
+//
+// Where a worker has more than kSegmentKeys keys of a tile it takes them in segments of that many, each one a
+// tile to the kernels, and adds up their results itself (tree_fold). The tensor cores' fp32 sums
+// cut off what an addition of 16 keys rounds, always towards zero, so that their error grows with the keys: equal
+// values came out 5.7e-3 too small over 2^20 keys of one worker, 5.7e-4 over 2^17. Segments are a kernel form of
+// their own (SEG), chosen where the tables allow a tile of more keys: with them in every form, calls of short
+// contexts took up to 4 % longer (drafts of 1024 keys 50.2 -> 51.9 us, trees of 16 94.3 -> 95.4). 2048 tokens at the end
+// of 2^20 keys, 32 heads of 128 on 8, fp16, take 30.0 ms in them, 29.1 without.
 #pragma once
 
 #include "pa_tree.cuh"
@@ -26,12 +34,15 @@ struct alignas(8) TreeJoin {
 };
 
 struct TreeSplit {
-  float* part_o;    // [2 * workers][NR][hv], not yet divided by the sum
-  float2* part_ml;  // [2 * workers][NR]: running maximum (base 2) and sum
+  // [2 * workers][NR][hv], not yet divided by the sum; one a worker more, for the segment at hand, where there are any
+  float* part_o;
+  float2* part_ml;  // the same [NR]: running maximum (base 2) and sum
   struct TreeJoin* join;  // [workers]
   int workers;
   int min_units;    // fewest places of the line worth a worker
   int tile_tokens, tile_parts;  // (pa_window_split.cuh) whole tokens of a row tile, parts of a token's heads
+  float2* fold_ml;  // [2][workers][NR] of the segments so far; by halves of the columns where two threads have them
+  int segment;      // units of a segment
 };
 
 // a / b for a >= 0, b > 0: the 64-bit division takes several times the 32-bit one's time.
@@ -106,7 +117,27 @@ struct TreeTile {
   int s0, s1;  // units [s0, s1)
   int slot;    // of a partial result; -1: the whole tile
   int parts;   // of a divided tile whose first keys are here, else 0
+  static constexpr bool kSegments = false;
 };
+
+// The same of a kernel that takes segments.
+template <class Tile>
+struct TreeSegment : Tile {
+  // Of a segment, whose slot is the worker's third: 4 * (the slot that the tile has + 2), and 1 for the first
+  // one, 2 for the last one; else 0.
+  int seg;
+  int end;  // the tile's, where it goes on in another segment; else 0
+  static constexpr bool kSegments = true;
+};
+
+// Keys of a segment. (A tile of 256 rows takes 0.9 ms for them and 4 to 10 us at its ends.)
+constexpr int kSegmentKeys = 1 << 16;
+
+// Whether a tile of this many rows may have more keys than that.
+inline bool tree_segments(const TreeParams& P, int rows) {
+  const int64_t seen = int64_t(P.window) + P.sinks + rows;
+  return (P.window && seen < P.max_keys ? seen : P.max_keys) > kSegmentKeys;
+}
 
 // One worker's way along the line (warp-collective, every lane the same).
 template <int UNIT, int NR, int LEAD>
@@ -214,25 +245,91 @@ __device__ __noinline__ bool tree_begin(const TreeParams& P, const TreeSplit& S,
   Walk w;
   const bool some = w.begin(P, S, worker, lane);
   at->walk = w;
+  if constexpr (Tile::kSegments) at->tile.end = 0;
   __syncwarp();
   return some;
+}
+
+// The first segment of the tile at hand, or its next one.
+template <class Walk, class Tile>
+__device__ __noinline__ void tree_next_segment(const TreeSplit& S, TreePlace<Walk, Tile>* at) {
+  Tile d = at->tile;
+  if (d.end) {
+    d.s0 = d.s1;
+    d.seg &= ~1;
+    d.parts = 0;
+  } else {
+    d.end = d.s1;
+    d.seg = 4 * (d.slot + 2) | 1;
+    d.slot = 2 * S.workers + at->walk.worker;
+  }
+  d.s1 = min(d.s0 + S.segment, d.end);
+  if (d.s1 == d.end) {
+    d.seg |= 2;
+    d.end = 0;
+  }
+  __syncwarp();
+  at->tile = d;
+  __syncwarp();
 }
 
 template <class Walk, class Tile>
 __device__ __noinline__ bool tree_next(const TreeParams& P, const TreeSplit& S, TreePlace<Walk, Tile>* at) {
+  if constexpr (Tile::kSegments)
+    if (at->tile.end) {
+      tree_next_segment(S, at);
+      return true;
+    }
   Walk w = at->walk;
   Tile d;
   const bool some = w.next(P, S, d);
+  if constexpr (Tile::kSegments) d.seg = d.end = 0;
   __syncwarp();
   if (some) at->tile = d;
   at->walk = w;
   __syncwarp();
+  if constexpr (Tile::kSegments)
+    if (some && d.s1 - d.s0 > S.segment) tree_next_segment(S, at);
   return some;
 }
 
 // The note of a divided tile (parts = 0: none).
-__device__ __forceinline__ void tree_note(const TreeSplit& S, int worker, const TreeTile& t) {
-  S.join[worker] = TreeJoin{t.parts, t.slot, t.q_start, t.q, t.kvh, t.r0};
+template <class Tile>
+__device__ __forceinline__ void tree_note(const TreeSplit& S, int worker, const Tile& t) {
+  int slot = t.slot;
+  if constexpr (Tile::kSegments)
+    if (t.seg) slot = (t.seg >> 2) - 2;
+  S.join[worker] = TreeJoin{t.parts, slot, t.q_start, t.q, t.kvh, t.r0};
+}
+
+// Adds a segment's result for one row, which lies in the worker's third slot as a partial result does (column d at
+// d * stride from `at`), to the tile's segments before it: in the tile's own slot, or for a whole tile
+// in the worker's second one, which its last tile takes later. With the last segment a
+// whole tile's row goes to `out`. `ml` is the segment's maximum and sum. By a thread for its columns [d0, d1) of the
+// row, the half-th of two at most that have the row, each with a maximum and a sum of its own, or (STEP = 32) by
+// a warp. Rare, hence not inlined.
+template <int HD, int NR, int STEP>
+__device__ __noinline__ void tree_fold(const TreeSplit& S, int worker, int seg, int half, int row, float2 ml, int64_t at,
+                                       int stride, __half* out, int d0, int d1) {
+  const int to = (seg >> 2) - 2, slot = to < 0 ? 2 * worker + 1 : to;
+  const bool first = seg & 1, last = seg & 2;
+  float2* mine = S.fold_ml + (int64_t(half) * S.workers + worker) * NR + row;
+  const float2 old = first ? make_float2(-INFINITY, 0.f) : *mine;
+  if (STEP == 32) __syncwarp();  // (read by every lane before one of them writes it)
+  const float top = fmaxf(old.x, ml.x), ref = top == -INFINITY ? 0.f : top;
+  const float wa = ex2(old.x - ref), wb = ex2(ml.x - ref), sum = old.y * wa + ml.y * wb;
+  *mine = make_float2(top, sum);
+  if (last && to >= 0 && half == 0) S.part_ml[int64_t(to) * NR + row] = make_float2(top, sum);
+  const float* from = S.part_o + (int64_t(2 * S.workers + worker) * HD) * NR + at;
+  float* acc = S.part_o + int64_t(slot) * HD * NR + at;
+  // (a sum that is no number stays so however little it weighs)
+  const auto times = [](float x, float w) { return isfinite(x) ? x * w : x; };
+  for (int d = d0; d < d1; d += STEP) {
+    float x = times(from[int64_t(d) * stride], wb);
+    if (!first) x += times(acc[int64_t(d) * stride], wa);
+    if (last && to < 0) out[d] = __float2half_rn(x / sum);
+    else acc[int64_t(d) * stride] = x;
+  }
 }
 
 // Joins the partial results of the divided tiles: CTA (c, y) the rows [8 y, 8 y + 8)

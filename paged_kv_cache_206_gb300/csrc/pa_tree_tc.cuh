@@ -66,7 +66,7 @@ namespace pa {
 // are attended, 49 % of the tensor pipe's time; chains of S, softmax and P V of two query tiles that wait for each
 // other); 8 x 512 tokens over 8 bits, window 2048, 32 heads, in 162 us (0.76; the widening warps share the schedulers
 // with the softmax, issue slots 42 % full).
-template <int HD, bool Q8, int QT, bool WIN>
+template <int HD, bool Q8, int QT, bool WIN, bool SEG>
 struct TreeTc {
   static constexpr int kConv = 1;  // warps that widen a 64-row part of codes
   static constexpr bool kLook = WIN && !Q8;  // there are warps that look the V tiles through,
@@ -120,7 +120,8 @@ struct TreeTc {
   static constexpr uint32_t bars_off = bad_off + kBad * kTreeWords * 4;
   static constexpr int kBars = kLanded + kStages + 2 * kKSlots + 2 * kVSlots + kMeta + 2 * kExps + 15 + 2 * kAhead +
                                (WIN ? 2 : 0) + (kLook ? kVSlots + 2 : 0);
-  using Tile = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Whole = std::conditional_t<WIN, WindowTile, TreeTile>;
+  using Tile = std::conditional_t<SEG, TreeSegment<Whole>, Whole>;
   using Walk = std::conditional_t<WIN, WindowWalk<kTok, 64, kRows, kLead>, TreeWalk<kTok, kRows, kLead>>;
   using Place = TreePlace<Walk, Tile>;
   static constexpr uint32_t tile_off = (bars_off + kBars * 8 + 15) & ~15u;  // [kAhead] row tiles
@@ -147,18 +148,6 @@ __device__ __forceinline__ bool tree_wait2(uint64_t* a, uint32_t pa, uint64_t* b
   do {
     if (__all_sync(0xffffffffu, mbar_try_wait(a, pa) & mbar_try_wait(b, pb))) return true;
   } while (__all_sync(0xffffffffu, uint32_t(clock()) - t0 <= limit));
-  return false;
-}
-
-// What is left of a wait that ran out although what it waits for may well go on, told by `count`: until that
-// stands still for as long as the limit.
-inline __device__ __noinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, uint32_t limit,
-                                                   const volatile uint32_t* count) {
-  uint32_t before;
-  do {
-    before = __shfl_sync(0xffffffffu, *count, 0);
-    if (tree_wait(bar, parity, limit)) return true;
-  } while (__shfl_sync(0xffffffffu, *count, 0) != before);
   return false;
 }
 
@@ -362,12 +351,12 @@ __device__ __noinline__ void tree_apart(const TreeParams& P, uint32_t sbuf, cons
   *own = make_float2(top, sum);
 }
 
-template <int HD, bool Q8, int QT, bool WIN>
-__global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
+template <int HD, bool Q8, int QT, bool WIN, bool SEG>
+__global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN, SEG>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const __grid_constant__ std::conditional_t<WIN, CUtensorMap, int> tmq,
                    const __grid_constant__ TreeParams P, const __grid_constant__ TreeSplit S) {
-  using Cfg = TreeTc<HD, Q8, QT, WIN>;
+  using Cfg = TreeTc<HD, Q8, QT, WIN, SEG>;
   using Tile = typename Cfg::Tile;
   constexpr int TOK = Cfg::kTok, H2 = Cfg::kHalves, KS = Cfg::kKSlots, VS = Cfg::kVSlots;
   constexpr uint32_t kTmemCols = 512;
@@ -406,15 +395,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
   uint64_t* stat_full = s_full + 17;          // (kLook) [row tile's parity] maxima and sums told
   uint64_t* vready = s_full + 19;             // (kLook) [slot] V looked through
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::tmem_off);
-  // (WIN) Key tiles whose S are issued. Every wait is for a step a few key tiles away but one, that of the
-  // queries for the row tile before: a second and a half at 800,000 key tiles.
-  volatile uint32_t* issued = tmem_slot + 1;
   const int worker = blockIdx.x;
 
   if (tid == 0) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
-    *issued = 0;
     for (int i = 0; i < Cfg::kLanded; ++i) mbar_init(&sfull[i], 1);
     for (int i = 0; i < Cfg::kStages; ++i) mbar_init(&sempty[i], Cfg::kConv);
     for (int i = 0; i < KS; ++i) {
@@ -699,7 +684,6 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           tc_commit(&s_full[x]);
           if (g == QT - 1) tc_commit(&kempty[kslot]);
           if (last) tc_commit(q_empty);  // the queries may be replaced
-          if (g == QT - 1) *issued = uint32_t(n0 + i + 1);
         }
         __syncwarp();
         if (g == QT - 1 && ++kslot == KS) {
@@ -843,8 +827,7 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
     while (ok && following.q >= 0) {
       t = following;
       // the queries, once the last row tile's S are complete
-      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit) &&
-          !tree_wait_long(q_empty, (tile - 1) & 1, P.wait_limit, issued)) {
+      if (tile > 0 && !tree_wait(q_empty, (tile - 1) & 1, P.wait_limit)) {
         ok = false;
         break;
       }
@@ -1264,6 +1247,12 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
           if (tid - 128 < kTreeWords) bad_s[(tile % Cfg::kBad) * kTreeWords + tid - 128] = 0;
         }
       }
+      if constexpr (SEG) {
+        const int seg = told[(heard - 1) % Cfg::kAhead].seg;
+        if (seg && row_ok && ok)
+          tree_fold<HD, Cfg::kRows, 1>(S, worker, seg, QT == 1 ? g : 0, tr, make_float2(M, sum), tr, Cfg::kRows,
+                                       P.out + (tok * P.num_heads + t.kvh * G + head) * HD, col0, col0 + cols);
+      }
       n0 += tiles;
       ++tile;
     }
@@ -1343,6 +1332,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
               window_patch<Q8, TOK, 64>(P, t, t.L - t.q + qi, whole ? mine : nullptr, part, Cfg::kRows, HD / 2, 1, HD);
             __syncwarp();
           }
+          if constexpr (SEG) if (t.seg && row_ok)
+            tree_fold<HD, Cfg::kRows, 1>(S, worker, t.seg, 1, tr, st[tr], tr, Cfg::kRows, mine, HD / 2, HD);
         }
         ++oc;
       };
@@ -1556,10 +1547,14 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN>::kThreads, 1)
 }
 
 // Launches the kernel of a tile shape and its combine pass; with `need`, only
-// says how much workspace they take.
+// says how much workspace they take. (long: called by the others, for tiles in segments)
 cudaError_t tree_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
                     void* ws, cudaStream_t s);
 cudaError_t window_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
                       void* ws, cudaStream_t s);
+cudaError_t tree_tc_long(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
+                         void* ws, cudaStream_t s);
+cudaError_t window_tc_long(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
+                           void* ws, cudaStream_t s);
 
 }  // namespace pa

@@ -41,14 +41,15 @@ inline bool window_query_map(CUtensorMap* m, const TreeParams& P) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <int HD, bool Q8, int QT, bool WIN>
+template <int HD, bool Q8, int QT, bool WIN, bool SEG>
 cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cudaStream_t stream) {
-  using Cfg = TreeTc<HD, Q8, QT, WIN>;
-  const size_t rows = size_t(2) * sms * Cfg::kRows;
+  using Cfg = TreeTc<HD, Q8, QT, WIN, SEG>;
+  const size_t rows = size_t(SEG ? 3 : 2) * sms * Cfg::kRows;
   const size_t o_off = PA_STATUS_BYTES, ml_off = align256(o_off + rows * HD * 4);
   const size_t join_off = align256(ml_off + rows * sizeof(float2));
+  const size_t fold_off = align256(join_off + sms * sizeof(TreeJoin));
   if (need) {
-    *need = align256(join_off + sms * sizeof(TreeJoin));
+    *need = align256(fold_off + (SEG ? 2 * size_t(sms) * Cfg::kRows * sizeof(float2) : 0));
     return cudaSuccess;
   }
   TreeSplit S;
@@ -57,7 +58,9 @@ cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cu
   S.join = reinterpret_cast<TreeJoin*>(static_cast<char*>(ws) + join_off);
   S.tile_tokens = std::max(Cfg::kRows / P.group, 1);
   S.tile_parts = (P.group - 1) / Cfg::kRows + 1;
+  S.fold_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + fold_off);
   S.workers = sms;
+  S.segment = SEG ? kSegmentKeys / Cfg::kTok : 0;
   S.min_units = (Cfg::kLead + 1) * (WIN ? Cfg::kTok : 1);
   const int box = std::min(P.block_size & -P.block_size, 64);
   CUtensorMap tmk, tmv;
@@ -66,7 +69,7 @@ cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cu
   std::conditional_t<WIN, CUtensorMap, int> tmq{};
   if constexpr (WIN)
     if (128 % P.group == 0 && !window_query_map(&tmq, P)) return cudaErrorInvalidValue;
-  auto kern = tree_tc_kernel<HD, Q8, QT, WIN>;
+  auto kern = tree_tc_kernel<HD, Q8, QT, WIN, SEG>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Cfg::bytes);
   if (e != cudaSuccess) return e;
   kern<<<unsigned(sms), Cfg::kThreads, Cfg::bytes, stream>>>(tmk, tmv, tmq, P, S);
@@ -83,12 +86,14 @@ cudaError_t tree_tc_run(const TreeParams& P, int sms, size_t* need, void* ws, cu
   return cudaLaunchKernelEx(&cfg, tree_combine_cols_kernel<HD, Cfg::kRows>, P, S);
 }
 
-template <int HD, bool WIN>
+template <int HD, bool WIN, bool SEG>
 cudaError_t tree_tc_pick(const TreeParams& P, bool q8, int64_t rows, int sms, size_t* need, void* ws,
                  cudaStream_t s) {
   if (rows > 128)
-    return q8 ? tree_tc_run<HD, true, 2, WIN>(P, sms, need, ws, s) : tree_tc_run<HD, false, 2, WIN>(P, sms, need, ws, s);
-  return q8 ? tree_tc_run<HD, true, 1, WIN>(P, sms, need, ws, s) : tree_tc_run<HD, false, 1, WIN>(P, sms, need, ws, s);
+    return q8 ? tree_tc_run<HD, true, 2, WIN, SEG>(P, sms, need, ws, s)
+              : tree_tc_run<HD, false, 2, WIN, SEG>(P, sms, need, ws, s);
+  return q8 ? tree_tc_run<HD, true, 1, WIN, SEG>(P, sms, need, ws, s)
+            : tree_tc_run<HD, false, 1, WIN, SEG>(P, sms, need, ws, s);
 }
 
 }  // namespace pa

@@ -52,10 +52,14 @@ extern "C" pa_status pa_window_workspace(const pa_config* cfg, const pa_window* 
   if (!workspace_bytes) return PA_ERR_INVALID_ARG;
   // the larger of the two caches' needs, so that it does not depend on them
   *workspace_bytes = PA_STATUS_BYTES;
+  pa::TreeParams P{};
+  pa::tree_lengths(*cfg, P);
+  P.window = win->window;
+  P.sinks = win->sinks;
   for (const bool q8 : {false, true}) {
     size_t need = 0;
     cudaError_t e;
-    if (pa::window_tiles(*cfg, pa::TreeParams{}, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
+    if (pa::window_tiles(*cfg, P, q8, &need, nullptr, nullptr, &e) && need > *workspace_bytes)
       *workspace_bytes = need;
   }
   return PA_OK;

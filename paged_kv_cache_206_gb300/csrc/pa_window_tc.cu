@@ -5,8 +5,9 @@ namespace pa {
 
 cudaError_t window_tc(const TreeParams& P, int head_size, bool q8, int64_t rows, int sms, size_t* need,
                     void* ws, cudaStream_t s) {
-  return head_size == 64 ? tree_tc_pick<64, true>(P, q8, rows, sms, need, ws, s)
-                         : tree_tc_pick<128, true>(P, q8, rows, sms, need, ws, s);
+  if (tree_segments(P, rows > 128 ? 256 : 128)) return window_tc_long(P, head_size, q8, rows, sms, need, ws, s);
+  return head_size == 64 ? tree_tc_pick<64, true, false>(P, q8, rows, sms, need, ws, s)
+                         : tree_tc_pick<128, true, false>(P, q8, rows, sms, need, ws, s);
 }
 
 }  // namespace pa

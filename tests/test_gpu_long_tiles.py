@@ -1,5 +1,4 @@
-"""Row tiles that take longer than a wait may: a role that waits for the end of one goes on as long as
-the roles that it waits for do."""
+"""Row tiles that take longer than a wait may: they are taken in segments, so that no wait is for all of one."""
 import numpy as np
 import pytest
 
@@ -20,13 +19,13 @@ def torch():
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("batch,q", [(4, 30), (1, 200)])
 def test_row_tiles_longer_than_the_limit(torch, call, bits, batch, q):
-    """32 row tiles of a million keys for all workers, some 3 ms each: most workers end one and begin another.
-    The limit stands at a quarter of a millisecond, a hundred times what a key tile takes. Keys of zero, so
+    """32 row tiles of two million keys for all workers, some 6 ms each: most workers end one and begin another.
+    The limit stands at 2 ms, twice what a segment of 65536 keys takes. Keys of zero, so
     that every weight is the same, values of 1 in three quarters of the blocks and -1 in the others:
     sums are of whole numbers below 2^24 (a power of two's multiples), so only the join of at most 152 parts
     (half a step each in the sums of weights and of values) and the result's rounding are off:
     2 * 152 * 2^-24 + 2^-12 < 3e-4 of 1/2 to 1."""
-    bs, nb, d, H, Hk, keys = 128, 64, 64, 32, 8, 2**20
+    bs, nb, d, H, Hk, keys = 128, 64, 64, 32, 8, 2**21
     cols, ones = keys // bs, keys // bs * 3 // 4
     g = torch.Generator(device="cuda").manual_seed(q)
     dtype = torch.float16 if bits == 16 else torch.float8_e4m3fn
@@ -48,7 +47,7 @@ def test_row_tiles_longer_than_the_limit(torch, call, bits, batch, q):
     else:
         step = pa.TreeStep(key, value.to(dtype), *exps, **shape)
         run = lambda: step.run(query, tables, lens, qs, None, out)  # noqa: E731
-    pa.testing_set_wait_limit(2**19)
+    pa.testing_set_wait_limit(2**22)
     try:
         run()
         assert step.status() == (pa.PA_OK, 0)
