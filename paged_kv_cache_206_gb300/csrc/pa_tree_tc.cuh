@@ -1377,15 +1377,11 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN, SEG>::kThreads, 1)
     // The largest exponent of the tile in slot `es`, unit u of the row tile, of the rows that are the context's
     // (WIN: attended by some row); of each kind the first part's warp tells the softmax, and whether
     // some lie far below it.
-    auto nothing = [&](int key) {
-      bool none = key >= t.L;
-      if constexpr (WIN) none = none || window_hidden(P, t.lo, key, 1);
-      return none;
-    };
     auto look = [&](int u, int es, int ph, int m, int& top) {
       if (!tree_wait(&exps_full[kv * Cfg::kExps + es], ph, P.wait_limit)) return false;
       const uint32_t e4 = *reinterpret_cast<const uint32_t*>(smem + Cfg::exps_off + es * 256 + kv * 128 + lane * 4);
-      const int key0 = key_of(t, u, lane >> 4) + (lane & 15) * 4, left = t.L - key0;  // this lane's four
+      // this lane's four (of trees not by key_of: the halves' own sums took trees of 16 from 92.5 to 94.6 us)
+      const int key0 = WIN ? key_of(t, u, lane >> 4) + (lane & 15) * 4 : u * TOK + lane * 4, left = t.L - key0;
       // (WIN: the keys between the sinks and the first row's window are nobody's)
       int behind = 0;
       uint32_t gap = 0;
@@ -1420,7 +1416,8 @@ __global__ void __launch_bounds__(TreeTc<HD, Q8, QT, WIN, SEG>::kThreads, 1)
         break;
       }
       for (int i = 0; i < tiles; ++i) {
-        const int key0 = key_of(t, t.s0 + i, part & 1) - (part & 1) * 64;  // of row 0, as this part counts
+        // of row 0, as this part counts
+        const int key0 = WIN ? key_of(t, t.s0 + i, part & 1) - (part & 1) * 64 : (t.s0 + i) * TOK;
         uint8_t* exps = smem + Cfg::exps_off + em * 256 + kv * 128;
         if (!tree_wait(&landed[2 * round], lphase, P.wait_limit)) {
           ok = false;
