@@ -28,22 +28,29 @@ struct TreeParams {
   uint32_t wait_limit;  // cycles a wait on another role's progress may take
 };
 
+// The status bit of a length (no word is there to tell it to on the host, where tests run the division of the work).
+__host__ __device__ __forceinline__ void tree_bad_length(const TreeParams& P) {
+#ifdef __CUDA_ARCH__
+  set_status(P.status, PA_STATUS_BIT_PLAN);
+#endif
+}
+
 // Whether a sequence's lengths keep the constraints.
-__device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int L) {
+__host__ __device__ __forceinline__ bool tree_lengths_ok(const TreeParams& P, int q, int L) {
   return q >= 0 && q <= P.max_q && q <= P.tokens && L >= q && L <= P.max_keys;
 }
 
 // Whether a row is padding although it counts as one: without q_seqlens, that of a sequence without keys.
-__device__ __forceinline__ bool tree_padding(const TreeParams& P, int L) { return !P.q_seqlens && L == 0; }
+__host__ __device__ __forceinline__ bool tree_padding(const TreeParams& P, int L) { return !P.q_seqlens && L == 0; }
 
 // Whether the tokens end before sequence rows begun at q_start do (the rows past them are left out).
-__device__ __forceinline__ bool tree_rows_missing(const TreeParams& P, int q_start, int q) {
+__host__ __device__ __forceinline__ bool tree_rows_missing(const TreeParams& P, int q_start, int q) {
   return P.tokens - q_start < q;
 }
 
 // a + b tokens, at most all of them: where the rows of a sequence begin is a sum of the
 // lengths before it, which may be any.
-__device__ __forceinline__ int tree_tokens(const TreeParams& P, int a, int b) {
+__host__ __device__ __forceinline__ int tree_tokens(const TreeParams& P, int a, int b) {
   return int(min(uint32_t(a) + uint32_t(b), uint32_t(P.tokens)));
 }
 

@@ -46,7 +46,7 @@ struct TreeSplit {
 };
 
 // a / b for a >= 0, b > 0: the 64-bit division takes several times the 32-bit one's time.
-__device__ __forceinline__ int64_t tree_div(int64_t a, int64_t b) {
+__host__ __device__ __forceinline__ int64_t tree_div(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
   return a / b;
 }

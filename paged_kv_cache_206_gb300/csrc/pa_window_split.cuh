@@ -30,9 +30,9 @@ struct WindowTile : TreeTile {
   int token0;     // the first row's token
 
   // where the c-th chunk stands in the sequence
-  __device__ __forceinline__ int chunk(int c) const { return c < far ? c : c + skip; }
+  __host__ __device__ __forceinline__ int chunk(int c) const { return c < far ? c : c + skip; }
   // the position of the first row's token
-  __device__ __forceinline__ int first() const { return L - q + token0; }
+  __host__ __device__ __forceinline__ int first() const { return L - q + token0; }
   // The token of the n-th row: the first one's and (its place in the group + n) / group, as a product with
   // 2^32 / group, which is exact while that and the group stay below 2^16.
   __device__ __forceinline__ int token(const TreeParams& P, int n) const {
@@ -90,7 +90,7 @@ template <int UNIT, int NR, int LEAD>
 struct WindowLine {
   int tt, parts;  // whole tokens of a tile, parts of a token's heads
 
-  __device__ __forceinline__ explicit WindowLine(const TreeSplit& S) : tt(S.tile_tokens), parts(S.tile_parts) {}
+  __host__ __device__ __forceinline__ explicit WindowLine(const TreeSplit& S) : tt(S.tile_tokens), parts(S.tile_parts) {}
 
   // Sequence b's tokens, and the tiles that they make for a kv head. The tokens count as stated (at
   // most all that there are) whether the lengths keep the constraints or not.
@@ -99,13 +99,13 @@ struct WindowLine {
   };
 
   // The keys between the sinks and the window of a token at position p.
-  static __device__ __forceinline__ int64_t left_out(const TreeParams& P, int64_t p) {
+  static __host__ __device__ __forceinline__ int64_t left_out(const TreeParams& P, int64_t p) {
     const int64_t n = p + 1 - P.window - P.sinks;
     return n > 0 ? n : 0;
   }
 
   // The places of the first t of a sequence's tiles.
-  __device__ __forceinline__ int64_t upto(const TreeParams& P, const Seq& s, int t) const {
+  __host__ __device__ __forceinline__ int64_t upto(const TreeParams& P, const Seq& s, int t) const {
     if (t == 0) return 0;
     if (s.tiles == 1) return s.L - left_out(P, s.L - s.q) + LEAD * UNIT;
     const int64_t n = t, pre = s.L - s.q, c = pre + 1 - P.window - P.sinks;
@@ -116,25 +116,25 @@ struct WindowLine {
     return sum;
   }
 
-  __device__ __forceinline__ Seq load(const TreeParams& P, int b) const {
+  __host__ __device__ __forceinline__ Seq load(const TreeParams& P, int b) const {
     if (b >= P.batch) return Seq{0, 0, 0};
     Seq s;
     s.q = P.q_seqlens ? P.q_seqlens[b] : 1;
     s.L = P.context_lens[b];
     const bool ok = tree_lengths_ok(P, s.q, s.L);
-    if (!ok && !tree_padding(P, s.L)) set_status(P.status, PA_STATUS_BIT_PLAN);
+    if (!ok && !tree_padding(P, s.L)) tree_bad_length(P);
     s.q = tree_tokens(P, 0, max(s.q, 0));
     s.tiles = !ok || s.q == 0 ? 0 : s.q <= tt ? 1 : (s.q - 1) / tt + 1;
     return s;
   }
   // Places of all parts of all kv heads.
-  __device__ __forceinline__ int64_t total(const TreeParams& P, const Seq& s) const {
+  __host__ __device__ __forceinline__ int64_t total(const TreeParams& P, const Seq& s) const {
     return upto(P, s, s.tiles) * (P.kv_heads * parts);
   }
 
   // The last worker whose piece begins before place u: total * k / n < u. (The product leaves 64 bits
   // for thousands of sequences of 2^30 keys only.)
-  static __device__ __forceinline__ int last_before(int64_t total, int64_t u, int n) {
+  static __host__ __device__ __forceinline__ int last_before(int64_t total, int64_t u, int n) {
     const int64_t k = u < (int64_t(1) << 44) ? tree_div(u * n - 1, total)
                                              : int64_t((static_cast<unsigned __int128>(u) * n - 1) / total);
     return min(int(k), n - 1);
@@ -151,6 +151,31 @@ struct WindowWalk {
   int head, tile;    // part of a kv head's heads, token tile
   int q_start, b, nact, worker;
   typename Line::Seq seq;
+
+  // The worker's piece of a line of `total` places; none for a worker that is not needed.
+  __host__ __device__ __forceinline__ bool share(const TreeSplit& S) {
+    nact = total >= int64_t(S.workers) * S.min_units ? S.workers : max(int(tree_div(total, S.min_units)), 1);
+    if (worker >= nact) return false;
+    // piece c begins at total * c / nact
+    const int64_t each = tree_div(total, nact), rest = total - each * nact;
+    u = u0 = each * worker + tree_div(rest * worker, nact);
+    u1 = each * (worker + 1) + tree_div(rest * (worker + 1), nact);
+    return true;
+  }
+
+  // The tile of the sequence at hand, which begins at place `before`, that place u0 belongs to: the last one that
+  // begins at or before it.
+  __host__ __device__ __forceinline__ void enter(const TreeParams& P, const Line& line, int64_t before) {
+    const int64_t of_head = line.upto(P, seq, seq.tiles);
+    head = int(tree_div(u0 - before, of_head));
+    at = before + head * of_head;
+    int end = seq.tiles;
+    while (end - tile > 1) {
+      const int mid = (tile + end) >> 1;
+      if (line.upto(P, seq, mid) <= u0 - at) tile = mid; else end = mid;
+    }
+    at += line.upto(P, seq, tile);
+  }
 
   __device__ __forceinline__ bool begin(const TreeParams& P, const TreeSplit& S, int w, int lane) {
     constexpr unsigned FULL = 0xffffffffu;
@@ -185,12 +210,7 @@ struct WindowWalk {
       for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(FULL, rest, o);
       total += rest;
     }
-    nact = total >= int64_t(S.workers) * S.min_units ? S.workers : max(int(tree_div(total, S.min_units)), 1);
-    if (worker >= nact) return false;
-    // piece c begins at total * c / nact
-    const int64_t each = tree_div(total, nact), rest = total - each * nact;
-    u = u0 = each * worker + tree_div(rest * worker, nact);
-    u1 = each * (worker + 1) + tree_div(rest * (worker + 1), nact);
+    if (!share(S)) return false;
     // the sequence that place u0 belongs to
     int64_t before = 0;
     for (int b0 = 0; b0 < P.batch && u0 < u1; b0 += 32) {
@@ -208,16 +228,7 @@ struct WindowWalk {
         seq.q = __shfl_sync(FULL, seq.q, l);
         seq.L = __shfl_sync(FULL, seq.L, l);
         seq.tiles = __shfl_sync(FULL, seq.tiles, l);
-        // its tile: the last one that begins at or before u0
-        const int64_t of_head = line.upto(P, seq, seq.tiles);
-        head = int(tree_div(u0 - before, of_head));
-        at = before + head * of_head;
-        int end = seq.tiles;
-        while (end - tile > 1) {
-          const int mid = (tile + end) >> 1;
-          if (line.upto(P, seq, mid) <= u0 - at) tile = mid; else end = mid;
-        }
-        at += line.upto(P, seq, tile);
+        enter(P, line, before);
         return true;
       }
       before += __shfl_sync(FULL, places, 31);
@@ -227,7 +238,7 @@ struct WindowWalk {
     return false;
   }
 
-  __device__ __forceinline__ bool next(const TreeParams& P, const TreeSplit& S, WindowTile& w) {
+  __host__ __device__ __forceinline__ bool next(const TreeParams& P, const TreeSplit& S, WindowTile& w) {
     const Line line(S);
     const int tt = line.tt, parts = line.parts;
     while (u < u1) {
@@ -275,7 +286,7 @@ struct WindowWalk {
         }
       }
       if (w.s0 == w.s1) continue;  // nothing but a lead, or less than a unit: the next worker's
-      if (missing) set_status(P.status, PA_STATUS_BIT_PLAN);
+      if (missing) tree_bad_length(P);
       w.slot = w.s0 == 0 && w.s1 == units ? -1 : 2 * worker + (first ? 0 : 1);
       w.parts = 0;
       if (w.s0 == 0 && w.s1 < units) w.parts = Line::last_before(total, end, nact) - worker + 1;
