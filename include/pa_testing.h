@@ -22,8 +22,8 @@ extern "C" {
 /*
  * pa_testing_set_wait_limit -- the cycle limit of the decode kernels' waits
  * (the CUDA-core, mma.sync and 64-row tcgen05 kernels) and of the tree
- * attention's, for every later pa_forward / pa_forward_device_plan /
- * pa_forward_noalloc / pa_tree_forward call of the
+ * and the windowed attention's, for every later pa_forward / pa_forward_device_plan /
+ * pa_forward_noalloc / pa_tree_forward / pa_window_forward call of the
  * process; 0 restores the default (about two seconds). Under a lowered limit
  * the CUDA-core and mma.sync kernels poll their copies without suspending, so
  * a copy that has not landed within the limit makes the wait run out; the

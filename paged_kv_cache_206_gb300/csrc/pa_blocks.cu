@@ -11,8 +11,8 @@
 // Chains of a few loads are all it is: 256 decode steps take 4.4 us, in a cluster of 8 CTAs as in one CTA
 // alone; the 8,000 blocks of 64 prompts are given back in 18 us by one CTA and in 6 by the cluster. The
 // places of the prompts' 130,000 tokens took the cluster 18 us; a grid behind it, whose CTAs each
-// sum the tokens again and whose threads take four at a time, takes 6 of which 4 lie under the
-// cluster's end.
+// sum the tokens again and whose threads take four at a time, takes 2 to 4 (its launch lies under the
+// cluster's end, its work behind it).
 #include <cuda_runtime.h>
 
 #include <algorithm>

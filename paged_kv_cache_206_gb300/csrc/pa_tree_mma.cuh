@@ -45,7 +45,7 @@ namespace pa {
 // of 128 dims in fp16, take 78 us for 416 MB, of which 6 pass before the first copies (the lengths from
 // memory 1, the place on the line 3, a look into the block table 1) and 3 at the join, and the slowest SM ends 10
 // behind the median one; without any arithmetic the copies take 75. A window of 4096 over 8 bits takes 80 to 90 for
-// 421 MB (copies alone 83 where it takes 91). One step with 1024 keys takes 14.3: the same 5, four
+// 421 MB, by the GPU (80.1, 88.5 and 89.9 on three of them; copies alone 83 where it took 91). One step with 1024 keys takes 14.3: the same 5, four
 // units 3, partial rows and their join 5.
 template <int HD, bool Q8, int NT, bool WIN, bool SEG>
 struct TreeMma {

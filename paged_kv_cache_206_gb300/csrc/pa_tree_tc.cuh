@@ -62,7 +62,7 @@ namespace pa {
 //                (the 8-bit cache's widening warps do that on the way); of heads of 128 dims and 256 rows they
 //                also write half of each row out
 // Sinks and window share a key tile by halves of 64 keys.
-// What it reaches: 18,700 tokens of prompts, window 1024, 32 heads on 8, in 318 us (0.97 PFLOP/s of the pairs that
+// What it reaches: 18,700 tokens of prompts, window 1024, 32 heads on 8, in 310 to 317 us (0.98 PFLOP/s of the pairs that
 // are attended, 49 % of the tensor pipe's time; chains of S, softmax and P V of two query tiles that wait for each
 // other); 8 x 512 tokens over 8 bits, window 2048, 32 heads, in 162 us (0.76; the widening warps share the schedulers
 // with the softmax, issue slots 42 % full).

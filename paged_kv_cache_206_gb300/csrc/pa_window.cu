@@ -23,7 +23,13 @@ pa_status check_window(const pa_config* cfg, const pa_window* win) {
 // one, else the warp-level tensor instructions with the least of 64, 128 and 256 dims that hold a head,
 // in tiles of 8 rows or several of 16. 32 sequences, 8 kv heads of 128 dims, window 1024: 20 rows take 41 us here and
 // 57 there in fp16, 53 and 43 in 8 bits; 32 rows 42 and 60, 53 and 46; 64 rows 44 and 107, 54 and 76.
-// Window 4096: 20 rows 99 and 178 us, 105 and 108; 32 rows 100 and 184, 106 and 111.
+// Window 4096: 20 rows 99 and 178 us, 105 and 108; 32 rows 100 and 184, 106 and 111. Of 64 dims, window
+// 1024: 20 rows 34 and 36 us in fp16, 36 rows 34 and 45, and 46 and 50 in 8 bits. Sizes that the tcgen05 kernel does not
+// have read the keys again for every 16 rows: prompts of 1024 to 8192 tokens, window 1024, take 3.5 ms at 256 dims
+// (2.0 in 8 bits) and 2.4 at 96 (1.9).
+// The rows are those of the longest sequence that the step allows, whatever the others are: 63 decode steps and a part
+// of 512 tokens, window 2048, take 129 us in one call, 86 and 36 in two (fp16; 154, and 50 and 41 in 8 bits), so
+// prompts' parts are better a call of their own.
 bool window_tiles(const pa_config& c, const TreeParams& P, bool q8, size_t* need, void* ws, cudaStream_t stream,
                   cudaError_t* e) {
   const int hd = c.head_size_k > c.head_size_v ? c.head_size_k : c.head_size_v;

@@ -109,6 +109,17 @@ def test_trees(torch, bits, case):
 
 
 @pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_segments_without_keys(torch, bits, kind):
+    """The last segment begins behind the own last key of the first row tile, of 64 tokens."""
+    c = TreeCase(torch, bits, [66, 3], [65538, 90], 4, 1, 64, 64, 128, kind, poison=waves)
+    c.step.cfg.num_sms = 1
+    c.run()
+    assert c.step.status() == (pa.PA_OK, 0)
+    c.check()
+
+
+@pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("q,H,d", [(2, 4, 128), (20, 4, 128), (70, 4, 128), (70, 4, 64)])
 def test_values_that_are_no_numbers_stay_in_the_rows_that_see_them(torch, bits, q, H, d):
     """One at the start of a window that the first rows see, in a segment before the last one; one that all see in
