@@ -148,6 +148,27 @@ def test_values_that_are_no_numbers_stay_in_the_rows_that_see_them(torch, bits, 
             <= np.delete(bound, [dim for _, dim in places], axis=2)).all()
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("q,H,Hk,d", [(1, 8, 2, 128), (4, 8, 2, 64), (3, 16, 4, 256), (16, 8, 2, 128), (40, 8, 2, 64),
+                                      (200, 4, 1, 128), (2, 6, 2, 96)])
+def test_the_forms_with_segments_give_the_same_bits(torch, bits, q, H, Hk, d):
+    """A batch of short contexts under tables that allow long ones."""
+    qs = [q, 1, q, max(q // 2, 1)] * 9
+    ctx = [n + 37 * i + 5 for i, n in enumerate(qs)]
+    window = WindowCase(torch, bits, qs, ctx, H, Hk, d, d, 64, 70000, 20)
+    tree = TreeCase(torch, bits, qs, ctx, H, Hk, d, d, 64, "tree")
+    for c, call, more in ((window, pa.WindowStep, dict(window=70000, sinks=20)), (tree, pa.TreeStep, {})):
+        want = c.run().clone()
+        wide = torch.full((len(qs), 2048), -1, dtype=torch.int32, device="cuda")
+        wide[:, :c.args[1].shape[1]] = c.args[1]
+        (k, ke), (v, ve) = c.dev
+        step = call(k, v, ke, ve, batch=len(qs), num_heads=H, max_seqlen_q=max(qs), max_blocks_per_seq=2048, **more)
+        out = torch.full_like(c.out, 7.0)
+        step.run(c.args[0], wide, *c.args[2:], out)
+        assert step.status() == c.step.status() == (pa.PA_OK, 0)
+        assert torch.equal(out, want)
+
+
 def test_the_workspace_of_long_contexts_has_room_for_them(torch):
     """A third slot a worker where a tile may have more than 65536 keys, and only there."""
     def need(keys, **kw):
